@@ -76,6 +76,11 @@ enum sfa_dtype { SFA_BF16 = 0, SFA_F32 = 1, SFA_Q8_0 = 2 };
                                  with SFA_ATTEND_KERNEL=ws, a bf16 V element at or above
                                  65520 in magnitude); the results involving it are not
                                  finite                                                  */
+#define SFA_DEV_BAD_LENGTH 0x40 /* sfa_build_page_maps: a negative length, more new tokens
+                                   than rows, or a sequence beyond its page table's row or
+                                   its cell map (those tokens get no cell)               */
+#define SFA_DEV_NO_PAGES 0x80   /* sfa_build_page_maps: the free list ran out: the pages
+                                   that it lacks are -1 in the page table                */
 
 /*
  * sfa_pool_index_keys -- one mean-pooled index key per block of compress_ratio tokens, taken
@@ -526,6 +531,105 @@ typedef struct {
     int64_t n_rows;
 } sfa_row_copy;
 int sfa_copy_cache_rows_multi(int n, const sfa_row_copy *copies, sfa_stream_t stream);
+
+/*
+ * One step of a paged cache, on the device.  Page g of the cache is the page_size consecutive
+ * cells from g * page_size; page_table [n_seq][table_stride] int32 gives the page of positions
+ * [k*page_size, (k+1)*page_size) of sequence s in entry [s][k].  A step is
+ *   sfa_build_page_maps     pages, cells and positions of the step's new tokens from lengths,
+ *   sfa_write_cells         their K, V and index-key rows into the cells,
+ *   sfa_chunk_attend_paged  their attention over everything cached, the new tokens included
+ * (or, through cell_of, sfa_pool_index_keys_paged, the indexer and sfa_gather_attend_paged).
+ * No call reads a length on the host: with fixed capacities the step is one CUDA graph.
+ *
+ * sfa_build_page_maps -- for each sequence s with a_s = len_old[s] cached tokens and
+ * n_s = len_new[s] new ones:
+ *   cu_new[s] = sum_{r<s} n_r (n_seq + 1 entries),  len_total[s] = a_s + n_s;
+ *   the pages of positions a_s .. a_s + n_s - 1 that its table does not hold yet (from page
+ *   ceil(a_s / page_size) on) are taken from free_pages [n_free], in order from entry
+ *   *free_head, sequence by sequence, and entered in page_table; *free_head_out is the first
+ *   entry not taken;
+ *   new token i = cu_new[s] + j: q_seq[i] = s, q_pos[i] = a_s + j and slot[i] = its cell; rows
+ *   i >= cu_new[n_seq] of the three (up to n_tok_cap, their length) get -1;
+ *   cell_of [n_seq][n_pos_cap], nullable: cell_of[s][a_s + j] = slot[i]; the entries of cached
+ *   positions are left as they are (they were written by the calls that cached them).
+ * A token with no cell -- its page is missing from the free list (SFA_DEV_NO_PAGES), is no page
+ * of [0, n_pages) (SFA_DEV_BAD_CELL) or lies beyond its table's row (SFA_DEV_BAD_LENGTH) -- gets
+ * slot -1, and a page that could not be taken -1 in the table.  Tokens past n_tok_cap are
+ * dropped (no row, not counted in cu_new and len_total) and flagged SFA_DEV_BAD_LENGTH;
+ * a negative length counts as 0, flagged likewise.
+ * One launch; the same lengths and free list give the same maps.  free_head_out may not be
+ * free_head, nor len_total one of the lengths.  Limits: n_seq <= 16384; n_pages * page_size,
+ * table_stride * page_size and n_tok_cap below 2^31.
+ */
+int sfa_build_page_maps(const int32_t *len_old, const int32_t *len_new, int n_seq, int page_size,
+                        const int32_t *free_pages, int64_t n_free, const int32_t *free_head,
+                        int n_pages, int32_t *page_table, int64_t table_stride, int32_t *cu_new,
+                        int32_t *len_total, int32_t *q_seq, int32_t *q_pos, int32_t *slot,
+                        int64_t n_tok_cap, int32_t *cell_of, int64_t n_pos_cap,
+                        int32_t *free_head_out, int32_t *dev_status, sfa_stream_t stream);
+
+/*
+ * sfa_write_cells -- for n (<= SFA_MAX_CELL_WRITES) caches at once, row i of src into cell
+ * slot[i], i < n_rows: the n_inner * d elements at src + i * src_stride (elements of src_dtype)
+ * become dst[slot[i]] of dst [n_cells][n_inner][d].  src_dtype SFA_BF16 or SFA_F32; dst_dtype
+ * the same (a copy), SFA_BF16 from SFA_F32 (rounded to nearest even), or SFA_Q8_0 (rows
+ * [n_cells][n_inner][sfa_q8_0_row_bytes(d)] by the rule of sfa_quantize_kv_q8_0; d in {64, 128,
+ * 512, 576}, finite inputs, SFA_DEV_FP16_RANGE as there).
+ * A negative slot is skipped (padding, a token without a cell); one >= n_cells is skipped and
+ * flagged SFA_DEV_BAD_CELL.  The slots of one call must differ (sfa_build_page_maps' do, if
+ * the free list holds each page once): two rows for one cell leave a mix of both there.
+ * One launch.  dst 16-byte aligned, src aligned to its type, src_stride >= n_inner * d.
+ * SFA_ERR_UNSUPPORTED for SFA_BF16 into SFA_F32.
+ */
+#define SFA_MAX_CELL_WRITES 4
+typedef struct {
+    const void *src;
+    int64_t src_stride;
+    void *dst;
+    int src_dtype, dst_dtype;
+    int n_inner, d;
+} sfa_cell_write;
+int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_t *slot, int64_t n_rows,
+                    int64_t n_cells, int32_t *dev_status, sfa_stream_t stream);
+
+/*
+ * sfa_chunk_attend_paged -- causal attention of each sequence's chunk of new tokens over its
+ * cached tokens, the chunk's own included, through the page table.  Query i = cu_new[s] + j of
+ * the n_s = cu_new[s+1] - cu_new[s] new tokens of sequence s sits at position
+ * p_i = len_total[s] - n_s + j:
+ *   O_ih = softmax_{t <= p_i}(scale Q_ih . K[cell(s, t)][g]) V[cell(s, t)][g],
+ *   cell(s, t) = page_table[s][t / page_size] * page_size + t % page_size,  g = h / (h_q / h_kv).
+ * The queries of a chunk and the heads of a KV head share every K/V tile, so a chunk costs
+ * tensor-core time and not a gather per query (sfa_dense_attend_paged); a chunk of one token is
+ * a decode step, its list split over the SMs.
+ *
+ *   Q    [n_q][h_q][dkq] bf16 (SFA_F32: fp32), the chunks packed; rows >= cu_new[n_seq] unread
+ *   K    [n_cells][h_kv][dkq], V [n_cells][h_kv][dv] of dtype, or V NULL: V = K[..., :dv];
+ *        SFA_Q8_0: q8_0 rows, Q bf16
+ *   O    [n_q][h_q][dv] of o_dtype (SFA_F32, or SFA_BF16: rounded once at the end);  lse
+ *        [n_q][h_q] fp32, nullable.  Rows of no chunk are left as they were.
+ *   n_new_max, n_kv_max: host bounds on the chunks' lengths and on len_total; they size the
+ *        work.  A longer chunk's first n_new_max queries and a longer list's first n_kv_max
+ *        keys are attended and SFA_DEV_BAD_QUERY is set, as it is for offsets that do not
+ *        ascend within [0, n_q] (an empty chunk) and for len_total[s] < n_s (positions below 0
+ *        attend nothing).
+ *   workspace: sfa_chunk_attend_workspace_bytes(...) bytes for the same arguments.
+ * A page table entry outside [0, n_cells / page_size) sets SFA_DEV_BAD_CELL; its positions are
+ * left out.  A query that attends nothing gives O = 0 and lse = -inf.  What unattended cells
+ * hold does not matter where no query of the chunk attends them (unwritten cells may hold NaN).
+ * Limits: (dkq, dv) in {(576, 512) with V NULL, (512, 512), (128, 128), (64, 64)}, h_q/h_kv <= 64.
+ * At most two launches.
+ */
+size_t sfa_chunk_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv, int dkq,
+                                        int dv, int has_v, int n_new_max, int64_t n_kv_max,
+                                        int o_dtype);
+int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtype, int64_t n_cells,
+                           const int32_t *page_table, int64_t table_stride, int page_size,
+                           int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv, float scale,
+                           const int32_t *cu_new, const int32_t *len_total, int n_new_max,
+                           int64_t n_kv_max, void *O, int o_dtype, float *lse, void *workspace,
+                           size_t workspace_bytes, int32_t *dev_status, sfa_stream_t stream);
 
 /* Copies *dev_status to *host_out after the work already enqueued on `stream` (this call
  * synchronises the stream). */

@@ -20,6 +20,7 @@ SFA_OK, SFA_ERR_INVALID_ARG, SFA_ERR_UNSUPPORTED, SFA_ERR_CUDA, SFA_ERR_WORKSPAC
 SFA_BF16, SFA_F32, SFA_Q8_0 = 0, 1, 2
 SFA_DEV_BAD_BLOCK, SFA_DEV_BAD_NSEL, SFA_DEV_BAD_QUERY, SFA_DEV_TIMEOUT = 1, 2, 4, 8
 SFA_DEV_BAD_CELL, SFA_DEV_FP16_RANGE = 16, 32
+SFA_DEV_BAD_LENGTH, SFA_DEV_NO_PAGES = 64, 128
 SFA_PART_ALL, SFA_PART_SELECTED, SFA_PART_WINDOW = 0, 1, 2
 SFA_REFINE_MAX_BLOCKS = 131072  # longest row sfa_topk_blocks_refine takes
 
@@ -34,7 +35,15 @@ class _RowCopy(ctypes.Structure):
                 ("row_bytes", ctypes.c_int64), ("n_rows", ctypes.c_int64)]
 
 
+class _CellWrite(ctypes.Structure):
+    """sfa_cell_write of include/sfa.h."""
+    _fields_ = [("src", ctypes.c_void_p), ("src_stride", ctypes.c_int64),
+                ("dst", ctypes.c_void_p), ("src_dtype", ctypes.c_int),
+                ("dst_dtype", ctypes.c_int), ("n_inner", ctypes.c_int), ("d", ctypes.c_int)]
+
+
 SFA_MAX_ROW_COPIES = 8
+SFA_MAX_CELL_WRITES = 4
 
 # name -> (restype, argtypes); mirrors include/sfa.h
 SIGNATURES = {
@@ -87,6 +96,14 @@ SIGNATURES = {
     "sfa_quantize_kv_q8_0": (_int, [_vp, _int, _i64, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
     "sfa_copy_cache_rows": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp]),
     "sfa_copy_cache_rows_multi": (_int, [_int, _vp, _vp]),
+    "sfa_build_page_maps": (_int, [_vp, _vp, _int, _int, _vp, _i64, _vp, _int, _vp, _i64, _vp,
+                                   _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "sfa_write_cells": (_int, [_int, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "sfa_chunk_attend_workspace_bytes": (_sz, [_int, _int, _int, _int, _int, _int, _int, _int,
+                                               _int, _i64, _int]),
+    "sfa_chunk_attend_paged": (_int, [_vp, _vp, _vp, _int, _i64, _vp, _i64, _int, _int, _int,
+                                      _int, _int, _int, _int, _f32, _vp, _vp, _int, _i64, _vp,
+                                      _int, _vp, _vp, _sz, _vp, _vp]),
     "sfa_read_device_status": (_int, [_vp, _vp, _vp]),
     "sfa_status_string": (ctypes.c_char_p, [_int]),
 }
@@ -563,6 +580,158 @@ def sfa_copy_cache_rows(dst, src, stream=None) -> None:
     rc = lib().sfa_copy_cache_rows(ctypes.c_void_p(dst.data_ptr()), dp,
                                    ctypes.c_void_p(src.data_ptr()), sp, row, n, _stream(stream))
     _check("sfa_copy_cache_rows", rc)
+
+
+def _one_device(first, *rest):
+    """The tensors' common CUDA device, checked; made the current one for the call (the library
+    launches on the current device)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("libsfa takes CUDA tensors only")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NO_GUARD
+
+
+class _NoGuard:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_GUARD = _NoGuard()
+
+
+def _i32_vec(name, t, n=None):
+    """t is a contiguous int32 vector (of n entries)."""
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, not {t.shape[0]}")
+
+
+def _page_table(page_table, n_seq):
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_seq:
+        raise ValueError(f"page_table must be an int32 [{n_seq}][pages] tensor")
+
+
+def sfa_build_page_maps(len_old, len_new, page_size: int, free_pages, free_head, n_pages: int,
+                        page_table, cu_new, len_total, q_seq, q_pos, slot, free_head_out,
+                        cell_of=None, dev_status=None, stream=None):
+    """One step's bookkeeping of a paged cache on the device: pages from free_pages (from entry
+    free_head on) into page_table, the new tokens' sequences, positions and cells (q_seq, q_pos,
+    slot: rows past the last token get -1), the packed offsets cu_new [n_seq + 1], len_total, and
+    the new positions' entries of the per-position map cell_of [n_seq][n_pos] when given."""
+    n_seq, n_tok = len_old.shape[0], slot.shape[0]
+    for name, t, n in (("len_old", len_old, None), ("len_new", len_new, n_seq),
+                       ("free_pages", free_pages, None), ("free_head", free_head, 1),
+                       ("cu_new", cu_new, n_seq + 1), ("len_total", len_total, n_seq),
+                       ("slot", slot, None), ("q_seq", q_seq, n_tok), ("q_pos", q_pos, n_tok),
+                       ("free_head_out", free_head_out, 1)):
+        _i32_vec(name, t, n)
+    _page_table(page_table, n_seq)
+    n_pos = 0
+    if cell_of is not None:
+        if cell_of.shape[0] != n_seq:
+            raise ValueError(f"cell_of must have {n_seq} rows")
+        _, n_pos, _ = _paged_dims(cell_of, None)
+    with _one_device(len_old, len_new, free_pages, free_head, page_table, cu_new, len_total, q_seq,
+                     q_pos, slot, free_head_out, cell_of, dev_status):
+        rc = lib().sfa_build_page_maps(
+            _p(len_old), _p(len_new), n_seq, page_size, _p(free_pages), free_pages.shape[0],
+            _p(free_head), n_pages, _p(page_table), page_table.shape[1], _p(cu_new),
+            _p(len_total), _p(q_seq), _p(q_pos), _p(slot), n_tok, _p(cell_of), n_pos,
+            _p(free_head_out), _p(dev_status), _stream(stream))
+    _check("sfa_build_page_maps", rc)
+
+
+def _cell_write(src, dst, n_rows, n_cells):
+    if src.dim() == 2:      # [rows][d]: one inner row
+        src = src.unsqueeze(1)
+    if dst.dim() == 2:
+        dst = dst.unsqueeze(1)
+    n, h, d = src.shape
+    q8 = dst.dtype == torch.uint8
+    row = sfa_q8_0_row_bytes(d) if q8 else d
+    if n < n_rows or tuple(dst.shape) != (n_cells, h, row) or not dst.is_contiguous():
+        raise ValueError(f"a cache of these rows is a contiguous [{n_cells}][{h}][{row}] tensor "
+                         f"and they are at least {n_rows}")
+    if src.dtype == torch.uint8 or (d > 1 and src.stride(2) != 1) or (h > 1 and src.stride(1) != d):
+        raise ValueError("the rows are bf16 or fp32, each contiguous")
+    return _CellWrite(src.data_ptr(), src.stride(0) if n > 1 else h * d, dst.data_ptr(),
+                      _dtype_code(src), _dtype_code(dst), h, d)
+
+
+def sfa_write_cells(writes, slot, dev_status=None, stream=None):
+    """For every (rows, cache) pair of writes, at most SFA_MAX_CELL_WRITES, in one launch: row i
+    of rows ([n][d] or [n][h][d], rows at any stride) into cell slot[i] of cache ([n_cells][d] or
+    [n_cells][h][d], of the same type, bf16 for fp32 rows, or uint8 q8_0 rows).  Negative slots
+    are skipped; the others must differ."""
+    writes = list(writes)
+    if len(writes) > SFA_MAX_CELL_WRITES:
+        raise ValueError(f"at most {SFA_MAX_CELL_WRITES} caches per call")
+    _i32_vec("slot", slot)
+    if not writes:
+        return
+    n_rows, n_cells = slot.shape[0], writes[0][1].shape[0]
+    arr = (_CellWrite * len(writes))(*[_cell_write(x, y, n_rows, n_cells) for x, y in writes])
+    with _one_device(slot, dev_status, *[t for w in writes for t in w]):
+        rc = lib().sfa_write_cells(len(writes), ctypes.cast(arr, ctypes.c_void_p), _p(slot), n_rows,
+                                   n_cells, _p(dev_status), _stream(stream))
+    _check("sfa_write_cells", rc)
+
+
+def sfa_chunk_attend_workspace_bytes(dtype_code: int, n_seq: int, n_q: int, h_q: int, h_kv: int,
+                                     dkq: int, dv: int, has_v: bool, n_new_max: int, n_kv_max: int,
+                                     o_dtype: int = SFA_F32) -> int:
+    return int(lib().sfa_chunk_attend_workspace_bytes(dtype_code, n_seq, n_q, h_q, h_kv, dkq, dv,
+                                                      int(has_v), n_new_max, n_kv_max, o_dtype))
+
+
+def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_total, n_new_max: int,
+                           n_kv_max: int, scale: float, O, lse=None, workspace=None,
+                           dev_status=None, stream=None):
+    """Causal attention of each sequence's chunk of new tokens (rows cu_new[s] .. cu_new[s + 1] of
+    Q [n_q][h_q][dkq]) over its len_total[s] cached tokens, the chunk's own included: K
+    [n_cells][h_kv][dkq] and V [n_cells][h_kv][dv] or None, through page_table [n_seq][pages].
+    O [n_q][h_q][dv] fp32 or bf16, lse [n_q][h_q] fp32."""
+    n_q, h_q, dkq = Q.shape
+    n_cells, h_kv, _ = K.shape
+    n_seq, dv = len_total.shape[0], O.shape[-1]
+    _check_qkv(Q, K, V)
+    _i32_vec("len_total", len_total)
+    _i32_vec("cu_new", cu_new, n_seq + 1)
+    _page_table(page_table, n_seq)
+    code = _dtype_code(K)
+    row = (lambda d: sfa_q8_0_row_bytes(d)) if code == SFA_Q8_0 else (lambda d: d)
+    if K.shape[2] != row(dkq):
+        raise ValueError("Q and K must share a head size")
+    if V is not None and tuple(V.shape) != (n_cells, h_kv, row(dv)):
+        raise ValueError("V must be [n_cells][h_kv][dv] like K")
+    if tuple(O.shape) != (n_q, h_q, dv) or O.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("O must be an fp32 or bf16 [n_q][h_q][dv] tensor")
+    if lse is not None and (tuple(lse.shape) != (n_q, h_q) or lse.dtype != torch.float32):
+        raise ValueError("lse must be an fp32 [n_q][h_q] tensor")
+    o_code = _dtype_code(O)
+    with _one_device(Q, K, V, page_table, cu_new, len_total, O, lse, workspace, dev_status):
+        if workspace is None:
+            need = lib().sfa_chunk_attend_workspace_bytes(code, n_seq, n_q, h_q, h_kv, dkq, dv,
+                                                          int(V is not None), n_new_max, n_kv_max,
+                                                          o_code)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+                if stream is not None:   # freed on return: not before that stream is done
+                    workspace.record_stream(stream)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib().sfa_chunk_attend_paged(
+            _p(Q), _p(K), _p(V), code, n_cells, _p(page_table), page_table.shape[1], page_size,
+            n_seq, n_q, h_q, h_kv, dkq, dv, float(scale), _p(cu_new), _p(len_total), n_new_max,
+            n_kv_max, _p(O), o_code, _p(lse), _p(workspace), ws_bytes, _p(dev_status),
+            _stream(stream))
+    _check("sfa_chunk_attend_paged", rc)
 
 
 def sfa_read_device_status(dev_status, stream=None) -> int:

@@ -1,0 +1,460 @@
+// chunk.cu -- causal attention of each sequence's chunk of new tokens over its pages
+// (sfa_chunk_attend_paged): the SIMT kernel, the merge of split lists, the launch plan and the
+// C entry points.
+#include "chunk_common.cuh"
+
+namespace sfa {
+namespace chunk {
+namespace {
+
+// ------------------------------------------------------------------------------ SIMT kernel
+// One CTA: 32 rows (query, head) of one KV head against TK keys at a time, everything in fp32:
+// eight warps each score an eighth of the head dim (4 x TK / 4 products a lane from registers,
+// 16-byte shared loads), the eight sums and the softmax meet in shared memory, and the value
+// dims are split over all threads.  fp32 caches take it (the tensor cores have no fp32 kind),
+// and q8_0 ones.
+constexpr int kRows = 32;
+constexpr int kThreads = 256;
+
+template <int DKQ, int DV, bool VK>
+struct Simt {
+    static constexpr int TK = DKQ > 128 ? 16 : 32;
+    static constexpr int PK = DKQ + 4, PV = DV + 4;   // row pitches: conflict-free 16-byte reads
+    static constexpr int kFloats = kRows * PK + TK * PK + (VK ? 0 : TK * PV) + 8 * kRows * TK +
+                                   TK * kRows + 3 * kRows;
+    static constexpr size_t bytes() { return kFloats * 4 + TK * 8; }
+};
+
+__device__ __forceinline__ float4 load4(const void *base, int64_t elem, int dtype) {
+    if (dtype == SFA_F32) return *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + elem);
+    const uint2 u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + elem);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+// Rows (cell, g) of a cache into shared memory as fp32: D elements at pitch D + 4, zeros where
+// the cell is -1.
+template <int D>
+__device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype, const int64_t *cells,
+                                          int n, int h_kv, int g) {
+    constexpr int C = D / 4;
+    for (int e = threadIdx.x; e < n * C; e += kThreads) {
+        const int r = e / C, c = e - r * C;
+        const int64_t cell = cells[r];
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (cell >= 0) {
+            const int64_t row = cell * h_kv + g;
+            if (dtype == SFA_Q8_0) {
+                const uint8_t *y = reinterpret_cast<const uint8_t *>(src) + row * q8_row_bytes(D);
+                const char4 q = *reinterpret_cast<const char4 *>(y + 4 * c);
+                const float s = __half2float(*reinterpret_cast<const __half *>(y + D + 2 * (c / 8)));
+                v = make_float4(s * q.x, s * q.y, s * q.z, s * q.w);
+            } else {
+                v = load4(src, row * D + 4 * c, dtype);
+            }
+        }
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + 4 * c) = v;
+    }
+}
+
+// Writes four value dims of one row: the result, or a partial one of a split list.
+__device__ __forceinline__ void store4(const Params &p, int64_t row, int dv, int d, float4 v) {
+    if (p.o_bf16)
+        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + row * dv + d) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    else
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + row * dv + d) = v;
+}
+
+template <int DKQ, int DV, bool VK>
+__global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, int dtype) {
+    using L = Simt<DKQ, DV, VK>;
+    constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV;
+    extern __shared__ __align__(16) float sm[];
+    float *sQ = sm, *sK = sQ + kRows * PK, *sV = VK ? sK : sK + TK * PK;
+    float *sRed = (VK ? sK + TK * PK : sV + TK * L::PV);
+    float *sP = sRed + 8 * kRows * TK;    // [key][row]
+    float *sM = sP + TK * kRows, *sL = sM + kRows, *sA = sL + kRows;
+    int64_t *sCell = reinterpret_cast<int64_t *>(sA + kRows);
+    __shared__ Item s_item;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = blockIdx.z, g = blockIdx.y;
+    pdl_wait();
+    if (warp == 0) {
+        const Item it = find_item(p, blockIdx.x, blockIdx.x == 0 && g == 0 && split == 0);
+        if (lane == 0) s_item = it;
+    }
+    __syncthreads();
+    const Item it = s_item;
+    if (it.seq < 0) return;
+    const int r0 = it.tile * kRows;                        // first flattened row
+    const int n = min(it.q.n, p.n_new_max);
+    const int rows = min(kRows, (int)((int64_t)n * p.G - r0));
+    const int pos0 = it.q.total - it.q.n;                  // position of the chunk's first query
+    const int p_last = pos0 + (r0 + rows - 1) / p.G;
+    const int len = max(0, min(key_limit(p, it.q), p_last + 1));
+    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
+    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
+    const bool whole = len <= p.split_keys;                // this piece is the whole list
+    if (split > 0 && k0 >= k1) return;                     // no such piece
+
+    for (int e = tid; e < kRows * (DKQ / 4); e += kThreads) {
+        const int r = e / (DKQ / 4), c = e - r * (DKQ / 4);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            const int q = (r0 + r) / p.G, h = g * p.G + (r0 + r) % p.G;
+            v = load4(p.Q, ((int64_t)(it.q.c0 + q) * p.h_q + h) * DKQ + 4 * c,
+                      dtype == SFA_F32 ? SFA_F32 : SFA_BF16);
+        }
+        *reinterpret_cast<float4 *>(sQ + r * PK + 4 * c) = v;
+    }
+    if (tid < kRows) {
+        sM[tid] = -INFINITY;
+        sL[tid] = 0.f;
+    }
+    constexpr int CG = DV / 4;                  // column groups of 4 value dims
+    constexpr int RPT = kRows * CG / kThreads;  // rows of a thread's tile
+    static_assert(RPT >= 1 && kRows * CG % kThreads == 0, "the value dims split evenly");
+    const int cg = tid % CG, rg = tid / CG;
+    float acc[RPT][4];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+
+    for (int t0 = k0; t0 < k1; t0 += TK) {
+        __syncthreads();   // the previous tile is done with shared memory
+        if (tid < TK) sCell[tid] = t0 + tid < k1 ? cell_of(p, it.seq, t0 + tid) : -1;
+        __syncthreads();
+        load_rows<DKQ>(sK, p.K, dtype, sCell, TK, p.h_kv, g);
+        if constexpr (!VK) load_rows<DV>(sV, p.V, dtype, sCell, TK, p.h_kv, g);
+        __syncthreads();
+        {   // scores: warp w takes dims [w DKQ / 8, (w + 1) DKQ / 8)
+            constexpr int KPT = TK / 4;
+            float s[4][KPT];
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < KPT; ++b) s[a][b] = 0.f;
+            const float *q = sQ + (lane & 7) * PK, *k = sK + (lane >> 3) * PK;
+            for (int d = warp * (DKQ / 8); d < (warp + 1) * (DKQ / 8); d += 4) {
+                float4 x[4], y[KPT];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4 *>(q + 8 * a * PK + d);
+#pragma unroll
+                for (int b = 0; b < KPT; ++b) y[b] = *reinterpret_cast<const float4 *>(k + 4 * b * PK + d);
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < KPT; ++b)
+                        s[a][b] = fmaf(x[a].w, y[b].w, fmaf(x[a].z, y[b].z,
+                                  fmaf(x[a].y, y[b].y, fmaf(x[a].x, y[b].x, s[a][b]))));
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < KPT; ++b)
+                    sRed[(warp * kRows + 8 * a + (lane & 7)) * TK + 4 * b + (lane >> 3)] = s[a][b];
+        }
+        __syncthreads();
+        {   // softmax of row tid / 8: TK / 8 keys a thread
+            constexpr int KPT = TK / 8;
+            const int r = tid >> 3, kk = tid & 7;
+            const int pos = pos0 + (r0 + r) / p.G;
+            float s[KPT], mx = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < KPT; ++b) {
+                const int k = kk + 8 * b;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) v += sRed[(w * kRows + r) * TK + k];
+                s[b] = sCell[k] >= 0 && t0 + k <= pos ? v * p.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[b]);
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            const float mo = sM[r], mn = fmaxf(mo, mx);
+            float sum = 0.f;
+#pragma unroll
+            for (int b = 0; b < KPT; ++b) {
+                const float e = s[b] == -INFINITY ? 0.f : exp2f(s[b] - mn);
+                sP[(kk + 8 * b) * kRows + r] = e;
+                sum += e;
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            const float al = mn == -INFINITY ? 1.f : exp2f(mo - mn);
+            __syncwarp();
+            if (kk == 0) {
+                sM[r] = mn;
+                sL[r] = sL[r] * al + sum;
+                sA[r] = al;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+            const float al = sA[rg * RPT + r];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[r][c] *= al;
+        }
+#pragma unroll 4
+        for (int k = 0; k < TK; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(sV + k * PV + 4 * cg);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+                const float e = sP[k * kRows + rg * RPT + r];
+                if (e == 0.f) continue;   // a key this row does not attend may hold NaN
+                acc[r][0] = fmaf(e, v.x, acc[r][0]);
+                acc[r][1] = fmaf(e, v.y, acc[r][1]);
+                acc[r][2] = fmaf(e, v.z, acc[r][2]);
+                acc[r][3] = fmaf(e, v.w, acc[r][3]);
+            }
+        }
+    }
+    __syncthreads();
+    const int64_t part0 = (((int64_t)blockIdx.x * p.h_kv + g) * p.n_split + split) * kRows;
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const int row = rg * RPT + r;
+        if (row >= rows) break;
+        const float l = sL[row], m = sM[row];
+        if (whole) {
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // no key: zeros; NaN stays
+            const int64_t o = (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
+            store4(p, o, DV, 4 * cg, make_float4(acc[r][0] * inv, acc[r][1] * inv, acc[r][2] * inv, acc[r][3] * inv));
+            if (cg == 0 && p.lse) p.lse[o] = l > 0.f || l != l ? (m + log2f(l)) / kLog2e : -INFINITY;
+        } else {
+            *reinterpret_cast<float4 *>(p.part_o + (part0 + row) * DV + 4 * cg) =
+                make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+            if (cg == 0) {
+                p.part_ml[(part0 + row) * 2] = m;
+                p.part_ml[(part0 + row) * 2 + 1] = l;
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------- split merge
+// One CTA per (row tile, KV head, 8 rows), a warp per row: the pieces' (m, l) first, then their
+// weighted partial rows, 16 bytes a lane.  Lists of one piece were written by the attention
+// kernel itself.
+template <int DV>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
+    __shared__ Item s_item;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.y;
+    pdl_wait();
+    if (warp == 0) {
+        const Item it = find_item(p, blockIdx.x, false);
+        if (lane == 0) s_item = it;
+    }
+    __syncthreads();
+    const Item it = s_item;
+    if (it.seq < 0) return;
+    const int n = min(it.q.n, p.n_new_max);
+    int rows, q0, r0;   // rows of the tile; its first query, or its first flattened row
+    if (p.item_q > 0) {
+        q0 = it.tile * p.item_q;
+        r0 = q0 * p.G;
+        rows = min(p.item_q, n - q0) * p.G;
+    } else {
+        r0 = it.tile * p.item_rows;
+        rows = min(p.item_rows, (int)((int64_t)n * p.G - r0));
+    }
+    const int row = blockIdx.z * 8 + warp;
+    if (row >= rows) return;
+    const int p_last = it.q.total - it.q.n + (r0 + rows - 1) / p.G;
+    const int len = max(0, min(key_limit(p, it.q), p_last + 1));
+    if (len <= p.split_keys) return;
+    const int ns = (len + p.split_keys - 1) / p.split_keys;
+    const int64_t part0 = ((int64_t)blockIdx.x * p.h_kv + g) * p.n_split * p.item_rows + row;
+    float M = -INFINITY;
+    for (int c = lane; c < ns; c += 32) M = fmaxf(M, p.part_ml[(part0 + (int64_t)c * p.item_rows) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    constexpr int C = (DV + 127) / 128;
+    float4 acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int c = 0; c < ns; ++c) {
+        const int64_t r = part0 + (int64_t)c * p.item_rows;
+        const float m = p.part_ml[r * 2], w = m == -INFINITY ? 0.f : exp2f(m - M);
+        const float lc = p.part_ml[r * 2 + 1];
+        l += lc == 0.f ? 0.f : w * lc;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            if (k * 128 + lane * 4 < DV) {
+                const float4 v = *reinterpret_cast<const float4 *>(p.part_o + r * DV + k * 128 + lane * 4);
+                acc[k].x = fmaf(w, v.x, acc[k].x);
+                acc[k].y = fmaf(w, v.y, acc[k].y);
+                acc[k].z = fmaf(w, v.z, acc[k].z);
+                acc[k].w = fmaf(w, v.w, acc[k].w);
+            }
+        }
+    }
+    const bool any = l > 0.f || l != l;
+    const float inv = any ? 1.f / l : 0.f;
+    const int64_t o = (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+        if (k * 128 + lane * 4 < DV)
+            store4(p, o, DV, k * 128 + lane * 4, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+    if (lane == 0 && p.lse) p.lse[o] = any ? (M + log2f(l)) / kLog2e : -INFINITY;
+}
+
+// --------------------------------------------------------------------------------- the plan
+struct Plan {
+    int item_rows, item_q, items, n_split, split_keys;
+};
+
+// Row tiles of n_q queries in n_seq chunks of at most n_new_max, at most.
+int64_t items_bound(int n_seq, int n_q, int G, int n_new_max, int item_rows, int item_q) {
+    const int64_t per = item_q > 0 ? ((int64_t)n_new_max + item_q - 1) / item_q
+                                   : ((int64_t)n_new_max * G + item_rows - 1) / item_rows;
+    const int64_t all = (item_q > 0 ? n_q / item_q : (int64_t)n_q * G / item_rows) + n_seq;
+    return per * n_seq < all ? per * n_seq : all;
+}
+
+// The lists are cut so that the items fill the SMs: enough equal pieces of whole key tiles.
+Plan make_plan(int n_seq, int n_q, int G, int h_kv, int n_new_max, int64_t n_kv_max) {
+    Plan pl;
+    pl.item_rows = kRows;
+    pl.item_q = 0;
+    const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
+    pl.items = (int)(items > 0x7FFFFFFF ? 0x7FFFFFFF : items);
+    const int tile = 128;
+    const int64_t tiles = (n_kv_max + tile - 1) / tile;
+    int64_t ns = device_sm_count() / (items * h_kv > 0 ? items * h_kv : 1);
+    ns = ns < 1 ? 1 : ns > tiles ? tiles : ns;
+    ns = ns < 1 ? 1 : ns > 64 ? 64 : ns;
+    const int64_t per = (tiles + ns - 1) / ns;
+    pl.split_keys = (int)(per > 0 ? per * tile : tile);
+    pl.n_split = (int)((tiles + (per > 0 ? per : 1) - 1) / (per > 0 ? per : 1));
+    if (pl.n_split < 1) pl.n_split = 1;
+    return pl;
+}
+
+size_t plan_workspace(const Plan &pl, int h_kv, int dv) {
+    if (pl.n_split == 1) return 0;
+    return (size_t)pl.items * h_kv * pl.n_split * pl.item_rows * ((size_t)dv + 2) * sizeof(float);
+}
+
+bool shape_ok(int dkq, int dv, bool has_v) {
+    return (dkq == 576 && dv == 512 && !has_v) || (dkq == 512 && dv == 512) ||
+           (dkq == 128 && dv == 128) || (dkq == 64 && dv == 64);
+}
+
+template <int DKQ, int DV, bool VK>
+int launch_simt(const Params &p, int dtype, cudaStream_t st) {
+    if (!ensure_max_dynamic_smem(chunk_simt_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_simt_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+                   Simt<DKQ, DV, VK>::bytes(), st, p, dtype) != cudaSuccess) {
+        cudaGetLastError();
+        return SFA_ERR_CUDA;
+    }
+    return SFA_OK;
+}
+
+template <int DV>
+int launch_combine(const Params &p, cudaStream_t st) {
+    if (launch_pdl(chunk_combine_kernel<DV>, dim3(p.items, p.h_kv, (p.item_rows + 7) / 8), dim3(256),
+                   0, st, p) != cudaSuccess) {
+        cudaGetLastError();
+        return SFA_ERR_CUDA;
+    }
+    return SFA_OK;
+}
+
+// Sizes the plan and the workspace query share; SFA_OK, or what the entry point returns.
+int check_sizes(int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv, bool has_v, int n_new_max,
+                int64_t n_kv_max) {
+    if (n_seq < 0 || n_q < 0 || h_kv < 1 || h_q < 1 || h_q % h_kv != 0 || n_new_max < 0 ||
+        n_kv_max < 0 || n_kv_max > 0x7FFFFFFF)
+        return SFA_ERR_INVALID_ARG;
+    if (!has_v && dv > dkq) return SFA_ERR_INVALID_ARG;
+    if (!shape_ok(dkq, dv, has_v) || h_q / h_kv > 64 || h_kv > 65535) return SFA_ERR_UNSUPPORTED;
+    if ((int64_t)n_q * h_q > 0x7FFFFFFF) return SFA_ERR_UNSUPPORTED;
+    return SFA_OK;
+}
+
+}  // namespace
+}  // namespace chunk
+}  // namespace sfa
+
+extern "C" size_t sfa_chunk_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv,
+                                                   int dkq, int dv, int has_v, int n_new_max,
+                                                   int64_t n_kv_max, int o_dtype) {
+    using namespace sfa::chunk;
+    (void)dtype;
+    (void)o_dtype;
+    if (check_sizes(n_seq, n_q, h_q, h_kv, dkq, dv, has_v != 0, n_new_max, n_kv_max) != SFA_OK) return 0;
+    if (n_seq == 0 || n_q == 0 || n_new_max == 0) return 0;
+    return plan_workspace(make_plan(n_seq, n_q, h_q / h_kv, h_kv, n_new_max, n_kv_max), h_kv, dv);
+}
+
+extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtype,
+                                      int64_t n_cells, const int32_t *page_table,
+                                      int64_t table_stride, int page_size, int n_seq, int n_q,
+                                      int h_q, int h_kv, int dkq, int dv, float scale,
+                                      const int32_t *cu_new, const int32_t *len_total,
+                                      int n_new_max, int64_t n_kv_max, void *O, int o_dtype,
+                                      float *lse, void *workspace, size_t workspace_bytes,
+                                      int32_t *dev_status, sfa_stream_t stream) {
+    using namespace sfa;
+    using namespace sfa::chunk;
+    if (dtype != SFA_BF16 && dtype != SFA_F32 && dtype != SFA_Q8_0) return SFA_ERR_INVALID_ARG;
+    if (o_dtype != SFA_BF16 && o_dtype != SFA_F32) return SFA_ERR_INVALID_ARG;
+    const int rc = check_sizes(n_seq, n_q, h_q, h_kv, dkq, dv, V != nullptr, n_new_max, n_kv_max);
+    if (rc != SFA_OK) return rc;
+    if (page_size < 1 || table_stride < 0 || table_stride > 0x7FFFFFFF ||
+        table_stride * page_size > 0x7FFFFFFF || n_cells < 0 || n_cells > 0x7FFFFFFF)
+        return SFA_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale - scale != 0.f) return SFA_ERR_INVALID_ARG;
+    if (n_seq == 0 || n_q == 0 || n_new_max == 0) return SFA_OK;
+    if (!Q || !K || !page_table || !cu_new || !len_total || !O) return SFA_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(lse) ||
+        !aligned16(workspace))
+        return SFA_ERR_INVALID_ARG;
+    const Plan pl = make_plan(n_seq, n_q, h_q / h_kv, h_kv, n_new_max, n_kv_max);
+    const size_t need = plan_workspace(pl, h_kv, dv);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SFA_ERR_WORKSPACE;
+    Params p{};
+    p.Q = Q;
+    p.K = K;
+    p.V = V;
+    p.table = page_table;
+    p.cu = cu_new;
+    p.total = len_total;
+    p.O = O;
+    p.lse = lse;
+    p.part_o = reinterpret_cast<float *>(workspace);
+    p.part_ml = need > 0 ? p.part_o + (size_t)pl.items * h_kv * pl.n_split * pl.item_rows * dv : nullptr;
+    p.status = dev_status;
+    p.table_stride = table_stride;
+    p.page = page_size;
+    p.n_pages = (int)(n_cells / page_size);
+    p.n_seq = n_seq;
+    p.n_q = n_q;
+    p.h_q = h_q;
+    p.h_kv = h_kv;
+    p.G = h_q / h_kv;
+    p.o_bf16 = o_dtype == SFA_BF16;
+    p.items = pl.items;
+    p.item_rows = pl.item_rows;
+    p.item_q = pl.item_q;
+    p.n_split = pl.n_split;
+    p.split_keys = pl.split_keys;
+    p.n_new_max = n_new_max;
+    p.n_kv_max = n_kv_max;
+    p.scale_log2 = scale * kLog2e;
+    cudaStream_t st = (cudaStream_t)stream;
+    int r;
+    if (dkq == 576) r = launch_simt<576, 512, true>(p, dtype, st);
+    else if (dkq == 512) r = V ? launch_simt<512, 512, false>(p, dtype, st) : launch_simt<512, 512, true>(p, dtype, st);
+    else if (dkq == 128) r = V ? launch_simt<128, 128, false>(p, dtype, st) : launch_simt<128, 128, true>(p, dtype, st);
+    else r = V ? launch_simt<64, 64, false>(p, dtype, st) : launch_simt<64, 64, true>(p, dtype, st);
+    if (r != SFA_OK || pl.n_split == 1) return r;
+    return dv == 512 ? launch_combine<512>(p, st) : dv == 128 ? launch_combine<128>(p, st) : launch_combine<64>(p, st);
+}

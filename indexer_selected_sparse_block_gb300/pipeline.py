@@ -1,4 +1,5 @@
-"""One step of indexer-selected block-sparse attention through the C ABI, with its buffers.
+"""One step of indexer-selected block-sparse attention through the C ABI, with its buffers
+(``SfaStep``), and a paged cache with its bookkeeping on the device (``SfaPagedCache``).
 
 ``SfaStep`` owns the intermediate device buffers of the method (pooled keys, block scores,
 kept block lists, workspaces, outputs) and runs the stages as the C entry points:
@@ -246,3 +247,86 @@ class SfaStep:
             self.select(q_idx, w, q_seq, q_pos, stream=stream)
         self.attend(Q, K, V, q_seq, q_pos, scale, stream=stream)
         return self.O
+
+
+class SfaPagedCache:
+    """A paged cache of n_seq sequences with its device-side bookkeeping: the cells of K (V, and
+    the index keys X), the page table, the free list, the lengths, and the per-step buffers.
+
+      step(len_new, K, V, X)   the step's tokens get pages and cells (sfa_build_page_maps) and
+                               their rows are written into them (sfa_write_cells)
+      attend(Q, ...)           the new tokens' causal attention over their sequences
+                               (sfa_chunk_attend_paged)
+      release(seq)             a finished sequence's pages return to the free list
+
+    Neither step nor attend reads a length on the host, allocates (given a workspace) or
+    synchronises: with len_new, the rows and Q in fixed buffers they can be captured in a CUDA
+    graph (SfaStep.graphed), whose replays advance the lengths.  Rows past the step's last token
+    are padding.  cell_of is the position -> cell map the other paged entry points and SfaStep
+    take (pass the cache's X, K, V to them); q_seq and q_pos are the new tokens' sequences and
+    positions."""
+
+    def __init__(self, *, n_seq: int, n_pages: int, page_size: int, max_pages: int, n_tok_cap: int,
+                 h_kv: int, dkq: int, dv: int, separate_v: bool = False, d_idx: int = 0,
+                 dtype=torch.bfloat16, q8_0: bool = False, cell_map: bool = True, device="cuda"):
+        self.__dict__.update(n_seq=n_seq, n_pages=n_pages, page_size=page_size, dv=dv)
+        dev = torch.device(device)
+        n_cells = n_pages * page_size
+
+        def cells(d):
+            if q8_0:
+                return torch.zeros((n_cells, h_kv, B.sfa_q8_0_row_bytes(d)), dtype=torch.uint8,
+                                   device=dev)
+            return torch.zeros((n_cells, h_kv, d), dtype=dtype, device=dev)
+
+        def i32(*shape, fill=0):
+            return torch.full(shape, fill, dtype=torch.int32, device=dev)
+
+        self.K, self.V = cells(dkq), cells(dv) if separate_v else None
+        # index keys stay unquantized: the pool reads them raw
+        self.X = torch.zeros((n_cells, d_idx), dtype=dtype, device=dev) if d_idx else None
+        self.page_table = i32(n_seq, max_pages, fill=-1)
+        self.cell_of = i32(n_seq, max_pages * page_size, fill=-1) if cell_map else None
+        self.free_pages = torch.arange(n_pages, dtype=torch.int32, device=dev)
+        self.free_head, self._head_out = i32(1), i32(1)
+        self.length, self.len_total = i32(n_seq), i32(n_seq)   # before and after the step
+        self.cu_new = i32(n_seq + 1)
+        self.q_seq, self.q_pos, self.slot = (i32(n_tok_cap, fill=-1) for _ in range(3))
+        self.status = i32(1)
+
+    def step(self, len_new, K=None, V=None, X=None, stream=None):
+        """Pages and cells for len_new [n_seq] int32 new tokens a sequence (n_tok_cap in all, at
+        most) and their rows K, V, X [n_tok_cap][...], packed sequence by sequence, into them."""
+        B.sfa_build_page_maps(self.length, len_new, self.page_size, self.free_pages, self.free_head,
+                              self.n_pages, self.page_table, self.cu_new, self.len_total,
+                              self.q_seq, self.q_pos, self.slot, self._head_out,
+                              cell_of=self.cell_of, dev_status=self.status, stream=stream)
+        pairs = [(r, c) for r, c in ((K, self.K), (V, self.V), (X, self.X)) if r is not None]
+        B.sfa_write_cells(pairs, self.slot, dev_status=self.status, stream=stream)
+        copies = [(self.length.unsqueeze(0), self.len_total.unsqueeze(0)),
+                  (self.free_head, self._head_out)]
+        B.sfa_copy_cache_rows_multi(copies, stream=stream)
+
+    def attend(self, Q, n_new_max: int, n_kv_max: int, scale: float, O, lse=None, workspace=None,
+               stream=None):
+        """O (and lse) of the step's tokens over everything their sequences hold."""
+        B.sfa_chunk_attend_paged(Q, self.K, self.V, self.page_table, self.page_size, self.cu_new,
+                                 self.len_total, n_new_max, n_kv_max, scale, O, lse=lse,
+                                 workspace=workspace, dev_status=self.status, stream=stream)
+        return O
+
+    def release(self, seq: int):
+        """Empties sequence seq: its pages go to the end of the free list (reads its length and
+        the list's head on the host, so it is not for capture)."""
+        n = -(-int(self.length[seq]) // self.page_size)
+        pages = self.page_table[seq, :n]
+        pages = pages[pages >= 0]
+        head = int(self.free_head)
+        free = torch.cat([self.free_pages[head:], pages])
+        # in place: a captured step keeps reading these buffers
+        self.free_pages[self.n_pages - free.numel():] = free
+        self.free_head.fill_(self.n_pages - free.numel())
+        self.page_table[seq].fill_(-1)
+        if self.cell_of is not None:
+            self.cell_of[seq].fill_(-1)
+        self.length[seq] = 0

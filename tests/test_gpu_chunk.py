@@ -1,0 +1,298 @@
+"""Attention of chunks of new tokens over a paged cache, against the plain 64-bit form within
+bounds that follow from the arithmetic (paged_util.attend_reference)."""
+import math
+import random
+
+import pytest
+import torch
+
+from paged_util import UBF, attend_reference, check_close
+
+pytestmark = pytest.mark.gpu
+
+sfa = pytest.importorskip("indexer_selected_sparse_block_gb300")
+
+# Weights reach the value products as two bf16 halves for fp32 results (half a step of the second
+# half: UBF^2) and as one bf16 value for bf16 results; fp32 caches keep them in fp32.
+P_ROUND = {("bf16", "f32"): UBF ** 2, ("bf16", "bf16"): UBF, ("f32", "f32"): 0.0, ("f32", "bf16"): 0.0,
+           ("q8", "f32"): 0.0, ("q8", "bf16"): 0.0}
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    return torch.device("cuda:0")
+
+
+class Case:
+    """lens: (cached before, new) per sequence; the cells that hold no token are NaN."""
+
+    def __init__(self, dev, lens, page, shape, dtype="bf16", out="f32", seed=0, spare_q=0, kscale=1.0,
+                 scale=None, spare_pages=3):
+        self.dkq, self.dv, self.sep, self.h_q, self.h_kv = shape
+        self.lens, self.page, self.dtype, self.out, self.dev = lens, page, dtype, out, dev
+        g = torch.Generator().manual_seed(seed)
+        self.total = [a + n for a, n in lens]
+        self.cu = [0]
+        for _, n in lens:
+            self.cu.append(self.cu[-1] + n)
+        pages = [-(-t // page) for t in self.total]
+        n_pages = sum(pages) + spare_pages
+        order = torch.randperm(n_pages, generator=g).tolist()
+        width = max(pages + [1]) + 1
+        self.table, k = [], 0
+        for n in pages:
+            self.table.append(order[k:k + n] + [-1] * (width - n))
+            k += n
+        dt = TYPES.get(dtype, torch.float32)
+        draw = lambda d, f=1.0: (torch.randn((n_pages * page, self.h_kv, d), generator=g) * f).to(torch.bfloat16).to(dt)
+        self.K, self.V = draw(self.dkq, kscale), draw(self.dv) if self.sep else None
+        live = torch.zeros(n_pages * page, dtype=torch.bool)
+        for s, t in enumerate(self.total):
+            for pos in range(t):
+                live[self.table[s][pos // page] * page + pos % page] = True
+        n_q = self.cu[-1] + spare_q
+        self.Q = torch.randn((n_q, self.h_q, self.dkq), generator=g).to(torch.bfloat16)
+        self.Q[self.cu[-1]:] = float("nan")
+        self.scale = 1 / math.sqrt(self.dkq) if scale is None else scale
+        if dtype == "q8":
+            self.Kc, self.K = self._q8(self.K)
+            if self.sep:
+                self.Vc, self.V = self._q8(self.V)
+            else:
+                self.Vc = None
+        else:
+            if dtype == "f32":
+                self.Q = self.Q.float()
+            for t in (self.K, self.V):
+                if t is not None:
+                    t[~live] = float("nan")
+            self.Kc, self.Vc = self.K.to(dev), None if self.V is None else self.V.to(dev)
+
+    def _q8(self, x):
+        """The q8_0 rows of x on the device and the values they stand for."""
+        x = x.to(self.dev)
+        d = x.shape[-1]
+        y = torch.zeros(x.shape[:-1] + (sfa.sfa_q8_0_row_bytes(d),), dtype=torch.uint8, device=self.dev)
+        sfa.sfa_quantize_kv_q8_0(x, y)
+        codes = y[..., :d].contiguous().view(torch.int8).float()
+        sc = y[..., d:d + d // 16].contiguous().view(torch.float16).float()
+        return y, (codes * sc.repeat_interleave(32, -1)).cpu()
+
+    def call(self, n_new_max=None, n_kv_max=None, stream=None, table=None, cu=None, total=None, lse=True,
+             workspace=None):
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.dev)
+        n_q = self.Q.shape[0]
+        self.O = torch.full((n_q, self.h_q, self.dv), 7.0, dtype=TYPES[self.out], device=self.dev)
+        self.lse = torch.full((n_q, self.h_q), 7.0, device=self.dev) if lse else None
+        status = torch.zeros(1, dtype=torch.int32, device=self.dev)
+        args = (self.Q.to(self.dev), self.Kc, self.Vc, i32(table or self.table), self.page, i32(cu or self.cu),
+                i32(total or self.total))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        sfa.sfa_chunk_attend_paged(*args,
+                                   max([n for _, n in self.lens] + [1]) if n_new_max is None else n_new_max,
+                                   max(self.total + [1]) if n_kv_max is None else n_kv_max, self.scale,
+                                   self.O, lse=self.lse, dev_status=status, stream=stream,
+                                   workspace=workspace)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        torch.cuda.synchronize()
+        return sfa.sfa_read_device_status(status)
+
+    def check(self, table=None, kv_max=None, cu=None, total=None):
+        cu = cu or self.cu
+        ref, ref_l, tol, tol_l = attend_reference(
+            self.Q, self.K, self.V, table or self.table, self.page, cu, total or self.total, self.scale,
+            self.dv, kv_max=kv_max, p_round=P_ROUND[self.dtype, self.out],
+            o_round=UBF if self.out == "bf16" else 0.0)
+        n = self.cu[-1]
+        check_close(self.O[:n], ref[:n], tol[:n], "O")
+        if self.lse is not None:
+            check_close(self.lse[:n], ref_l[:n], tol_l[:n], "lse")
+            assert bool((self.lse[n:] == 7.0).all())
+        assert bool((self.O[n:].float() == 7.0).all())
+
+
+WIDE, W512, W512K = (576, 512, False, 16, 1), (512, 512, True, 16, 2), (512, 512, False, 16, 1)
+N128, N128K, N64, N64K = (128, 128, True, 16, 4), (128, 128, False, 4, 4), (64, 64, True, 8, 1), (64, 64, False, 8, 2)
+SHAPES = [WIDE, W512, W512K, N128, N128K, N64, N64K]
+RAGGED = [(0, 1), (0, 17), (5, 3), (127, 1), (128, 40), (0, 0), (255, 2), (300, 0), (61, 70)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "q8"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_ragged(dev, shape, dtype, out):
+    """Every shape and type: one to many new tokens, empty chunks, sequences of one token, lengths
+    on and off the tiles' and pages' edges, unused rows of Q."""
+    c = Case(dev, RAGGED, 16, shape, dtype, out, seed=shape[0], spare_q=5)
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [WIDE, N128])
+@pytest.mark.parametrize("page", [1, 2, 3, 8, 24, 40, 64, 96, 100, 128, 192, 256, 1000])
+def test_page_sizes(dev, shape, page):
+    """Pages smaller and larger than a tile, ending inside one or not, odd ones."""
+    c = Case(dev, [(0, 3), (190, 20), (500, 1), (130, 9)], page, shape, seed=page)
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+@pytest.mark.parametrize("length", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 193, 255, 256, 257, 511, 900])
+def test_single_tokens(dev, shape, length):
+    """Decode: one new token behind every length around a tile's edges."""
+    c = Case(dev, [(length - 1, 1)], 64, shape, seed=length)
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [(576, 512, False, h, k) for h, k in
+                                   [(1, 1), (3, 1), (12, 1), (15, 3), (33, 1), (64, 1), (32, 2)]]
+                         + [(128, 128, True, h, k) for h, k in [(1, 1), (5, 1), (48, 1), (6, 2), (7, 7), (64, 1)]]
+                         + [(64, 64, True, 20, 2), (64, 64, True, 63, 1), (512, 512, True, 24, 2)])
+def test_head_groups(dev, shape):
+    """Query heads per KV head that do and do not divide a tile's rows."""
+    c = Case(dev, [(70, 19), (3, 1), (0, 45)], 16, shape, seed=shape[3])
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("shape,new", [(WIDE, 1), (WIDE, 3), (N128, 1), (N64, 2), (W512, 1)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_long_split_lists(dev, shape, new, out):
+    """Few rows against a long list: it is cut over the SMs and merged; the same on every run."""
+    c = Case(dev, [(6000, new), (37, new), (2049, new)], 32, shape, out=out, seed=new)
+    need = sfa.sfa_chunk_attend_workspace_bytes(sfa.SFA_BF16, 3, 3 * new, shape[3], shape[4], shape[0],
+                                                shape[1], shape[2], new, 6000 + new)
+    assert need > 0                       # the plan really splits
+    assert c.call() == 0
+    c.check()
+    O, lse = c.O, c.lse
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=dev)       # NaN everywhere
+    assert c.call(workspace=ws) == 0
+    assert torch.equal(c.O, O) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("shape,dtype", [(WIDE, "bf16"), (N128, "bf16"), (N64, "bf16"), (W512, "bf16"), (N128, "f32")])
+def test_rising_scores(dev, shape, dtype):
+    """Each key scores higher than all before it, by much: every tile moves the running maximum."""
+    c = Case(dev, [(700, 40)], 64, shape, dtype, seed=4)
+    g = shape[3] // shape[4]
+    q = torch.sign(c.Q[:, ::g].float().mean(0, keepdim=True)) + 0.0
+    q[q == 0] = 1.0
+    c.Q = q.repeat_interleave(g, 1).expand(c.Q.shape).contiguous().to(c.Q.dtype)
+    ramp = torch.arange(740).float() / 740 * 4
+    for pos in range(740):
+        cell = c.table[0][pos // 64] * 64 + pos % 64
+        c.K[cell] = (q[0, :, :] * ramp[pos]).to(c.K.dtype)
+    c.Kc = c.K.to(dev)
+    c.scale = 1.0                         # scores up to 4 dkq in steps of dkq / 185
+    assert c.call() == 0
+    c.check()
+
+
+def test_large_and_negative_scores(dev):
+    """Scores of hundreds, a negative scale, and a zero one (a plain mean)."""
+    for scale in (3.0, -0.5, 0.0):
+        for shape in (WIDE, N128):
+            c = Case(dev, [(150, 20), (0, 1)], 16, shape, seed=6, scale=scale)
+            assert c.call() == 0
+            c.check()
+
+
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_pages(dev, shape, dtype):
+    """Page table entries that are no page: their positions are left out, a query that sees no
+    other gets zeros, and the status says so."""
+    c = Case(dev, [(0, 20), (150, 30), (64, 1)], 16, shape, dtype, seed=2)
+    t = [list(r) for r in c.table]
+    t[0][0] = -1                      # the first 16 queries of sequence 0 see nothing
+    t[1][3] = len(c.K) // 16          # one past the last page
+    t[1][9], t[2][4] = -2 ** 31, 2 ** 31 - 1
+    assert c.call(table=t) == sfa.SFA_DEV_BAD_CELL
+    c.check(table=t)
+    assert bool((c.O[:16] == 0).all()) and bool(torch.isneginf(c.lse[:16]).all())
+
+
+@pytest.mark.parametrize("shape,dtype", [(WIDE, "bf16"), (N128, "bf16"), (N64, "f32")])
+def test_bounds_that_do_not_hold(dev, shape, dtype):
+    """Host bounds and offsets that the device data breaks: flagged, what fits is computed, no row
+    outside is touched."""
+    bad = sfa.SFA_DEV_BAD_QUERY
+    c = Case(dev, [(100, 30), (20, 4)], 16, shape, dtype, seed=3)
+    assert c.call(n_kv_max=64) == bad                 # longer lists: their first 64 keys
+    c.check(kv_max=64)
+    assert c.call(n_new_max=8) == bad                 # a longer chunk: its first 8 queries
+    ref, _, tol, _ = attend_reference(c.Q, c.K, c.V, c.table, 16, c.cu, c.total, c.scale, c.dv,
+                                      p_round=P_ROUND[dtype, "f32"])
+    for r in (slice(0, 8), slice(30, 34)):
+        check_close(c.O[r], ref[r], tol[r], "O")
+    assert bool((c.O[8:30] == 7.0).all())
+    assert c.call(cu=[0, 30, 35]) == bad              # past the last row: an empty chunk
+    check_close(c.O[:30], ref[:30], tol[:30], "O")
+    assert bool((c.O[30:] == 7.0).all())
+    assert c.call(cu=[0, 30, 29]) == bad
+    check_close(c.O[:30], ref[:30], tol[:30], "O")
+    assert bool((c.O[30:] == 7.0).all())
+    assert c.call(total=[10, 24]) == bad              # fewer tokens than the chunk: 20 queries before 0
+    c.check(total=[10, 24])
+    assert bool((c.O[:20] == 0).all()) and bool(torch.isneginf(c.lse[:20]).all())
+    short = [r[:5] for r in c.table]                  # 80 positions of 130
+    assert c.call(table=short) == bad
+    c.check(table=short)
+
+
+def test_nonfinite_values(dev):
+    """NaN and infinities in attended cells reach the rows that attend them and no others."""
+    for shape, dtype in ((WIDE, "f32"), (N128, "f32")):
+        c = Case(dev, [(100, 30), (5, 3)], 16, shape, dtype, seed=9)
+        cell = c.table[0][110 // 16] * 16 + 110 % 16          # query 10 of the chunk: a later key
+        v = c.K if c.V is None else c.V
+        v[cell, :, 3] = float("inf")
+        c.Kc, c.Vc = c.K.to(dev), None if c.V is None else c.V.to(dev)
+        assert c.call() == 0
+        O = c.O.float()
+        assert bool(torch.isfinite(O[:10]).all()) and bool(torch.isfinite(O[30:]).all())
+        # where V is K's first dims the key's score is +-inf with the sign of q[3]: -inf is weight
+        # exp(-inf) = 0, an unattended key; +inf (and any score with V apart) attends it
+        seen = (c.Q[10:30, :, 3] > 0) if c.V is None else torch.ones(20, c.h_q, dtype=torch.bool)
+        assert not bool(torch.isfinite(O[10:30, :, 3].cpu()[seen]).any())
+
+
+def test_streams_and_no_lse(dev):
+    c = Case(dev, RAGGED, 16, WIDE, out="bf16", seed=1)
+    assert c.call(stream=torch.cuda.Stream(), lse=False) == 0
+    c.check()
+
+
+def test_nothing_to_do(dev):
+    c = Case(dev, [(5, 0), (0, 0)], 16, WIDE, seed=1, spare_q=4)
+    assert c.call() == 0
+    assert bool((c.O == 7.0).all())
+
+
+def test_agrees_with_the_dense_call(dev):
+    """The same queries through sfa_dense_attend_paged (a position map instead of the table)."""
+    for shape in (WIDE, W512, N128, N64):
+        c = Case(dev, [(300, 20), (77, 5)], 16, shape, seed=8)
+        assert c.call() == 0
+        n_pos = max(c.total)
+        cell_of = torch.tensor([[max(r[t // 16], 0) * 16 + t % 16 for t in range(n_pos)] for r in c.table],
+                               dtype=torch.int32, device=dev)
+        q_seq = torch.tensor([0] * 20 + [1] * 5, dtype=torch.int32, device=dev)
+        q_pos = torch.tensor(list(range(300, 320)) + list(range(77, 82)), dtype=torch.int32, device=dev)
+        O = torch.empty_like(c.O)
+        if shape[3] // shape[4] > 16:
+            continue
+        sfa.sfa_dense_attend_paged(c.Q.to(dev), c.Kc, c.Vc, cell_of, q_seq, q_pos, n_pos, c.scale, O)
+        ref, _, tol, _ = attend_reference(c.Q, c.K, c.V, c.table, 16, c.cu, c.total, c.scale, c.dv,
+                                          p_round=UBF ** 2)
+        check_close(c.O, O.double().cpu(), 2 * tol, "chunk against dense")
