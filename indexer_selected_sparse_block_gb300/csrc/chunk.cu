@@ -305,7 +305,9 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 }
 
 // --------------------------------------------------------------------------------- the plan
+enum Kernel { kSimt, kWide };
 struct Plan {
+    Kernel kernel;
     int item_rows, item_q, items, n_split, split_keys;
 };
 
@@ -317,22 +319,41 @@ int64_t items_bound(int n_seq, int n_q, int G, int n_new_max, int item_rows, int
     return per * n_seq < all ? per * n_seq : all;
 }
 
-// The lists are cut so that the items fill the SMs: enough equal pieces of whole key tiles.
-Plan make_plan(int n_seq, int n_q, int G, int h_kv, int n_new_max, int64_t n_kv_max) {
+// The kernel, and into how many equal pieces the longest list is cut: the number with the least
+// modelled time, waves of pieces (a key tile, and the start and end of a piece) plus the merge
+// (its launch and the partial results' way through memory).
+Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new_max,
+               int64_t n_kv_max, int64_t n_cells, bool o_bf16) {
     Plan pl;
-    pl.item_rows = kRows;
-    pl.item_q = 0;
+    const bool wide = dtype == SFA_BF16 && dv == 512 && n_cells > 0;
+    pl.kernel = wide ? kWide : kSimt;
+    pl.item_rows = wide ? 128 : kRows;
+    pl.item_q = wide ? 2 * wide_qpc(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
-    pl.items = (int)(items > 0x7FFFFFFF ? 0x7FFFFFFF : items);
+    pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
     const int tile = 128;
     const int64_t tiles = (n_kv_max + tile - 1) / tile;
-    int64_t ns = device_sm_count() / (items * h_kv > 0 ? items * h_kv : 1);
-    ns = ns < 1 ? 1 : ns > tiles ? tiles : ns;
-    ns = ns < 1 ? 1 : ns > 64 ? 64 : ns;
-    const int64_t per = (tiles + ns - 1) / ns;
-    pl.split_keys = (int)(per > 0 ? per * tile : tile);
-    pl.n_split = (int)((tiles + (per > 0 ? per : 1) - 1) / (per > 0 ? per : 1));
-    if (pl.n_split < 1) pl.n_split = 1;
+    const double slots = wide ? device_sm_count() / 2 : device_sm_count();
+    const double t_tile = wide ? (o_bf16 ? 1.4 : 2.1) : dv == 512 ? 30. : 8.;   // us
+    const double t_piece = 6., t_merge = 4.;
+    const double part_us = (double)pl.item_rows * dv * 4 * 2 / 4e6;             // a partial, both ways
+    const int64_t units = items * h_kv;
+    int64_t best = 1;
+    double best_us = 0;
+    for (int64_t ns = 1; ns <= tiles && ns <= 128; ++ns) {
+        const int64_t per = (tiles + ns - 1) / ns;
+        if (ns > 1 && (tiles + per - 1) / per != ns) continue;
+        if (ns > 1 && (double)units * ns * pl.item_rows * (dv + 2) * 4 > 1e9) break;
+        const int64_t waves = (int64_t)((units * ns + slots - 1) / slots);
+        const double us = waves * (per * t_tile + t_piece) + (ns > 1 ? t_merge + units * ns * part_us : 0.);
+        if (ns == 1 || us < best_us) {
+            best = ns;
+            best_us = us;
+        }
+    }
+    const int64_t per = (tiles + best - 1) / best;
+    pl.split_keys = best > 1 ? (int)(per * tile) : 0x7FFFFF80;
+    pl.n_split = (int)best;
     return pl;
 }
 
@@ -387,11 +408,10 @@ extern "C" size_t sfa_chunk_attend_workspace_bytes(int dtype, int n_seq, int n_q
                                                    int dkq, int dv, int has_v, int n_new_max,
                                                    int64_t n_kv_max, int o_dtype) {
     using namespace sfa::chunk;
-    (void)dtype;
-    (void)o_dtype;
     if (check_sizes(n_seq, n_q, h_q, h_kv, dkq, dv, has_v != 0, n_new_max, n_kv_max) != SFA_OK) return 0;
     if (n_seq == 0 || n_q == 0 || n_new_max == 0) return 0;
-    return plan_workspace(make_plan(n_seq, n_q, h_q / h_kv, h_kv, n_new_max, n_kv_max), h_kv, dv);
+    return plan_workspace(make_plan(dtype, n_seq, n_q, h_q / h_kv, h_kv, dv, n_new_max, n_kv_max, 1,
+                                    o_dtype == SFA_BF16), h_kv, dv);
 }
 
 extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtype,
@@ -417,7 +437,9 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(lse) ||
         !aligned16(workspace))
         return SFA_ERR_INVALID_ARG;
-    const Plan pl = make_plan(n_seq, n_q, h_q / h_kv, h_kv, n_new_max, n_kv_max);
+    // a cache of no cell: every page is a bad one, and any kernel's plan fits the workspace
+    const Plan pl = make_plan(dtype, n_seq, n_q, h_q / h_kv, h_kv, dv, n_new_max, n_cells > 0 ? n_kv_max : 0,
+                              n_cells, o_dtype == SFA_BF16);
     const size_t need = plan_workspace(pl, h_kv, dv);
     if (need > 0 && (!workspace || workspace_bytes < need)) return SFA_ERR_WORKSPACE;
     Params p{};
@@ -451,7 +473,8 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.scale_log2 = scale * kLog2e;
     cudaStream_t st = (cudaStream_t)stream;
     int r;
-    if (dkq == 576) r = launch_simt<576, 512, true>(p, dtype, st);
+    if (pl.kernel == kWide) r = launch_wide(p, dkq, n_cells, st);
+    else if (dkq == 576) r = launch_simt<576, 512, true>(p, dtype, st);
     else if (dkq == 512) r = V ? launch_simt<512, 512, false>(p, dtype, st) : launch_simt<512, 512, true>(p, dtype, st);
     else if (dkq == 128) r = V ? launch_simt<128, 128, false>(p, dtype, st) : launch_simt<128, 128, true>(p, dtype, st);
     else r = V ? launch_simt<64, 64, false>(p, dtype, st) : launch_simt<64, 64, true>(p, dtype, st);

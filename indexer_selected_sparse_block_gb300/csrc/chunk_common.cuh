@@ -127,5 +127,10 @@ __device__ __forceinline__ int64_t cell_of(const Params &p, int s, int t) {
     return (int64_t)e * p.page + (t - pg * p.page);
 }
 
+// The kernel for 512 value dims on tcgen05 CTA pairs (chunk_wide.cu): queries of one CTA's 64
+// rows, and the launch (p.item_q = twice that, p.item_rows = 128).
+int wide_qpc(int G);
+int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st);
+
 }  // namespace chunk
 }  // namespace sfa

@@ -1,0 +1,707 @@
+// chunk_wide.cu -- chunk attention with 512 value dims (576 / 512 head dims, bf16) on tcgen05
+// CTA pairs.
+//
+// A pair of CTAs (a cluster of two, cta_group::2) owns 128 rows (query, head) of one KV head,
+// 64 per CTA, and streams 128-key tiles:
+//   S[128 x 128]  = Q K^T     K' = dkq, each CTA holding 64 of the keys;
+//   O[128 x 512] += P V       two N = 256 products, each CTA holding 128 of their value dims.
+// The shapes follow from tensor memory and shared memory.  128 rows x 512 fp32 dims of O would
+// fill one CTA's tensor memory and leave none for S; a pair's M = 128 product puts a CTA's 64
+// rows on all 128 lanes (the lanes' halves hold the two halves of the columns), so O takes 256
+// columns and two S tiles 128.  And Q needs 72 KB a CTA instead of 144.
+//
+// Shared memory of a CTA: Q (9 slabs of [64 rows][64 dims], 128-byte swizzle), two tile buffers of
+// eight slabs [64 keys][64 dims], one slab for dims 512..575, P (16 KB).  A buffer's life:
+//   first load    its own 64 keys' dims 0..511 for S;
+//   second load   once S has read them, the value slabs that it lacks: CTA c needs all 128 keys
+//                 of dims 128 c .. and 256 + 128 c ..  Of its own keys it has those already where
+//                 V is K; the other CTA's keys of these dims replace the slabs whose dims belong
+//                 to the other CTA.  Slab p then holds for product (key half h, n) the operand at
+//                 4 n + 2 h in both CTAs, which is what one descriptor for the pair needs.
+//                 V apart: all eight slabs are replaced.
+// Order of the products: S(t + 1), then P V (t): the softmax of tile t runs while S(t + 1) does,
+// and its 16 KB of P are written once P V (t - 1) has left the buffer.
+//
+// For fp32 results the weights are carried as two bf16 halves (hi + lo, 2^-16 relative): P V then
+// runs by key half, the halves' hi and lo in the P buffer one after the other, S(t + 1) cut in
+// two between them.  For bf16 results one bf16 weight is enough: its rounding (2^-8 of a weight,
+// either sign) averages out below the result's own rounding.
+//
+// The running maximum moves only when a tile raises it by more than 2^8: weights up to 256 keep
+// their relative precision in bf16 and fp32, and O in tensor memory is rescaled seldom.
+//
+// Pages: a key half is loaded in boxes of gcd(page, 64) rows.  Where the list ends inside one, in
+// boxes of 8 rows and of one, those past the end from outside the tensor, which reads as
+// zeros: cells that hold no attended token may hold NaN.
+//
+// Warps 0-3: softmax, correction, result (a thread has one row and half of its keys and dims);
+// warp 4: first loads and Q; warp 5: second loads; warp 6: products (in the pair's first CTA).
+#include "chunk_common.cuh"
+
+namespace sfa {
+namespace chunk {
+namespace {
+
+constexpr int kT = 128;             // keys of a tile
+constexpr int kSlab = 64 * 128;     // bytes of 64 rows x 64 dims
+constexpr int kWideThreads = 224;
+constexpr float kLazy = 8.f;        // base-2 growth of the maximum that O is not rescaled for
+
+template <int DKQ>
+struct Wide {
+    static constexpr int kNSK = DKQ / 64;
+    static constexpr bool kRope = kNSK > 8;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffBuf = kNSK * kSlab;               // [2][8] slabs
+    static constexpr int kOffRope = kOffBuf + 16 * kSlab;
+    static constexpr int kOffP = kOffRope + (kRope ? kSlab : 0);
+    static constexpr int kOffMax = kOffP + 2 * kSlab;          // float [2][128]
+    static constexpr int kOffL = kOffMax + 2 * 128 * 4;        // float [128]
+    static constexpr int kOffItem = kOffL + 128 * 4;           // Item, padded
+    static constexpr int kOffBar = kOffItem + 64;
+    static constexpr int kBars = 1 + 4 * 8 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kBytes = kOffBar + kBars * 8 + 16;
+    static_assert(kBytes <= 227 * 1024, "fits one CTA per SM");
+};
+
+struct WideMaps {
+    CUtensorMap q, k[3], v[3];   // boxes of bx, min(bx, 8) and 1 rows
+};
+
+// --------------------------------------------------------------- pair (cta_group::2) wrappers
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// This shared address in the pair's first CTA, as a shared::cluster address.
+__device__ __forceinline__ uint32_t in_leader(uint32_t saddr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(saddr));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Waits for the phase of `parity`; the limit counts from the wait's own start.  Acquires at
+// cluster scope (arrivals may come from the other CTA).
+__device__ __forceinline__ bool wait2(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 63u) == 63u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kWaitLimitNs) return false;
+        }
+    }
+}
+// Tiled load into this CTA's shared memory, its bytes counted on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma2_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                          uint32_t leader_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrives on this barrier of both CTAs when the products issued so far are done.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------------------------- key rows
+// Where the 64 keys of a half tile lie, a lane's share of the boxes that load them.
+struct HalfRows {
+    bool whole;     // all 64 keys are in the list: boxes of bx rows
+    int row[2];     // first cell of this lane's boxes lane, lane + 32
+    int edge;       // not whole: the box of min(bx, 8) rows that the list ends in (else -1)
+    int single;     // cell of this lane's row of that box
+};
+// Keys pos0 .. pos0 + 63 of sequence s; the list ends before `end`.  Cells past it, and those of
+// pages that are none, are n_cells: outside the tensor, read as zeros.
+__device__ __forceinline__ HalfRows half_rows(const Params &p, int s, int pos0, int end, int bx, int n_cells) {
+    const int lane = threadIdx.x & 31;
+    auto cell = [&](int pos) -> int {
+        if (pos >= end) return n_cells;
+        const int pg = pos / p.page;
+        const int e = __ldg(p.table + (int64_t)s * p.table_stride + pg);
+        return e < 0 || e >= p.n_pages ? n_cells : e * p.page + (pos - pg * p.page);
+    };
+    HalfRows h;
+    h.whole = pos0 + 64 <= end;
+    h.edge = -1;
+    h.single = n_cells;
+    const int b = h.whole ? bx : min(bx, 8);
+    const int n = 64 / b;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        h.row[i] = lane + 32 * i < n ? cell(pos0 + (lane + 32 * i) * b) : n_cells;
+    if (!h.whole && end > pos0 && (end - pos0) % b != 0) {
+        h.edge = (end - pos0) / b;
+        if (lane < b) h.single = cell(pos0 + h.edge * b + lane);
+    }
+    return h;
+}
+// One slab [64 keys][64 dims from x] of KV head g; by a whole warp.
+__device__ __forceinline__ void load_slab(const HalfRows &h, uint32_t dst, const CUtensorMap *maps,
+                                          int x, int g, int bx, uint32_t leader_bar) {
+    const int lane = threadIdx.x & 31;
+    const int b = h.whole ? bx : min(bx, 8);
+    const int n = 64 / b;
+    const CUtensorMap *map = maps + (h.whole ? 0 : 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int box = lane + 32 * i;
+        if (box < n && box != h.edge) tma2_load(dst + box * b * 128, map, x, g, h.row[i], leader_bar);
+    }
+    if (h.edge >= 0 && lane < b)
+        tma2_load(dst + (h.edge * b + lane) * 128, maps + 2, x, g, h.single, leader_bar);
+}
+
+// --------------------------------------------------------------------------------- the kernel
+template <int DKQ, bool VK, bool HL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    chunk_wide_kernel(const __grid_constant__ WideMaps maps, const Params p, int bx, int qpc, int n_cells) {
+    using L = Wide<DKQ>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
+    float *sL = reinterpret_cast<float *>(smem + L::kOffL);
+    Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const uint32_t bar0 = smem_u32(bars);
+    // barriers, as shared addresses; [buffer][pair] ones at + (buffer * 4 + pair) * 8
+    const uint32_t b_q = bar0, b_fullA = bar0 + 8, b_fullB = b_fullA + 64, b_doneQ = b_fullB + 64,
+                   b_doneP = b_doneQ + 64, b_rope = b_doneP + 64, b_ropeDone = b_rope + 8,
+                   b_s = b_ropeDone + 8, b_p = b_s + 16, b_pv = b_p + 16, b_drain = b_pv + 16;
+    static_assert(L::kBars == 1 + 32 + 2 + 2 + 2 + 2 + 1, "barrier list");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = (int)cluster_rank();
+    const int item = blockIdx.x >> 1, g = blockIdx.y, split = blockIdx.z;
+    pdl_wait();
+    if (warp == 0) {
+        const Item it = find_item(p, item, blockIdx.x == 0 && g == 0 && split == 0);
+        if (lane == 0) *sItem = it;
+    }
+    __syncthreads();
+    const Item it = *sItem;
+    if (it.seq < 0) return;
+    const int q0 = it.tile * p.item_q;                        // first query of the tile
+    const int nq = min(p.item_q, min(it.q.n, p.n_new_max) - q0);
+    const int pos0 = it.q.total - it.q.n + q0;                // its position
+    const int len = max(0, min(key_limit(p, it.q), pos0 + nq));
+    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
+    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
+    if (split > 0 && k0 >= k1) return;                        // no such piece
+    const bool whole = len <= p.split_keys;
+    const int n_tiles = (k1 - k0 + kT - 1) / kT;
+    const int G = p.G;
+
+    // a thread's row: query ql of this CTA's qpc, head h; both halves of the lanes have every row
+    const int row = (warp & 1) * 32 + lane, hh = (warp >> 1) & 1;
+    const int ql = row / G, h = row - ql * G;
+    const bool live = warp < 4 && ql < qpc && c * qpc + ql < nq;
+    const int64_t orow = (int64_t)(it.q.c0 + q0 + c * qpc + ql) * p.h_q + g * G + h;
+
+    if (n_tiles == 0) {   // nothing to attend: zeros
+        if (live) {
+            for (int d = hh * 256; d < hh * 256 + 256; d += 4) {
+                if (p.o_bf16)
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d) = make_uint2(0, 0);
+                else
+                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * 512 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (hh == 0 && p.lse) p.lse[orow] = -INFINITY;
+        }
+        return;
+    }
+
+    if (tid == 0) {
+        const int ip = (int)(b_p - bar0) / 8;
+        // P (half 0) ready: four warps of each CTA; P half 1: two of each
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 8 : i == ip + 1 ? 4 : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 6) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tO = tmem + 128;   // S: 2 x 64 columns, O: 2 x 128
+    const uint32_t buf0 = smem_u32(smem + L::kOffBuf), sQ = smem_u32(smem + L::kOffQ),
+                   sRope = smem_u32(smem + L::kOffRope), sP = smem_u32(smem + L::kOffP);
+    // once a wait ran out no other is made
+    bool ok = true;
+    auto wait1 = [&](uint32_t bar, uint32_t parity) {
+        if (ok && (*abort_flag || !wait2(bar, parity))) {
+            ok = false;
+            *abort_flag = 1;
+            set_status(p.status, SFA_DEV_TIMEOUT);
+        }
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {   // by a whole warp, which agrees on ok
+        wait1(bar, parity);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+    };
+
+    if (warp == 4) {
+        // ------------------------------------------------------------------ Q and first loads
+        if (lane == 0) {
+            prefetch_tensormap(&maps.q);
+            prefetch_tensormap(&maps.k[0]);
+            if (c == 0) mbar_arrive_expect_tx(bars, 2u * L::kNSK * 128u * (uint32_t)(qpc * G));
+            for (int d = 0; d < L::kNSK; ++d)
+                tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + c * qpc, in_leader(b_q));
+        }
+        __syncwarp();
+        for (int t = 0; t < n_tiles && ok; ++t) {
+            const HalfRows r = half_rows(p, it.seq, k0 + t * kT + c * 64, k1, bx, n_cells);
+            const uint32_t b = t & 1, par = (t >> 1) & 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pr = ((i & 1) << 1) | (i >> 1);   // pairs 0, 2, 1, 3: in the order of use
+                const uint32_t at = (b * 4 + pr) * 8;
+                wait(b_doneP + at, par ^ 1);
+                if (!ok) break;
+                if (c == 0 && lane == 0) mbar_arrive_expect_tx(bars + (b_fullA + at - bar0) / 8, 4u * kSlab);
+                __syncwarp();
+                const uint32_t lb = in_leader(b_fullA + at);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    load_slab(r, buf0 + (b * 8 + 2 * pr + s) * kSlab, maps.k, (2 * pr + s) * 64, g, bx, lb);
+            }
+            if (L::kRope && ok) {
+                wait(b_ropeDone, (t & 1) ^ 1);
+                if (!ok) break;
+                if (c == 0 && lane == 0) mbar_arrive_expect_tx(bars + (b_rope - bar0) / 8, 2u * kSlab);
+                __syncwarp();
+                load_slab(r, sRope, maps.k, 512, g, bx, in_leader(b_rope));
+            }
+        }
+    } else if (warp == 5) {
+        // ------------------------------------------------------------------------ second loads
+        if (!VK && lane == 0) prefetch_tensormap(&maps.v[0]);
+        for (int t = 0; t < n_tiles && ok; ++t) {
+            const int kt = k0 + t * kT;
+            HalfRows r[2];
+            if (!VK) {
+                r[0] = half_rows(p, it.seq, kt, k1, bx, n_cells);
+                r[1] = half_rows(p, it.seq, kt + 64, k1, bx, n_cells);
+            } else {
+                r[0] = half_rows(p, it.seq, kt + (1 - c) * 64, k1, bx, n_cells);
+            }
+            const uint32_t b = t & 1, par = (t >> 1) & 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int half = i >> 1, n = i & 1, pr = 2 * n + half;
+                const uint32_t at = (b * 4 + pr) * 8;
+                wait(b_doneQ + at, par);
+                if (!ok) break;
+                if (c == 0 && lane == 0)
+                    mbar_arrive_expect_tx(bars + (b_fullB + at - bar0) / 8, (VK ? 2u : 4u) * kSlab);
+                __syncwarp();
+                if (VK && half == c) continue;   // its own keys: there already
+                const uint32_t lb = in_leader(b_fullB + at);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    load_slab(r[VK ? 0 : half], buf0 + (b * 8 + 2 * pr + s) * kSlab,
+                              VK ? maps.k : maps.v, (4 * n + 2 * c + s) * 64, g, bx, lb);
+            }
+        }
+    } else if (warp == 6) {
+        // ----------------------------------------------------------------------------- products
+        if (c == 0 && lane == 0) {
+            const uint32_t idS = idesc_bf16_f32(128, 128);
+            const uint32_t idPV = idesc_bf16_f32(128, 256) | (1u << 16);   // V: N-major
+            const uint64_t dQ = sw128_desc(sQ, 16, 1024), dBuf = sw128_desc(buf0, 16, 1024),
+                           dRope = sw128_desc(sRope, 16, 1024), dP = sw128_desc(sP, 16, 1024),
+                           dV = sw128_desc(buf0, kSlab, 1024);
+            auto s_pairs = [&](int t, int i0, int i1) {   // S(t), pairs i0 .. i1 - 1 in their order
+                const uint32_t b = t & 1, par = (t >> 1) & 1;
+                for (int i = i0; i < i1; ++i) {
+                    const int pr = ((i & 1) << 1) | (i >> 1);
+                    wait1(b_fullA + (b * 4 + pr) * 8, par);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma2(tS + b * 64, dQ + (uint64_t)(((2 * pr + s) * kSlab + kk * 32) >> 4),
+                                 dBuf + (uint64_t)(((b * 8 + 2 * pr + s) * kSlab + kk * 32) >> 4), idS,
+                                 (i > 0 || s > 0 || kk > 0) ? 1u : 0u);
+                    commit2(b_doneQ + (b * 4 + pr) * 8);
+                }
+            };
+            auto s_end = [&](int t) {
+                const uint32_t b = t & 1;
+                if (L::kRope) {
+                    wait1(b_rope, t & 1);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma2(tS + b * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
+                             dRope + (uint64_t)((kk * 32) >> 4), idS, 1u);
+                    commit2(b_ropeDone);
+                }
+                commit2(b_s + b * 8);
+            };
+            auto pv_half = [&](int t, int half) {
+                const uint32_t b = t & 1, par = (t >> 1) & 1;
+                if (HL || half == 0) wait1(b_p + half * 8, t & 1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int pr = 2 * n + half;
+                    wait1(b_fullB + (b * 4 + pr) * 8, par);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = 0; x < (HL ? 2 : 1); ++x)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma2(tO + n * 128, dP + (uint64_t)(((HL ? x : half) * kSlab + kk * 32) >> 4),
+                                 dV + (uint64_t)(((b * 8 + 2 * pr) * kSlab + kk * 2048) >> 4), idPV,
+                                 (t > 0 || half > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                    commit2(b_doneP + (b * 4 + pr) * 8);
+                }
+                if (HL || half == 1) commit2(b_pv + half * 8);
+            };
+            wait1(b_q, 0);
+            s_pairs(0, 0, 4);
+            if (ok) s_end(0);
+            for (int t = 0; t < n_tiles && ok; ++t) {
+                const bool more = t + 1 < n_tiles;
+                if (HL) {
+                    if (more) s_pairs(t + 1, 0, 2);
+                    if (ok) pv_half(t, 0);
+                    if (more && ok) {
+                        s_pairs(t + 1, 2, 4);
+                        if (ok) s_end(t + 1);
+                    }
+                    if (ok) pv_half(t, 1);
+                } else {
+                    if (more) {
+                        s_pairs(t + 1, 0, 4);
+                        if (ok) s_end(t + 1);
+                    }
+                    if (ok) pv_half(t, 0);
+                    if (ok) pv_half(t, 1);
+                }
+            }
+            if (!ok) {   // what was issued has to end before tensor memory is given back
+                commit2(b_drain);
+                wait2(b_drain, 0);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------------------ softmax
+        const int pos = pos0 + c * qpc + ql;                  // the row's last key
+        const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
+        const bool neg = p.scale_log2 < 0.f;
+        // a zero scale: weights of 1 to 1e-28
+        const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
+        const uint32_t p_ready[2] = {in_leader(b_p), in_leader(b_p + 8)};
+        float m = -INFINITY, l = 0.f;                         // base 2; this thread's keys only
+        for (int t = 0; t < n_tiles; ++t) {
+            const uint32_t b = t & 1, par = (t >> 1) & 1;
+            const int kb = k0 + t * kT + hh * 64;             // the first of the thread's keys
+            uint32_t v0, v1;                                  // keys 2 i and 2 i + 1 have a cell
+            {
+                bool v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int key = kb + 2 * lane + i;
+                    v[i] = true;
+                    if (key < k1) {
+                        const int e = __ldg(p.table + (int64_t)it.seq * p.table_stride + key / p.page);
+                        if (e < 0 || e >= p.n_pages) {
+                            v[i] = false;
+                            set_status(p.status, SFA_DEV_BAD_CELL);
+                        }
+                    }
+                }
+                v0 = __ballot_sync(0xFFFFFFFFu, v[0]);
+                v1 = __ballot_sync(0xFFFFFFFFu, v[1]);
+            }
+            const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
+            wait(b_s + b * 8, par);
+            tc_fence_after();
+            float s[64];
+            {
+                uint32_t r0[32], r1[32];
+                tmem_ld32(tS + b * 64 + lane_addr, r0);
+                tmem_ld32(tS + b * 64 + 32 + lane_addr, r1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    s[j] = __uint_as_float(r0[j]);
+                    s[32 + j] = __uint_as_float(r1[j]);
+                }
+            }
+            tc_fence_before();
+            if (neg) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) s[j] = -s[j];
+            }
+            if (last < 63 || (v0 & v1) != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (j > last || !(((j & 1 ? v1 : v0) >> (j >> 1)) & 1)) s[j] = -INFINITY;
+            }
+            float mx = s[0];
+#pragma unroll
+            for (int j = 1; j < 64; ++j) mx = fmaxf(mx, s[j]);
+            sMax[b * 128 + tid] = mx;
+            named_barrier(1, 128);
+            mx = fmaxf(mx, sMax[b * 128 + (tid ^ 64)]) * sc;
+            float alpha = 1.f;
+            if (mx > m + kLazy || (m == -INFINITY && mx > m)) {
+                alpha = ex2(m - mx);
+                m = mx;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            float sum = 0.f;
+            uint32_t hi[32], lo[HL ? 32 : 1];
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+                const float e0 = ex2(fmaf(s[j], sc, -mm)), e1 = ex2(fmaf(s[j + 1], sc, -mm));
+                sum += e0 + e1;
+                hi[j / 2] = pack_bf16(e0, e1);
+                if constexpr (HL)
+                    lo[j / 2] = pack_bf16(e0 - __uint_as_float(hi[j / 2] << 16),
+                                          e1 - __uint_as_float(hi[j / 2] & 0xFFFF0000u));
+            }
+            l = l * alpha + sum;
+            // the products of the tile before are done with P and O
+            if (t > 0) wait(b_pv + 8, (t - 1) & 1);
+            if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f) && ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + x * 32 + lane_addr, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+                    tmem_st32(tO + x * 32 + lane_addr, r);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            auto write = [&](const uint32_t (&w)[32], uint32_t slab) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     slab + row * 128 + ((x ^ (row & 7)) << 4)),
+                                 "r"(w[4 * x]), "r"(w[4 * x + 1]), "r"(w[4 * x + 2]), "r"(w[4 * x + 3])
+                                 : "memory");
+            };
+            if constexpr (HL) {
+                if (hh == 1) {   // O is rescaled; then P's second half, when the first is used up
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(p_ready[0]);
+                    wait(b_pv, t & 1);
+                }
+                write(hi, sP);
+                write(lo, sP + kSlab);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(p_ready[hh]);
+            } else {
+                write(hi, sP + hh * kSlab);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(p_ready[0]);
+            }
+        }
+        // -------------------------------------------------------------------------------- result
+        sL[tid] = l;
+        named_barrier(1, 128);
+        l += sL[tid ^ 64];
+        wait(b_pv + 8, (n_tiles - 1) & 1);
+        tc_fence_after();
+        if (ok) {
+            const bool any = l > 0.f || l != l;
+            const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
+            const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
+                                 (c * qpc + ql) * G + h;
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) {
+                uint32_t r[32];
+                tmem_ld32(tO + x * 32 + lane_addr, r);
+                tmem_ld_wait();
+                // columns x * 32 ..: dims 256 (x / 4) + 128 hh + 32 (x % 4) ..
+                const int d = (x >> 2) * 256 + hh * 128 + (x & 3) * 32;
+                if (!live) continue;
+                if (whole && p.o_bf16) {
+                    uint4 *o = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack_bf16(__uint_as_float(r[8 * j + 2 * k]) * inv,
+                                             __uint_as_float(r[8 * j + 2 * k + 1]) * inv);
+                        o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float4 *o = reinterpret_cast<float4 *>(
+                        (whole ? reinterpret_cast<float *>(p.O) + orow * 512 : p.part_o + part * 512) + d);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
+                                           __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
+                }
+            }
+            if (live && hh == 0) {
+                if (!whole) {
+                    p.part_ml[part * 2] = m;
+                    p.part_ml[part * 2 + 1] = l;
+                } else if (p.lse) {
+                    p.lse[orow] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
+                }
+            }
+        }
+    }
+
+    // -------------------------------------------------------------------------------- teardown
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {   // copies in flight land in shared memory that is still ours
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+    }
+    __syncwarp();
+    cluster_sync_all();   // neither CTA leaves while the other's products or arrivals need it
+    tc_fence_after();
+    if (warp == 6)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Tensor map of rows [n][heads][d] bf16 with boxes of `rows` x `heads_box` x 64 elements.
+bool encode_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t n, int heads_box, int rows) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows}, es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DKQ, bool VK, bool HL>
+int launch_wide_t(const Params &p, const WideMaps &maps, int bx, int qpc, int64_t n_cells, cudaStream_t st) {
+    if (!ensure_max_dynamic_smem(chunk_wide_kernel<DKQ, VK, HL>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_wide_kernel<DKQ, VK, HL>, dim3(2 * p.items, p.h_kv, p.n_split), dim3(kWideThreads),
+                   (size_t)Wide<DKQ>::kBytes, st, maps, p, bx, qpc, (int)n_cells) != cudaSuccess) {
+        cudaGetLastError();
+        return SFA_ERR_CUDA;
+    }
+    return SFA_OK;
+}
+
+}  // namespace
+
+// Queries of one CTA's 64 rows.
+int wide_qpc(int G) { return 64 / G; }
+
+int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st) {
+    int bx = p.page, y = 64;   // gcd(page, 64)
+    while (y) {
+        const int r = bx % y;
+        bx = y;
+        y = r;
+    }
+    const int qpc = wide_qpc(p.G);
+    WideMaps maps;
+    if (!encode_rows(&maps.q, p.Q, dkq, p.h_q, p.n_q, p.G, qpc)) return SFA_ERR_CUDA;
+    const int rows[3] = {bx, bx < 8 ? bx : 8, 1};
+    for (int i = 0; i < 3; ++i) {
+        if (!encode_rows(&maps.k[i], p.K, dkq, p.h_kv, n_cells, 1, rows[i])) return SFA_ERR_CUDA;
+        if (p.V && !encode_rows(&maps.v[i], p.V, 512, p.h_kv, n_cells, 1, rows[i])) return SFA_ERR_CUDA;
+    }
+    const bool hl = !p.o_bf16;
+    if (dkq == 576)
+        return hl ? launch_wide_t<576, true, true>(p, maps, bx, qpc, n_cells, st)
+                  : launch_wide_t<576, true, false>(p, maps, bx, qpc, n_cells, st);
+    if (p.V)
+        return hl ? launch_wide_t<512, false, true>(p, maps, bx, qpc, n_cells, st)
+                  : launch_wide_t<512, false, false>(p, maps, bx, qpc, n_cells, st);
+    return hl ? launch_wide_t<512, true, true>(p, maps, bx, qpc, n_cells, st)
+              : launch_wide_t<512, true, false>(p, maps, bx, qpc, n_cells, st);
+}
+
+}  // namespace chunk
+}  // namespace sfa
