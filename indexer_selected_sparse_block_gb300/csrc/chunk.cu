@@ -456,6 +456,7 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.status = dev_status;
     p.table_stride = table_stride;
     p.page = page_size;
+    p.page_div.set(page_size);
     p.n_pages = (int)(n_cells / page_size);
     p.n_seq = n_seq;
     p.n_q = n_q;

@@ -14,6 +14,24 @@ namespace chunk {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1, as a product: with 2^(k-1) < d <= 2^k and
+// m = floor(2^(31+k) / d) + 1, m d = 2^(31+k) + r with 0 < r <= d <= 2^k, so n m / 2^(31+k) exceeds
+// n / d by n r / (d 2^(31+k)) < 1 / d: the integer part is the same.  m < 2^32 as d > 2^(k-1),
+// except for d = 2^k, whose m = 2^31 + 1 is smaller still.
+struct FastDiv {
+    uint32_t m;
+    int s;
+    __host__ void set(int d) {
+        int k = 0;
+        while ((1ll << k) < d) ++k;
+        s = 31 + k;
+        m = (uint32_t)((1ull << s) / (uint32_t)d + 1);
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return (int)(((uint64_t)(uint32_t)n * m) >> s);
+    }
+};
+
 struct Params {
     const void *Q, *K, *V;
     const int32_t *table, *cu, *total;
@@ -21,6 +39,7 @@ struct Params {
     float *lse, *part_o, *part_ml;
     int32_t *status;
     int64_t table_stride;
+    FastDiv page_div;
     int page, n_pages, n_seq, n_q, h_q, h_kv, G;
     int o_bf16;          // O is bf16 (else fp32)
     int items;           // row tiles of all sequences, at most
@@ -113,12 +132,13 @@ __device__ __forceinline__ int key_limit(const Params &p, const Seq &q) {
     int64_t t = q.total;
     if (t > p.n_kv_max) t = p.n_kv_max;
     if (t > p.table_stride * p.page) t = p.table_stride * p.page;
+    if (t > 0x7FFFFFFF - 1023) t = 0x7FFFFFFF - 1023;   // a tile's end is an int
     return (int)(t > 0 ? t : 0);
 }
 
 // Cell of position t of sequence s, or -1 (flagged) when the page table's entry is no page.
 __device__ __forceinline__ int64_t cell_of(const Params &p, int s, int t) {
-    const int pg = t / p.page;
+    const int pg = p.page_div.div(t);
     const int e = __ldg(p.table + (int64_t)s * p.table_stride + pg);
     if (e < 0 || e >= p.n_pages) {
         set_status(p.status, SFA_DEV_BAD_CELL);

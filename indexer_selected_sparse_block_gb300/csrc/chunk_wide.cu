@@ -10,15 +10,13 @@
 // rows on all 128 lanes (the lanes' halves hold the two halves of the columns), so O takes 256
 // columns and two S tiles 128.  And Q needs 72 KB a CTA instead of 144.
 //
-// Shared memory of a CTA: Q (9 slabs of [64 rows][64 dims], 128-byte swizzle), two tile buffers of
-// eight slabs [64 keys][64 dims], one slab for dims 512..575, P (16 KB).  A buffer's life:
-//   first load    its own 64 keys' dims 0..511 for S;
-//   second load   once S has read them, the value slabs that it lacks: CTA c needs all 128 keys
-//                 of dims 128 c .. and 256 + 128 c ..  Of its own keys it has those already where
-//                 V is K; the other CTA's keys of these dims replace the slabs whose dims belong
-//                 to the other CTA.  Slab p then holds for product (key half h, n) the operand at
-//                 4 n + 2 h in both CTAs, which is what one descriptor for the pair needs.
-//                 V apart: all eight slabs are replaced.
+// Shared memory of a CTA: Q (9 slabs of [64 rows][64 dims], 128-byte swizzle), a ring of eight
+// operands of 16 KB (two slabs [64 keys][64 dims]), one slab for dims 512..575, P (16 KB).  The
+// operands pass through the ring in the order of their products: for S its own 64 keys' dims two
+// slabs at a time, for P V the 64 keys of a half with the 128 value dims of a CTA.  Where V is K a
+// value slab is read from L2 a second time: keeping it from S to P V would take half the ring
+// away from the loads in flight (measured: two tile buffers that keep them 4.65 us a tile, each
+// load's latency in sight).
 // Order of the products: S(t + 1), then P V (t): the softmax of tile t runs while S(t + 1) does,
 // and its 16 KB of P are written once P V (t - 1) has left the buffer.
 //
@@ -35,7 +33,7 @@
 // zeros: cells that hold no attended token may hold NaN.
 //
 // Warps 0-3: softmax, correction, result (a thread has one row and half of its keys and dims);
-// warp 4: first loads and Q; warp 5: second loads; warp 6: products (in the pair's first CTA).
+// warp 4: loads; warp 5: products (in the pair's first CTA).
 #include "chunk_common.cuh"
 
 namespace sfa {
@@ -44,7 +42,8 @@ namespace {
 
 constexpr int kT = 128;             // keys of a tile
 constexpr int kSlab = 64 * 128;     // bytes of 64 rows x 64 dims
-constexpr int kWideThreads = 224;
+constexpr int kWideThreads = 192;
+constexpr int kRing = 8;            // operands of two slabs in the ring
 constexpr float kLazy = 8.f;        // base-2 growth of the maximum that O is not rescaled for
 
 template <int DKQ>
@@ -52,14 +51,14 @@ struct Wide {
     static constexpr int kNSK = DKQ / 64;
     static constexpr bool kRope = kNSK > 8;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffBuf = kNSK * kSlab;               // [2][8] slabs
-    static constexpr int kOffRope = kOffBuf + 16 * kSlab;
+    static constexpr int kOffBuf = kNSK * kSlab;               // [kRing][2] slabs
+    static constexpr int kOffRope = kOffBuf + 2 * kRing * kSlab;
     static constexpr int kOffP = kOffRope + (kRope ? kSlab : 0);
     static constexpr int kOffMax = kOffP + 2 * kSlab;          // float [2][128]
     static constexpr int kOffL = kOffMax + 2 * 128 * 4;        // float [128]
     static constexpr int kOffItem = kOffL + 128 * 4;           // Item, padded
     static constexpr int kOffBar = kOffItem + 64;
-    static constexpr int kBars = 1 + 4 * 8 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kBars = 1 + 2 * kRing + 2 + 2 + 2 + 2 + 1;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
     static_assert(kBytes <= 227 * 1024, "fits one CTA per SM");
 };
@@ -88,19 +87,24 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Waits for the phase of `parity`; the limit counts from the wait's own start.  Acquires at
-// cluster scope (arrivals may come from the other CTA).
-__device__ __forceinline__ bool wait2(uint32_t bar, uint32_t parity) {
+// Waits for the phase of `parity`; the limit counts from the wait's own start.  Copies and
+// products (the async proxy) need no wider acquire than the CTA's; the arrivals of the other
+// CTA's threads (wait2_cluster) do, which costs about 200 cycles a wait.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait2_t(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
         uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
+        if constexpr (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        else
+            ok = mbar_try_wait(bar, parity);
         if (ok) return true;
         if ((it & 63u) == 63u) {
             const uint64_t now = global_timer_ns();
@@ -161,6 +165,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -168,58 +182,77 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------------------------------- key rows
-// Where the 64 keys of a half tile lie, a lane's share of the boxes that load them.
+// How the 64 keys of a half tile are loaded, a lane's share: 64 >> bs boxes of 1 << bs rows, this
+// lane's being lane and lane + 32; where the list ends inside one (`edge`) that one row by row.
+// The page table is read a tile ahead (`entry`: the raw entries), the cells follow from it.
 struct HalfRows {
-    bool whole;     // all 64 keys are in the list: boxes of bx rows
-    int row[2];     // first cell of this lane's boxes lane, lane + 32
-    int edge;       // not whole: the box of min(bx, 8) rows that the list ends in (else -1)
-    int single;     // cell of this lane's row of that box
+    int pos0, bs, edge;
+    int entry[2], single;
+    int row[2], srow;
 };
-// Keys pos0 .. pos0 + 63 of sequence s; the list ends before `end`.  Cells past it, and those of
-// pages that are none, are n_cells: outside the tensor, read as zeros.
-__device__ __forceinline__ HalfRows half_rows(const Params &p, int s, int pos0, int end, int bx, int n_cells) {
+// Keys pos0 .. pos0 + 63; the list ends before `end`.
+__device__ __forceinline__ void read_entries(HalfRows &h, const Params &p, const int32_t *table, int pos0,
+                                             int end, int bxs) {
     const int lane = threadIdx.x & 31;
-    auto cell = [&](int pos) -> int {
-        if (pos >= end) return n_cells;
-        const int pg = pos / p.page;
-        const int e = __ldg(p.table + (int64_t)s * p.table_stride + pg);
-        return e < 0 || e >= p.n_pages ? n_cells : e * p.page + (pos - pg * p.page);
-    };
-    HalfRows h;
-    h.whole = pos0 + 64 <= end;
+    auto entry = [&](int pos) -> int { return pos < end ? __ldg(table + p.page_div.div(pos)) : -1; };
+    h.pos0 = pos0;
+    const bool whole = pos0 + 64 <= end;
+    h.bs = whole ? bxs : min(bxs, 3);
     h.edge = -1;
-    h.single = n_cells;
-    const int b = h.whole ? bx : min(bx, 8);
-    const int n = 64 / b;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        h.row[i] = lane + 32 * i < n ? cell(pos0 + (lane + 32 * i) * b) : n_cells;
-    if (!h.whole && end > pos0 && (end - pos0) % b != 0) {
-        h.edge = (end - pos0) / b;
-        if (lane < b) h.single = cell(pos0 + h.edge * b + lane);
-    }
-    return h;
-}
-// One slab [64 keys][64 dims from x] of KV head g; by a whole warp.
-__device__ __forceinline__ void load_slab(const HalfRows &h, uint32_t dst, const CUtensorMap *maps,
-                                          int x, int g, int bx, uint32_t leader_bar) {
-    const int lane = threadIdx.x & 31;
-    const int b = h.whole ? bx : min(bx, 8);
-    const int n = 64 / b;
-    const CUtensorMap *map = maps + (h.whole ? 0 : 1);
+    h.single = -1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int box = lane + 32 * i;
-        if (box < n && box != h.edge) tma2_load(dst + box * b * 128, map, x, g, h.row[i], leader_bar);
+        h.entry[i] = box < (64 >> h.bs) ? entry(pos0 + (box << h.bs)) : -1;
     }
-    if (h.edge >= 0 && lane < b)
-        tma2_load(dst + (h.edge * b + lane) * 128, maps + 2, x, g, h.single, leader_bar);
+    const int in = end - pos0;
+    if (!whole && in > 0 && (in & ((1 << h.bs) - 1)) != 0) {
+        h.edge = in >> h.bs;
+        if (lane < (1 << h.bs)) h.single = entry(pos0 + (h.edge << h.bs) + lane);
+    }
+}
+// Entries -> cells.  Keys past the list's end and those of pages that are none get n_cells: outside
+// the tensor, read as zeros.
+__device__ __forceinline__ void find_rows(HalfRows &h, const Params &p, int n_cells) {
+    const int lane = threadIdx.x & 31;
+    auto cell = [&](int e, int pos) -> int {
+        return e < 0 || e >= p.n_pages ? n_cells : e * p.page + (pos - p.page_div.div(pos) * p.page);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) h.row[i] = cell(h.entry[i], h.pos0 + ((lane + 32 * i) << h.bs));
+    h.srow = cell(h.single, h.pos0 + (h.edge << h.bs) + lane);
+}
+// One or two slabs [64 keys][64 dims from x, x + 64] of KV head g; by a whole warp, one lane of
+// which issues (elect.sync and coordinates that are the same in all lanes: a copy or product
+// issued under a lane test costs the warp four times as long).
+template <int SLABS>
+__device__ __forceinline__ void load_slabs(const HalfRows &h, uint32_t dst, const CUtensorMap *maps,
+                                           int x, int g, int bxs, uint32_t leader_bar) {
+    auto box = [&](const CUtensorMap *map, uint32_t at, int row) {
+        if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s) tma2_load(dst + s * kSlab + at, map, x + 64 * s, g, row, leader_bar);
+        }
+    };
+    if (h.bs == 6) {
+        box(maps, 0, __shfl_sync(0xFFFFFFFFu, h.row[0], 0));
+        return;
+    }
+    const CUtensorMap *map = maps + (h.bs == bxs ? 0 : 1);
+    const int n = 64 >> h.bs;
+    for (int b = 0; b < n; ++b) {
+        const int row = __shfl_sync(0xFFFFFFFFu, b < 32 ? h.row[0] : h.row[1], b & 31);
+        if (b != h.edge) box(map, (uint32_t)(b << h.bs) << 7, row);
+    }
+    if (h.edge >= 0)
+        for (int i = 0; i < (1 << h.bs); ++i)
+            box(maps + 2, (uint32_t)((h.edge << h.bs) + i) << 7, __shfl_sync(0xFFFFFFFFu, h.srow, i));
 }
 
 // --------------------------------------------------------------------------------- the kernel
 template <int DKQ, bool VK, bool HL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
-    chunk_wide_kernel(const __grid_constant__ WideMaps maps, const Params p, int bx, int qpc, int n_cells) {
+    chunk_wide_kernel(const __grid_constant__ WideMaps maps, const Params p, int bxs, int qpc, int n_cells) {
     using L = Wide<DKQ>;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
@@ -229,11 +262,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t bar0 = smem_u32(bars);
-    // barriers, as shared addresses; [buffer][pair] ones at + (buffer * 4 + pair) * 8
-    const uint32_t b_q = bar0, b_fullA = bar0 + 8, b_fullB = b_fullA + 64, b_doneQ = b_fullB + 64,
-                   b_doneP = b_doneQ + 64, b_rope = b_doneP + 64, b_ropeDone = b_rope + 8,
-                   b_s = b_ropeDone + 8, b_p = b_s + 16, b_pv = b_p + 16, b_drain = b_pv + 16;
-    static_assert(L::kBars == 1 + 32 + 2 + 2 + 2 + 2 + 1, "barrier list");
+    // barriers, as shared addresses
+    const uint32_t b_q = bar0, b_full = bar0 + 8, b_empty = b_full + 8 * kRing, b_rope = b_empty + 8 * kRing,
+                   b_ropeDone = b_rope + 8, b_s = b_ropeDone + 8, b_p = b_s + 16, b_pv = b_p + 16,
+                   b_drain = b_pv + 16;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = (int)cluster_rank();
@@ -283,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 6) {
+    if (warp == 5) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(tmem_slot))
                      : "memory");
@@ -300,166 +332,169 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                    sRope = smem_u32(smem + L::kOffRope), sP = smem_u32(smem + L::kOffP);
     // once a wait ran out no other is made
     bool ok = true;
-    auto wait1 = [&](uint32_t bar, uint32_t parity) {
-        if (ok && (*abort_flag || !wait2(bar, parity))) {
+    auto wait = [&](uint32_t bar, uint32_t parity, bool cluster = false) {   // by a whole warp
+        if (ok && !(cluster ? wait2_t<true>(bar, parity) : wait2_t<false>(bar, parity))) {
             ok = false;
             *abort_flag = 1;
             set_status(p.status, SFA_DEV_TIMEOUT);
         }
-    };
-    auto wait = [&](uint32_t bar, uint32_t parity) {   // by a whole warp, which agrees on ok
-        wait1(bar, parity);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = __all_sync(0xFFFFFFFFu, ok);   // its lanes agree
     };
 
     if (warp == 4) {
-        // ------------------------------------------------------------------ Q and first loads
+        // ------------------------------------------------------------------------------- loads
         if (lane == 0) {
             prefetch_tensormap(&maps.q);
             prefetch_tensormap(&maps.k[0]);
+            if (!VK) prefetch_tensormap(&maps.v[0]);
             if (c == 0) mbar_arrive_expect_tx(bars, 2u * L::kNSK * 128u * (uint32_t)(qpc * G));
             for (int d = 0; d < L::kNSK; ++d)
                 tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + c * qpc, in_leader(b_q));
         }
         __syncwarp();
-        for (int t = 0; t < n_tiles && ok; ++t) {
-            const HalfRows r = half_rows(p, it.seq, k0 + t * kT + c * 64, k1, bx, n_cells);
-            const uint32_t b = t & 1, par = (t >> 1) & 1;
+        // cells of the tile whose P V is next and of the one after it; entries of the third
+        HalfRows rows[2], next[2], ahead[2];
+        const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
+        const uint32_t lead = in_leader(bar0);
+        auto read_ahead = [&](int t) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pr = ((i & 1) << 1) | (i >> 1);   // pairs 0, 2, 1, 3: in the order of use
-                const uint32_t at = (b * 4 + pr) * 8;
-                wait(b_doneP + at, par ^ 1);
-                if (!ok) break;
-                if (c == 0 && lane == 0) mbar_arrive_expect_tx(bars + (b_fullA + at - bar0) / 8, 4u * kSlab);
-                __syncwarp();
-                const uint32_t lb = in_leader(b_fullA + at);
+            for (int i = 0; i < 2; ++i) read_entries(ahead[i], p, table, k0 + t * kT + i * 64, k1, bxs);
+        };
+        read_ahead(0);
+        uint32_t e = 0;              // operands so far
+        auto operand = [&](const HalfRows &r, const CUtensorMap *m, int x) {
+            const uint32_t i = e % kRing;
+            wait(b_empty + i * 8, ((e / kRing) & 1) ^ 1);
+            ++e;
+            if (!ok) return;
+            if (c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (b_full - bar0) / 8 + i, 4u * kSlab);
+            __syncwarp();
+            load_slabs<2>(r, buf0 + 2 * i * kSlab, m, x, g, bxs, lead + (b_full - bar0) + i * 8);
+        };
+        auto s_ops = [&](int i0, int i1) {
+            for (int i = i0; i < i1 && ok; ++i) {
+                if (c == 0) operand(next[0], maps.k, 128 * i);
+                else operand(next[1], maps.k, 128 * i);
+            }
+        };
+        auto s_rope = [&](int t) {
+            if (!L::kRope || !ok) return;
+            wait(b_ropeDone, (t & 1) ^ 1);
+            if (!ok) return;
+            if (c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (b_rope - bar0) / 8, 2u * kSlab);
+            __syncwarp();
+            if (c == 0) load_slabs<1>(next[0], sRope, maps.k, 512, g, bxs, lead + (b_rope - bar0));
+            else load_slabs<1>(next[1], sRope, maps.k, 512, g, bxs, lead + (b_rope - bar0));
+        };
+        auto pv_ops = [&](const HalfRows &r) {
+            for (int n = 0; n < 2 && ok; ++n) operand(r, VK ? maps.k : maps.v, 256 * n + 128 * c);
+        };
+        for (int t = -1; t < n_tiles && ok; ++t) {
+            const bool more = t + 1 < n_tiles;
+            if (more) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    load_slab(r, buf0 + (b * 8 + 2 * pr + s) * kSlab, maps.k, (2 * pr + s) * 64, g, bx, lb);
+                for (int i = 0; i < 2; ++i) {
+                    next[i] = ahead[i];
+                    find_rows(next[i], p, n_cells);
+                }
+                read_ahead(t + 2);
             }
-            if (L::kRope && ok) {
-                wait(b_ropeDone, (t & 1) ^ 1);
-                if (!ok) break;
-                if (c == 0 && lane == 0) mbar_arrive_expect_tx(bars + (b_rope - bar0) / 8, 2u * kSlab);
-                __syncwarp();
-                load_slab(r, sRope, maps.k, 512, g, bx, in_leader(b_rope));
+            if (more) s_ops(0, HL ? 2 : 4);
+            if (!HL && more) s_rope(t + 1);
+            if (t >= 0) pv_ops(rows[0]);
+            if (HL && more) {
+                s_ops(2, 4);
+                s_rope(t + 1);
             }
+            if (t >= 0) pv_ops(rows[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) rows[i] = next[i];
         }
     } else if (warp == 5) {
-        // ------------------------------------------------------------------------ second loads
-        if (!VK && lane == 0) prefetch_tensormap(&maps.v[0]);
-        for (int t = 0; t < n_tiles && ok; ++t) {
-            const int kt = k0 + t * kT;
-            HalfRows r[2];
-            if (!VK) {
-                r[0] = half_rows(p, it.seq, kt, k1, bx, n_cells);
-                r[1] = half_rows(p, it.seq, kt + 64, k1, bx, n_cells);
-            } else {
-                r[0] = half_rows(p, it.seq, kt + (1 - c) * 64, k1, bx, n_cells);
-            }
-            const uint32_t b = t & 1, par = (t >> 1) & 1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int half = i >> 1, n = i & 1, pr = 2 * n + half;
-                const uint32_t at = (b * 4 + pr) * 8;
-                wait(b_doneQ + at, par);
-                if (!ok) break;
-                if (c == 0 && lane == 0)
-                    mbar_arrive_expect_tx(bars + (b_fullB + at - bar0) / 8, (VK ? 2u : 4u) * kSlab);
-                __syncwarp();
-                if (VK && half == c) continue;   // its own keys: there already
-                const uint32_t lb = in_leader(b_fullB + at);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    load_slab(r[VK ? 0 : half], buf0 + (b * 8 + 2 * pr + s) * kSlab,
-                              VK ? maps.k : maps.v, (4 * n + 2 * c + s) * 64, g, bx, lb);
-            }
-        }
-    } else if (warp == 6) {
         // ----------------------------------------------------------------------------- products
-        if (c == 0 && lane == 0) {
+        if (c == 0) {   // the whole warp waits, one lane issues
             const uint32_t idS = idesc_bf16_f32(128, 128);
             const uint32_t idPV = idesc_bf16_f32(128, 256) | (1u << 16);   // V: N-major
             const uint64_t dQ = sw128_desc(sQ, 16, 1024), dBuf = sw128_desc(buf0, 16, 1024),
                            dRope = sw128_desc(sRope, 16, 1024), dP = sw128_desc(sP, 16, 1024),
                            dV = sw128_desc(buf0, kSlab, 1024);
-            auto s_pairs = [&](int t, int i0, int i1) {   // S(t), pairs i0 .. i1 - 1 in their order
-                const uint32_t b = t & 1, par = (t >> 1) & 1;
+            uint32_t e = 0;
+            auto s_ops = [&](int t, int i0, int i1) {
                 for (int i = i0; i < i1; ++i) {
-                    const int pr = ((i & 1) << 1) | (i >> 1);
-                    wait1(b_fullA + (b * 4 + pr) * 8, par);
+                    const uint32_t r = e % kRing;
+                    wait(b_full + r * 8, (e / kRing) & 1);
+                    ++e;
                     if (!ok) return;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma2(tS + b * 64, dQ + (uint64_t)(((2 * pr + s) * kSlab + kk * 32) >> 4),
-                                 dBuf + (uint64_t)(((b * 8 + 2 * pr + s) * kSlab + kk * 32) >> 4), idS,
+                            mma2(tS + (t & 1) * 64, dQ + (uint64_t)(((2 * i + s) * kSlab + kk * 32) >> 4),
+                                 dBuf + (uint64_t)(((2 * r + s) * kSlab + kk * 32) >> 4), idS,
                                  (i > 0 || s > 0 || kk > 0) ? 1u : 0u);
-                    commit2(b_doneQ + (b * 4 + pr) * 8);
+                    commit2(b_empty + r * 8);
+                    }
+                    __syncwarp();
                 }
             };
             auto s_end = [&](int t) {
-                const uint32_t b = t & 1;
                 if (L::kRope) {
-                    wait1(b_rope, t & 1);
+                    wait(b_rope, t & 1);
                     if (!ok) return;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma2(tS + b * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
-                             dRope + (uint64_t)((kk * 32) >> 4), idS, 1u);
-                    commit2(b_ropeDone);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma2(tS + (t & 1) * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
+                                 dRope + (uint64_t)((kk * 32) >> 4), idS, 1u);
+                        commit2(b_ropeDone);
+                    }
+                    __syncwarp();
                 }
-                commit2(b_s + b * 8);
+                if (elect_one()) commit2(b_s + (t & 1) * 8);
+                __syncwarp();
             };
-            auto pv_half = [&](int t, int half) {
-                const uint32_t b = t & 1, par = (t >> 1) & 1;
-                if (HL || half == 0) wait1(b_p + half * 8, t & 1);
+            auto pv_ops = [&](int t, int half) {
+                if (HL || half == 0) wait(b_p + half * 8, t & 1, true);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const int pr = 2 * n + half;
-                    wait1(b_fullB + (b * 4 + pr) * 8, par);
+                    const uint32_t r = e % kRing;
+                    wait(b_full + r * 8, (e / kRing) & 1);
+                    ++e;
                     if (!ok) return;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
                     for (int x = 0; x < (HL ? 2 : 1); ++x)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma2(tO + n * 128, dP + (uint64_t)(((HL ? x : half) * kSlab + kk * 32) >> 4),
-                                 dV + (uint64_t)(((b * 8 + 2 * pr) * kSlab + kk * 2048) >> 4), idPV,
+                                 dV + (uint64_t)((2 * r * kSlab + kk * 2048) >> 4), idPV,
                                  (t > 0 || half > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                    commit2(b_doneP + (b * 4 + pr) * 8);
+                    commit2(b_empty + r * 8);
+                    if (n == 1 && (HL || half == 1)) commit2(b_pv + half * 8);
+                    }
+                    __syncwarp();
                 }
-                if (HL || half == 1) commit2(b_pv + half * 8);
             };
-            wait1(b_q, 0);
-            s_pairs(0, 0, 4);
-            if (ok) s_end(0);
-            for (int t = 0; t < n_tiles && ok; ++t) {
+            wait(b_q, 0);
+            for (int t = -1; t < n_tiles && ok; ++t) {
                 const bool more = t + 1 < n_tiles;
-                if (HL) {
-                    if (more) s_pairs(t + 1, 0, 2);
-                    if (ok) pv_half(t, 0);
-                    if (more && ok) {
-                        s_pairs(t + 1, 2, 4);
-                        if (ok) s_end(t + 1);
-                    }
-                    if (ok) pv_half(t, 1);
-                } else {
-                    if (more) {
-                        s_pairs(t + 1, 0, 4);
-                        if (ok) s_end(t + 1);
-                    }
-                    if (ok) pv_half(t, 0);
-                    if (ok) pv_half(t, 1);
+                if (more) s_ops(t + 1, 0, HL ? 2 : 4);
+                if (!HL && more && ok) s_end(t + 1);
+                if (t >= 0 && ok) pv_ops(t, 0);
+                if (HL && more && ok) {
+                    s_ops(t + 1, 2, 4);
+                    if (ok) s_end(t + 1);
                 }
+                if (t >= 0 && ok) pv_ops(t, 1);
             }
             if (!ok) {   // what was issued has to end before tensor memory is given back
-                commit2(b_drain);
-                wait2(b_drain, 0);
+                if (elect_one()) commit2(b_drain);
+                __syncwarp();
+                wait2_t<false>(b_drain, 0);
             }
         }
     } else {
@@ -471,27 +506,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
         const uint32_t p_ready[2] = {in_leader(b_p), in_leader(b_p + 8)};
         float m = -INFINITY, l = 0.f;                         // base 2; this thread's keys only
+        const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
+        int entry[2];
+        auto read_entry = [&](int key0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int key = key0 + 2 * lane + i;
+                entry[i] = key < k1 ? __ldg(table + p.page_div.div(key)) : -1;
+            }
+        };
+        read_entry(k0 + hh * 64);
         for (int t = 0; t < n_tiles; ++t) {
             const uint32_t b = t & 1, par = (t >> 1) & 1;
             const int kb = k0 + t * kT + hh * 64;             // the first of the thread's keys
-            uint32_t v0, v1;                                  // keys 2 i and 2 i + 1 have a cell
-            {
-                bool v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int key = kb + 2 * lane + i;
-                    v[i] = true;
-                    if (key < k1) {
-                        const int e = __ldg(p.table + (int64_t)it.seq * p.table_stride + key / p.page);
-                        if (e < 0 || e >= p.n_pages) {
-                            v[i] = false;
-                            set_status(p.status, SFA_DEV_BAD_CELL);
-                        }
-                    }
-                }
-                v0 = __ballot_sync(0xFFFFFFFFu, v[0]);
-                v1 = __ballot_sync(0xFFFFFFFFu, v[1]);
-            }
+            // keys 2 i and 2 i + 1 have a cell (their entries were read a tile ago)
+            const bool ok0 = kb + 2 * lane >= k1 || (entry[0] >= 0 && entry[0] < p.n_pages);
+            const bool ok1 = kb + 2 * lane + 1 >= k1 || (entry[1] >= 0 && entry[1] < p.n_pages);
+            if (!ok0 || !ok1) set_status(p.status, SFA_DEV_BAD_CELL);
+            const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, ok0), v1 = __ballot_sync(0xFFFFFFFFu, ok1);
+            read_entry(kb + kT);
             const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
             wait(b_s + b * 8, par);
             tc_fence_after();
@@ -645,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     __syncwarp();
     cluster_sync_all();   // neither CTA leaves while the other's products or arrivals need it
     tc_fence_after();
-    if (warp == 6)
+    if (warp == 5)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -662,10 +695,10 @@ bool encode_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t n
 }
 
 template <int DKQ, bool VK, bool HL>
-int launch_wide_t(const Params &p, const WideMaps &maps, int bx, int qpc, int64_t n_cells, cudaStream_t st) {
+int launch_wide_t(const Params &p, const WideMaps &maps, int bxs, int qpc, int64_t n_cells, cudaStream_t st) {
     if (!ensure_max_dynamic_smem(chunk_wide_kernel<DKQ, VK, HL>)) return SFA_ERR_CUDA;
     if (launch_pdl(chunk_wide_kernel<DKQ, VK, HL>, dim3(2 * p.items, p.h_kv, p.n_split), dim3(kWideThreads),
-                   (size_t)Wide<DKQ>::kBytes, st, maps, p, bx, qpc, (int)n_cells) != cudaSuccess) {
+                   (size_t)Wide<DKQ>::kBytes, st, maps, p, bxs, qpc, (int)n_cells) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
@@ -678,12 +711,9 @@ int launch_wide_t(const Params &p, const WideMaps &maps, int bx, int qpc, int64_
 int wide_qpc(int G) { return 64 / G; }
 
 int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st) {
-    int bx = p.page, y = 64;   // gcd(page, 64)
-    while (y) {
-        const int r = bx % y;
-        bx = y;
-        y = r;
-    }
+    int bxs = 0;   // rows of a box: gcd(page, 64), a power of two
+    while (bxs < 6 && p.page % (2 << bxs) == 0) ++bxs;
+    const int bx = 1 << bxs;
     const int qpc = wide_qpc(p.G);
     WideMaps maps;
     if (!encode_rows(&maps.q, p.Q, dkq, p.h_q, p.n_q, p.G, qpc)) return SFA_ERR_CUDA;
@@ -694,13 +724,13 @@ int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st) {
     }
     const bool hl = !p.o_bf16;
     if (dkq == 576)
-        return hl ? launch_wide_t<576, true, true>(p, maps, bx, qpc, n_cells, st)
-                  : launch_wide_t<576, true, false>(p, maps, bx, qpc, n_cells, st);
+        return hl ? launch_wide_t<576, true, true>(p, maps, bxs, qpc, n_cells, st)
+                  : launch_wide_t<576, true, false>(p, maps, bxs, qpc, n_cells, st);
     if (p.V)
-        return hl ? launch_wide_t<512, false, true>(p, maps, bx, qpc, n_cells, st)
-                  : launch_wide_t<512, false, false>(p, maps, bx, qpc, n_cells, st);
-    return hl ? launch_wide_t<512, true, true>(p, maps, bx, qpc, n_cells, st)
-              : launch_wide_t<512, true, false>(p, maps, bx, qpc, n_cells, st);
+        return hl ? launch_wide_t<512, false, true>(p, maps, bxs, qpc, n_cells, st)
+                  : launch_wide_t<512, false, false>(p, maps, bxs, qpc, n_cells, st);
+    return hl ? launch_wide_t<512, true, true>(p, maps, bxs, qpc, n_cells, st)
+              : launch_wide_t<512, true, false>(p, maps, bxs, qpc, n_cells, st);
 }
 
 }  // namespace chunk
