@@ -10,13 +10,12 @@
 // rows on all 128 lanes (the lanes' halves hold the two halves of the columns), so O takes 256
 // columns and two S tiles 128.  And Q needs 72 KB a CTA instead of 144.
 //
-// Shared memory of a CTA: Q (9 slabs of [64 rows][64 dims], 128-byte swizzle), a ring of eight
-// operands of 16 KB (two slabs [64 keys][64 dims]), one slab for dims 512..575, P (16 KB).  The
-// operands pass through the ring in the order of their products: for S its own 64 keys' dims two
-// slabs at a time, for P V the 64 keys of a half with the 128 value dims of a CTA.  Where V is K a
-// value slab is read from L2 a second time: keeping it from S to P V would take half the ring
-// away from the loads in flight (measured: two tile buffers that keep them 4.65 us a tile, each
-// load's latency in sight).
+// Shared memory of a CTA: Q (9 slabs of [64 rows][64 dims], 128-byte swizzle), eight operand
+// slots of 16 KB (two slabs [64 keys][64 dims]), one slab for dims 512..575, P (16 KB).  Slots 0-3
+// hold S's operands, the CTA's own 64 keys, 128 dims each; slots 4-7 P V's, slot 4 + 2 half + n the
+// 64 keys of `half` with value dims 256 n + 128 c ..  Where V is K a value slab is read from L2 a
+// second time: keeping it from S to P V would take half the slots away from the loads in flight
+// (measured: two tile buffers that keep them 4.65 us a tile, each load's latency in sight).
 // Order of the products: S(t + 1), then P V (t): the softmax of tile t runs while S(t + 1) does,
 // and its 16 KB of P are written once P V (t - 1) has left the buffer.
 //
@@ -32,8 +31,11 @@
 // boxes of 8 rows and of one, those past the end from outside the tensor, which reads as
 // zeros: cells that hold no attended token may hold NaN.
 //
-// Warps 0-3: softmax, correction, result (a thread has one row and half of its keys and dims);
-// warp 4: loads; warp 5: products (in the pair's first CTA).
+// Warps 0-7: softmax, correction, result: a thread has one row, a quarter of its keys and a
+// quarter of its value dims; warps 8-11: loads, one S and one P V operand of a tile each (a
+// warp's barrier wait, expect and copy take about 330 cycles whatever the copy's size, a further
+// copy 15: four warps reach 83 bytes a cycle and SM, one 25); warp 12: products (in the pair's
+// first CTA).
 #include "chunk_common.cuh"
 
 namespace sfa {
@@ -42,8 +44,8 @@ namespace {
 
 constexpr int kT = 128;             // keys of a tile
 constexpr int kSlab = 64 * 128;     // bytes of 64 rows x 64 dims
-constexpr int kWideThreads = 192;
-constexpr int kRing = 8;            // operands of two slabs in the ring
+constexpr int kWideThreads = 416;
+constexpr int kSlots = 8;           // operands of two slabs
 constexpr float kLazy = 8.f;        // base-2 growth of the maximum that O is not rescaled for
 
 template <int DKQ>
@@ -51,14 +53,13 @@ struct Wide {
     static constexpr int kNSK = DKQ / 64;
     static constexpr bool kRope = kNSK > 8;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffBuf = kNSK * kSlab;               // [kRing][2] slabs
-    static constexpr int kOffRope = kOffBuf + 2 * kRing * kSlab;
+    static constexpr int kOffBuf = kNSK * kSlab;               // [kSlots][2] slabs
+    static constexpr int kOffRope = kOffBuf + 2 * kSlots * kSlab;
     static constexpr int kOffP = kOffRope + (kRope ? kSlab : 0);
-    static constexpr int kOffMax = kOffP + 2 * kSlab;          // float [2][128]
-    static constexpr int kOffL = kOffMax + 2 * 128 * 4;        // float [128]
-    static constexpr int kOffItem = kOffL + 128 * 4;           // Item, padded
+    static constexpr int kOffMax = kOffP + 2 * kSlab;          // float [2][256]
+    static constexpr int kOffItem = kOffMax + 2 * 256 * 4;     // Item, padded
     static constexpr int kOffBar = kOffItem + 64;
-    static constexpr int kBars = 1 + 2 * kRing + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kBars = 1 + 2 * kSlots + 2 + 2 + 2 + 2 + 1;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
     static_assert(kBytes <= 227 * 1024, "fits one CTA per SM");
 };
@@ -112,6 +113,17 @@ __device__ __forceinline__ bool wait2_t(uint32_t bar, uint32_t parity) {
             else if (now - t0 > kWaitLimitNs) return false;
         }
     }
+}
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // does not block
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // Tiled load into this CTA's shared memory, its bytes counted on a barrier of the pair's first CTA.
 __device__ __forceinline__ void tma2_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -256,14 +268,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     using L = Wide<DKQ>;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
-    float *sL = reinterpret_cast<float *>(smem + L::kOffL);
     Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t bar0 = smem_u32(bars);
     // barriers, as shared addresses
-    const uint32_t b_q = bar0, b_full = bar0 + 8, b_empty = b_full + 8 * kRing, b_rope = b_empty + 8 * kRing,
+    const uint32_t b_q = bar0, b_full = bar0 + 8, b_empty = b_full + 8 * kSlots, b_rope = b_empty + 8 * kSlots,
                    b_ropeDone = b_rope + 8, b_s = b_ropeDone + 8, b_p = b_s + 16, b_pv = b_p + 16,
                    b_drain = b_pv + 16;
 
@@ -289,33 +300,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const int n_tiles = (k1 - k0 + kT - 1) / kT;
     const int G = p.G;
 
-    // a thread's row: query ql of this CTA's qpc, head h; both halves of the lanes have every row
-    const int row = (warp & 1) * 32 + lane, hh = (warp >> 1) & 1;
+    // a softmax thread's row: query ql of this CTA's qpc, head h.  Both halves hh of the tensor
+    // memory lanes have every row, and two warps (cg) share a lane's columns.
+    const int row = (warp & 1) * 32 + lane, hh = (warp >> 1) & 1, cg = warp >> 2;
     const int ql = row / G, h = row - ql * G;
-    const bool live = warp < 4 && ql < qpc && c * qpc + ql < nq;
+    const bool live = warp < 8 && ql < qpc && c * qpc + ql < nq;
     const int64_t orow = (int64_t)(it.q.c0 + q0 + c * qpc + ql) * p.h_q + g * G + h;
 
     if (n_tiles == 0) {   // nothing to attend: zeros
         if (live) {
-            for (int d = hh * 256; d < hh * 256 + 256; d += 4) {
+            for (int d = (2 * hh + cg) * 128; d < (2 * hh + cg + 1) * 128; d += 4) {
                 if (p.o_bf16)
                     *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d) = make_uint2(0, 0);
                 else
                     *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * 512 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (hh == 0 && p.lse) p.lse[orow] = -INFINITY;
+            if (hh == 0 && cg == 0 && p.lse) p.lse[orow] = -INFINITY;
         }
         return;
     }
 
     if (tid == 0) {
         const int ip = (int)(b_p - bar0) / 8;
-        // P (half 0) ready: four warps of each CTA; P half 1: two of each
-        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 8 : i == ip + 1 ? 4 : 1);
+        // P (half 0) ready: eight warps of each CTA; P half 1: four of each
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 16 : i == ip + 1 ? 8 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 5) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(tmem_slot))
                      : "memory");
@@ -332,158 +344,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                    sRope = smem_u32(smem + L::kOffRope), sP = smem_u32(smem + L::kOffP);
     // once a wait ran out no other is made
     bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity, bool cluster = false) {   // by a whole warp
+    auto wait = [&](uint32_t bar, uint32_t parity, bool cluster = false) {
         if (ok && !(cluster ? wait2_t<true>(bar, parity) : wait2_t<false>(bar, parity))) {
             ok = false;
             *abort_flag = 1;
             set_status(p.status, SFA_DEV_TIMEOUT);
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);   // its lanes agree
     };
+    const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
 
-    if (warp == 4) {
+    if (warp >= 8 && warp < 12) {
         // ------------------------------------------------------------------------------- loads
-        if (lane == 0) {
-            prefetch_tensormap(&maps.q);
-            prefetch_tensormap(&maps.k[0]);
-            if (!VK) prefetch_tensormap(&maps.v[0]);
+        const int j = warp - 8, half = j >> 1, n = j & 1;
+        const uint32_t lead = in_leader(bar0);
+        if (j == 0 && elect_one()) {
             if (c == 0) mbar_arrive_expect_tx(bars, 2u * L::kNSK * 128u * (uint32_t)(qpc * G));
             for (int d = 0; d < L::kNSK; ++d)
-                tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + c * qpc, in_leader(b_q));
+                tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + c * qpc, lead);
         }
         __syncwarp();
-        // cells of the tile whose P V is next and of the one after it; entries of the third
-        HalfRows rows[2], next[2], ahead[2];
-        const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
-        const uint32_t lead = in_leader(bar0);
-        auto read_ahead = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) read_entries(ahead[i], p, table, k0 + t * kT + i * 64, k1, bxs);
-        };
-        read_ahead(0);
-        uint32_t e = 0;              // operands so far
-        auto operand = [&](const HalfRows &r, const CUtensorMap *m, int x) {
-            const uint32_t i = e % kRing;
-            wait(b_empty + i * 8, ((e / kRing) & 1) ^ 1);
-            ++e;
-            if (!ok) return;
-            if (c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (b_full - bar0) / 8 + i, 4u * kSlab);
+        // keys of S (this CTA's half) and of P V (half), their table entries read a tile ahead
+        HalfRows hs, hv;
+        read_entries(hs, p, table, k0 + c * 64, k1, bxs);
+        read_entries(hv, p, table, k0 + half * 64, k1, bxs);
+        auto slot_free = [&](uint32_t full, uint32_t empty, uint32_t parity, uint32_t bytes) {
+            wait(empty, parity);
+            ok = __all_sync(0xFFFFFFFFu, ok);   // the warp's lanes agree
+            if (ok && c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (full - bar0) / 8, bytes);
             __syncwarp();
-            load_slabs<2>(r, buf0 + 2 * i * kSlab, m, x, g, bxs, lead + (b_full - bar0) + i * 8);
-        };
-        auto s_ops = [&](int i0, int i1) {
-            for (int i = i0; i < i1 && ok; ++i) {
-                if (c == 0) operand(next[0], maps.k, 128 * i);
-                else operand(next[1], maps.k, 128 * i);
-            }
-        };
-        auto s_rope = [&](int t) {
-            if (!L::kRope || !ok) return;
-            wait(b_ropeDone, (t & 1) ^ 1);
-            if (!ok) return;
-            if (c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (b_rope - bar0) / 8, 2u * kSlab);
-            __syncwarp();
-            if (c == 0) load_slabs<1>(next[0], sRope, maps.k, 512, g, bxs, lead + (b_rope - bar0));
-            else load_slabs<1>(next[1], sRope, maps.k, 512, g, bxs, lead + (b_rope - bar0));
-        };
-        auto pv_ops = [&](const HalfRows &r) {
-            for (int n = 0; n < 2 && ok; ++n) operand(r, VK ? maps.k : maps.v, 256 * n + 128 * c);
         };
         for (int t = -1; t < n_tiles && ok; ++t) {
-            const bool more = t + 1 < n_tiles;
-            if (more) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    next[i] = ahead[i];
-                    find_rows(next[i], p, n_cells);
+            if (t + 1 < n_tiles) {
+                find_rows(hs, p, n_cells);
+                const uint32_t full = b_full + j * 8;
+                slot_free(full, b_empty + j * 8, (t & 1), 4u * kSlab);
+                if (!ok) break;
+                load_slabs<2>(hs, buf0 + 2 * j * kSlab, maps.k, 128 * j, g, bxs, lead + (full - bar0));
+                if (L::kRope && j == 3) {
+                    slot_free(b_rope, b_ropeDone, (t & 1), 2u * kSlab);
+                    if (!ok) break;
+                    load_slabs<1>(hs, sRope, maps.k, 512, g, bxs, lead + (b_rope - bar0));
                 }
-                read_ahead(t + 2);
+                read_entries(hs, p, table, k0 + (t + 2) * kT + c * 64, k1, bxs);
             }
-            if (more) s_ops(0, HL ? 2 : 4);
-            if (!HL && more) s_rope(t + 1);
-            if (t >= 0) pv_ops(rows[0]);
-            if (HL && more) {
-                s_ops(2, 4);
-                s_rope(t + 1);
+            if (t >= 0) {
+                find_rows(hv, p, n_cells);
+                const uint32_t full = b_full + (4 + j) * 8;
+                slot_free(full, b_empty + (4 + j) * 8, (t & 1) ^ 1, 4u * kSlab);
+                if (!ok) break;
+                load_slabs<2>(hv, buf0 + 2 * (4 + j) * kSlab, VK ? maps.k : maps.v, 256 * n + 128 * c, g,
+                              bxs, lead + (full - bar0));
+                read_entries(hv, p, table, k0 + (t + 1) * kT + half * 64, k1, bxs);
             }
-            if (t >= 0) pv_ops(rows[1]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) rows[i] = next[i];
         }
-    } else if (warp == 5) {
+    } else if (warp == 12) {
         // ----------------------------------------------------------------------------- products
-        if (c == 0) {   // the whole warp waits, one lane issues
+        if (c == 0 && elect_one()) {
             const uint32_t idS = idesc_bf16_f32(128, 128);
             const uint32_t idPV = idesc_bf16_f32(128, 256) | (1u << 16);   // V: N-major
             const uint64_t dQ = sw128_desc(sQ, 16, 1024), dBuf = sw128_desc(buf0, 16, 1024),
                            dRope = sw128_desc(sRope, 16, 1024), dP = sw128_desc(sP, 16, 1024),
-                           dV = sw128_desc(buf0, kSlab, 1024);
-            uint32_t e = 0;
+                           dV = sw128_desc(buf0 + 8 * kSlab, kSlab, 1024);
+            // an operand's barrier is looked at before the products of the one ahead of it
+            bool there = false;
+            auto take = [&](uint32_t bar, uint32_t parity) {
+                if (!there) wait(bar, parity);
+                tc_fence_after();
+            };
             auto s_ops = [&](int t, int i0, int i1) {
                 for (int i = i0; i < i1; ++i) {
-                    const uint32_t r = e % kRing;
-                    wait(b_full + r * 8, (e / kRing) & 1);
-                    ++e;
+                    take(b_full + i * 8, t & 1);
                     if (!ok) return;
-                    tc_fence_after();
-                    if (elect_one()) {
+                    there = i < 3 ? mbar_test_wait(b_full + (i + 1) * 8, t & 1)
+                                  : L::kRope && mbar_test_wait(b_rope, t & 1);
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma2(tS + (t & 1) * 64, dQ + (uint64_t)(((2 * i + s) * kSlab + kk * 32) >> 4),
-                                 dBuf + (uint64_t)(((2 * r + s) * kSlab + kk * 32) >> 4), idS,
+                                 dBuf + (uint64_t)(((2 * i + s) * kSlab + kk * 32) >> 4), idS,
                                  (i > 0 || s > 0 || kk > 0) ? 1u : 0u);
-                    commit2(b_empty + r * 8);
-                    }
-                    __syncwarp();
+                    commit2(b_empty + i * 8);
                 }
             };
             auto s_end = [&](int t) {
                 if (L::kRope) {
-                    wait(b_rope, t & 1);
+                    take(b_rope, t & 1);
                     if (!ok) return;
-                    tc_fence_after();
-                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma2(tS + (t & 1) * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
-                                 dRope + (uint64_t)((kk * 32) >> 4), idS, 1u);
-                        commit2(b_ropeDone);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma2(tS + (t & 1) * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
+                             dRope + (uint64_t)((kk * 32) >> 4), idS, 1u);
+                    commit2(b_ropeDone);
                 }
-                if (elect_one()) commit2(b_s + (t & 1) * 8);
-                __syncwarp();
+                commit2(b_s + (t & 1) * 8);
+                there = false;
             };
             auto pv_ops = [&](int t, int half) {
                 if (HL || half == 0) wait(b_p + half * 8, t & 1, true);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const uint32_t r = e % kRing;
-                    wait(b_full + r * 8, (e / kRing) & 1);
-                    ++e;
+                    const int i = 2 * half + n;
+                    take(b_full + (4 + i) * 8, t & 1);
                     if (!ok) return;
-                    tc_fence_after();
-                    if (elect_one()) {
+                    there = n == 0 ? mbar_test_wait(b_full + (5 + i) * 8, t & 1) : false;
 #pragma unroll
                     for (int x = 0; x < (HL ? 2 : 1); ++x)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma2(tO + n * 128, dP + (uint64_t)(((HL ? x : half) * kSlab + kk * 32) >> 4),
-                                 dV + (uint64_t)((2 * r * kSlab + kk * 2048) >> 4), idPV,
+                                 dV + (uint64_t)((2 * i * kSlab + kk * 2048) >> 4), idPV,
                                  (t > 0 || half > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                    commit2(b_empty + r * 8);
-                    if (n == 1 && (HL || half == 1)) commit2(b_pv + half * 8);
-                    }
-                    __syncwarp();
+                    commit2(b_empty + (4 + i) * 8);
                 }
+                if (HL || half == 1) commit2(b_pv + half * 8);
             };
             wait(b_q, 0);
             for (int t = -1; t < n_tiles && ok; ++t) {
                 const bool more = t + 1 < n_tiles;
                 if (more) s_ops(t + 1, 0, HL ? 2 : 4);
                 if (!HL && more && ok) s_end(t + 1);
+                if (HL) there = false;
                 if (t >= 0 && ok) pv_ops(t, 0);
                 if (HL && more && ok) {
                     s_ops(t + 1, 2, 4);
@@ -492,135 +473,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 if (t >= 0 && ok) pv_ops(t, 1);
             }
             if (!ok) {   // what was issued has to end before tensor memory is given back
-                if (elect_one()) commit2(b_drain);
-                __syncwarp();
+                commit2(b_drain);
                 wait2_t<false>(b_drain, 0);
             }
         }
-    } else {
+        __syncwarp();
+    } else if (warp < 8) {
         // ------------------------------------------------------------------------------ softmax
         const int pos = pos0 + c * qpc + ql;                  // the row's last key
-        const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const bool neg = p.scale_log2 < 0.f;
         // a zero scale: weights of 1 to 1e-28
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
-        const uint32_t p_ready[2] = {in_leader(b_p), in_leader(b_p + 8)};
-        float m = -INFINITY, l = 0.f;                         // base 2; this thread's keys only
-        const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
-        int entry[2];
-        auto read_entry = [&](int key0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int key = key0 + 2 * lane + i;
-                entry[i] = key < k1 ? __ldg(table + p.page_div.div(key)) : -1;
-            }
-        };
-        read_entry(k0 + hh * 64);
+        const uint32_t p_ready0 = in_leader(b_p), p_ready1 = p_ready0 + 8;
+        float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
+        const int kq = k0 + hh * 64 + cg * 32;                // the thread's first key
+        auto read_entry = [&](int key) { return key < k1 ? __ldg(table + p.page_div.div(key)) : 0; };
+        int entry = read_entry(kq + lane);
         for (int t = 0; t < n_tiles; ++t) {
             const uint32_t b = t & 1, par = (t >> 1) & 1;
-            const int kb = k0 + t * kT + hh * 64;             // the first of the thread's keys
-            // keys 2 i and 2 i + 1 have a cell (their entries were read a tile ago)
-            const bool ok0 = kb + 2 * lane >= k1 || (entry[0] >= 0 && entry[0] < p.n_pages);
-            const bool ok1 = kb + 2 * lane + 1 >= k1 || (entry[1] >= 0 && entry[1] < p.n_pages);
-            if (!ok0 || !ok1) set_status(p.status, SFA_DEV_BAD_CELL);
-            const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, ok0), v1 = __ballot_sync(0xFFFFFFFFu, ok1);
-            read_entry(kb + kT);
+            const int kb = kq + t * kT;
+            // bit j: key kb + j has a cell (its entry was read a tile ago)
+            const bool cell = kb + lane >= k1 || (entry >= 0 && entry < p.n_pages);
+            if (!cell) set_status(p.status, SFA_DEV_BAD_CELL);
+            const uint32_t cells = __ballot_sync(0xFFFFFFFFu, cell);
+            entry = read_entry(kb + kT + lane);
             const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
             wait(b_s + b * 8, par);
             tc_fence_after();
-            float s[64];
-            {
-                uint32_t r0[32], r1[32];
-                tmem_ld32(tS + b * 64 + lane_addr, r0);
-                tmem_ld32(tS + b * 64 + 32 + lane_addr, r1);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    s[j] = __uint_as_float(r0[j]);
-                    s[32 + j] = __uint_as_float(r1[j]);
-                }
-            }
+            uint32_t r[32];
+            tmem_ld32(tS + b * 64 + cg * 32 + lane_addr, r);
+            tmem_ld_wait();
             tc_fence_before();
+            float s[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(r[j]);
             if (neg) {
 #pragma unroll
-                for (int j = 0; j < 64; ++j) s[j] = -s[j];
+                for (int j = 0; j < 32; ++j) s[j] = -s[j];
             }
-            if (last < 63 || (v0 & v1) != 0xFFFFFFFFu) {
+            if (last < 31 || cells != 0xFFFFFFFFu) {
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (j > last || !(((j & 1 ? v1 : v0) >> (j >> 1)) & 1)) s[j] = -INFINITY;
+                for (int j = 0; j < 32; ++j)
+                    if (j > last || !((cells >> j) & 1)) s[j] = -INFINITY;
             }
-            float mx = s[0];
+            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int j = 1; j < 64; ++j) mx = fmaxf(mx, s[j]);
-            sMax[b * 128 + tid] = mx;
-            named_barrier(1, 128);
-            mx = fmaxf(mx, sMax[b * 128 + (tid ^ 64)]) * sc;
+            for (int j = 4; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float *mb = sMax + b * 256;
+            mb[tid] = mx[0];
+            named_barrier(1, 256);
+            mx[0] = fmaxf(fmaxf(mx[0], mb[tid ^ 64]), fmaxf(mb[tid ^ 128], mb[tid ^ 192])) * sc;
             float alpha = 1.f;
-            if (mx > m + kLazy || (m == -INFINITY && mx > m)) {
-                alpha = ex2(m - mx);
-                m = mx;
+            if (mx[0] > m + kLazy || (m == -INFINITY && mx[0] > m)) {
+                alpha = ex2(m - mx[0]);
+                m = mx[0];
             }
             const float mm = m == -INFINITY ? 0.f : m;
-            float sum = 0.f;
-            uint32_t hi[32], lo[HL ? 32 : 1];
+            float sum[2] = {0.f, 0.f};
+            uint32_t hi[16], lo[HL ? 16 : 1];
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
+            for (int j = 0; j < 32; j += 2) {
                 const float e0 = ex2(fmaf(s[j], sc, -mm)), e1 = ex2(fmaf(s[j + 1], sc, -mm));
-                sum += e0 + e1;
+                sum[0] += e0;
+                sum[1] += e1;
                 hi[j / 2] = pack_bf16(e0, e1);
                 if constexpr (HL)
                     lo[j / 2] = pack_bf16(e0 - __uint_as_float(hi[j / 2] << 16),
                                           e1 - __uint_as_float(hi[j / 2] & 0xFFFF0000u));
             }
-            l = l * alpha + sum;
+            l = l * alpha + (sum[0] + sum[1]);
             // the products of the tile before are done with P and O
             if (t > 0) wait(b_pv + 8, (t - 1) & 1);
-            if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f) && ok) {
+            if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
                 tc_fence_after();
 #pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    uint32_t r[32];
-                    tmem_ld32(tO + x * 32 + lane_addr, r);
+                for (int x = 0; x < 4; ++x) {
+                    tmem_ld32(tO + (cg * 4 + x) * 32 + lane_addr, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-                    tmem_st32(tO + x * 32 + lane_addr, r);
+                    tmem_st32(tO + (cg * 4 + x) * 32 + lane_addr, r);
                 }
                 tmem_st_wait();
                 tc_fence_before();
             }
-            auto write = [&](const uint32_t (&w)[32], uint32_t slab) {
+            auto write = [&](const uint32_t *w, uint32_t slab) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
+                for (int x = 0; x < 4; ++x)
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     slab + row * 128 + ((x ^ (row & 7)) << 4)),
+                                     slab + row * 128 + (((cg * 4 + x) ^ (row & 7)) << 4)),
                                  "r"(w[4 * x]), "r"(w[4 * x + 1]), "r"(w[4 * x + 2]), "r"(w[4 * x + 3])
                                  : "memory");
             };
             if constexpr (HL) {
                 if (hh == 1) {   // O is rescaled; then P's second half, when the first is used up
                     __syncwarp();
-                    if (lane == 0) arrive_cluster(p_ready[0]);
+                    if (lane == 0) arrive_cluster(p_ready0);
                     wait(b_pv, t & 1);
                 }
                 write(hi, sP);
                 write(lo, sP + kSlab);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(p_ready[hh]);
+                if (lane == 0) arrive_cluster(hh == 1 ? p_ready1 : p_ready0);
             } else {
                 write(hi, sP + hh * kSlab);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(p_ready[0]);
+                if (lane == 0) arrive_cluster(p_ready0);
             }
         }
         // -------------------------------------------------------------------------------- result
-        sL[tid] = l;
-        named_barrier(1, 128);
-        l += sL[tid ^ 64];
+        {   // the buffer that the last tile's maxima did not use
+            float *lb = sMax + (n_tiles & 1) * 256;
+            lb[tid] = l;
+            named_barrier(1, 256);
+            l = (l + lb[tid ^ 64]) + (lb[tid ^ 128] + lb[tid ^ 192]);
+        }
         wait(b_pv + 8, (n_tiles - 1) & 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         if (ok) {
             const bool any = l > 0.f || l != l;
@@ -628,12 +601,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
                                  (c * qpc + ql) * G + h;
 #pragma unroll 1
-            for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < 4; ++x) {
                 uint32_t r[32];
-                tmem_ld32(tO + x * 32 + lane_addr, r);
+                tmem_ld32(tO + (cg * 4 + x) * 32 + lane_addr, r);
                 tmem_ld_wait();
-                // columns x * 32 ..: dims 256 (x / 4) + 128 hh + 32 (x % 4) ..
-                const int d = (x >> 2) * 256 + hh * 128 + (x & 3) * 32;
+                // columns 128 cg + 32 x ..: dims 256 cg + 128 hh + 32 x ..
+                const int d = cg * 256 + hh * 128 + x * 32;
                 if (!live) continue;
                 if (whole && p.o_bf16) {
                     uint4 *o = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d);
@@ -655,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                                            __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
                 }
             }
-            if (live && hh == 0) {
+            if (live && hh == 0 && cg == 0) {
                 if (!whole) {
                     p.part_ml[part * 2] = m;
                     p.part_ml[part * 2 + 1] = l;
@@ -678,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     __syncwarp();
     cluster_sync_all();   // neither CTA leaves while the other's products or arrivals need it
     tc_fence_after();
-    if (warp == 5)
+    if (warp == 12)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
