@@ -80,33 +80,22 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t saddr) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(saddr));
     return r;
 }
+// Arrives on a barrier of the other CTA.  What it publishes is this CTA's own shared memory, for
+// the async proxy (fenced before): no release at cluster scope, which would also wait for the
+// thread's loads in flight (measured: 1.8 to 3.9 thousand cycles a tile).
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
 }
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Waits for the phase of `parity`; the limit counts from the wait's own start.  Copies and
-// products (the async proxy) need no wider acquire than the CTA's; the arrivals of the other
-// CTA's threads (wait2_cluster) do, which costs about 200 cycles a wait.
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait2_t(uint32_t bar, uint32_t parity) {
+// Waits for the phase of `parity`; the limit counts from the wait's own start.
+__device__ __forceinline__ bool wait2(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
-        uint32_t ok;
-        if constexpr (CLUSTER)
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(bar), "r"(parity)
-                : "memory");
-        else
-            ok = mbar_try_wait(bar, parity);
-        if (ok) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 63u) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
@@ -344,8 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                    sRope = smem_u32(smem + L::kOffRope), sP = smem_u32(smem + L::kOffP);
     // once a wait ran out no other is made
     bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity, bool cluster = false) {
-        if (ok && !(cluster ? wait2_t<true>(bar, parity) : wait2_t<false>(bar, parity))) {
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok && !wait2(bar, parity)) {
             ok = false;
             *abort_flag = 1;
             set_status(p.status, SFA_DEV_TIMEOUT);
@@ -441,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 there = false;
             };
             auto pv_ops = [&](int t, int half) {
-                if (HL || half == 0) wait(b_p + half * 8, t & 1, true);
+                if (HL || half == 0) wait(b_p + half * 8, t & 1);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const int i = 2 * half + n;
@@ -474,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             }
             if (!ok) {   // what was issued has to end before tensor memory is given back
                 commit2(b_drain);
-                wait2_t<false>(b_drain, 0);
+                wait2(b_drain, 0);
             }
         }
         __syncwarp();
