@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 }
 
 // --------------------------------------------------------------------------------- the plan
-enum Kernel { kSimt, kWide };
+enum Kernel { kSimt, kWide, kNarrow };
 struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, n_split, split_keys;
@@ -325,16 +325,16 @@ int64_t items_bound(int n_seq, int n_q, int G, int n_new_max, int item_rows, int
 Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new_max,
                int64_t n_kv_max, int64_t n_cells, bool o_bf16) {
     Plan pl;
-    const bool wide = dtype == SFA_BF16 && dv == 512 && n_cells > 0;
-    pl.kernel = wide ? kWide : kSimt;
-    pl.item_rows = wide ? 128 : kRows;
-    pl.item_q = wide ? 2 * wide_qpc(G) : 0;
+    const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
+    pl.kernel = wide ? kWide : tc ? kNarrow : kSimt;
+    pl.item_rows = wide ? 128 : tc ? 256 : kRows;
+    pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
     pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
     const int tile = 128;
     const int64_t tiles = (n_kv_max + tile - 1) / tile;
     const double slots = wide ? device_sm_count() / 2 : device_sm_count();
-    const double t_tile = wide ? (o_bf16 ? 1.4 : 2.1) : dv == 512 ? 30. : 8.;   // us
+    const double t_tile = tc ? (o_bf16 ? 1.4 : 2.1) : dv == 512 ? 30. : 8.;   // us
     const double t_piece = 6., t_merge = 4.;
     const double part_us = (double)pl.item_rows * dv * 4 * 2 / 4e6;             // a partial, both ways
     const int64_t units = items * h_kv;
@@ -475,6 +475,7 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     cudaStream_t st = (cudaStream_t)stream;
     int r;
     if (pl.kernel == kWide) r = launch_wide(p, dkq, n_cells, st);
+    else if (pl.kernel == kNarrow) r = launch_narrow(p, dkq, n_cells, st);
     else if (dkq == 576) r = launch_simt<576, 512, true>(p, dtype, st);
     else if (dkq == 512) r = V ? launch_simt<512, 512, false>(p, dtype, st) : launch_simt<512, 512, true>(p, dtype, st);
     else if (dkq == 128) r = V ? launch_simt<128, 128, false>(p, dtype, st) : launch_simt<128, 128, true>(p, dtype, st);

@@ -149,8 +149,12 @@ __device__ __forceinline__ int64_t cell_of(const Params &p, int s, int t) {
 
 // The kernel for 512 value dims on tcgen05 CTA pairs (chunk_wide.cu): queries of one CTA's 64
 // rows, and the launch (p.item_q = twice that, p.item_rows = 128).
-int wide_qpc(int G);
+inline int wide_qpc(int G) { return 64 / G; }
 int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st);
+// The kernel for 128- and 64-wide heads on tcgen05 (chunk_narrow.cu): queries of one 128-row tile,
+// and the launch (p.item_q = twice that, p.item_rows = 256).
+inline int narrow_qpt(int G) { return 128 / G; }
+int launch_narrow(const Params &p, int d, int64_t n_cells, cudaStream_t st);
 
 }  // namespace chunk
 }  // namespace sfa

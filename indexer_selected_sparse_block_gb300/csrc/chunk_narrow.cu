@@ -1,0 +1,449 @@
+// chunk_narrow.cu -- chunk attention with 128- and 64-wide heads (bf16) on tcgen05.
+//
+// One CTA owns two row tiles of 128 rows (query, head) of one KV head and streams tiles of 128
+// keys that both share.  Per row tile:
+//   S[128 x 128] = Q K^T (operands in shared memory), the softmax, one row a thread,
+//   O[128 x D]  += P V, P in tensor memory where S was (the weights never pass through shared
+//                  memory, whose bandwidth the products already use up), V from shared memory.
+// While one row tile's softmax runs, the other's products do: P V (t) and S(t + 1) of a row tile
+// are issued together, so a row tile's chain is S, softmax, P V and the two chains interleave.
+// Tensor memory: two S / P tiles of 128 columns, two O tiles of D.
+//
+// For fp32 results the weights are two bf16 halves (hi + lo, 2^-16 relative) and P V runs twice; for
+// bf16 results one bf16 weight is enough.  The running maximum moves only when a tile raises it by
+// more than 2^8, and O in tensor memory is rescaled only then.
+//
+// Warps 0-3 and 4-7: softmax, correction and result of the two row tiles; warp 8: Q and K; warp 9:
+// V; warp 10: products (one lane).  Pages as in chunk_wide.cu.
+#include "chunk_tc.cuh"
+
+namespace sfa {
+namespace chunk {
+namespace {
+
+constexpr int kT = 128;
+constexpr int kThreads = 352;
+
+template <int D, bool VK>
+struct Narrow {
+    static constexpr int kSlabs = D / 64;
+    static constexpr int kTileBytes = kSlabs * 128 * 128;      // 128 rows x D bf16
+    static constexpr int kKS = VK ? 5 : D == 128 ? 3 : 5;      // stages of K and of V
+    static constexpr int kVS = VK ? 0 : D == 128 ? 2 : 5;
+    static constexpr int kOffQ = 0;                            // two row tiles
+    static constexpr int kOffK = 2 * kTileBytes;
+    static constexpr int kOffV = kOffK + kKS * kTileBytes;
+    static constexpr int kOffItem = kOffV + kVS * kTileBytes;
+    static constexpr int kOffBar = kOffItem + 64;
+    static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 2 + 2 + 2 + 1;
+    static constexpr int kBytes = kOffBar + kBars * 8 + 16;
+    static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+};
+
+struct NarrowMaps {
+    CUtensorMap q;
+    KeyMaps kv;
+};
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// D[tmem] (+)= A[tmem: lane = row, two bf16 of K a column] * B[smem desc].
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+template <int D, bool VK, bool HL>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_narrow_kernel(const __grid_constant__ NarrowMaps maps, const Params p, int bxs, int qpt, int n_cells) {
+    using L = Narrow<D, VK>;
+    constexpr int KS = L::kKS, VS = L::kVS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const uint32_t bar0 = smem_u32(bars);
+    const uint32_t b_q = bar0, b_kFull = b_q + 16, b_kEmpty = b_kFull + 8 * KS, b_vFull = b_kEmpty + 8 * KS,
+                   b_vEmpty = b_vFull + 8 * VS, b_s = b_vEmpty + 8 * VS, b_p = b_s + 16, b_o = b_p + 16,
+                   b_drain = b_o + 16;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int item = blockIdx.x, g = blockIdx.y, split = blockIdx.z;
+    pdl_wait();
+    if (warp == 0) {
+        const Item it = find_item(p, item, blockIdx.x == 0 && g == 0 && split == 0);
+        if (lane == 0) *sItem = it;
+    }
+    __syncthreads();
+    const Item it = *sItem;
+    if (it.seq < 0) return;
+    const int q0 = it.tile * p.item_q;                        // first query of the item
+    const int nq = min(p.item_q, min(it.q.n, p.n_new_max) - q0);
+    const int pos0 = it.q.total - it.q.n + q0;                // its position
+    const int len = max(0, min(key_limit(p, it.q), pos0 + nq));
+    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
+    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
+    if (split > 0 && k0 >= k1) return;                        // no such piece
+    const bool whole = len <= p.split_keys;
+    const int n_tiles = (k1 - k0 + kT - 1) / kT;
+    const int G = p.G;
+    const bool two = nq > qpt;                                // the second row tile has rows
+
+    // a softmax thread's row: query ql of row tile w, head h
+    const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int ql = row / G, h = row - ql * G;
+    const bool live = warp < 8 && ql < qpt && w * qpt + ql < nq;
+    const int64_t orow = (int64_t)(it.q.c0 + q0 + w * qpt + ql) * p.h_q + g * G + h;
+
+    if (n_tiles == 0) {   // nothing to attend: zeros
+        if (live) {
+            for (int d = 0; d < D; d += 4) {
+                if (p.o_bf16)
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * D + d) = make_uint2(0, 0);
+                else
+                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (p.lse) p.lse[orow] = -INFINITY;
+        }
+        return;
+    }
+
+    if (tid == 0) {
+        const int ip = (int)(b_p - bar0) / 8;
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip || i == ip + 1 ? 4 : 1);   // P: four warps
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 10) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;   // S / P: 2 x 128 columns, O: 2 x D
+    const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sV = smem_u32(smem + L::kOffV);
+    // once a wait ran out no other is made
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok && !wait2(bar, parity)) {
+            ok = false;
+            *abort_flag = 1;
+            set_status(p.status, SFA_DEV_TIMEOUT);
+        }
+    };
+    const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
+
+    if (warp == 8 || (warp == 9 && !VK)) {
+        // --------------------------------------------------------------------------------- loads
+        const bool is_k = warp == 8;
+        if (is_k && elect_one()) {
+            for (int i = 0; i < (two ? 2 : 1); ++i) {
+                mbar_arrive_expect_tx(bars + i, (uint32_t)(L::kSlabs * 128 * qpt * G));
+                for (int d = 0; d < L::kSlabs; ++d)
+                    tma1_load(sQ + i * L::kTileBytes + d * 16384, &maps.q, d * 64, g * G,
+                              it.q.c0 + q0 + i * qpt, b_q + 8 * i);
+            }
+        }
+        __syncwarp();
+        const int S = is_k ? KS : VS;
+        const uint32_t full0 = is_k ? b_kFull : b_vFull, empty0 = is_k ? b_kEmpty : b_vEmpty, at0 = is_k ? sK : sV;
+        const CUtensorMap *m = is_k ? maps.kv.k : maps.kv.v;
+        HalfRows r[2];   // table entries read a tile ahead
+#pragma unroll
+        for (int i = 0; i < 2; ++i) read_entries(r[i], p, table, k0 + i * 64, k1, bxs);
+        int s = 0;
+        uint32_t par = 1;
+        for (int t = 0; t < n_tiles; ++t) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) find_rows(r[i], p, n_cells);
+            wait(empty0 + 8 * s, par);
+            ok = __all_sync(0xFFFFFFFFu, ok);   // the warp's lanes agree
+            if (!ok) break;
+            if (elect_one()) mbar_arrive_expect_tx(bars + (full0 - bar0) / 8 + s, (uint32_t)L::kTileBytes);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                load_slabs<L::kSlabs, 16384, false>(r[i], at0 + s * L::kTileBytes + i * 8192, m, 0, g, bxs, full0 + 8 * s);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) read_entries(r[i], p, table, k0 + (t + 1) * kT + i * 64, k1, bxs);
+            if (++s == S) {
+                s = 0;
+                par ^= 1;
+            }
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------------------------------------ products
+        if (elect_one()) {
+            const uint32_t idS = idesc_bf16_f32(128, 128);
+            const uint32_t idPV = idesc_bf16_f32(128, D) | (1u << 16);   // V: N-major
+            const uint64_t dQ = sw128_desc(sQ, 16, 1024), dK = sw128_desc(sK, 16, 1024),
+                           dV = sw128_desc(VK ? sK : sV, 16384, 1024);
+            auto s_op = [&](int i, int s) {   // S of row tile i from K stage s
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    tc_mma_bf16(tmem + i * 128, dQ + (uint64_t)((i * L::kTileBytes + o) >> 4),
+                                dK + (uint64_t)((s * L::kTileBytes + o) >> 4), idS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(reinterpret_cast<uint64_t *>(bars) + (b_s - bar0) / 8 + i);
+            };
+            auto pv_op = [&](int i, int s, bool first) {
+#pragma unroll
+                for (int x = 0; x < (HL ? 2 : 1); ++x)
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 64 + kk * 8,
+                               dV + (uint64_t)((s * L::kTileBytes + kk * 2048) >> 4), idPV,
+                               (!first || x > 0 || kk > 0) ? 1u : 0u);
+            };
+            auto free_stage = [&](uint32_t empty, int s) { tc_commit(bars + (empty - bar0) / 8 + s); };
+            int ks = 0, vs = 0;            // stages of K (t + 1) and V (t); VK: of K (t + 1) and K (t)
+            uint32_t kp = 0, vp = 0;
+            auto next_k = [&]() {
+                if (++ks == KS) {
+                    ks = 0;
+                    kp ^= 1;
+                }
+            };
+            wait(b_q, 0);
+            wait(b_kFull, 0);
+            if (ok) {
+                tc_fence_after();
+                s_op(0, 0);
+                if (two) {
+                    wait(b_q + 8, 0);
+                    tc_fence_after();
+                    if (ok) s_op(1, 0);
+                }
+                if (!VK) free_stage(b_kEmpty, 0);
+            }
+            next_k();
+            for (int t = 0; t < n_tiles && ok; ++t) {
+                const bool more = t + 1 < n_tiles;
+                if (!VK) wait(b_vFull + 8 * vs, vp);
+                for (int i = 0; i < (two ? 2 : 1) && ok; ++i) {
+                    wait(b_p + 8 * i, t & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    pv_op(i, vs, t == 0);
+                    if (!more) tc_commit(bars + (b_o - bar0) / 8 + i);
+                    if (more) {
+                        if (i == 0) wait(b_kFull + 8 * ks, kp);
+                        if (!ok) break;
+                        tc_fence_after();
+                        s_op(i, ks);
+                    }
+                }
+                if (!ok) break;
+                free_stage(VK ? b_kEmpty : b_vEmpty, vs);
+                if (more && !VK) free_stage(b_kEmpty, ks);
+                next_k();
+                if (++vs == (VK ? KS : VS)) {
+                    vs = 0;
+                    vp ^= 1;
+                }
+            }
+            if (!ok) {   // what was issued has to end before tensor memory is given back
+                tc_commit(bars + (b_drain - bar0) / 8);
+                wait2(b_drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8 && (w == 0 || two)) {
+        // -------------------------------------------------------------------------------- softmax
+        const int pos = pos0 + w * qpt + ql;                  // the row's last key
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + w * 128 + lane_addr, tO = tmem + 256 + w * D + lane_addr;
+        const bool neg = p.scale_log2 < 0.f;
+        const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);  // a zero scale: weights of 1 to 1e-28
+        float m = -INFINITY, l = 0.f;                         // base 2
+        auto read_entry = [&](int key) { return key < k1 ? __ldg(table + p.page_div.div(key)) : 0; };
+        int entry[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) entry[x] = read_entry(k0 + 32 * x + lane);
+        for (int t = 0; t < n_tiles; ++t) {
+            const int kb = k0 + t * kT;
+            uint32_t cells[4];   // bit j of word x: key kb + 32 x + j has a cell
+            bool all = true;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const bool cell = kb + 32 * x + lane >= k1 || (entry[x] >= 0 && entry[x] < p.n_pages);
+                if (!cell) set_status(p.status, SFA_DEV_BAD_CELL);
+                cells[x] = __ballot_sync(0xFFFFFFFFu, cell);
+                all = all && cells[x] == 0xFFFFFFFFu;
+                entry[x] = read_entry(kb + kT + 32 * x + lane);
+            }
+            const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
+            wait(b_s + 8 * w, t & 1);
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t r[32];
+                tmem_ld32(tS + 32 * x, r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s[32 * x + j] = __uint_as_float(r[j]);
+            }
+            tmem_ld_wait();
+            if (neg) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j) s[j] = -s[j];
+            }
+            if (last < 127 || !all) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (j > last || !((cells[j >> 5] >> (j & 31)) & 1)) s[j] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            float alpha = 1.f;
+            if (mx[0] > m + kLazy || (m == -INFINITY && mx[0] > m)) {
+                alpha = ex2(m - mx[0]);
+                m = mx[0];
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            // S(t) is committed behind P V (t - 1): O can be rescaled
+            if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + 32 * x, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+                    tmem_st32(tO + 32 * x, r);
+                }
+            }
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t hi[16], lo[HL ? 16 : 1];
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float e0 = ex2(fmaf(s[32 * x + j], sc, -mm)), e1 = ex2(fmaf(s[32 * x + j + 1], sc, -mm));
+                    sum[j & 2] += e0;
+                    sum[(j & 2) + 1] += e1;
+                    hi[j / 2] = pack_bf16(e0, e1);
+                    if constexpr (HL)
+                        lo[j / 2] = pack_bf16(e0 - __uint_as_float(hi[j / 2] << 16),
+                                              e1 - __uint_as_float(hi[j / 2] & 0xFFFF0000u));
+                }
+                tmem_st16(tS + 16 * x, hi);
+                if constexpr (HL) tmem_st16(tS + 64 + 16 * x, lo);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + (b_p - bar0) / 8 + w);
+            l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        }
+        // --------------------------------------------------------------------------------- result
+        wait(b_o + 8 * w, 0);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+        if (ok) {
+            const bool any = l > 0.f || l != l;
+            const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
+            const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
+                                 (w * qpt + ql) * G + h;
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+                uint32_t r[32];
+                tmem_ld32(tO + 32 * x, r);
+                tmem_ld_wait();
+                if (!live) continue;
+                if (whole && p.o_bf16) {
+                    uint4 *o = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * D + 32 * x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = pack_bf16(__uint_as_float(r[8 * j + 2 * k]) * inv,
+                                             __uint_as_float(r[8 * j + 2 * k + 1]) * inv);
+                        o[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else {
+                    float4 *o = reinterpret_cast<float4 *>(
+                        (whole ? reinterpret_cast<float *>(p.O) + orow * D : p.part_o + part * D) + 32 * x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
+                                           __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
+                }
+            }
+            if (live) {
+                if (!whole) {
+                    p.part_ml[part * 2] = m;
+                    p.part_ml[part * 2 + 1] = l;
+                } else if (p.lse) {
+                    p.lse[orow] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------------------------- teardown
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {   // copies in flight land in shared memory that is still ours
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+    }
+    tc_fence_after();
+    __syncwarp();
+    if (warp == 10) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool VK, bool HL>
+int launch_narrow_t(const Params &p, const NarrowMaps &maps, int bxs, int qpt, int64_t n_cells, cudaStream_t st) {
+    if (!ensure_max_dynamic_smem(chunk_narrow_kernel<D, VK, HL>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_narrow_kernel<D, VK, HL>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+                   (size_t)Narrow<D, VK>::kBytes, st, maps, p, bxs, qpt, (int)n_cells) != cudaSuccess) {
+        cudaGetLastError();
+        return SFA_ERR_CUDA;
+    }
+    return SFA_OK;
+}
+
+template <int D>
+int launch_narrow_d(const Params &p, const NarrowMaps &maps, int bxs, int qpt, int64_t n_cells, cudaStream_t st) {
+    const bool hl = !p.o_bf16;
+    if (p.V)
+        return hl ? launch_narrow_t<D, false, true>(p, maps, bxs, qpt, n_cells, st)
+                  : launch_narrow_t<D, false, false>(p, maps, bxs, qpt, n_cells, st);
+    return hl ? launch_narrow_t<D, true, true>(p, maps, bxs, qpt, n_cells, st)
+              : launch_narrow_t<D, true, false>(p, maps, bxs, qpt, n_cells, st);
+}
+
+}  // namespace
+
+int launch_narrow(const Params &p, int d, int64_t n_cells, cudaStream_t st) {
+    const int qpt = narrow_qpt(p.G);
+    int bxs;
+    NarrowMaps maps;
+    if (!encode_rows(&maps.q, p.Q, d, p.h_q, p.n_q, p.G, qpt) || !encode_keys(&maps.kv, &bxs, p, d, d, n_cells))
+        return SFA_ERR_CUDA;
+    return d == 128 ? launch_narrow_d<128>(p, maps, bxs, qpt, n_cells, st)
+                    : launch_narrow_d<64>(p, maps, bxs, qpt, n_cells, st);
+}
+
+}  // namespace chunk
+}  // namespace sfa

@@ -1,0 +1,218 @@
+// chunk_tc.cuh -- what the chunk attention kernels on tcgen05 share: bounded waits, tensor memory
+// access, and the loads of a tile's keys through the page table.
+#pragma once
+
+#include "chunk_common.cuh"
+
+namespace sfa {
+namespace chunk {
+
+constexpr float kLazy = 8.f;   // base-2 growth of the maximum that O is not rescaled for
+
+struct KeyMaps {
+    CUtensorMap k[3], v[3];    // boxes of 1 << bxs, min(1 << bxs, 8) and 1 rows
+};
+
+// Waits for the phase of `parity`; the limit counts from the wait's own start.
+__device__ __forceinline__ bool wait2(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 63u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kWaitLimitNs) return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // does not block
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Tiled loads into this CTA's shared memory, their bytes counted on a barrier of this CTA
+// (tma_load) or, in a pair, of its first CTA (tma2_load).
+__device__ __forceinline__ void tma2_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                          uint32_t leader_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma1_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// ------------------------------------------------------------------------------- key rows
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
+
+// How the 64 keys of a half tile are loaded, a lane's share: 64 >> bs boxes of 1 << bs rows, this
+// lane's being lane and lane + 32; where the list ends inside one (`edge`) that one row by row.
+// The page table is read a tile ahead (`entry`: the raw entries), the cells follow from it.
+struct HalfRows {
+    int pos0, bs, edge;
+    int entry[2], single;
+    int row[2], srow;
+};
+// Keys pos0 .. pos0 + 63; the list ends before `end`.
+__device__ __forceinline__ void read_entries(HalfRows &h, const Params &p, const int32_t *table, int pos0,
+                                             int end, int bxs) {
+    const int lane = threadIdx.x & 31;
+    auto entry = [&](int pos) -> int { return pos < end ? __ldg(table + p.page_div.div(pos)) : -1; };
+    h.pos0 = pos0;
+    const bool whole = pos0 + 64 <= end;
+    h.bs = whole ? bxs : min(bxs, 3);
+    h.edge = -1;
+    h.single = -1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int box = lane + 32 * i;
+        h.entry[i] = box < (64 >> h.bs) ? entry(pos0 + (box << h.bs)) : -1;
+    }
+    const int in = end - pos0;
+    if (!whole && in > 0 && (in & ((1 << h.bs) - 1)) != 0) {
+        h.edge = in >> h.bs;
+        if (lane < (1 << h.bs)) h.single = entry(pos0 + (h.edge << h.bs) + lane);
+    }
+}
+// Entries -> cells.  Keys past the list's end and those of pages that are none get n_cells: outside
+// the tensor, read as zeros.
+__device__ __forceinline__ void find_rows(HalfRows &h, const Params &p, int n_cells) {
+    const int lane = threadIdx.x & 31;
+    auto cell = [&](int e, int pos) -> int {
+        return e < 0 || e >= p.n_pages ? n_cells : e * p.page + (pos - p.page_div.div(pos) * p.page);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) h.row[i] = cell(h.entry[i], h.pos0 + ((lane + 32 * i) << h.bs));
+    h.srow = cell(h.single, h.pos0 + (h.edge << h.bs) + lane);
+}
+// SLABS slabs [64 keys][64 dims from x, x + 64, ..] of KV head g, STRIDE bytes apart; by a whole
+// warp, one lane of which issues (elect.sync and coordinates that are the same in all lanes: a
+// copy or product issued under a lane test costs the warp four times as long).  PAIR: the bytes
+// are counted in the pair's first CTA.
+template <int SLABS, int STRIDE, bool PAIR>
+__device__ __forceinline__ void load_slabs(const HalfRows &h, uint32_t dst, const CUtensorMap *maps,
+                                           int x, int g, int bxs, uint32_t bar) {
+    auto copy = [&](const CUtensorMap *map, uint32_t at, int row) {
+#pragma unroll
+        for (int s = 0; s < SLABS; ++s) {
+            if (PAIR) tma2_load(dst + s * STRIDE + at, map, x + 64 * s, g, row, bar);
+            else tma1_load(dst + s * STRIDE + at, map, x + 64 * s, g, row, bar);
+        }
+    };
+    // the whole half in N boxes: the rows to all lanes, then every copy at once
+    auto whole = [&](auto n_boxes) {
+        constexpr int N = decltype(n_boxes)::value;
+        int r[N];
+#pragma unroll
+        for (int b = 0; b < N; ++b) r[b] = __shfl_sync(0xFFFFFFFFu, h.row[0], b);
+        if (elect_one()) {
+#pragma unroll
+            for (int b = 0; b < N; ++b) copy(maps, (uint32_t)b * (64 / N) * 128, r[b]);
+        }
+    };
+    if (h.bs == bxs && h.edge < 0) {
+        if (bxs == 6) return whole(Const<1>{});
+        if (bxs == 5) return whole(Const<2>{});
+        if (bxs == 4) return whole(Const<4>{});
+        if (bxs == 3) return whole(Const<8>{});
+    }
+    // the list's end, or pages whose size has no factor of 8
+    const CUtensorMap *map = maps + (h.bs == bxs ? 0 : 1);
+    const int n = 64 >> h.bs;
+    for (int b = 0; b < n; ++b) {
+        const int row = __shfl_sync(0xFFFFFFFFu, b < 32 ? h.row[0] : h.row[1], b & 31);
+        if (b != h.edge && elect_one()) copy(map, (uint32_t)(b << h.bs) << 7, row);
+    }
+    if (h.edge >= 0)
+        for (int i = 0; i < (1 << h.bs); ++i) {
+            const int row = __shfl_sync(0xFFFFFFFFu, h.srow, i);
+            if (elect_one()) copy(maps + 2, (uint32_t)((h.edge << h.bs) + i) << 7, row);
+        }
+}
+
+// Tensor map of rows [n][heads][d] bf16 with boxes of `rows` x `heads_box` x 64 elements.
+inline bool encode_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t n, int heads_box, int rows) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows}, es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The boxes' rows (1 << *bxs = gcd(page, 64)) and the maps of K (and V, unless null).
+inline bool encode_keys(KeyMaps *m, int *bxs, const Params &p, int dkq, int dv, int64_t n_cells) {
+    int s = 0;
+    while (s < 6 && p.page % (2 << s) == 0) ++s;
+    *bxs = s;
+    const int rows[3] = {1 << s, s < 3 ? 1 << s : 8, 1};
+    for (int i = 0; i < 3; ++i) {
+        if (!encode_rows(&m->k[i], p.K, dkq, p.h_kv, n_cells, 1, rows[i])) return false;
+        if (p.V && !encode_rows(&m->v[i], p.V, dv, p.h_kv, n_cells, 1, rows[i])) return false;
+    }
+    return true;
+}
+
+}  // namespace chunk
+}  // namespace sfa

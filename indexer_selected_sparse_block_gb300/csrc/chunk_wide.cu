@@ -36,7 +36,7 @@
 // warp's barrier wait, expect and copy take about 330 cycles whatever the copy's size, a further
 // copy 15: four warps reach 83 bytes a cycle and SM, one 25); warp 12: products (in the pair's
 // first CTA).
-#include "chunk_common.cuh"
+#include "chunk_tc.cuh"
 
 namespace sfa {
 namespace chunk {
@@ -46,7 +46,6 @@ constexpr int kT = 128;             // keys of a tile
 constexpr int kSlab = 64 * 128;     // bytes of 64 rows x 64 dims
 constexpr int kWideThreads = 416;
 constexpr int kSlots = 8;           // operands of two slabs
-constexpr float kLazy = 8.f;        // base-2 growth of the maximum that O is not rescaled for
 
 template <int DKQ>
 struct Wide {
@@ -65,7 +64,8 @@ struct Wide {
 };
 
 struct WideMaps {
-    CUtensorMap q, k[3], v[3];   // boxes of bx, min(bx, 8) and 1 rows
+    CUtensorMap q;
+    KeyMaps kv;
 };
 
 // --------------------------------------------------------------- pair (cta_group::2) wrappers
@@ -91,38 +91,6 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Waits for the phase of `parity`; the limit counts from the wait's own start.
-__device__ __forceinline__ bool wait2(uint32_t bar, uint32_t parity) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 63u) {
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > kWaitLimitNs) return false;
-        }
-    }
-}
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // does not block
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Tiled load into this CTA's shared memory, its bytes counted on a barrier of the pair's first CTA.
-__device__ __forceinline__ void tma2_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                          uint32_t leader_bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
-        : "memory");
-}
 __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -139,117 +107,6 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xFFFFFFFF;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// ------------------------------------------------------------------------------- key rows
-// How the 64 keys of a half tile are loaded, a lane's share: 64 >> bs boxes of 1 << bs rows, this
-// lane's being lane and lane + 32; where the list ends inside one (`edge`) that one row by row.
-// The page table is read a tile ahead (`entry`: the raw entries), the cells follow from it.
-struct HalfRows {
-    int pos0, bs, edge;
-    int entry[2], single;
-    int row[2], srow;
-};
-// Keys pos0 .. pos0 + 63; the list ends before `end`.
-__device__ __forceinline__ void read_entries(HalfRows &h, const Params &p, const int32_t *table, int pos0,
-                                             int end, int bxs) {
-    const int lane = threadIdx.x & 31;
-    auto entry = [&](int pos) -> int { return pos < end ? __ldg(table + p.page_div.div(pos)) : -1; };
-    h.pos0 = pos0;
-    const bool whole = pos0 + 64 <= end;
-    h.bs = whole ? bxs : min(bxs, 3);
-    h.edge = -1;
-    h.single = -1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int box = lane + 32 * i;
-        h.entry[i] = box < (64 >> h.bs) ? entry(pos0 + (box << h.bs)) : -1;
-    }
-    const int in = end - pos0;
-    if (!whole && in > 0 && (in & ((1 << h.bs) - 1)) != 0) {
-        h.edge = in >> h.bs;
-        if (lane < (1 << h.bs)) h.single = entry(pos0 + (h.edge << h.bs) + lane);
-    }
-}
-// Entries -> cells.  Keys past the list's end and those of pages that are none get n_cells: outside
-// the tensor, read as zeros.
-__device__ __forceinline__ void find_rows(HalfRows &h, const Params &p, int n_cells) {
-    const int lane = threadIdx.x & 31;
-    auto cell = [&](int e, int pos) -> int {
-        return e < 0 || e >= p.n_pages ? n_cells : e * p.page + (pos - p.page_div.div(pos) * p.page);
-    };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) h.row[i] = cell(h.entry[i], h.pos0 + ((lane + 32 * i) << h.bs));
-    h.srow = cell(h.single, h.pos0 + (h.edge << h.bs) + lane);
-}
-// One or two slabs [64 keys][64 dims from x, x + 64] of KV head g; by a whole warp, one lane of
-// which issues (elect.sync and coordinates that are the same in all lanes: a copy or product
-// issued under a lane test costs the warp four times as long).
-template <int SLABS>
-__device__ __forceinline__ void load_slabs(const HalfRows &h, uint32_t dst, const CUtensorMap *maps,
-                                           int x, int g, int bxs, uint32_t leader_bar) {
-    auto box = [&](const CUtensorMap *map, uint32_t at, int row) {
-        if (elect_one()) {
-#pragma unroll
-            for (int s = 0; s < SLABS; ++s) tma2_load(dst + s * kSlab + at, map, x + 64 * s, g, row, leader_bar);
-        }
-    };
-    if (h.bs == 6) {
-        box(maps, 0, __shfl_sync(0xFFFFFFFFu, h.row[0], 0));
-        return;
-    }
-    const CUtensorMap *map = maps + (h.bs == bxs ? 0 : 1);
-    const int n = 64 >> h.bs;
-    for (int b = 0; b < n; ++b) {
-        const int row = __shfl_sync(0xFFFFFFFFu, b < 32 ? h.row[0] : h.row[1], b & 31);
-        if (b != h.edge) box(map, (uint32_t)(b << h.bs) << 7, row);
-    }
-    if (h.edge >= 0)
-        for (int i = 0; i < (1 << h.bs); ++i)
-            box(maps + 2, (uint32_t)((h.edge << h.bs) + i) << 7, __shfl_sync(0xFFFFFFFFu, h.srow, i));
-}
-
 // --------------------------------------------------------------------------------- the kernel
 template <int DKQ, bool VK, bool HL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
@@ -368,11 +225,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 const uint32_t full = b_full + j * 8;
                 slot_free(full, b_empty + j * 8, (t & 1), 4u * kSlab);
                 if (!ok) break;
-                load_slabs<2>(hs, buf0 + 2 * j * kSlab, maps.k, 128 * j, g, bxs, lead + (full - bar0));
+                load_slabs<2, kSlab, true>(hs, buf0 + 2 * j * kSlab, maps.kv.k, 128 * j, g, bxs, lead + (full - bar0));
                 if (L::kRope && j == 3) {
                     slot_free(b_rope, b_ropeDone, (t & 1), 2u * kSlab);
                     if (!ok) break;
-                    load_slabs<1>(hs, sRope, maps.k, 512, g, bxs, lead + (b_rope - bar0));
+                    load_slabs<1, kSlab, true>(hs, sRope, maps.kv.k, 512, g, bxs, lead + (b_rope - bar0));
                 }
                 read_entries(hs, p, table, k0 + (t + 2) * kT + c * 64, k1, bxs);
             }
@@ -381,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 const uint32_t full = b_full + (4 + j) * 8;
                 slot_free(full, b_empty + (4 + j) * 8, (t & 1) ^ 1, 4u * kSlab);
                 if (!ok) break;
-                load_slabs<2>(hv, buf0 + 2 * (4 + j) * kSlab, VK ? maps.k : maps.v, 256 * n + 128 * c, g,
+                load_slabs<2, kSlab, true>(hv, buf0 + 2 * (4 + j) * kSlab, VK ? maps.kv.k : maps.kv.v, 256 * n + 128 * c, g,
                               bxs, lead + (full - bar0));
                 read_entries(hv, p, table, k0 + (t + 1) * kT + half * 64, k1, bxs);
             }
@@ -644,18 +501,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Tensor map of rows [n][heads][d] bf16 with boxes of `rows` x `heads_box` x 64 elements.
-bool encode_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t n, int heads_box, int rows) {
-    EncodeTiledFn enc = encode_tiled();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n};
-    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows}, es[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int DKQ, bool VK, bool HL>
 int launch_wide_t(const Params &p, const WideMaps &maps, int bxs, int qpc, int64_t n_cells, cudaStream_t st) {
     if (!ensure_max_dynamic_smem(chunk_wide_kernel<DKQ, VK, HL>)) return SFA_ERR_CUDA;
@@ -669,21 +514,13 @@ int launch_wide_t(const Params &p, const WideMaps &maps, int bxs, int qpc, int64
 
 }  // namespace
 
-// Queries of one CTA's 64 rows.
-int wide_qpc(int G) { return 64 / G; }
-
 int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st) {
-    int bxs = 0;   // rows of a box: gcd(page, 64), a power of two
-    while (bxs < 6 && p.page % (2 << bxs) == 0) ++bxs;
-    const int bx = 1 << bxs;
     const int qpc = wide_qpc(p.G);
+    int bxs;
     WideMaps maps;
-    if (!encode_rows(&maps.q, p.Q, dkq, p.h_q, p.n_q, p.G, qpc)) return SFA_ERR_CUDA;
-    const int rows[3] = {bx, bx < 8 ? bx : 8, 1};
-    for (int i = 0; i < 3; ++i) {
-        if (!encode_rows(&maps.k[i], p.K, dkq, p.h_kv, n_cells, 1, rows[i])) return SFA_ERR_CUDA;
-        if (p.V && !encode_rows(&maps.v[i], p.V, 512, p.h_kv, n_cells, 1, rows[i])) return SFA_ERR_CUDA;
-    }
+    if (!encode_rows(&maps.q, p.Q, dkq, p.h_q, p.n_q, p.G, qpc) ||
+        !encode_keys(&maps.kv, &bxs, p, dkq, 512, n_cells))
+        return SFA_ERR_CUDA;
     const bool hl = !p.o_bf16;
     if (dkq == 576)
         return hl ? launch_wide_t<576, true, true>(p, maps, bxs, qpc, n_cells, st)
