@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -582,40 +583,65 @@ def sfa_copy_cache_rows(dst, src, stream=None) -> None:
     _check("sfa_copy_cache_rows", rc)
 
 
-def _one_device(first, *rest):
-    """The tensors' common CUDA device, checked; made the current one for the call (the library
-    launches on the current device)."""
-    dev = first.device
-    if dev.type != "cuda":
+# The paged-serving calls are made every step on small tensors, where the host's time counts:
+# their tensors are checked in one look each, their addresses passed as plain integers.
+_I32, _BF16, _F32, _U8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+_CODES = {_BF16: SFA_BF16, _F32: SFA_F32, _U8: SFA_Q8_0}
+
+
+def _no_tensor(name, t, dev, what):
+    """The error for a tensor that a call cannot take."""
+    if not t.is_cuda:
         raise ValueError("libsfa takes CUDA tensors only")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device} in one call")
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NO_GUARD
+    if t.get_device() != dev:
+        raise ValueError(f"tensors on cuda:{dev} and {t.device} in one call")
+    raise ValueError(f"{name} must be {what}")
 
 
-class _NoGuard:
+def _vec(name, t, n, dev):
+    """Address of t, a contiguous int32 vector (of n entries, unless n < 0) on device dev."""
+    if (t.dtype is not _I32 or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous()
+            or (n >= 0 and t.numel() != n) or dev < 0):
+        _no_tensor(name, t, dev, f"a contiguous int32 vector{f' of {n} entries' if n >= 0 else ''}")
+    return t.data_ptr()
+
+
+def _rows(name, t, n, dev):
+    """Address of t, a contiguous int32 [n][any] matrix on device dev."""
+    if (t.dtype is not _I32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous()
+            or t.size(0) != n or dev < 0):
+        _no_tensor(name, t, dev, f"a contiguous int32 [{n}][..] tensor")
+    return t.data_ptr()
+
+
+def _status_ptr(t, dev):
+    return None if t is None else _vec("dev_status", t, 1, dev)
+
+
+class _OnDevice:
+    """Makes `dev` the current device (the library launches on it) and back."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
     def __enter__(self):
-        return None
+        self.old = torch.cuda.current_device()
+        if self.old != self.dev:
+            torch.cuda.set_device(self.dev)
 
     def __exit__(self, *exc):
+        if self.old != self.dev:
+            torch.cuda.set_device(self.old)
         return False
 
 
-_NO_GUARD = _NoGuard()
-
-
-def _i32_vec(name, t, n=None):
-    """t is a contiguous int32 vector (of n entries)."""
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, not {t.shape[0]}")
-
-
-def _page_table(page_table, n_seq):
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_seq:
-        raise ValueError(f"page_table must be an int32 [{n_seq}][pages] tensor")
+def _stream_on(stream, dev):
+    """The stream's handle; None: the current stream of device dev."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def sfa_build_page_maps(len_old, len_new, page_size: int, free_pages, free_head, n_pages: int,
@@ -625,44 +651,47 @@ def sfa_build_page_maps(len_old, len_new, page_size: int, free_pages, free_head,
     free_head on) into page_table, the new tokens' sequences, positions and cells (q_seq, q_pos,
     slot: rows past the last token get -1), the packed offsets cu_new [n_seq + 1], len_total, and
     the new positions' entries of the per-position map cell_of [n_seq][n_pos] when given."""
-    n_seq, n_tok = len_old.shape[0], slot.shape[0]
-    for name, t, n in (("len_old", len_old, None), ("len_new", len_new, n_seq),
-                       ("free_pages", free_pages, None), ("free_head", free_head, 1),
-                       ("cu_new", cu_new, n_seq + 1), ("len_total", len_total, n_seq),
-                       ("slot", slot, None), ("q_seq", q_seq, n_tok), ("q_pos", q_pos, n_tok),
-                       ("free_head_out", free_head_out, 1)):
-        _i32_vec(name, t, n)
-    _page_table(page_table, n_seq)
-    n_pos = 0
-    if cell_of is not None:
-        if cell_of.shape[0] != n_seq:
-            raise ValueError(f"cell_of must have {n_seq} rows")
-        _, n_pos, _ = _paged_dims(cell_of, None)
-    with _one_device(len_old, len_new, free_pages, free_head, page_table, cu_new, len_total, q_seq,
-                     q_pos, slot, free_head_out, cell_of, dev_status):
-        rc = lib().sfa_build_page_maps(
-            _p(len_old), _p(len_new), n_seq, page_size, _p(free_pages), free_pages.shape[0],
-            _p(free_head), n_pages, _p(page_table), page_table.shape[1], _p(cu_new),
-            _p(len_total), _p(q_seq), _p(q_pos), _p(slot), n_tok, _p(cell_of), n_pos,
-            _p(free_head_out), _p(dev_status), _stream(stream))
-    _check("sfa_build_page_maps", rc)
+    dev, n_seq, n_tok = len_old.get_device(), len_old.numel(), slot.numel()
+    args = (_vec("len_old", len_old, -1, dev), _vec("len_new", len_new, n_seq, dev), n_seq, page_size,
+            _vec("free_pages", free_pages, -1, dev), free_pages.numel(),
+            _vec("free_head", free_head, 1, dev), n_pages,
+            _rows("page_table", page_table, n_seq, dev), page_table.size(1),
+            _vec("cu_new", cu_new, n_seq + 1, dev), _vec("len_total", len_total, n_seq, dev),
+            _vec("q_seq", q_seq, n_tok, dev), _vec("q_pos", q_pos, n_tok, dev),
+            _vec("slot", slot, -1, dev), n_tok,
+            None if cell_of is None else _rows("cell_of", cell_of, n_seq, dev),
+            0 if cell_of is None else cell_of.size(1), _vec("free_head_out", free_head_out, 1, dev),
+            _status_ptr(dev_status, dev))
+    with _OnDevice(dev):
+        rc = lib().sfa_build_page_maps(*args, _stream_on(stream, dev))
+    if rc:
+        raise SfaError("sfa_build_page_maps", rc)
 
 
-def _cell_write(src, dst, n_rows, n_cells):
+_CELL_WRITE = struct.Struct("@QqQiiii")     # sfa_cell_write of include/sfa.h
+
+
+def _cell_write(src, dst, n_rows, n_cells, dev):
+    st, dt = src.dtype, dst.dtype
     if src.dim() == 2:      # [rows][d]: one inner row
-        src = src.unsqueeze(1)
-    if dst.dim() == 2:
-        dst = dst.unsqueeze(1)
-    n, h, d = src.shape
-    q8 = dst.dtype == torch.uint8
-    row = sfa_q8_0_row_bytes(d) if q8 else d
-    if n < n_rows or tuple(dst.shape) != (n_cells, h, row) or not dst.is_contiguous():
-        raise ValueError(f"a cache of these rows is a contiguous [{n_cells}][{h}][{row}] tensor "
-                         f"and they are at least {n_rows}")
-    if src.dtype == torch.uint8 or (d > 1 and src.stride(2) != 1) or (h > 1 and src.stride(1) != d):
-        raise ValueError("the rows are bf16 or fp32, each contiguous")
-    return _CellWrite(src.data_ptr(), src.stride(0) if n > 1 else h * d, dst.data_ptr(),
-                      _dtype_code(src), _dtype_code(dst), h, d)
+        n, d = src.shape
+        h = 1
+        ok = src.stride(1) == 1 or d == 1
+    elif src.dim() == 3:
+        n, h, d = src.shape
+        _, sh, sd = src.stride()
+        ok = (sd == 1 or d == 1) and (sh == d or h == 1)
+    else:
+        ok, n, h, d = False, 0, 1, 1
+    if not ok or n < n_rows or src.get_device() != dev or (st is not _BF16 and st is not _F32):
+        _no_tensor("a write's rows", src, dev, f"bf16 or fp32, [>= {n_rows}][d] or [>= {n_rows}]"
+                   "[h][d], each row contiguous")
+    row = sfa_q8_0_row_bytes(d) if dt is _U8 else d
+    if (dst.get_device() != dev or dt not in _CODES or not dst.is_contiguous() or dst.size(0) != n_cells
+            or dst.numel() != n_cells * h * row or dst.size(-1) != row):
+        _no_tensor("a write's cache", dst, dev, f"a contiguous [{n_cells}][{h}][{row}] tensor for "
+                   "these rows")
+    return (src.data_ptr(), src.stride(0) if n > 1 else h * d, dst.data_ptr(), _CODES[st], _CODES[dt], h, d)
 
 
 def sfa_write_cells(writes, slot, dev_status=None, stream=None):
@@ -673,15 +702,18 @@ def sfa_write_cells(writes, slot, dev_status=None, stream=None):
     writes = list(writes)
     if len(writes) > SFA_MAX_CELL_WRITES:
         raise ValueError(f"at most {SFA_MAX_CELL_WRITES} caches per call")
-    _i32_vec("slot", slot)
+    dev = slot.get_device()
+    at = _vec("slot", slot, -1, dev)
     if not writes:
         return
-    n_rows, n_cells = slot.shape[0], writes[0][1].shape[0]
-    arr = (_CellWrite * len(writes))(*[_cell_write(x, y, n_rows, n_cells) for x, y in writes])
-    with _one_device(slot, dev_status, *[t for w in writes for t in w]):
-        rc = lib().sfa_write_cells(len(writes), ctypes.cast(arr, ctypes.c_void_p), _p(slot), n_rows,
-                                   n_cells, _p(dev_status), _stream(stream))
-    _check("sfa_write_cells", rc)
+    n_rows, n_cells = slot.numel(), writes[0][1].size(0)
+    packed = b"".join([_CELL_WRITE.pack(*_cell_write(x, y, n_rows, n_cells, dev)) for x, y in writes])
+    status = _status_ptr(dev_status, dev)
+    with _OnDevice(dev):
+        rc = lib().sfa_write_cells(len(writes), packed, at, n_rows, n_cells, status,
+                                   _stream_on(stream, dev))
+    if rc:
+        raise SfaError("sfa_write_cells", rc)
 
 
 def sfa_chunk_attend_workspace_bytes(dtype_code: int, n_seq: int, n_q: int, h_q: int, h_kv: int,
@@ -698,40 +730,44 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
     Q [n_q][h_q][dkq]) over its len_total[s] cached tokens, the chunk's own included: K
     [n_cells][h_kv][dkq] and V [n_cells][h_kv][dv] or None, through page_table [n_seq][pages].
     O [n_q][h_q][dv] fp32 or bf16, lse [n_q][h_q] fp32."""
+    dev = Q.get_device()
     n_q, h_q, dkq = Q.shape
-    n_cells, h_kv, _ = K.shape
-    n_seq, dv = len_total.shape[0], O.shape[-1]
+    n_cells, h_kv, k_row = K.shape
+    n_seq, dv = len_total.numel(), O.size(-1)
     _check_qkv(Q, K, V)
-    _i32_vec("len_total", len_total)
-    _i32_vec("cu_new", cu_new, n_seq + 1)
-    _page_table(page_table, n_seq)
-    code = _dtype_code(K)
-    row = (lambda d: sfa_q8_0_row_bytes(d)) if code == SFA_Q8_0 else (lambda d: d)
-    if K.shape[2] != row(dkq):
+    code, o_code = _dtype_code(K), _CODES.get(O.dtype)
+    q8 = code == SFA_Q8_0
+    if k_row != (sfa_q8_0_row_bytes(dkq) if q8 else dkq):
         raise ValueError("Q and K must share a head size")
-    if V is not None and tuple(V.shape) != (n_cells, h_kv, row(dv)):
+    if V is not None and tuple(V.shape) != (n_cells, h_kv, sfa_q8_0_row_bytes(dv) if q8 else dv):
         raise ValueError("V must be [n_cells][h_kv][dv] like K")
-    if tuple(O.shape) != (n_q, h_q, dv) or O.dtype not in (torch.float32, torch.bfloat16):
+    if O.shape != (n_q, h_q, dv) or o_code not in (SFA_F32, SFA_BF16):
         raise ValueError("O must be an fp32 or bf16 [n_q][h_q][dv] tensor")
-    if lse is not None and (tuple(lse.shape) != (n_q, h_q) or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != (n_q, h_q) or lse.dtype is not _F32):
         raise ValueError("lse must be an fp32 [n_q][h_q] tensor")
-    o_code = _dtype_code(O)
-    with _one_device(Q, K, V, page_table, cu_new, len_total, O, lse, workspace, dev_status):
+    for t in (Q, K, V, O, lse, workspace):
+        if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            _no_tensor("every tensor", t, dev, "contiguous")
+    table, cu = _rows("page_table", page_table, n_seq, dev), _vec("cu_new", cu_new, n_seq + 1, dev)
+    total, status = _vec("len_total", len_total, n_seq, dev), _status_ptr(dev_status, dev)
+    L = lib()
+    with _OnDevice(dev):
+        raw = _stream_on(stream, dev)
         if workspace is None:
-            need = lib().sfa_chunk_attend_workspace_bytes(code, n_seq, n_q, h_q, h_kv, dkq, dv,
-                                                          int(V is not None), n_new_max, n_kv_max,
-                                                          o_code)
+            need = L.sfa_chunk_attend_workspace_bytes(code, n_seq, n_q, h_q, h_kv, dkq, dv,
+                                                      V is not None, n_new_max, n_kv_max, o_code)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+                workspace = torch.empty(need, dtype=_U8, device=Q.device)
                 if stream is not None:   # freed on return: not before that stream is done
                     workspace.record_stream(stream)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = lib().sfa_chunk_attend_paged(
-            _p(Q), _p(K), _p(V), code, n_cells, _p(page_table), page_table.shape[1], page_size,
-            n_seq, n_q, h_q, h_kv, dkq, dv, float(scale), _p(cu_new), _p(len_total), n_new_max,
-            n_kv_max, _p(O), o_code, _p(lse), _p(workspace), ws_bytes, _p(dev_status),
-            _stream(stream))
-    _check("sfa_chunk_attend_paged", rc)
+        rc = L.sfa_chunk_attend_paged(
+            Q.data_ptr(), K.data_ptr(), None if V is None else V.data_ptr(), code, n_cells, table,
+            page_table.size(1), page_size, n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu, total, n_new_max,
+            n_kv_max, O.data_ptr(), o_code, None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), status, raw)
+    if rc:
+        raise SfaError("sfa_chunk_attend_paged", rc)
 
 
 def sfa_read_device_status(dev_status, stream=None) -> int:

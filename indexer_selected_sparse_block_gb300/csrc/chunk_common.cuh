@@ -14,24 +14,6 @@ namespace chunk {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1, as a product: with 2^(k-1) < d <= 2^k and
-// m = floor(2^(31+k) / d) + 1, m d = 2^(31+k) + r with 0 < r <= d <= 2^k, so n m / 2^(31+k) exceeds
-// n / d by n r / (d 2^(31+k)) < 1 / d: the integer part is the same.  m < 2^32 as d > 2^(k-1),
-// except for d = 2^k, whose m = 2^31 + 1 is smaller still.
-struct FastDiv {
-    uint32_t m;
-    int s;
-    __host__ void set(int d) {
-        int k = 0;
-        while ((1ll << k) < d) ++k;
-        s = 31 + k;
-        m = (uint32_t)((1ull << s) / (uint32_t)d + 1);
-    }
-    __device__ __forceinline__ int div(int n) const {
-        return (int)(((uint64_t)(uint32_t)n * m) >> s);
-    }
-};
-
 struct Params {
     const void *Q, *K, *V;
     const int32_t *table, *cu, *total;

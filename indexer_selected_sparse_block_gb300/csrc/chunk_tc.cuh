@@ -189,6 +189,34 @@ __device__ __forceinline__ void load_slabs(const HalfRows &h, uint32_t dst, cons
         }
 }
 
+// The same for a half tile within one page (pages of a multiple of 64 rows), by one thread: rows
+// row0 .. row0 + v - 1 and zeros behind them.
+template <int SLABS, int STRIDE, bool PAIR>
+__device__ __forceinline__ void load_slabs_one(int row0, int v, uint32_t dst, const CUtensorMap *maps,
+                                               int x, int g, int n_cells, uint32_t bar) {
+    auto copy = [&](const CUtensorMap *map, uint32_t at, int row) {
+#pragma unroll
+        for (int s = 0; s < SLABS; ++s) {
+            if (PAIR) tma2_load(dst + s * STRIDE + at, map, x + 64 * s, g, row, bar);
+            else tma1_load(dst + s * STRIDE + at, map, x + 64 * s, g, row, bar);
+        }
+    };
+    if (v == 64 || v == 0) {
+        copy(maps, 0, v ? row0 : n_cells);
+        return;
+    }
+#pragma unroll 1
+    for (int b = 0; b < 8; ++b) {
+        const int in = v - 8 * b;   // rows of this box in the list
+        if (in >= 8 || in <= 0) {
+            copy(maps + 1, b * 1024, in > 0 ? row0 + 8 * b : n_cells);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) copy(maps + 2, b * 1024 + i * 128, i < in ? row0 + 8 * b + i : n_cells);
+        }
+    }
+}
+
 // Tensor map of rows [n][heads][d] bf16 with boxes of `rows` x `heads_box` x 64 elements.
 inline bool encode_rows(CUtensorMap *map, const void *base, int d, int heads, int64_t n, int heads_box, int rows) {
     EncodeTiledFn enc = encode_tiled();

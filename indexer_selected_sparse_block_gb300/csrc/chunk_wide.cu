@@ -209,38 +209,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + c * qpc, lead);
         }
         __syncwarp();
-        // keys of S (this CTA's half) and of P V (half), their table entries read a tile ahead
-        HalfRows hs, hv;
-        read_entries(hs, p, table, k0 + c * 64, k1, bxs);
-        read_entries(hv, p, table, k0 + half * 64, k1, bxs);
-        auto slot_free = [&](uint32_t full, uint32_t empty, uint32_t parity, uint32_t bytes) {
-            wait(empty, parity);
-            ok = __all_sync(0xFFFFFFFFu, ok);   // the warp's lanes agree
-            if (ok && c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (full - bar0) / 8, bytes);
-            __syncwarp();
-        };
-        for (int t = -1; t < n_tiles && ok; ++t) {
-            if (t + 1 < n_tiles) {
-                find_rows(hs, p, n_cells);
-                const uint32_t full = b_full + j * 8;
-                slot_free(full, b_empty + j * 8, (t & 1), 4u * kSlab);
-                if (!ok) break;
-                load_slabs<2, kSlab, true>(hs, buf0 + 2 * j * kSlab, maps.kv.k, 128 * j, g, bxs, lead + (full - bar0));
-                if (L::kRope && j == 3) {
-                    slot_free(b_rope, b_ropeDone, (t & 1), 2u * kSlab);
-                    if (!ok) break;
-                    load_slabs<1, kSlab, true>(hs, sRope, maps.kv.k, 512, g, bxs, lead + (b_rope - bar0));
+        const uint32_t s_full = b_full + j * 8, s_empty = b_empty + j * 8, v_full = s_full + 32, v_empty = s_empty + 32;
+        const uint32_t s_at = buf0 + 2 * j * kSlab, v_at = s_at + 8 * kSlab;
+        const CUtensorMap *vm = VK ? maps.kv.k : maps.kv.v;
+        const int vx = 256 * n + 128 * c;
+        // keys of S: this CTA's half; of P V: `half`.  Their table entries are read a tile ahead.
+        if (bxs == 6) {
+            // a half tile lies in one page: one thread does it all, the next slot looked at ahead
+            if (elect_one()) {
+                auto entry = [&](int pos) { return pos < k1 ? __ldg(table + p.page_div.div(pos)) : -1; };
+                auto row = [&](int e, int pos) {
+                    return e < 0 || e >= p.n_pages ? n_cells : e * p.page + (pos - p.page_div.div(pos) * p.page);
+                };
+                auto rows_in = [&](int r, int pos) { return r == n_cells ? 0 : max(0, min(64, k1 - pos)); };
+                auto expect = [&](uint32_t full, uint32_t bytes) {
+                    if (c == 0) mbar_arrive_expect_tx(bars + (full - bar0) / 8, bytes);
+                };
+                int ps = k0 + c * 64, pv = k0 + half * 64;
+                int es = entry(ps), ev = entry(pv);
+                bool there = true;
+                for (int t = -1; t < n_tiles && ok; ++t) {
+                    if (t + 1 < n_tiles) {
+                        const int r = row(es, ps), v = rows_in(r, ps);
+                        es = entry(ps + kT);
+                        if (!there) wait(s_empty, t & 1);
+                        if (!ok) break;
+                        expect(s_full, 4u * kSlab);
+                        load_slabs_one<2, kSlab, true>(r, v, s_at, maps.kv.k, 128 * j, g, n_cells, lead + (s_full - bar0));
+                        if (L::kRope && j == 3) {
+                            wait(b_ropeDone, t & 1);
+                            if (!ok) break;
+                            expect(b_rope, 2u * kSlab);
+                            load_slabs_one<1, kSlab, true>(r, v, sRope, maps.kv.k, 512, g, n_cells, lead + (b_rope - bar0));
+                        }
+                        ps += kT;
+                    }
+                    if (t >= 0) {
+                        there = mbar_test_wait(v_empty, (t & 1) ^ 1);
+                        const int r = row(ev, pv), v = rows_in(r, pv);
+                        ev = entry(pv + kT);
+                        if (!there) wait(v_empty, (t & 1) ^ 1);
+                        if (!ok) break;
+                        there = t + 2 < n_tiles && mbar_test_wait(s_empty, (t + 1) & 1);
+                        expect(v_full, 4u * kSlab);
+                        load_slabs_one<2, kSlab, true>(r, v, v_at, vm, vx, g, n_cells, lead + (v_full - bar0));
+                        pv += kT;
+                    } else {
+                        there = n_tiles > 1 && mbar_test_wait(s_empty, 0);
+                    }
                 }
-                read_entries(hs, p, table, k0 + (t + 2) * kT + c * 64, k1, bxs);
             }
-            if (t >= 0) {
-                find_rows(hv, p, n_cells);
-                const uint32_t full = b_full + (4 + j) * 8;
-                slot_free(full, b_empty + (4 + j) * 8, (t & 1) ^ 1, 4u * kSlab);
-                if (!ok) break;
-                load_slabs<2, kSlab, true>(hv, buf0 + 2 * (4 + j) * kSlab, VK ? maps.kv.k : maps.kv.v, 256 * n + 128 * c, g,
-                              bxs, lead + (full - bar0));
-                read_entries(hv, p, table, k0 + (t + 1) * kT + half * 64, k1, bxs);
+            __syncwarp();
+        } else {
+            HalfRows hs, hv;
+            read_entries(hs, p, table, k0 + c * 64, k1, bxs);
+            read_entries(hv, p, table, k0 + half * 64, k1, bxs);
+            auto slot_free = [&](uint32_t full, uint32_t empty, uint32_t parity, uint32_t bytes) {
+                wait(empty, parity);
+                ok = __all_sync(0xFFFFFFFFu, ok);   // the warp's lanes agree
+                if (ok && c == 0 && elect_one()) mbar_arrive_expect_tx(bars + (full - bar0) / 8, bytes);
+                __syncwarp();
+            };
+            for (int t = -1; t < n_tiles && ok; ++t) {
+                if (t + 1 < n_tiles) {
+                    find_rows(hs, p, n_cells);
+                    slot_free(s_full, s_empty, (t & 1), 4u * kSlab);
+                    if (!ok) break;
+                    load_slabs<2, kSlab, true>(hs, s_at, maps.kv.k, 128 * j, g, bxs, lead + (s_full - bar0));
+                    if (L::kRope && j == 3) {
+                        slot_free(b_rope, b_ropeDone, (t & 1), 2u * kSlab);
+                        if (!ok) break;
+                        load_slabs<1, kSlab, true>(hs, sRope, maps.kv.k, 512, g, bxs, lead + (b_rope - bar0));
+                    }
+                    read_entries(hs, p, table, k0 + (t + 2) * kT + c * 64, k1, bxs);
+                }
+                if (t >= 0) {
+                    find_rows(hv, p, n_cells);
+                    slot_free(v_full, v_empty, (t & 1) ^ 1, 4u * kSlab);
+                    if (!ok) break;
+                    load_slabs<2, kSlab, true>(hv, v_at, vm, vx, g, bxs, lead + (v_full - bar0));
+                    read_entries(hv, p, table, k0 + (t + 1) * kT + half * 64, k1, bxs);
+                }
             }
         }
     } else if (warp == 12) {

@@ -14,7 +14,10 @@ struct MapParams {
     const int32_t *len_old, *len_new, *free_pages, *free_head;
     int32_t *table, *cu, *total, *q_seq, *q_pos, *slot, *cell_of, *head_out, *status;
     int64_t n_free, table_stride, n_tok_cap, n_pos_cap;
+    int64_t table_pos;   // positions a table's row holds, below 2^31
+    FastDiv page_div;
     int n_seq, page, n_pages;
+    int vec;             // 16-byte stores of slot, q_seq and q_pos
 };
 
 // The lengths a sequence counts with: negative ones as 0.
@@ -27,21 +30,26 @@ __device__ __forceinline__ void map_lengths(const MapParams &p, int s, int64_t &
     n = n < 0 ? 0 : n;
 }
 
+// Pages of the first t positions (t < 2^31).
+__device__ __forceinline__ int map_pages(const MapParams &p, int64_t t) {
+    return t > 0 ? p.page_div.div((int)t - 1) + 1 : 0;
+}
 // Pages sequence s takes for n new tokens behind a cached ones: those of its table's row only.
 __device__ __forceinline__ int64_t map_taken(const MapParams &p, int64_t a, int64_t n) {
-    const int64_t p0 = (a + p.page - 1) / p.page;
-    int64_t p1 = (a + n + p.page - 1) / p.page;
-    p1 = p1 < p.table_stride ? p1 : p.table_stride;
-    return p1 > p0 ? p1 - p0 : 0;
+    if (a >= p.table_pos) return 0;
+    const int64_t e = a + n < p.table_pos ? a + n : p.table_pos;
+    return map_pages(p, e) - map_pages(p, a);
 }
 
 // cu[s] = sum of the new lengths before s and base[s] = pages taken before s: exclusive prefix
 // sums over the sequences, which every CTA makes for itself in shared memory (8 bytes read per
-// sequence, from L2; no CTA waits for another).  Then a thread per token: its sequence by
-// bisection in cu, its page from the table (the partly filled last page) or from the free list,
-// its cell; the first token of a page that is taken also writes the table's entry.  Integer
-// sums in a fixed order: the maps are the same on every run.
-// A decode step is one CTA and latency; a whole prompt is 16 bytes of stores per token.
+// sequence, from L2; no CTA waits for another).  Then a thread for four tokens: their sequence
+// by bisection in cu, their page from the table (the partly filled last page) or from the free
+// list, their cells; the first token of a page that is taken also writes the table's entry.
+// Integer sums in a fixed order: the maps are the same on every run.
+// A decode step is one CTA and latency (3.3 us); whole prompts are 16 bytes of stores per token:
+// 4.2 M tokens in 44 us with one token a thread and 64-bit divisions, PROMPT_US with four a thread,
+// 16-byte stores and one 32-bit division (a product) for the four.
 __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(const MapParams p) {
     extern __shared__ int32_t s_map[];
     int32_t *s_cu = s_map;                    // [n_seq + 1], clipped to n_tok_cap
@@ -57,7 +65,7 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(const MapParams 
         int64_t a, n;
         bool bad;
         map_lengths(p, s, a, n, bad);
-        if (bad || a + n > p.table_stride * p.page) flags |= SFA_DEV_BAD_LENGTH;
+        if (bad || a + n > p.table_pos) flags |= SFA_DEV_BAD_LENGTH;
         tok += n;
     }
     // block-wide exclusive sum of v
@@ -126,129 +134,228 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(const MapParams 
     __syncthreads();
     const int64_t live = s_cu[p.n_seq];
     flags = 0;
-    for (int64_t i = (int64_t)blockIdx.x * kMapThreads + tid; i < p.n_tok_cap;
-         i += (int64_t)gridDim.x * kMapThreads) {
-        if (i >= live) {
-            p.slot[i] = p.q_seq[i] = p.q_pos[i] = -1;
-            continue;
-        }
-        int lo = 0, hi = p.n_seq - 1;   // the last s with cu[s] <= i
-        while (lo < hi) {
-            const int m = (lo + hi + 1) >> 1;
-            if (s_cu[m] <= i) lo = m;
-            else hi = m - 1;
-        }
-        const int s = lo;
-        const int64_t a = max(p.len_old[s], 0);
-        const int64_t pos = a + (i - s_cu[s]);
-        const int64_t pg = pos / p.page, off = pos - pg * p.page;
-        int32_t cell = -1;
-        if (pg < p.table_stride) {
-            const int64_t p0 = (a + p.page - 1) / p.page;
-            int32_t *entry = p.table + (int64_t)s * p.table_stride + pg;
-            int32_t page;
-            if (pg >= p0) {
-                const int64_t f = s_base[s] + (pg - p0);
-                page = f < p.n_free ? p.free_pages[f] : -1;
-                if (page < 0 || page >= p.n_pages) {
-                    flags |= page < 0 ? SFA_DEV_NO_PAGES : SFA_DEV_BAD_CELL;
-                    page = -1;
+    int s = -1, pg = -1;                // the sequence and page of the token before
+    int64_t a = 0, s_end = 0;           // the sequence's cached tokens, the end of its rows
+    int32_t page = -1;
+    int old_pages = 0;
+    const int64_t groups = (p.n_tok_cap + 3) / 4;
+    for (int64_t q = (int64_t)blockIdx.x * kMapThreads + tid; q < groups;
+         q += (int64_t)gridDim.x * kMapThreads) {
+        int4 cell4, seq4, pos4;
+        int *cells = &cell4.x, *seqs = &seq4.x, *poss = &pos4.x;
+        int off = 0;
+        s_end = 0;                      // found anew for the group's first token
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t i = 4 * q + k;
+            if (i >= live) {
+                cells[k] = seqs[k] = poss[k] = -1;
+                continue;
+            }
+            int64_t pos;
+            bool fresh_page;
+            if (i >= s_end) {           // another sequence: the last s with cu[s] <= i
+                int lo = 0, hi = p.n_seq - 1;
+                while (lo < hi) {
+                    const int m = (lo + hi + 1) >> 1;
+                    if (s_cu[m] <= i) lo = m;
+                    else hi = m - 1;
                 }
-                if (off == 0) *entry = page;
+                s = lo;
+                s_end = s_cu[s + 1];
+                a = max(p.len_old[s], 0);
+                old_pages = a < p.table_pos ? map_pages(p, a) : 0;
+                pos = a + (i - s_cu[s]);
+                if (pos < p.table_pos) {
+                    pg = p.page_div.div((int)pos);
+                    off = (int)pos - pg * p.page;
+                }
+                fresh_page = true;
             } else {
-                page = *entry;
-                if (page < 0 || page >= p.n_pages) {
-                    flags |= SFA_DEV_BAD_CELL;
-                    page = -1;
+                pos = a + (i - s_cu[s]);
+                fresh_page = ++off == p.page;
+                if (fresh_page) {
+                    off = 0;
+                    ++pg;
                 }
             }
-            if (page >= 0) cell = (int32_t)((int64_t)page * p.page + off);
+            int32_t cell = -1;
+            if (pos < p.table_pos) {
+                if (fresh_page) {
+                    int32_t *entry = p.table + (int64_t)s * p.table_stride + pg;
+                    const bool taken = pg >= old_pages;
+                    if (taken) {
+                        const int64_t f = (int64_t)s_base[s] + (pg - old_pages);
+                        page = f < p.n_free ? p.free_pages[f] : -1;
+                    } else {
+                        page = *entry;
+                    }
+                    if (page < 0 || page >= p.n_pages) {
+                        flags |= taken && page < 0 ? SFA_DEV_NO_PAGES : SFA_DEV_BAD_CELL;
+                        page = -1;
+                    }
+                    if (taken && off == 0) *entry = page;
+                }
+                if (page >= 0) cell = page * p.page + off;
+            }
+            cells[k] = cell;
+            seqs[k] = s;
+            poss[k] = (int32_t)(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
         }
-        p.q_seq[i] = s;
-        p.q_pos[i] = (int32_t)(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
-        p.slot[i] = cell;
+        if (p.vec && 4 * q + 4 <= p.n_tok_cap) {
+            reinterpret_cast<int4 *>(p.slot)[q] = cell4;
+            reinterpret_cast<int4 *>(p.q_seq)[q] = seq4;
+            reinterpret_cast<int4 *>(p.q_pos)[q] = pos4;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (4 * q + k < p.n_tok_cap) {
+                    p.slot[4 * q + k] = cells[k];
+                    p.q_seq[4 * q + k] = seqs[k];
+                    p.q_pos[4 * q + k] = poss[k];
+                }
+        }
         if (p.cell_of) {
-            if (pos < p.n_pos_cap) p.cell_of[(int64_t)s * p.n_pos_cap + pos] = cell;
-            else flags |= SFA_DEV_BAD_LENGTH;
+            int32_t *row = p.cell_of + (int64_t)seqs[0] * p.n_pos_cap + poss[0];
+            if (seqs[0] >= 0 && seqs[3] == seqs[0] && (int64_t)poss[0] + 4 <= p.n_pos_cap &&
+                (reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
+                *reinterpret_cast<int4 *>(row) = cell4;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (seqs[k] < 0) continue;
+                    if (poss[k] < p.n_pos_cap) p.cell_of[(int64_t)seqs[k] * p.n_pos_cap + poss[k]] = cells[k];
+                    else flags |= SFA_DEV_BAD_LENGTH;
+                }
+            }
         }
     }
     if (flags) set_status(p.status, flags);
 }
 
 // ------------------------------------------------------------------------------ cell writes
+enum WriteKind { kCopy16, kCopy2, kRound16, kRound1, kQ8 };
 struct CellWrites {
     sfa_cell_write w[SFA_MAX_CELL_WRITES];
-    int vec[SFA_MAX_CELL_WRITES];   // 16-byte accesses on both sides
+    int kind[SFA_MAX_CELL_WRITES];
+    int units[SFA_MAX_CELL_WRITES];      // pieces of a row: 16 bytes stored, one element, a q8_0 block
+    FastDiv div[SFA_MAX_CELL_WRITES];    // by units
 };
 
-// One warp per (row, cache): the row's slot once, then the row.  Copies move 16 bytes a lane;
-// fp32 rows for a bf16 cache are rounded to nearest, as every bf16 cache value here is; q8_0
-// rows follow the rule of sfa_quantize_kv_q8_0 (one warp per block of 32: binary32 scale and
-// codes, the scale then rounded to binary16).
+// The rows' pieces in one line, four a thread in flight: their slots, their loads, their stores.
+// A row's neighbours in the line are its neighbours in memory on both sides.  With a warp to a row
+// a row of 72 pieces left a third of the lanes idle (65536 rows of 1408 bytes: 39 us, WRITE_US now).
+template <int KIND>
+__device__ __forceinline__ void write_pieces(const sfa_cell_write &w, int units, const FastDiv &div,
+                                             const int32_t *__restrict__ slot, int64_t n_rows,
+                                             int64_t n_cells, int32_t *status) {
+    constexpr int U = 4, B = 256 * U;
+    const int elems = w.n_inner * w.d;
+    const int64_t total = n_rows * units;
+    const int es = w.src_dtype == SFA_F32 ? 4 : 2;   // copies: of both sides
+    for (int64_t b = (int64_t)blockIdx.x * B; b < total; b += (int64_t)gridDim.x * B) {
+        const int64_t r0 = b / units;
+        const int u0 = (int)(b - r0 * units) + threadIdx.x;
+        const int n = (int)min((int64_t)B, total - b);
+        int64_t row[U], cell[U];
+        int piece[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int r = div.div(u0 + 256 * k);
+            piece[k] = u0 + 256 * k - r * units;
+            row[k] = r0 + r;
+            cell[k] = (int)threadIdx.x + 256 * k < n ? slot[row[k]] : -1;
+            if (cell[k] >= n_cells) {
+                set_status(status, SFA_DEV_BAD_CELL);
+                cell[k] = -1;
+            }
+        }
+        if constexpr (KIND == kCopy16) {
+            uint4 v[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (cell[k] >= 0)
+                    v[k] = __ldcs(reinterpret_cast<const uint4 *>(
+                        reinterpret_cast<const uint8_t *>(w.src) + row[k] * w.src_stride * es + 16 * piece[k]));
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (cell[k] >= 0)
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(w.dst) + cell[k] * elems * es + 16 * piece[k]) = v[k];
+        } else if constexpr (KIND == kRound16) {
+            float4 v[U][2];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (cell[k] >= 0) {
+                    const float4 *x = reinterpret_cast<const float4 *>(
+                        reinterpret_cast<const float *>(w.src) + row[k] * w.src_stride + 8 * piece[k]);
+                    v[k][0] = __ldcs(x);
+                    v[k][1] = __ldcs(x + 1);
+                }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (cell[k] >= 0)
+                    *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(w.dst) + cell[k] * elems + 8 * piece[k]) =
+                        make_uint4(pack_bf16(v[k][0].x, v[k][0].y), pack_bf16(v[k][0].z, v[k][0].w),
+                                   pack_bf16(v[k][1].x, v[k][1].y), pack_bf16(v[k][1].z, v[k][1].w));
+        } else {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (cell[k] < 0) continue;
+                if constexpr (KIND == kCopy2)
+                    reinterpret_cast<uint16_t *>(w.dst)[cell[k] * units + piece[k]] =
+                        reinterpret_cast<const uint16_t *>(w.src)[row[k] * w.src_stride * (es / 2) + piece[k]];
+                else
+                    reinterpret_cast<__nv_bfloat16 *>(w.dst)[cell[k] * elems + piece[k]] =
+                        __float2bfloat16_rn(reinterpret_cast<const float *>(w.src)[row[k] * w.src_stride + piece[k]]);
+            }
+        }
+    }
+}
+
+// fp32 rows for a bf16 cache are rounded to nearest, as every bf16 cache value here is; q8_0 rows
+// follow the rule of sfa_quantize_kv_q8_0 (one warp per block of 32: binary32 scale and codes,
+// the scale then rounded to binary16).
 __global__ void __launch_bounds__(256)
     write_cells_kernel(const CellWrites cw, const int32_t *__restrict__ slot, int64_t n_rows,
                        int64_t n_cells, int32_t *status) {
     pdl_wait();
     const sfa_cell_write &w = cw.w[blockIdx.y];
-    const int vec = cw.vec[blockIdx.y];
-    const int lane = threadIdx.x & 31;
-    const int64_t stride = (int64_t)gridDim.x * 8;
-    const int elems = w.n_inner * w.d;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n_rows; i += stride) {
+    const int kind = cw.kind[blockIdx.y], units = cw.units[blockIdx.y];
+    const FastDiv &div = cw.div[blockIdx.y];
+    if (kind == kCopy16) return write_pieces<kCopy16>(w, units, div, slot, n_rows, n_cells, status);
+    if (kind == kRound16) return write_pieces<kRound16>(w, units, div, slot, n_rows, n_cells, status);
+    if (kind == kCopy2) return write_pieces<kCopy2>(w, units, div, slot, n_rows, n_cells, status);
+    if (kind == kRound1) return write_pieces<kRound1>(w, units, div, slot, n_rows, n_cells, status);
+    const int lane = threadIdx.x & 31, nb = w.d / 32, rb = q8_row_bytes(w.d);
+    const int64_t total = n_rows * units, stride = (int64_t)gridDim.x * 8;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < total; u += stride) {
+        const int64_t i = u / units;
+        const int b = (int)(u - i * units);
         const int64_t c = slot[i];
         if (c < 0) continue;
         if (c >= n_cells) {
             if (lane == 0) set_status(status, SFA_DEV_BAD_CELL);
             continue;
         }
-        if (w.dst_dtype == SFA_Q8_0) {
-            const int nb = w.d / 32, rb = q8_row_bytes(w.d);
-            for (int b = 0; b < w.n_inner * nb; ++b) {
-                const int h = b / nb, k = b - h * nb;
-                const int64_t e = i * w.src_stride + (int64_t)b * 32 + lane;
-                const float x = w.src_dtype == SFA_F32
-                                    ? reinterpret_cast<const float *>(w.src)[e]
-                                    : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(w.src)[e]);
-                uint8_t *y = reinterpret_cast<uint8_t *>(w.dst) + (c * w.n_inner + h) * rb;
-                float amax = fabsf(x);
+        const int h = b / nb, k = b - h * nb;
+        const int64_t e = i * w.src_stride + (int64_t)b * 32 + lane;
+        const float x = w.src_dtype == SFA_F32
+                            ? reinterpret_cast<const float *>(w.src)[e]
+                            : __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(w.src)[e]);
+        uint8_t *y = reinterpret_cast<uint8_t *>(w.dst) + (c * w.n_inner + h) * rb;
+        float amax = fabsf(x);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                const float delta = __fdiv_rn(amax, 127.f);
-                const int q = delta == 0.f ? 0 : (int)roundf(__fdiv_rn(x, delta));
-                y[k * 32 + lane] = (uint8_t)(int8_t)q;
-                if (lane == 0) {
-                    const __half sc = __float2half_rn(delta);
-                    *reinterpret_cast<__half *>(y + w.d + 2 * k) = sc;
-                    if (__hisinf(sc)) set_status(status, SFA_DEV_FP16_RANGE);
-                }
-                const int used = w.d + w.d / 16;
-                if (k == nb - 1 && lane < rb - used) y[used + lane] = 0;
-            }
-        } else if (w.src_dtype == w.dst_dtype) {
-            const int es = w.src_dtype == SFA_F32 ? 4 : 2;
-            const uint8_t *x = reinterpret_cast<const uint8_t *>(w.src) + i * w.src_stride * es;
-            uint8_t *y = reinterpret_cast<uint8_t *>(w.dst) + c * elems * es;
-            if (vec) {
-                for (int e = lane; e < elems * es / 16; e += 32)
-                    reinterpret_cast<uint4 *>(y)[e] = reinterpret_cast<const uint4 *>(x)[e];
-            } else {
-                for (int e = lane; e < elems * es / 2; e += 32)
-                    reinterpret_cast<uint16_t *>(y)[e] = reinterpret_cast<const uint16_t *>(x)[e];
-            }
-        } else {   // fp32 -> bf16
-            const float *x = reinterpret_cast<const float *>(w.src) + i * w.src_stride;
-            __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(w.dst) + c * elems;
-            if (vec) {
-                for (int e = lane; e < elems / 4; e += 32) {
-                    const float4 v = reinterpret_cast<const float4 *>(x)[e];
-                    reinterpret_cast<uint2 *>(y)[e] =
-                        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-                }
-            } else {
-                for (int e = lane; e < elems; e += 32) y[e] = __float2bfloat16_rn(x[e]);
-            }
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const float delta = __fdiv_rn(amax, 127.f);
+        const int q = delta == 0.f ? 0 : (int)roundf(__fdiv_rn(x, delta));
+        y[k * 32 + lane] = (uint8_t)(int8_t)q;
+        if (lane == 0) {
+            const __half sc = __float2half_rn(delta);
+            *reinterpret_cast<__half *>(y + w.d + 2 * k) = sc;
+            if (__hisinf(sc)) set_status(status, SFA_DEV_FP16_RANGE);
         }
+        const int used = w.d + w.d / 16;
+        if (k == nb - 1 && lane < rb - used) y[used + lane] = 0;
     }
 }
 
@@ -281,13 +388,34 @@ extern "C" int sfa_build_page_maps(const int32_t *len_old, const int32_t *len_ne
     if (table_stride > 0x7FFFFFFF || table_stride * page_size > 0x7FFFFFFF)
         return SFA_ERR_INVALID_ARG;
     if (n_seq > kMapMaxSeq) return SFA_ERR_UNSUPPORTED;
-    MapParams p{len_old, len_new, free_pages, free_head, page_table, cu_new, len_total, q_seq,
-                q_pos, slot, cell_of, free_head_out, dev_status, n_free, table_stride, n_tok_cap,
-                n_pos_cap, n_seq, page_size, n_pages};
+    MapParams p{};
+    p.len_old = len_old;
+    p.len_new = len_new;
+    p.free_pages = free_pages;
+    p.free_head = free_head;
+    p.table = page_table;
+    p.cu = cu_new;
+    p.total = len_total;
+    p.q_seq = q_seq;
+    p.q_pos = q_pos;
+    p.slot = slot;
+    p.cell_of = cell_of;
+    p.head_out = free_head_out;
+    p.status = dev_status;
+    p.n_free = n_free;
+    p.table_stride = table_stride;
+    p.n_tok_cap = n_tok_cap;
+    p.n_pos_cap = n_pos_cap;
+    p.table_pos = table_stride * page_size;
+    p.page_div.set(page_size);
+    p.n_seq = n_seq;
+    p.page = page_size;
+    p.n_pages = n_pages;
+    p.vec = aligned16(slot) && aligned16(q_seq) && aligned16(q_pos);
     const size_t smem = (2 * (size_t)n_seq + 1) * sizeof(int32_t);
     if (smem > 48 * 1024 && !ensure_max_dynamic_smem(page_maps_kernel)) return SFA_ERR_CUDA;
-    int64_t blocks = (n_tok_cap + kMapThreads - 1) / kMapThreads;
-    const int64_t most = 2 * (int64_t)device_sm_count();
+    int64_t blocks = (n_tok_cap + 4 * kMapThreads - 1) / (4 * kMapThreads);
+    const int64_t most = 4 * (int64_t)device_sm_count();
     blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
     if (launch_pdl(page_maps_kernel, dim3((unsigned)blocks), dim3(kMapThreads), smem,
                    (cudaStream_t)stream, p) != cudaSuccess) {
@@ -305,6 +433,7 @@ extern "C" int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_
         n_cells > 0x7FFFFFFF)
         return SFA_ERR_INVALID_ARG;
     CellWrites cw{};
+    int64_t blocks = 0;
     for (int k = 0; k < n; ++k) {
         const sfa_cell_write &w = writes[k];
         const bool q8 = w.dst_dtype == SFA_Q8_0;
@@ -324,14 +453,17 @@ extern "C" int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_
                 return SFA_ERR_INVALID_ARG;
         }
         cw.w[k] = w;
-        // 16 bytes a lane where every row of both sides starts on such a boundary
-        // (the fp32 -> bf16 case stores 8 bytes a lane)
-        cw.vec[k] = !q8 && aligned16(w.src) && (w.src_stride * ss) % 16 == 0 &&
-                    (elems * ss) % 16 == 0 && (ss != ds ? (elems * ds) % 8 == 0 : (elems * ds) % 16 == 0);
+        // 16 bytes a store where every row of both sides starts on such a boundary
+        const bool vec = aligned16(w.src) && (w.src_stride * ss) % 16 == 0 && (elems * ds) % 16 == 0;
+        const bool copy = w.src_dtype == w.dst_dtype;
+        cw.kind[k] = q8 ? kQ8 : copy ? (vec ? kCopy16 : kCopy2) : (vec ? kRound16 : kRound1);
+        cw.units[k] = (int)(q8 ? elems / 32 : vec ? elems * ds / 16 : copy ? elems * ds / 2 : elems);
+        cw.div[k].set(cw.units[k]);
+        const int64_t work = (n_rows * cw.units[k] + (q8 ? 7 : 1023)) / (q8 ? 8 : 1024);
+        if (work > blocks) blocks = work;
     }
     if (n == 0 || n_rows == 0) return SFA_OK;
     if (!slot) return SFA_ERR_INVALID_ARG;
-    int64_t blocks = (n_rows + 7) / 8;
     const int64_t most = 8 * (int64_t)device_sm_count();
     if (blocks > most) blocks = most;
     if (launch_pdl(write_cells_kernel, dim3((unsigned)blocks, (unsigned)n), dim3(256), 0,
