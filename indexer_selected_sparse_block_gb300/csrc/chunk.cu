@@ -269,28 +269,48 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
     if (len <= p.split_keys) return;
     const int ns = (len + p.split_keys - 1) / p.split_keys;
     const int64_t part0 = ((int64_t)blockIdx.x * p.h_kv + g) * p.n_split * p.item_rows + row;
-    float M = -INFINITY;
-    for (int c = lane; c < ns; c += 32) M = fmaxf(M, p.part_ml[(part0 + (int64_t)c * p.item_rows) * 2]);
+    // lane c holds (m, l) of piece c, c + 32, ..
+    constexpr int W = 4;            // 128 pieces at most
+    float m[W], w[W], M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int x = 0; x < W; ++x) {
+        const int c = lane + 32 * x;
+        const float2 ml = c < ns ? *reinterpret_cast<const float2 *>(p.part_ml + (part0 + (int64_t)c * p.item_rows) * 2)
+                                 : make_float2(-INFINITY, 0.f);
+        m[x] = ml.x;
+        w[x] = ml.y;
+        M = fmaxf(M, m[x]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+#pragma unroll
+    for (int x = 0; x < W; ++x) {   // the piece's share of the sum, then its weight
+        const float e = m[x] == -INFINITY ? 0.f : exp2f(m[x] - M);
+        l += w[x] == 0.f ? 0.f : e * w[x];
+        w[x] = e;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     constexpr int C = (DV + 127) / 128;
     float4 acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int c = 0; c < ns; ++c) {
-        const int64_t r = part0 + (int64_t)c * p.item_rows;
-        const float m = p.part_ml[r * 2], w = m == -INFINITY ? 0.f : exp2f(m - M);
-        const float lc = p.part_ml[r * 2 + 1];
-        l += lc == 0.f ? 0.f : w * lc;
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-            if (k * 128 + lane * 4 < DV) {
-                const float4 v = *reinterpret_cast<const float4 *>(p.part_o + r * DV + k * 128 + lane * 4);
-                acc[k].x = fmaf(w, v.x, acc[k].x);
-                acc[k].y = fmaf(w, v.y, acc[k].y);
-                acc[k].z = fmaf(w, v.z, acc[k].z);
-                acc[k].w = fmaf(w, v.w, acc[k].w);
+    for (int x = 0; x < W; ++x) {
+        if (32 * x >= ns) break;
+#pragma unroll 4
+        for (int c = 32 * x; c < min(ns, 32 * x + 32); ++c) {
+            const float e = __shfl_sync(0xFFFFFFFFu, w[x], c & 31);
+            const float *src = p.part_o + (part0 + (int64_t)c * p.item_rows) * DV + lane * 4;
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                if (k * 128 + lane * 4 < DV) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + k * 128);
+                    acc[k].x = fmaf(e, v.x, acc[k].x);
+                    acc[k].y = fmaf(e, v.y, acc[k].y);
+                    acc[k].z = fmaf(e, v.z, acc[k].z);
+                    acc[k].w = fmaf(e, v.w, acc[k].w);
+                }
             }
         }
     }

@@ -38,6 +38,7 @@ struct Narrow {
     static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 2 + 2 + 2 + 1;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
     static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+    static_assert((kKS + kVS) * kTileBytes >= 8 * D * 128, "the result's way through shared memory");
 };
 
 struct NarrowMaps {
@@ -80,21 +81,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int item = blockIdx.x, g = blockIdx.y, split = blockIdx.z;
+    // the barriers and tensor memory need nothing from global memory: they overlap the search
+    if (tid == 0) {
+        const int ip = (int)(b_p - bar0) / 8;
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip || i == ip + 1 ? 4 : 1);   // P: four warps
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 10) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
     pdl_wait();
     if (warp == 0) {
         const Item it = find_item(p, item, blockIdx.x == 0 && g == 0 && split == 0);
         if (lane == 0) *sItem = it;
     }
+    __syncwarp();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;   // S / P: 2 x 128 columns, O: 2 x D
+    auto leave = [&]() {
+        if (warp == 10) tmem_dealloc(tmem, 512);
+    };
     const Item it = *sItem;
-    if (it.seq < 0) return;
+    if (it.seq < 0) return leave();
     const int q0 = it.tile * p.item_q;                        // first query of the item
     const int nq = min(p.item_q, min(it.q.n, p.n_new_max) - q0);
     const int pos0 = it.q.total - it.q.n + q0;                // its position
     const int len = max(0, min(key_limit(p, it.q), pos0 + nq));
     const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
     const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
-    if (split > 0 && k0 >= k1) return;                        // no such piece
+    if (split > 0 && k0 >= k1) return leave();                // no such piece
     const bool whole = len <= p.split_keys;
     const int n_tiles = (k1 - k0 + kT - 1) / kT;
     const int G = p.G;
@@ -116,24 +135,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.lse) p.lse[orow] = -INFINITY;
         }
-        return;
+        return leave();
     }
 
-    if (tid == 0) {
-        const int ip = (int)(b_p - bar0) / 8;
-        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip || i == ip + 1 ? 4 : 1);   // P: four warps
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 10) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;   // S / P: 2 x 128 columns, O: 2 x D
     const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sV = smem_u32(smem + L::kOffV);
     // once a wait ran out no other is made
     bool ok = true;
@@ -239,7 +243,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     pv_op(i, vs, t == 0);
-                    if (!more) tc_commit(bars + (b_o - bar0) / 8 + i);
                     if (more) {
                         if (i == 0) wait(b_kFull + 8 * ks, kp);
                         if (!ok) break;
@@ -248,6 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
+                if (!more)   // both row tiles' results go out through the stages of K and V
+                    for (int i = 0; i < 2; ++i) tc_commit(bars + (b_o - bar0) / 8 + i);
                 free_stage(VK ? b_kEmpty : b_vEmpty, vs);
                 if (more && !VK) free_stage(b_kEmpty, ks);
                 next_k();
@@ -361,32 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
             const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
                                  (w * qpt + ql) * G + h;
-#pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-                uint32_t r[32];
-                tmem_ld32(tO + 32 * x, r);
-                tmem_ld_wait();
-                if (!live) continue;
-                if (whole && p.o_bf16) {
-                    uint4 *o = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * D + 32 * x);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = pack_bf16(__uint_as_float(r[8 * j + 2 * k]) * inv,
-                                             __uint_as_float(r[8 * j + 2 * k + 1]) * inv);
-                        o[j] = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                } else {
-                    float4 *o = reinterpret_cast<float4 *>(
-                        (whole ? reinterpret_cast<float *>(p.O) + orow * D : p.part_o + part * D) + 32 * x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
-                                           __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
-                }
-            }
+            store_tile<D, D>(p, sK + warp * (D * 128), tO, inv, live, whole ? orow : part, whole, 0);
             if (live) {
                 if (!whole) {
                     p.part_ml[part * 2] = m;

@@ -99,6 +99,55 @@ __device__ __forceinline__ void tma1_load(uint32_t dst, const CUtensorMap *map, 
 }
 
 // ------------------------------------------------------------------------------- key rows
+// A warp's 32 rows (its tensor memory lanes) x C value dims of O from column tcol, times each
+// row's inv, to the output (whole) or the partial results: rows of DV values at `row`, dims d0 ...
+// By way of shared memory (C * 128 bytes at `stage`): a row's values leave as one line.  (Each lane
+// storing its own row's 16 bytes took 5.8 us for 64 rows of 512 fp32 values and 32 sectors a
+// store.)  16-byte pieces are exchanged by the row's number, so neither side meets bank conflicts.
+template <int C, int DV>
+__device__ __forceinline__ void store_tile(const Params &p, uint32_t stage, uint32_t tcol, float inv,
+                                           bool live, int64_t row, bool whole, int d0) {
+    constexpr int PIECES = C / 4;   // of a row
+    const int lane = threadIdx.x & 31;
+    const uint32_t mine = stage + lane * (C * 4);
+#pragma unroll 1
+    for (int x = 0; x < C / 32; ++x) {
+        uint32_t r[32];
+        tmem_ld32(tcol + 32 * x, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(r[4 * j + k]) * inv;
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             mine + (((x * 8 + j) ^ (lane & (PIECES - 1))) << 4)),
+                         "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+                         : "memory");
+        }
+    }
+    __syncwarp();
+    constexpr int ROWS = 32 / PIECES;   // rows of one step: 1 for C = 128, 2 for C = 64
+    const int sub = lane / PIECES, piece = lane & (PIECES - 1);
+#pragma unroll 4
+    for (int i = 0; i < 32; i += ROWS) {
+        const int rr = i + sub;
+        const bool on = __shfl_sync(0xFFFFFFFFu, (int)live, rr) != 0;
+        const int64_t to = __shfl_sync(0xFFFFFFFFu, row, rr) * DV + d0 + 4 * piece;
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(stage + rr * (C * 4) + ((piece ^ (rr & (PIECES - 1))) << 4)));
+        if (!on) continue;
+        if (!whole) *reinterpret_cast<float4 *>(p.part_o + to) = v;
+        else if (p.o_bf16)
+            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + to) =
+                make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        else
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + to) = v;
+    }
+}
+
 template <int N>
 struct Const {
     static constexpr int value = N;

@@ -127,21 +127,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = (int)cluster_rank();
     const int item = blockIdx.x >> 1, g = blockIdx.y, split = blockIdx.z;
+    // the barriers, tensor memory and the pair's meeting need nothing from global memory: they
+    // overlap the search for the item
+    if (tid == 0) {
+        const int ip = (int)(b_p - bar0) / 8;
+        // P (half 0) ready: eight warps of each CTA; P half 1: four of each
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 16 : i == ip + 1 ? 8 : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
     pdl_wait();
     if (warp == 0) {
         const Item it = find_item(p, item, blockIdx.x == 0 && g == 0 && split == 0);
         if (lane == 0) *sItem = it;
     }
+    __syncwarp();
+    tc_fence_before();
     __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto leave = [&]() {   // both CTAs of the pair, with nothing in flight
+        if (warp == 12)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    };
     const Item it = *sItem;
-    if (it.seq < 0) return;
+    if (it.seq < 0) return leave();
     const int q0 = it.tile * p.item_q;                        // first query of the tile
     const int nq = min(p.item_q, min(it.q.n, p.n_new_max) - q0);
     const int pos0 = it.q.total - it.q.n + q0;                // its position
     const int len = max(0, min(key_limit(p, it.q), pos0 + nq));
     const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
     const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
-    if (split > 0 && k0 >= k1) return;                        // no such piece
+    if (split > 0 && k0 >= k1) return leave();                // no such piece
     const bool whole = len <= p.split_keys;
     const int n_tiles = (k1 - k0 + kT - 1) / kT;
     const int G = p.G;
@@ -163,28 +189,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             }
             if (hh == 0 && cg == 0 && p.lse) p.lse[orow] = -INFINITY;
         }
-        return;
+        return leave();
     }
 
-    if (tid == 0) {
-        const int ip = (int)(b_p - bar0) / 8;
-        // P (half 0) ready: eight warps of each CTA; P half 1: four of each
-        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 16 : i == ip + 1 ? 8 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                         smem_u32(tmem_slot))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO = tmem + 128;   // S: 2 x 64 columns, O: 2 x 128
     const uint32_t buf0 = smem_u32(smem + L::kOffBuf), sQ = smem_u32(smem + L::kOffQ),
                    sRope = smem_u32(smem + L::kOffRope), sP = smem_u32(smem + L::kOffP);
@@ -495,34 +502,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
             const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
                                  (c * qpc + ql) * G + h;
-#pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-                uint32_t r[32];
-                tmem_ld32(tO + (cg * 4 + x) * 32 + lane_addr, r);
-                tmem_ld_wait();
-                // columns 128 cg + 32 x ..: dims 256 cg + 128 hh + 32 x ..
-                const int d = cg * 256 + hh * 128 + x * 32;
-                if (!live) continue;
-                if (whole && p.o_bf16) {
-                    uint4 *o = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack_bf16(__uint_as_float(r[8 * j + 2 * k]) * inv,
-                                             __uint_as_float(r[8 * j + 2 * k + 1]) * inv);
-                        o[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-                    float4 *o = reinterpret_cast<float4 *>(
-                        (whole ? reinterpret_cast<float *>(p.O) + orow * 512 : p.part_o + part * 512) + d);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
-                                           __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
-                }
-            }
+            // columns 128 cg ..: dims 256 cg + 128 hh ..; every operand is used up
+            store_tile<128, 512>(p, buf0 + warp * 16384, tO + cg * 128 + lane_addr, inv, live,
+                                 whole ? orow : part, whole, cg * 256 + hh * 128);
             if (live && hh == 0 && cg == 0) {
                 if (!whole) {
                     p.part_ml[part * 2] = m;

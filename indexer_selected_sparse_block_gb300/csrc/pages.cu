@@ -8,6 +8,7 @@ namespace {
 
 // ------------------------------------------------------------------------ page tables, slots
 constexpr int kMapThreads = 512;
+constexpr int64_t kMapFourFrom = 1 << 18;
 constexpr int kMapMaxSeq = 16384;   // offsets and page bases of every sequence fit shared memory
 
 struct MapParams {
@@ -50,7 +51,8 @@ __device__ __forceinline__ int64_t map_taken(const MapParams &p, int64_t a, int6
 // A decode step is one CTA and latency (3.3 us); whole prompts are 16 bytes of stores per token:
 // 4.2 M tokens in 44 us with one token a thread and 64-bit divisions, PROMPT_US with four a thread,
 // 16-byte stores and one 32-bit division (a product) for the four.
-__global__ void __launch_bounds__(kMapThreads) page_maps_kernel(const MapParams p) {
+template <int N>
+__global__ void __launch_bounds__(kMapThreads, N == 4 ? 3 : 4) page_maps_kernel(const MapParams p) {
     extern __shared__ int32_t s_map[];
     int32_t *s_cu = s_map;                    // [n_seq + 1], clipped to n_tok_cap
     int32_t *s_base = s_map + p.n_seq + 1;    // [n_seq]
@@ -138,16 +140,15 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(const MapParams 
     int64_t a = 0, s_end = 0;           // the sequence's cached tokens, the end of its rows
     int32_t page = -1;
     int old_pages = 0;
-    const int64_t groups = (p.n_tok_cap + 3) / 4;
+    const int64_t groups = (p.n_tok_cap + N - 1) / N;
     for (int64_t q = (int64_t)blockIdx.x * kMapThreads + tid; q < groups;
          q += (int64_t)gridDim.x * kMapThreads) {
-        int4 cell4, seq4, pos4;
-        int *cells = &cell4.x, *seqs = &seq4.x, *poss = &pos4.x;
+        int cells[N], seqs[N], poss[N];
         int off = 0;
         s_end = 0;                      // found anew for the group's first token
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t i = 4 * q + k;
+        for (int k = 0; k < N; ++k) {
+            const int64_t i = N * q + k;
             if (i >= live) {
                 cells[k] = seqs[k] = poss[k] = -1;
                 continue;
@@ -202,27 +203,28 @@ __global__ void __launch_bounds__(kMapThreads) page_maps_kernel(const MapParams 
             seqs[k] = s;
             poss[k] = (int32_t)(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
         }
-        if (p.vec && 4 * q + 4 <= p.n_tok_cap) {
-            reinterpret_cast<int4 *>(p.slot)[q] = cell4;
-            reinterpret_cast<int4 *>(p.q_seq)[q] = seq4;
-            reinterpret_cast<int4 *>(p.q_pos)[q] = pos4;
+        auto vec = [](const int *v) { return make_int4(v[0], v[1 % N], v[2 % N], v[3 % N]); };
+        if (N == 4 && p.vec && 4 * q + 4 <= p.n_tok_cap) {
+            reinterpret_cast<int4 *>(p.slot)[q] = vec(cells);
+            reinterpret_cast<int4 *>(p.q_seq)[q] = vec(seqs);
+            reinterpret_cast<int4 *>(p.q_pos)[q] = vec(poss);
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (4 * q + k < p.n_tok_cap) {
-                    p.slot[4 * q + k] = cells[k];
-                    p.q_seq[4 * q + k] = seqs[k];
-                    p.q_pos[4 * q + k] = poss[k];
+            for (int k = 0; k < N; ++k)
+                if (N * q + k < p.n_tok_cap) {
+                    p.slot[N * q + k] = cells[k];
+                    p.q_seq[N * q + k] = seqs[k];
+                    p.q_pos[N * q + k] = poss[k];
                 }
         }
         if (p.cell_of) {
             int32_t *row = p.cell_of + (int64_t)seqs[0] * p.n_pos_cap + poss[0];
-            if (seqs[0] >= 0 && seqs[3] == seqs[0] && (int64_t)poss[0] + 4 <= p.n_pos_cap &&
+            if (N == 4 && seqs[0] >= 0 && seqs[N - 1] == seqs[0] && (int64_t)poss[0] + 4 <= p.n_pos_cap &&
                 (reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
-                *reinterpret_cast<int4 *>(row) = cell4;
+                *reinterpret_cast<int4 *>(row) = vec(cells);
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < N; ++k) {
                     if (seqs[k] < 0) continue;
                     if (poss[k] < p.n_pos_cap) p.cell_of[(int64_t)seqs[k] * p.n_pos_cap + poss[k]] = cells[k];
                     else flags |= SFA_DEV_BAD_LENGTH;
@@ -413,12 +415,16 @@ extern "C" int sfa_build_page_maps(const int32_t *len_old, const int32_t *len_ne
     p.n_pages = n_pages;
     p.vec = aligned16(slot) && aligned16(q_seq) && aligned16(q_pos);
     const size_t smem = (2 * (size_t)n_seq + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024 && !ensure_max_dynamic_smem(page_maps_kernel)) return SFA_ERR_CUDA;
-    int64_t blocks = (n_tok_cap + 4 * kMapThreads - 1) / (4 * kMapThreads);
-    const int64_t most = 4 * (int64_t)device_sm_count();
+    // four tokens a thread once every thread of the device has one
+    const bool four = n_tok_cap > (int64_t)kMapFourFrom;
+    const int per_block = (four ? 4 : 1) * kMapThreads;
+    int64_t blocks = (n_tok_cap + per_block - 1) / per_block;
+    const int64_t most = (four ? 3 : 4) * (int64_t)device_sm_count();   // resident at once
     blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
-    if (launch_pdl(page_maps_kernel, dim3((unsigned)blocks), dim3(kMapThreads), smem,
-                   (cudaStream_t)stream, p) != cudaSuccess) {
+    auto kernel = four ? page_maps_kernel<4> : page_maps_kernel<1>;
+    if (smem > 48 * 1024 && !ensure_max_dynamic_smem(kernel)) return SFA_ERR_CUDA;
+    if (launch_pdl(kernel, dim3((unsigned)blocks), dim3(kMapThreads), smem, (cudaStream_t)stream, p) !=
+        cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
