@@ -9,6 +9,7 @@ built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -598,50 +599,45 @@ def _no_tensor(name, t, dev, what):
     raise ValueError(f"{name} must be {what}")
 
 
-def _vec(name, t, n, dev):
-    """Address of t, a contiguous int32 vector (of n entries, unless n < 0) on device dev."""
-    if (t.dtype is not _I32 or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous()
-            or (n >= 0 and t.numel() != n) or dev < 0):
-        _no_tensor(name, t, dev, f"a contiguous int32 vector{f' of {n} entries' if n >= 0 else ''}")
-    return t.data_ptr()
+def _device_of(t):
+    """Index of t's device, the call's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libsfa takes CUDA tensors only")
+    return dev
 
 
-def _rows(name, t, n, dev):
+def _ints(name, t, n, dev):
+    """Address of t: n contiguous int32 values on device dev."""
+    if t.dtype is _I32 and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _no_tensor(name, t, dev, f"a contiguous int32 tensor of {n} entries")
+
+
+def _int_rows(name, t, n, dev):
     """Address of t, a contiguous int32 [n][any] matrix on device dev."""
     if (t.dtype is not _I32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous()
-            or t.size(0) != n or dev < 0):
+            or t.size(0) != n):
         _no_tensor(name, t, dev, f"a contiguous int32 [{n}][..] tensor")
     return t.data_ptr()
 
 
-def _status_ptr(t, dev):
-    return None if t is None else _vec("dev_status", t, 1, dev)
-
-
-class _OnDevice:
-    """Makes `dev` the current device (the library launches on it) and back."""
-
-    def __init__(self, dev):
-        self.dev = dev
-
-    def __enter__(self):
-        self.old = torch.cuda.current_device()
-        if self.old != self.dev:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.old != self.dev:
-            torch.cuda.set_device(self.old)
-        return False
-
-
-def _stream_on(stream, dev):
-    """The stream's handle; None: the current stream of device dev."""
+def _call(fn, dev, stream, *args):
+    """The entry point on device dev (the library launches on the current one), on `stream` or the
+    device's current stream; raises on an error status."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device_index != dev:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index == dev:
+        raw = stream.cuda_stream
+    else:
         raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
-    return stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc:
+        raise SfaError(fn.__name__, rc)
 
 
 def sfa_build_page_maps(len_old, len_new, page_size: int, free_pages, free_head, n_pages: int,
@@ -651,21 +647,19 @@ def sfa_build_page_maps(len_old, len_new, page_size: int, free_pages, free_head,
     free_head on) into page_table, the new tokens' sequences, positions and cells (q_seq, q_pos,
     slot: rows past the last token get -1), the packed offsets cu_new [n_seq + 1], len_total, and
     the new positions' entries of the per-position map cell_of [n_seq][n_pos] when given."""
-    dev, n_seq, n_tok = len_old.get_device(), len_old.numel(), slot.numel()
-    args = (_vec("len_old", len_old, -1, dev), _vec("len_new", len_new, n_seq, dev), n_seq, page_size,
-            _vec("free_pages", free_pages, -1, dev), free_pages.numel(),
-            _vec("free_head", free_head, 1, dev), n_pages,
-            _rows("page_table", page_table, n_seq, dev), page_table.size(1),
-            _vec("cu_new", cu_new, n_seq + 1, dev), _vec("len_total", len_total, n_seq, dev),
-            _vec("q_seq", q_seq, n_tok, dev), _vec("q_pos", q_pos, n_tok, dev),
-            _vec("slot", slot, -1, dev), n_tok,
-            None if cell_of is None else _rows("cell_of", cell_of, n_seq, dev),
-            0 if cell_of is None else cell_of.size(1), _vec("free_head_out", free_head_out, 1, dev),
-            _status_ptr(dev_status, dev))
-    with _OnDevice(dev):
-        rc = lib().sfa_build_page_maps(*args, _stream_on(stream, dev))
-    if rc:
-        raise SfaError("sfa_build_page_maps", rc)
+    dev = _device_of(len_old)
+    n_seq, n_tok, n_free, n_pos, cells = len_old.numel(), slot.numel(), free_pages.numel(), 0, None
+    if cell_of is not None:
+        cells, n_pos = _int_rows("cell_of", cell_of, n_seq, dev), cell_of.size(1)
+    _call(lib().sfa_build_page_maps, dev, stream, _ints("len_old", len_old, n_seq, dev),
+          _ints("len_new", len_new, n_seq, dev), n_seq, page_size,
+          _ints("free_pages", free_pages, n_free, dev), n_free, _ints("free_head", free_head, 1, dev),
+          n_pages, _int_rows("page_table", page_table, n_seq, dev), page_table.size(1),
+          _ints("cu_new", cu_new, n_seq + 1, dev), _ints("len_total", len_total, n_seq, dev),
+          _ints("q_seq", q_seq, n_tok, dev), _ints("q_pos", q_pos, n_tok, dev),
+          _ints("slot", slot, n_tok, dev), n_tok, cells, n_pos,
+          _ints("free_head_out", free_head_out, 1, dev),
+          None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
 
 
 _CELL_WRITE = struct.Struct("@QqQiiii")     # sfa_cell_write of include/sfa.h
@@ -702,18 +696,15 @@ def sfa_write_cells(writes, slot, dev_status=None, stream=None):
     writes = list(writes)
     if len(writes) > SFA_MAX_CELL_WRITES:
         raise ValueError(f"at most {SFA_MAX_CELL_WRITES} caches per call")
-    dev = slot.get_device()
-    at = _vec("slot", slot, -1, dev)
+    dev = _device_of(slot)
+    n_rows = slot.numel()
+    at = _ints("slot", slot, n_rows, dev)
     if not writes:
         return
-    n_rows, n_cells = slot.numel(), writes[0][1].size(0)
+    n_cells = writes[0][1].size(0)
     packed = b"".join([_CELL_WRITE.pack(*_cell_write(x, y, n_rows, n_cells, dev)) for x, y in writes])
-    status = _status_ptr(dev_status, dev)
-    with _OnDevice(dev):
-        rc = lib().sfa_write_cells(len(writes), packed, at, n_rows, n_cells, status,
-                                   _stream_on(stream, dev))
-    if rc:
-        raise SfaError("sfa_write_cells", rc)
+    _call(lib().sfa_write_cells, dev, stream, len(writes), packed, at, n_rows, n_cells,
+          None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
 
 
 def sfa_chunk_attend_workspace_bytes(dtype_code: int, n_seq: int, n_q: int, h_q: int, h_kv: int,
@@ -721,6 +712,13 @@ def sfa_chunk_attend_workspace_bytes(dtype_code: int, n_seq: int, n_q: int, h_q:
                                      o_dtype: int = SFA_F32) -> int:
     return int(lib().sfa_chunk_attend_workspace_bytes(dtype_code, n_seq, n_q, h_q, h_kv, dkq, dv,
                                                       int(has_v), n_new_max, n_kv_max, o_dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _chunk_workspace(dev, *sizes):
+    """sfa_chunk_attend_workspace_bytes on device dev: sizes in, a size out."""
+    with torch.cuda.device(dev):
+        return int(lib().sfa_chunk_attend_workspace_bytes(*sizes))
 
 
 def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_total, n_new_max: int,
@@ -735,39 +733,36 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
     n_cells, h_kv, k_row = K.shape
     n_seq, dv = len_total.numel(), O.size(-1)
     _check_qkv(Q, K, V)
-    code, o_code = _dtype_code(K), _CODES.get(O.dtype)
+    code, o_code = _CODES.get(K.dtype), _CODES.get(O.dtype)
     q8 = code == SFA_Q8_0
-    if k_row != (sfa_q8_0_row_bytes(dkq) if q8 else dkq):
-        raise ValueError("Q and K must share a head size")
-    if V is not None and tuple(V.shape) != (n_cells, h_kv, sfa_q8_0_row_bytes(dv) if q8 else dv):
+    if code is None or k_row != (sfa_q8_0_row_bytes(dkq) if q8 else dkq):
+        raise ValueError("Q and K must share a head size, K bf16, fp32 or q8_0 rows")
+    if V is not None and V.shape != (n_cells, h_kv, sfa_q8_0_row_bytes(dv) if q8 else dv):
         raise ValueError("V must be [n_cells][h_kv][dv] like K")
     if O.shape != (n_q, h_q, dv) or o_code not in (SFA_F32, SFA_BF16):
         raise ValueError("O must be an fp32 or bf16 [n_q][h_q][dv] tensor")
     if lse is not None and (lse.shape != (n_q, h_q) or lse.dtype is not _F32):
         raise ValueError("lse must be an fp32 [n_q][h_q] tensor")
     for t in (Q, K, V, O, lse, workspace):
-        if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous() or dev < 0):
             _no_tensor("every tensor", t, dev, "contiguous")
-    table, cu = _rows("page_table", page_table, n_seq, dev), _vec("cu_new", cu_new, n_seq + 1, dev)
-    total, status = _vec("len_total", len_total, n_seq, dev), _status_ptr(dev_status, dev)
-    L = lib()
-    with _OnDevice(dev):
-        raw = _stream_on(stream, dev)
-        if workspace is None:
-            need = L.sfa_chunk_attend_workspace_bytes(code, n_seq, n_q, h_q, h_kv, dkq, dv,
-                                                      V is not None, n_new_max, n_kv_max, o_code)
-            if need:
-                workspace = torch.empty(need, dtype=_U8, device=Q.device)
-                if stream is not None:   # freed on return: not before that stream is done
-                    workspace.record_stream(stream)
-        rc = L.sfa_chunk_attend_paged(
-            Q.data_ptr(), K.data_ptr(), None if V is None else V.data_ptr(), code, n_cells, table,
-            page_table.size(1), page_size, n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu, total, n_new_max,
-            n_kv_max, O.data_ptr(), o_code, None if lse is None else lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), status, raw)
-    if rc:
-        raise SfaError("sfa_chunk_attend_paged", rc)
+    table, cu = _int_rows("page_table", page_table, n_seq, dev), _ints("cu_new", cu_new, n_seq + 1, dev)
+    total = _ints("len_total", len_total, n_seq, dev)
+    ws_bytes = 0
+    if workspace is None:
+        ws_bytes = _chunk_workspace(dev, code, n_seq, n_q, h_q, h_kv, dkq, dv, V is not None, n_new_max,
+                                    n_kv_max, o_code)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=_U8, device=Q.device)
+            if stream is not None:   # freed on return: not before that stream is done
+                workspace.record_stream(stream)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _call(lib().sfa_chunk_attend_paged, dev, stream, Q.data_ptr(), K.data_ptr(),
+          None if V is None else V.data_ptr(), code, n_cells, table, page_table.size(1), page_size,
+          n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu, total, n_new_max, n_kv_max, O.data_ptr(), o_code,
+          None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+          ws_bytes, None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
 
 
 def sfa_read_device_status(dev_status, stream=None) -> int:
