@@ -2,7 +2,7 @@
 //
 // One CTA owns two row tiles of 128 rows (query, head) of one KV head and streams tiles of 128
 // keys that both share.  Per row tile:
-//   S[128 x 128] = Q K^T (operands in shared memory), the softmax, one row a thread,
+//   S[128 x 128] = Q K^T (operands in shared memory), the softmax, half a row a thread,
 //   O[128 x D]  += P V, P in tensor memory where S was (the weights never pass through shared
 //                  memory, whose bandwidth the products already use up), V from shared memory.
 // While one row tile's softmax runs, the other's products do: P V (t) and S(t + 1) of a row tile
@@ -13,8 +13,12 @@
 // bf16 results one bf16 weight is enough.  The running maximum moves only when a tile raises it by
 // more than 2^8, and O in tensor memory is rescaled only then.
 //
-// Warps 0-3 and 4-7: softmax, correction and result of the two row tiles; warp 8: Q and K; warp 9:
-// V; warp 10: products (one lane).  Pages as in chunk_wide.cu.
+// The chain is what bounds it: with one row a thread (four warps a row tile) the softmax took
+// most of 3800 cycles a tile, the products 2048.
+//
+// Warps 0-7 and 8-15: softmax, correction and result of the two row tiles, the first four of each
+// for keys 0-63 of a tile and the lower half of the value dims; warp 16: Q and K; warp 17: V;
+// warp 18: products (one lane).  Pages as in chunk_wide.cu.
 #include "chunk_tc.cuh"
 
 namespace sfa {
@@ -22,7 +26,7 @@ namespace chunk {
 namespace {
 
 constexpr int kT = 128;
-constexpr int kThreads = 352;
+constexpr int kThreads = 608;
 
 template <int D, bool VK>
 struct Narrow {
@@ -33,7 +37,8 @@ struct Narrow {
     static constexpr int kOffQ = 0;                            // two row tiles
     static constexpr int kOffK = 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kKS * kTileBytes;
-    static constexpr int kOffItem = kOffV + kVS * kTileBytes;
+    static constexpr int kOffMax = kOffV + kVS * kTileBytes;   // float [2][256]
+    static constexpr int kOffItem = kOffMax + 2 * 256 * 4;
     static constexpr int kOffBar = kOffItem + 64;
     static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 2 + 2 + 2 + 1;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
@@ -70,6 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using L = Narrow<D, VK>;
     constexpr int KS = L::kKS, VS = L::kVS;
     extern __shared__ __align__(1024) uint8_t smem[];
+    float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
     Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
@@ -84,11 +90,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the barriers and tensor memory need nothing from global memory: they overlap the search
     if (tid == 0) {
         const int ip = (int)(b_p - bar0) / 8;
-        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip || i == ip + 1 ? 4 : 1);   // P: four warps
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip || i == ip + 1 ? 8 : 1);   // P: eight warps
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 10) {
+    if (warp == 18) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -103,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;   // S / P: 2 x 128 columns, O: 2 x D
     auto leave = [&]() {
-        if (warp == 10) tmem_dealloc(tmem, 512);
+        if (warp == 18) tmem_dealloc(tmem, 512);
     };
     const Item it = *sItem;
     if (it.seq < 0) return leave();
@@ -119,21 +125,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = p.G;
     const bool two = nq > qpt;                                // the second row tile has rows
 
-    // a softmax thread's row: query ql of row tile w, head h
-    const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+    // a softmax thread's row: query ql of row tile w, head h; kg: its half of the keys and dims
+    const int w = warp >> 3, kg = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const int ql = row / G, h = row - ql * G;
-    const bool live = warp < 8 && ql < qpt && w * qpt + ql < nq;
+    const bool live = warp < 16 && ql < qpt && w * qpt + ql < nq;
     const int64_t orow = (int64_t)(it.q.c0 + q0 + w * qpt + ql) * p.h_q + g * G + h;
 
     if (n_tiles == 0) {   // nothing to attend: zeros
         if (live) {
-            for (int d = 0; d < D; d += 4) {
+            for (int d = kg * (D / 2); d < (kg + 1) * (D / 2); d += 4) {
                 if (p.o_bf16)
                     *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * D + d) = make_uint2(0, 0);
                 else
                     *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (p.lse) p.lse[orow] = -INFINITY;
+            if (kg == 0 && p.lse) p.lse[orow] = -INFINITY;
         }
         return leave();
     }
@@ -150,9 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
 
-    if (warp == 8 || (warp == 9 && !VK)) {
+    if (warp == 16 || (warp == 17 && !VK)) {
         // --------------------------------------------------------------------------------- loads
-        const bool is_k = warp == 8;
+        const bool is_k = warp == 16;
         if (is_k && elect_one()) {
             for (int i = 0; i < (two ? 2 : 1); ++i) {
                 mbar_arrive_expect_tx(bars + i, (uint32_t)(L::kSlabs * 128 * qpt * G));
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 par ^= 1;
             }
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ------------------------------------------------------------------------------ products
         if (elect_one()) {
             const uint32_t idS = idesc_bf16_f32(128, 128);
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < (HL ? 2 : 1); ++x)
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + 256 + i * D, tmem + i * 128 + x * 64 + kk * 8,
+                        mma_ts(tmem + 256 + i * D, tmem + i * 128 + (kk >> 2) * 64 + x * 32 + (kk & 3) * 8,
                                dV + (uint64_t)((s * L::kTileBytes + kk * 2048) >> 4), idPV,
                                (!first || x > 0 || kk > 0) ? 1u : 0u);
             };
@@ -267,80 +273,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 8 && (w == 0 || two)) {
+    } else if (warp < 16 && (w == 0 || two)) {
         // -------------------------------------------------------------------------------- softmax
         const int pos = pos0 + w * qpt + ql;                  // the row's last key
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + w * 128 + lane_addr, tO = tmem + 256 + w * D + lane_addr;
+        // the thread's 64 columns of S; its weights take their place: 32 columns, and 32 for lo
+        const uint32_t tS = tmem + w * 128 + kg * 64 + lane_addr, tO = tmem + 256 + w * D + kg * (D / 2) + lane_addr;
         const bool neg = p.scale_log2 < 0.f;
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);  // a zero scale: weights of 1 to 1e-28
-        float m = -INFINITY, l = 0.f;                         // base 2
+        const float sgn = neg ? -sc : sc;
+        float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
+        float *mine = sMax + tid, *other = sMax + (tid ^ 128);
+        const int kq = k0 + kg * 64;                          // the thread's first key
         auto read_entry = [&](int key) { return key < k1 ? __ldg(table + p.page_div.div(key)) : 0; };
-        int entry[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) entry[x] = read_entry(k0 + 32 * x + lane);
+        int entry[2] = {read_entry(kq + lane), read_entry(kq + 32 + lane)};
         for (int t = 0; t < n_tiles; ++t) {
-            const int kb = k0 + t * kT;
-            uint32_t cells[4];   // bit j of word x: key kb + 32 x + j has a cell
-            bool all = true;
+            const int kb = kq + t * kT;
+            uint32_t cells[2];   // bit j of word x: key kb + 32 x + j has a cell
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 const bool cell = kb + 32 * x + lane >= k1 || (entry[x] >= 0 && entry[x] < p.n_pages);
                 if (!cell) set_status(p.status, SFA_DEV_BAD_CELL);
                 cells[x] = __ballot_sync(0xFFFFFFFFu, cell);
-                all = all && cells[x] == 0xFFFFFFFFu;
                 entry[x] = read_entry(kb + kT + 32 * x + lane);
             }
             const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
+            const bool masked = last < 63 || (cells[0] & cells[1]) != 0xFFFFFFFFu;
             wait(b_s + 8 * w, t & 1);
             tc_fence_after();
-            float s[128];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t r[32];
-                tmem_ld32(tS + 32 * x, r);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) s[32 * x + j] = __uint_as_float(r[j]);
-            }
+            uint32_t r[2][32];
+            tmem_ld32(tS, r[0]);
+            tmem_ld32(tS + 32, r[1]);
             tmem_ld_wait();
-            if (neg) {
+            if (masked) {
 #pragma unroll
-                for (int j = 0; j < 128; ++j) s[j] = -s[j];
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (32 * x + j > last || !((cells[x] >> j) & 1)) r[x][j] = neg ? 0x7F800000u : 0xFF800000u;
             }
-            if (last < 127 || !all) {
+            float mx[4];
+            {   // of the scores times the scale's sign
+                float hi[4], lo[4];
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j > last || !((cells[j >> 5] >> (j & 31)) & 1)) s[j] = -INFINITY;
+                for (int j = 0; j < 4; ++j) hi[j] = lo[j] = __uint_as_float(r[0][j]);
+                if (neg) {
+#pragma unroll
+                    for (int j = 4; j < 64; ++j) lo[j & 3] = fminf(lo[j & 3], __uint_as_float(r[j >> 5][j & 31]));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = -lo[j];
+                } else {
+#pragma unroll
+                    for (int j = 4; j < 64; ++j) hi[j & 3] = fmaxf(hi[j & 3], __uint_as_float(r[j >> 5][j & 31]));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = hi[j];
+                }
             }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
-            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // S(t + 1) waits for every thread's weights of t: no maximum is overwritten unread
+            *mine = mx[0];
+            named_barrier(1 + w, 256);
+            mx[0] = fmaxf(mx[0], *other) * sc;
             float alpha = 1.f;
             if (mx[0] > m + kLazy || (m == -INFINITY && mx[0] > m)) {
                 alpha = ex2(m - mx[0]);
                 m = mx[0];
             }
             const float mm = m == -INFINITY ? 0.f : m;
-            // S(t) is committed behind P V (t - 1): O can be rescaled
-            if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-#pragma unroll 1
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t r[32];
-                    tmem_ld32(tO + 32 * x, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-                    tmem_st32(tO + 32 * x, r);
-                }
-            }
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 uint32_t hi[16], lo[HL ? 16 : 1];
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    const float e0 = ex2(fmaf(s[32 * x + j], sc, -mm)), e1 = ex2(fmaf(s[32 * x + j + 1], sc, -mm));
+                    const float e0 = ex2(fmaf(__uint_as_float(r[x][j]), sgn, -mm)),
+                                e1 = ex2(fmaf(__uint_as_float(r[x][j + 1]), sgn, -mm));
                     sum[j & 2] += e0;
                     sum[(j & 2) + 1] += e1;
                     hi[j / 2] = pack_bf16(e0, e1);
@@ -349,7 +356,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               e1 - __uint_as_float(hi[j / 2] & 0xFFFF0000u));
                 }
                 tmem_st16(tS + 16 * x, hi);
-                if constexpr (HL) tmem_st16(tS + 64 + 16 * x, lo);
+                if constexpr (HL) tmem_st16(tS + 32 + 16 * x, lo);
+            }
+            // S(t) is committed behind P V (t - 1): O can be rescaled
+            if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll 1
+                for (int x = 0; x < D / 64; ++x) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * x, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                    tmem_st32(tO + 32 * x, o);
+                }
             }
             tmem_st_wait();
             tc_fence_before();
@@ -359,6 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // --------------------------------------------------------------------------------- result
         wait(b_o + 8 * w, 0);
+        *mine = l;   // every maximum was read: the last weights are used up
+        named_barrier(1 + w, 256);
+        l += *other;
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         if (ok) {
@@ -366,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
             const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
                                  (w * qpt + ql) * G + h;
-            store_tile<D, D>(p, sK + warp * (D * 128), tO, inv, live, whole ? orow : part, whole, 0);
-            if (live) {
+            store_tile<D / 2, D>(p, sK + warp * (D * 64), tO, inv, live, whole ? orow : part, whole, kg * (D / 2));
+            if (live && kg == 0) {
                 if (!whole) {
                     p.part_ml[part * 2] = m;
                     p.part_ml[part * 2 + 1] = l;
@@ -389,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_after();
     __syncwarp();
-    if (warp == 10) tmem_dealloc(tmem, 512);
+    if (warp == 18) tmem_dealloc(tmem, 512);
 }
 
 template <int D, bool VK, bool HL>
