@@ -236,47 +236,99 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
 }
 
 // ----------------------------------------------------------------------------- split merge
-// One CTA per (row tile, KV head, 8 rows), a warp per row: the pieces' (m, l) first, then their
-// weighted partial rows, 16 bytes a lane.  Lists of one piece were written by the attention
-// kernel itself.
-template <int DV>
+// The rows of the lists that were cut: a warp for a row, four in turn (32 to a CTA), or, where a list may have
+// many pieces, eight warps for one, each with every eighth piece, summed in the warps' order.  Lane c
+// holds where piece c, c + 32, .. left its partial results and the row's (m, l) there.  The kernel is
+// a chain of latencies (the list, then its partial results), so the first pieces' rows are asked
+// for before the weights are known, 16 bytes a lane.  Lists of one piece were written by the
+// attention kernel itself.
+constexpr int kMaxPieces = 160;   // of a list
+constexpr int kManyPieces = 8;    // from here on eight warps for a row
+
+template <int DV, int WPR>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
-    __shared__ Item s_item;
+    constexpr int W = kMaxPieces / 32, C = (DV + 127) / 128, ROWS = WPR == 8 ? 1 : 32, B = 4;
+    __shared__ float s_acc[WPR == 8 ? 8 : 1][WPR == 8 ? DV : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = blockIdx.y;
+    const int row0 = blockIdx.z * ROWS + (WPR == 8 ? 0 : warp), first = WPR == 8 ? warp : 0;
     pdl_wait();
-    if (warp == 0) {
-        const Item it = find_item(p, blockIdx.x, false);
-        if (lane == 0) s_item = it;
-    }
-    __syncthreads();
-    const Item it = s_item;
-    if (it.seq < 0) return;
-    const int n = min(it.q.n, p.n_new_max);
-    int rows, q0, r0;   // rows of the tile; its first query, or its first flattened row
-    if (p.item_q > 0) {
-        q0 = it.tile * p.item_q;
-        r0 = q0 * p.G;
-        rows = min(p.item_q, n - q0) * p.G;
+    // the list: its rows, and the row tile of partial results of each piece (-1: none)
+    int rows, r0, c0, g, n_pieces;
+    int part[W];
+#pragma unroll
+    for (int x = 0; x < W; ++x) part[x] = -1;
+    if (p.slots > 0) {   // the work was dealt out: the list that slot blockIdx.x has the start of
+        const int c = blockIdx.x;
+        const int4 start = p.slot_info[2 * c + 1];
+        rows = start.z * p.G;
+        if (!start.x || row0 >= rows) return;
+        n_pieces = 0;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {   // lane 0: the start; lane l: the slot l behind it
+            if (n_pieces != 32 * x) break;   // ended
+            const int d = c + lane + 32 * x;
+            const int4 head = d > c && d < p.slots ? p.slot_info[2 * d] : make_int4(0, d >= p.slots, 0, 0);
+            const unsigned ends = __ballot_sync(0xFFFFFFFFu, head.y != 0);
+            n_pieces += ends ? __ffs(ends) : 32;
+            if (d == c) part[x] = 2 * c + 1;
+            else if (head.x && lane + 32 * x < n_pieces) part[x] = 2 * d;
+        }
+        r0 = 0;
+        c0 = start.y;
+        g = start.w;
     } else {
-        r0 = it.tile * p.item_rows;
-        rows = min(p.item_rows, (int)((int64_t)n * p.G - r0));
+        g = blockIdx.y;
+        const Item it = find_item(p, blockIdx.x, false);
+        if (it.seq < 0) return;
+        const int n = min(it.q.n, p.n_new_max);
+        if (p.item_q > 0) {
+            const int q0 = it.tile * p.item_q;
+            r0 = q0 * p.G;
+            rows = min(p.item_q, n - q0) * p.G;
+        } else {
+            r0 = it.tile * p.item_rows;
+            rows = min(p.item_rows, (int)((int64_t)n * p.G - r0));
+        }
+        if (row0 >= rows) return;
+        const int p_last = it.q.total - it.q.n + (r0 + rows - 1) / p.G;
+        const int len = max(0, min(key_limit(p, it.q), p_last + 1));
+        if (len <= p.split_keys) return;
+        n_pieces = (len + p.split_keys - 1) / p.split_keys;
+#pragma unroll
+        for (int x = 0; x < W; ++x)
+            if (lane + 32 * x < n_pieces) part[x] = (blockIdx.x * p.h_kv + g) * p.n_split + lane + 32 * x;
+        c0 = it.q.c0;
     }
-    const int row = blockIdx.z * 8 + warp;
-    if (row >= rows) return;
-    const int p_last = it.q.total - it.q.n + (r0 + rows - 1) / p.G;
-    const int len = max(0, min(key_limit(p, it.q), p_last + 1));
-    if (len <= p.split_keys) return;
-    const int ns = (len + p.split_keys - 1) / p.split_keys;
-    const int64_t part0 = ((int64_t)blockIdx.x * p.h_kv + g) * p.n_split * p.item_rows + row;
-    // lane c holds (m, l) of piece c, c + 32, ..
-    constexpr int W = 4;            // 128 pieces at most
+    // B of this warp's pieces from piece c on
+    auto where = [&](int c) {
+        int at = -1;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+            const int v = __shfl_sync(0xFFFFFFFFu, part[x], c & 31);
+            if (c >> 5 == x) at = v;
+        }
+        return at;
+    };
+    auto load = [&](int row, int c, float4 (&v)[B][C]) {
+#pragma unroll
+        for (int y = 0; y < B; ++y) {
+            const int at = where(c + y * WPR);
+            const float *src = p.part_o + ((int64_t)max(at, 0) * p.item_rows + row) * DV + lane * 4;
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                v[y][k] = at >= 0 && k * 128 + lane * 4 < DV ? *reinterpret_cast<const float4 *>(src + k * 128)
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+#pragma unroll 1
+    for (int row = row0; row < min(rows, (int)(blockIdx.z + 1) * ROWS); row += 8) {
+    float4 v[B][C];
+    load(row, first, v);
     float m[W], w[W], M = -INFINITY, l = 0.f;
 #pragma unroll
     for (int x = 0; x < W; ++x) {
-        const int c = lane + 32 * x;
-        const float2 ml = c < ns ? *reinterpret_cast<const float2 *>(p.part_ml + (part0 + (int64_t)c * p.item_rows) * 2)
-                                 : make_float2(-INFINITY, 0.f);
+        const float2 ml = part[x] >= 0 ? *reinterpret_cast<const float2 *>(p.part_ml + ((int64_t)part[x] * p.item_rows + row) * 2)
+                                       : make_float2(-INFINITY, 0.f);
         m[x] = ml.x;
         w[x] = ml.y;
         M = fmaxf(M, m[x]);
@@ -286,49 +338,71 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 #pragma unroll
     for (int x = 0; x < W; ++x) {   // the piece's share of the sum, then its weight
         const float e = m[x] == -INFINITY ? 0.f : exp2f(m[x] - M);
-        l += w[x] == 0.f ? 0.f : e * w[x];
+        l += w[x] == 0.f ? 0.f : (m[x] == -INFINITY ? w[x] : e * w[x]);
         w[x] = e;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    constexpr int C = (DV + 127) / 128;
     float4 acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = first; c < n_pieces; c += B * WPR) {
+        if (c != first) load(row, c, v);
 #pragma unroll
-    for (int x = 0; x < W; ++x) {
-        if (32 * x >= ns) break;
-#pragma unroll 4
-        for (int c = 32 * x; c < min(ns, 32 * x + 32); ++c) {
-            const float e = __shfl_sync(0xFFFFFFFFu, w[x], c & 31);
-            const float *src = p.part_o + (part0 + (int64_t)c * p.item_rows) * DV + lane * 4;
+        for (int y = 0; y < B; ++y) {
+            const int cy = c + y * WPR;
+            float e = 0.f;
+#pragma unroll
+            for (int x = 0; x < W; ++x) {
+                const float f = __shfl_sync(0xFFFFFFFFu, w[x], cy & 31);
+                if (cy >> 5 == x) e = f;
+            }
 #pragma unroll
             for (int k = 0; k < C; ++k) {
-                if (k * 128 + lane * 4 < DV) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + k * 128);
-                    acc[k].x = fmaf(e, v.x, acc[k].x);
-                    acc[k].y = fmaf(e, v.y, acc[k].y);
-                    acc[k].z = fmaf(e, v.z, acc[k].z);
-                    acc[k].w = fmaf(e, v.w, acc[k].w);
-                }
+                acc[k].x = fmaf(e, v[y][k].x, acc[k].x);
+                acc[k].y = fmaf(e, v[y][k].y, acc[k].y);
+                acc[k].z = fmaf(e, v[y][k].z, acc[k].z);
+                acc[k].w = fmaf(e, v[y][k].w, acc[k].w);
             }
         }
     }
     const bool any = l > 0.f || l != l;
     const float inv = any ? 1.f / l : 0.f;
-    const int64_t o = (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
+    const int64_t o = (int64_t)(c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
+    if (lane == 0 && first == 0 && p.lse) p.lse[o] = any ? (M + log2f(l)) / kLog2e : -INFINITY;
+    if constexpr (WPR == 8) {
 #pragma unroll
-    for (int k = 0; k < C; ++k)
-        if (k * 128 + lane * 4 < DV)
-            store4(p, o, DV, k * 128 + lane * 4, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
-    if (lane == 0 && p.lse) p.lse[o] = any ? (M + log2f(l)) / kLog2e : -INFINITY;
+        for (int k = 0; k < C; ++k)
+            if (k * 128 + lane * 4 < DV) *reinterpret_cast<float4 *>(&s_acc[warp][k * 128 + lane * 4]) = acc[k];
+        __syncthreads();
+        for (int d = 4 * threadIdx.x; d < DV; d += 4 * 256) {
+            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const float4 q = *reinterpret_cast<const float4 *>(&s_acc[y][d]);
+                t.x += q.x;
+                t.y += q.y;
+                t.z += q.z;
+                t.w += q.w;
+            }
+            store4(p, o, DV, d, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+            if (k * 128 + lane * 4 < DV)
+                store4(p, o, DV, k * 128 + lane * 4, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+    }
+    }
 }
 
 // --------------------------------------------------------------------------------- the plan
 enum Kernel { kSimt, kWide, kNarrow };
 struct Plan {
     Kernel kernel;
-    int item_rows, item_q, items, n_split, split_keys;
+    int item_rows, item_q, items;
+    int slots;                 // > 0: the work dealt out evenly (Share)
+    int n_split, split_keys;   // else: pieces of a list
 };
 
 // Row tiles of n_q queries in n_seq chunks of at most n_new_max, at most.
@@ -339,11 +413,16 @@ int64_t items_bound(int n_seq, int n_q, int G, int n_new_max, int item_rows, int
     return per * n_seq < all ? per * n_seq : all;
 }
 
-// The kernel, and into how many equal pieces the longest list is cut: the number with the least
-// modelled time, waves of pieces (a key tile, and the start and end of a piece) plus the merge
-// (its launch and the partial results' way through memory).
-Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new_max,
-               int64_t n_kv_max, int64_t n_cells, bool o_bf16) {
+// The kernel, and how the lists are spread over the SMs: each whole or in equal pieces, a CTA
+// (pair) for one, or, by the narrow heads' kernel, all of them dealt out evenly.  What the model
+// says takes least time:
+//   whole or cut:  waves of pieces (their key tiles, a piece's start and end), and the merge;
+//   dealt out:     the tiles' share of a slot, its pieces' starts and ends, and the merge.
+// (The wide kernel's pairs would, dealt out, read a cache at 76 places at a time, 147 KB in 1.4 us
+// each: more than DRAM has where row tiles share a cache larger than L2.  As one loop over pieces it
+// also ran 6% slower at 2048 tokens behind 131072.)
+Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new_max, int64_t n_kv_max,
+               int64_t n_cells, bool o_bf16) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
     pl.kernel = wide ? kWide : tc ? kNarrow : kSimt;
@@ -352,19 +431,20 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
     pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
     const int tile = 128;
-    const int64_t tiles = (n_kv_max + tile - 1) / tile;
-    const double slots = wide ? device_sm_count() / 2 : device_sm_count();
-    const double t_tile = tc ? (o_bf16 ? 1.4 : 2.1) : dv == 512 ? 30. : 8.;   // us
-    const double t_piece = 6., t_merge = 4.;
-    const double part_us = (double)pl.item_rows * dv * 4 * 2 / 4e6;             // a partial, both ways
-    const int64_t units = items * h_kv;
+    const int64_t tiles = n_kv_max > 0 ? (n_kv_max + tile - 1) / tile : 1, units = items * h_kv;
+    int64_t slots = wide ? device_sm_count() / 2 : device_sm_count();
+    if (slots > kMaxPieces) slots = kMaxPieces;
+    // us: a tile, a piece's start and end in a launch of its own and behind another one, the merge
+    const double t_tile = wide ? (o_bf16 ? 1.35 : 2.) : tc ? (o_bf16 ? 1.8 : 2.4) : dv == 512 ? 30. : 8.;
+    const double t_piece = 7., t_next = 4., t_merge = 6.;
+    const double part_us = (double)pl.item_rows * dv * 4 * 2 / 4e6;   // a partial, both ways
     int64_t best = 1;
     double best_us = 0;
     for (int64_t ns = 1; ns <= tiles && ns <= 128; ++ns) {
         const int64_t per = (tiles + ns - 1) / ns;
         if (ns > 1 && (tiles + per - 1) / per != ns) continue;
         if (ns > 1 && (double)units * ns * pl.item_rows * (dv + 2) * 4 > 1e9) break;
-        const int64_t waves = (int64_t)((units * ns + slots - 1) / slots);
+        const int64_t waves = (units * ns + slots - 1) / slots;
         const double us = waves * (per * t_tile + t_piece) + (ns > 1 ? t_merge + units * ns * part_us : 0.);
         if (ns == 1 || us < best_us) {
             best = ns;
@@ -374,12 +454,25 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     const int64_t per = (tiles + best - 1) / best;
     pl.split_keys = best > 1 ? (int)(per * tile) : 0x7FFFFF80;
     pl.n_split = (int)best;
+    pl.slots = 0;
+    if (pl.kernel == kNarrow && units > 0) {
+        // four tiles a slot at least: shorter pieces cost the merge more than they gain
+        const int64_t few = (units * tiles + 3) / 4, ss = few < slots ? few : slots;
+        // lists shorter than their bound leave whole ones' SMs idle, dealt out ones' not
+        const bool ragged = n_q < (int64_t)n_seq * n_new_max;
+        const double us = (double)units * tiles / ss * t_tile * (ragged ? 0.7 : 1.) + t_piece +
+                          (double)units / ss * t_next + (ss > 1 ? t_merge : 0.);
+        if (us < best_us) pl.slots = (int)ss;
+    }
     return pl;
 }
 
+// Row tiles of partial results: each DV values and (m, l) a row; behind them the slots' own notes.
+size_t plan_parts(const Plan &pl, int h_kv) {
+    return pl.slots > 0 ? 2 * (size_t)pl.slots : pl.n_split > 1 ? (size_t)pl.items * h_kv * pl.n_split : 0;
+}
 size_t plan_workspace(const Plan &pl, int h_kv, int dv) {
-    if (pl.n_split == 1) return 0;
-    return (size_t)pl.items * h_kv * pl.n_split * pl.item_rows * ((size_t)dv + 2) * sizeof(float);
+    return plan_parts(pl, h_kv) * pl.item_rows * ((size_t)dv + 2) * sizeof(float) + 2 * (size_t)pl.slots * sizeof(int4);
 }
 
 bool shape_ok(int dkq, int dv, bool has_v) {
@@ -400,8 +493,11 @@ int launch_simt(const Params &p, int dtype, cudaStream_t st) {
 
 template <int DV>
 int launch_combine(const Params &p, cudaStream_t st) {
-    if (launch_pdl(chunk_combine_kernel<DV>, dim3(p.items, p.h_kv, (p.item_rows + 7) / 8), dim3(256),
-                   0, st, p) != cudaSuccess) {
+    const bool many = p.slots == 0 && p.n_split >= kManyPieces;
+    const unsigned z = many ? p.item_rows : (p.item_rows + 31) / 32;
+    if (launch_pdl(many ? chunk_combine_kernel<DV, 8> : chunk_combine_kernel<DV, 1>,
+                   p.slots > 0 ? dim3(p.slots, 1, z) : dim3(p.items, p.h_kv, z), dim3(256), 0, st,
+                   p) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
@@ -472,7 +568,11 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.O = O;
     p.lse = lse;
     p.part_o = reinterpret_cast<float *>(workspace);
-    p.part_ml = need > 0 ? p.part_o + (size_t)pl.items * h_kv * pl.n_split * pl.item_rows * dv : nullptr;
+    if (need > 0) {
+        const size_t rows = plan_parts(pl, h_kv) * pl.item_rows;
+        p.part_ml = p.part_o + rows * dv;
+        p.slot_info = reinterpret_cast<int4 *>(p.part_ml + rows * 2);
+    }
     p.status = dev_status;
     p.table_stride = table_stride;
     p.page = page_size;
@@ -487,6 +587,7 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.items = pl.items;
     p.item_rows = pl.item_rows;
     p.item_q = pl.item_q;
+    p.slots = pl.slots;
     p.n_split = pl.n_split;
     p.split_keys = pl.split_keys;
     p.n_new_max = n_new_max;
@@ -500,6 +601,6 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     else if (dkq == 512) r = V ? launch_simt<512, 512, false>(p, dtype, st) : launch_simt<512, 512, true>(p, dtype, st);
     else if (dkq == 128) r = V ? launch_simt<128, 128, false>(p, dtype, st) : launch_simt<128, 128, true>(p, dtype, st);
     else r = V ? launch_simt<64, 64, false>(p, dtype, st) : launch_simt<64, 64, true>(p, dtype, st);
-    if (r != SFA_OK || pl.n_split == 1) return r;
+    if (r != SFA_OK || need == 0 || pl.slots == 1) return r;
     return dv == 512 ? launch_combine<512>(p, st) : dv == 128 ? launch_combine<128>(p, st) : launch_combine<64>(p, st);
 }

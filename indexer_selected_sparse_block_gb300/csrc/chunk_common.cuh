@@ -19,6 +19,7 @@ struct Params {
     const int32_t *table, *cu, *total;
     void *O;
     float *lse, *part_o, *part_ml;
+    int4 *slot_info;     // [slots][2], see Share
     int32_t *status;
     int64_t table_stride;
     FastDiv page_div;
@@ -27,6 +28,8 @@ struct Params {
     int items;           // row tiles of all sequences, at most
     int item_rows;       // rows of a tile
     int item_q;          // queries of a tile, 0: tiles cut the flattened rows anywhere
+    int slots;           // > 0: the work is dealt out evenly to this many CTAs, see Share;
+                         // 0: a CTA (pair) for each item, KV head and piece of n_split
     int n_split;         // pieces a list is cut into, at most
     int split_keys;      // keys of a piece
     int n_new_max;       // the caller's bound on a chunk's length
@@ -127,6 +130,195 @@ __device__ __forceinline__ int64_t cell_of(const Params &p, int s, int t) {
         return -1;
     }
     return (int64_t)e * p.page + (t - pg * p.page);
+}
+
+// A piece of work of the narrow heads' kernel: keys k0 .. k1 - 1 of the list of one row tile (nq
+// queries from q0 on, the first at position pos0) and KV head.  n_tiles 0 with whole: a list of no key.
+struct Piece {
+    int seq, c0, q0, nq, pos0, g, len, k0, k1;
+    int part;    // where its partial results go, in row tiles; -1: the piece is the whole list
+    int state;   // kRun, kSkip (nothing to do), kEnd (no further piece)
+    int head, ends;   // of a slot's share: the list began in an earlier slot; it ends in this one
+};
+enum { kRun, kSkip, kEnd };
+
+__device__ __forceinline__ void piece_rows(const Params &p, const Seq &q, int tile, Piece &w) {
+    w.c0 = q.c0;
+    w.q0 = tile * p.item_q;
+    w.nq = min(p.item_q, min(q.n, p.n_new_max) - w.q0);
+    w.pos0 = q.total - q.n + w.q0;
+    w.len = max(0, min(key_limit(p, q), w.pos0 + w.nq));
+}
+// One piece a CTA: `split` of item and KV head g; by a whole warp.
+__device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int split, bool flag) {
+    Piece w;
+    w.state = kEnd;
+    const Item it = find_item(p, item, flag);
+    if (it.seq < 0) return w;
+    w.seq = it.seq;
+    w.g = g;
+    piece_rows(p, it.q, it.tile, w);
+    w.k0 = (int)min((int64_t)w.len, (int64_t)split * p.split_keys);
+    w.k1 = (int)min((int64_t)w.len, (int64_t)w.k0 + p.split_keys);
+    w.part = w.len <= p.split_keys ? -1 : ((item * p.h_kv + g) * p.n_split + split);
+    w.state = split > 0 && w.k0 >= w.k1 ? kEnd : kRun;
+    return w;
+}
+
+// The work dealt out evenly.  Every row tile and KV head weighs as many keys as its list has, and
+// kPieceKeys more for the start and end of a piece (about 6 us; without them slots with ten short
+// lists took 156 us where the others took 100); in a line, sequence by sequence, KV head by KV head, row tile by row tile, the weights sum up to W, and
+// slot c takes the keys from c W / slots to (c + 1) W / slots: whole lists, and at each end perhaps
+// a part of one, cut on tile borders.  A slot then has at most two partial results, one that starts
+// inside a list (2 c) and one that ends inside one (2 c + 1), however long the lists are.
+// Of a border among those last keys the list is whole before it.
+// For the merge a slot says in slot_info of its partial results, [c][0] = (written, the list ends
+// here) for the one that starts inside a list, [c][1] = (written, first query, queries, KV head) for
+// the one that is a list's start: the pieces of that list are it and the following slots' [0], up to
+// the one where the list ends.
+// The weights of a sequence's row tiles grow by item_q from one to the next, so their sums have a
+// closed form and a place in the line is found without a pass over the tiles.
+constexpr int kPieceKeys = 448;
+struct Unit {
+    int seq, tile, g, w;
+    int64_t u0;           // its place in the line
+    Seq q;
+};
+// One sequence's part of the line, a lane's of a group of 32.
+struct SeqWork {
+    Seq q;
+    int n, tiles;
+    int64_t a, head, upto;   // head: the weights of one KV head; upto: all of the group's, to this lane
+};
+struct Share {
+    int64_t W, per, rem;     // all of the work, W / slots and what is left over
+    int64_t at, end;         // of this slot
+    SeqWork group;           // of the first 32 sequences
+};
+// Where slot c begins: the first rem slots have a key more than the others.
+__device__ __forceinline__ int64_t share_border(const Share &h, int c) {
+    return h.per * c + min((int64_t)c, h.rem);
+}
+// Sum of the weights of the first j row tiles of a sequence with n new tokens behind a cached ones
+// (j at most their number; the last one may be short).
+__device__ __forceinline__ int64_t tile_weights(const Params &p, int64_t a, int n, int tiles, int64_t j) {
+    const int64_t full = j < tiles ? j : tiles - 1;
+    return full * a + p.item_q * (full * (full + 1) / 2) + (j < tiles ? 0 : a + n) + j * kPieceKeys;
+}
+// By one whole warp, as all of the following.
+__device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) {
+    const int lane = threadIdx.x & 31, s = s0 + lane;
+    SeqWork v;
+    v.q = Seq{0, 0, 0};
+    if (s < p.n_seq) v.q = load_seq(p, s, flag);
+    v.n = min(v.q.n, p.n_new_max);
+    v.tiles = n_items(p, v.q.n);
+    v.a = max(v.q.total - v.q.n, 0);
+    v.head = v.n > 0 ? tile_weights(p, v.a, v.n, v.tiles, v.tiles) : 0;
+    v.upto = v.head * p.h_kv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, v.upto, o);
+        if (lane >= o) v.upto += y;
+    }
+    return v;
+}
+__device__ __forceinline__ Share share_of(const Params &p, bool flag) {
+    Share h;
+    h.group = seq_work(p, 0, flag);
+    h.W = __shfl_sync(0xFFFFFFFFu, h.group.upto, 31);
+    for (int s0 = 32; s0 < p.n_seq; s0 += 32) {
+        const SeqWork v = seq_work(p, s0, flag);
+        h.W += __shfl_sync(0xFFFFFFFFu, v.upto, 31);
+    }
+    h.per = h.W / p.slots;
+    h.rem = h.W - h.per * p.slots;
+    h.at = h.end = 0;
+    return h;
+}
+// The unit at place x < W of the line.
+__device__ __forceinline__ Unit share_unit(const Params &p, const Share &h, int64_t x) {
+    int64_t before = 0;
+    SeqWork v = h.group;
+    int s0 = 0;
+    unsigned in = __ballot_sync(0xFFFFFFFFu, x < v.upto);
+    while (!in && s0 + 32 < p.n_seq) {
+        before += __shfl_sync(0xFFFFFFFFu, v.upto, 31);
+        s0 += 32;
+        v = seq_work(p, s0, false);
+        in = __ballot_sync(0xFFFFFFFFu, x < before + v.upto);
+    }
+    const int l = in ? __ffs(in) - 1 : 31;
+    Unit u;
+    u.seq = s0 + l;
+    u.q.c0 = __shfl_sync(0xFFFFFFFFu, v.q.c0, l);
+    u.q.n = __shfl_sync(0xFFFFFFFFu, v.q.n, l);
+    u.q.total = __shfl_sync(0xFFFFFFFFu, v.q.total, l);
+    const int64_t head = __shfl_sync(0xFFFFFFFFu, v.head, l), a = __shfl_sync(0xFFFFFFFFu, v.a, l);
+    const int n = __shfl_sync(0xFFFFFFFFu, v.n, l), tiles = __shfl_sync(0xFFFFFFFFu, v.tiles, l);
+    int64_t r = x - before - __shfl_sync(0xFFFFFFFFu, v.upto - v.head * p.h_kv, l);
+    u.g = 0;
+    if (p.h_kv > 1) {
+        u.g = (int)(r / head);
+        r -= u.g * head;
+    }
+    int lo = 0, hi = tiles - 1;   // the last tile whose weights begin at or before r
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (tile_weights(p, a, n, tiles, m) <= r) lo = m;
+        else hi = m - 1;
+    }
+    u.tile = lo;
+    u.w = (int)(a + min((int64_t)(lo + 1) * p.item_q, (int64_t)n)) + kPieceKeys;
+    u.u0 = x - r + tile_weights(p, a, n, tiles, lo);
+    return u;
+}
+// Keys [k0, k1) of a unit with a list of len that slot c has; by its borders alone, so that
+// neighbours and the merge agree.
+__device__ __forceinline__ void share_keys(const Share &h, int c, const Unit &u, int len, int &k0, int &k1) {
+    const int64_t a = share_border(h, c) - u.u0, b = share_border(h, c + 1) - u.u0;
+    k0 = a <= 0 ? 0 : (int)min((a + 64) & ~(int64_t)127, (int64_t)len);
+    k1 = b >= u.w ? len : (int)min((b + 64) & ~(int64_t)127, (int64_t)len);
+}
+// Slot c's next piece.
+__device__ __forceinline__ Piece share_next(const Params &p, int c, Share &h) {
+    Piece w;
+    w.state = kEnd;
+    if (h.at >= h.end) return w;
+    const Unit u = share_unit(p, h, h.at);
+    w.seq = u.seq;
+    w.g = u.g;
+    piece_rows(p, u.q, u.tile, w);
+    share_keys(h, c, u, w.len, w.k0, w.k1);
+    const bool first = u.u0 >= share_border(h, c);   // the list's start is this slot's
+    const bool all = w.k0 == 0 && w.k1 == w.len;
+    w.part = all ? -1 : 2 * c + (w.k0 > 0 ? 0 : 1);
+    w.state = w.k0 < w.k1 || (all && first) ? kRun : kSkip;
+    w.head = !first;
+    w.ends = u.u0 + u.w <= share_border(h, c + 1);
+    h.at = min(h.end, u.u0 + u.w);
+    return w;
+}
+// Slot c's piece from place `at` of the line on (at < 0: its first), and the place behind it.  The
+// sequences' sums are made anew each time: a warp that does nothing else has the time, and the
+// kernel's other warps keep the registers.
+static __device__ __noinline__ Piece share_piece(const Params &p, int c, int64_t &at, bool flag) {
+    const bool lead = (threadIdx.x & 31) == 0;
+    Share h = share_of(p, flag);
+    if (at < 0 && lead) {
+        p.slot_info[2 * c] = make_int4(0, 1, 0, 0);
+        p.slot_info[2 * c + 1] = make_int4(0, 0, 0, 0);
+    }
+    h.at = at < 0 ? share_border(h, c) : at;
+    h.end = share_border(h, c + 1);
+    const Piece w = share_next(p, c, h);
+    if (w.state != kEnd && lead) {
+        if (w.head) p.slot_info[2 * c] = make_int4(w.state == kRun && w.part == 2 * c, w.ends, 0, 0);
+        if (w.state == kRun && w.part == 2 * c + 1)
+            p.slot_info[2 * c + 1] = make_int4(1, w.c0 + w.q0, w.nq, w.g);
+    }
+    at = h.at;
+    return w;
 }
 
 // The kernel for 512 value dims on tcgen05 CTA pairs (chunk_wide.cu): queries of one CTA's 64

@@ -18,7 +18,8 @@
 //
 // Warps 0-7 and 8-15: softmax, correction and result of the two row tiles, the first four of each
 // for keys 0-63 of a tile and the lower half of the value dims; warp 16: Q and K; warp 17: V;
-// warp 18: products (one lane).  Pages as in chunk_wide.cu.
+// warp 18: products (one lane); warp 19: the next piece of work.  A CTA has one piece, or its even
+// share of all (Share in chunk_common.cuh), piece after piece.  Pages as in chunk_wide.cu.
 #include "chunk_tc.cuh"
 
 namespace sfa {
@@ -26,7 +27,7 @@ namespace chunk {
 namespace {
 
 constexpr int kT = 128;
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 
 template <int D, bool VK>
 struct Narrow {
@@ -38,11 +39,12 @@ struct Narrow {
     static constexpr int kOffK = 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kKS * kTileBytes;
     static constexpr int kOffMax = kOffV + kVS * kTileBytes;   // float [2][256]
-    static constexpr int kOffItem = kOffMax + 2 * 256 * 4;
-    static constexpr int kOffBar = kOffItem + 64;
+    static constexpr int kOffPiece = kOffMax + 2 * 256 * 4;    // Piece [2], 64 bytes each
+    static constexpr int kOffBar = kOffPiece + 128;
     static constexpr int kBars = 2 + 2 * kKS + 2 * kVS + 2 + 2 + 2 + 1;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
     static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+    static_assert(sizeof(Piece) <= 64, "fits its place");
     static_assert((kKS + kVS) * kTileBytes >= 8 * D * 128, "the result's way through shared memory");
 };
 
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KS = L::kKS, VS = L::kVS;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
-    Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
+    uint8_t *sPiece = smem + L::kOffPiece;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -86,8 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    b_drain = b_o + 16;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int item = blockIdx.x, g = blockIdx.y, split = blockIdx.z;
-    // the barriers and tensor memory need nothing from global memory: they overlap the search
+    // the barriers and tensor memory need nothing from global memory: they overlap the search for
+    // the first piece
     if (tid == 0) {
         const int ip = (int)(b_p - bar0) / 8;
         for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip || i == ip + 1 ? 8 : 1);   // P: eight warps
@@ -99,52 +101,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();
-    if (warp == 0) {
-        const Item it = find_item(p, item, blockIdx.x == 0 && g == 0 && split == 0);
-        if (lane == 0) *sItem = it;
+    int64_t share_at = -1;   // warp 19's place in the line of all work
+    if (warp == 19) {
+        Piece f;
+        if (p.slots > 0) {
+            f = share_piece(p, blockIdx.x, share_at, blockIdx.x == 0);
+        } else {
+            f = piece_of(p, blockIdx.x, blockIdx.y, blockIdx.z, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
+        }
+        if (lane == 0) *reinterpret_cast<Piece *>(sPiece) = f;
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;   // S / P: 2 x 128 columns, O: 2 x D
-    auto leave = [&]() {
-        if (warp == 18) tmem_dealloc(tmem, 512);
-    };
-    const Item it = *sItem;
-    if (it.seq < 0) return leave();
-    const int q0 = it.tile * p.item_q;                        // first query of the item
-    const int nq = min(p.item_q, min(it.q.n, p.n_new_max) - q0);
-    const int pos0 = it.q.total - it.q.n + q0;                // its position
-    const int len = max(0, min(key_limit(p, it.q), pos0 + nq));
-    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
-    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
-    if (split > 0 && k0 >= k1) return leave();                // no such piece
-    const bool whole = len <= p.split_keys;
-    const int n_tiles = (k1 - k0 + kT - 1) / kT;
+    const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sV = smem_u32(smem + L::kOffV);
     const int G = p.G;
-    const bool two = nq > qpt;                                // the second row tile has rows
-
     // a softmax thread's row: query ql of row tile w, head h; kg: its half of the keys and dims
     const int w = warp >> 3, kg = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const int ql = row / G, h = row - ql * G;
-    const bool live = warp < 16 && ql < qpt && w * qpt + ql < nq;
-    const int64_t orow = (int64_t)(it.q.c0 + q0 + w * qpt + ql) * p.h_q + g * G + h;
-
-    if (n_tiles == 0) {   // nothing to attend: zeros
-        if (live) {
-            for (int d = kg * (D / 2); d < (kg + 1) * (D / 2); d += 4) {
-                if (p.o_bf16)
-                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * D + d) = make_uint2(0, 0);
-                else
-                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            if (kg == 0 && p.lse) p.lse[orow] = -INFINITY;
-        }
-        return leave();
-    }
-
-    const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sV = smem_u32(smem + L::kOffV);
     // once a wait ran out no other is made
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -154,9 +130,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             set_status(p.status, SFA_DEV_TIMEOUT);
         }
     };
-    const int32_t *table = p.table + (int64_t)it.seq * p.table_stride;
+    // the barriers' phases: tiles so far, those of the second row tile, and the pieces of both
+    uint32_t u0 = 0, u1 = 0, np = 0, np2 = 0;
+    for (int i_piece = 0;; ++i_piece) {
+    const Piece pc = *reinterpret_cast<const Piece *>(sPiece + (i_piece & 1) * 64);
+    if (pc.state == kEnd || *abort_flag) break;
+    const int g = pc.g, k0 = pc.k0, k1 = pc.k1, pos0 = pc.pos0, nq = pc.nq;
+    const bool whole = pc.part < 0;
+    const int n_tiles = pc.state == kSkip ? 0 : (k1 - k0 + kT - 1) / kT;
+    const bool two = nq > qpt;                                // the second row tile has rows
+    const bool live = pc.state == kRun && warp < 16 && ql < qpt && w * qpt + ql < nq;
+    const int64_t orow = (int64_t)(pc.c0 + pc.q0 + w * qpt + ql) * p.h_q + g * G + h;
+    const int32_t *table = p.table + (int64_t)pc.seq * p.table_stride;
 
-    if (warp == 16 || (warp == 17 && !VK)) {
+    if (warp == 19) {
+        Piece f;
+        f.state = kEnd;
+        if (p.slots > 0) f = share_piece(p, blockIdx.x, share_at, false);
+        if (lane == 0) *reinterpret_cast<Piece *>(sPiece + ((i_piece + 1) & 1) * 64) = f;
+        __syncwarp();
+    } else if (n_tiles == 0) {
+        if (live) {   // nothing to attend: zeros
+            for (int d = kg * (D / 2); d < (kg + 1) * (D / 2); d += 4) {
+                if (p.o_bf16)
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * D + d) = make_uint2(0, 0);
+                else
+                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (kg == 0 && p.lse) p.lse[orow] = -INFINITY;
+        }
+    } else if (warp == 16 || (warp == 17 && !VK)) {
         // --------------------------------------------------------------------------------- loads
         const bool is_k = warp == 16;
         if (is_k && elect_one()) {
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(bars + i, (uint32_t)(L::kSlabs * 128 * qpt * G));
                 for (int d = 0; d < L::kSlabs; ++d)
                     tma1_load(sQ + i * L::kTileBytes + d * 16384, &maps.q, d * 64, g * G,
-                              it.q.c0 + q0 + i * qpt, b_q + 8 * i);
+                              pc.c0 + pc.q0 + i * qpt, b_q + 8 * i);
             }
         }
         __syncwarp();
@@ -174,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         HalfRows r[2];   // table entries read a tile ahead
 #pragma unroll
         for (int i = 0; i < 2; ++i) read_entries(r[i], p, table, k0 + i * 64, k1, bxs);
-        int s = 0;
-        uint32_t par = 1;
+        int s = u0 % S;
+        uint32_t par = ((u0 / S) & 1) ^ 1;
         for (int t = 0; t < n_tiles; ++t) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) find_rows(r[i], p, n_cells);
@@ -220,32 +223,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                (!first || x > 0 || kk > 0) ? 1u : 0u);
             };
             auto free_stage = [&](uint32_t empty, int s) { tc_commit(bars + (empty - bar0) / 8 + s); };
-            int ks = 0, vs = 0;            // stages of K (t + 1) and V (t); VK: of K (t + 1) and K (t)
-            uint32_t kp = 0, vp = 0;
+            int ks = u0 % KS, vs = u0 % (VK ? KS : VS);   // stages of K (t + 1) and V (t); VK: of K (t + 1) and K (t)
+            uint32_t kp = (u0 / KS) & 1, vp = (u0 / (VK ? KS : VS)) & 1;
             auto next_k = [&]() {
                 if (++ks == KS) {
                     ks = 0;
                     kp ^= 1;
                 }
             };
-            wait(b_q, 0);
-            wait(b_kFull, 0);
+            wait(b_q, np & 1);
+            wait(b_kFull + 8 * ks, kp);
             if (ok) {
                 tc_fence_after();
-                s_op(0, 0);
+                s_op(0, ks);
                 if (two) {
-                    wait(b_q + 8, 0);
+                    wait(b_q + 8, np2 & 1);
                     tc_fence_after();
-                    if (ok) s_op(1, 0);
+                    if (ok) s_op(1, ks);
                 }
-                if (!VK) free_stage(b_kEmpty, 0);
+                if (!VK) free_stage(b_kEmpty, ks);
             }
             next_k();
             for (int t = 0; t < n_tiles && ok; ++t) {
                 const bool more = t + 1 < n_tiles;
                 if (!VK) wait(b_vFull + 8 * vs, vp);
                 for (int i = 0; i < (two ? 2 : 1) && ok; ++i) {
-                    wait(b_p + 8 * i, t & 1);
+                    wait(b_p + 8 * i, ((i ? u1 : u0) + t) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     pv_op(i, vs, t == 0);
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
             const bool masked = last < 63 || (cells[0] & cells[1]) != 0xFFFFFFFFu;
-            wait(b_s + 8 * w, t & 1);
+            wait(b_s + 8 * w, ((w ? u1 : u0) + t) & 1);
             tc_fence_after();
             uint32_t r[2][32];
             tmem_ld32(tS, r[0]);
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
         // --------------------------------------------------------------------------------- result
-        wait(b_o + 8 * w, 0);
+        wait(b_o + 8 * w, np & 1);
         *mine = l;   // every maximum was read: the last weights are used up
         named_barrier(1 + w, 256);
         l += *other;
@@ -386,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
             const bool any = l > 0.f || l != l;
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
-            const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
-                                 (w * qpt + ql) * G + h;
+            const int64_t part = (int64_t)pc.part * p.item_rows + (w * qpt + ql) * G + h;
             store_tile<D / 2, D>(p, sK + warp * (D * 64), tO, inv, live, whole ? orow : part, whole, kg * (D / 2));
             if (live && kg == 0) {
                 if (!whole) {
@@ -398,12 +400,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        fence_proxy_async_smem();   // the next piece's loads land where the results passed
     }
-
-    // ---------------------------------------------------------------------------------- teardown
+    if (n_tiles > 0) {
+        u0 += n_tiles;
+        ++np;
+        if (two) {
+            u1 += n_tiles;
+            ++np2;
+        }
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    }
+
+    // ---------------------------------------------------------------------------------- teardown
     if (*abort_flag) {   // copies in flight land in shared memory that is still ours
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 2000000ull) {
@@ -417,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool VK, bool HL>
 int launch_narrow_t(const Params &p, const NarrowMaps &maps, int bxs, int qpt, int64_t n_cells, cudaStream_t st) {
     if (!ensure_max_dynamic_smem(chunk_narrow_kernel<D, VK, HL>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_narrow_kernel<D, VK, HL>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+    if (launch_pdl(chunk_narrow_kernel<D, VK, HL>,
+                   p.slots > 0 ? dim3(p.slots) : dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
                    (size_t)Narrow<D, VK>::kBytes, st, maps, p, bxs, qpt, (int)n_cells) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
