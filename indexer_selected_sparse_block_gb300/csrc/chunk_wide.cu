@@ -19,9 +19,9 @@
 // Order of the products: S(t + 1), then P V (t): the softmax of tile t runs while S(t + 1) does,
 // and its 16 KB of P are written once P V (t - 1) has left the buffer.
 //
-// For fp32 results the weights are carried as two bf16 halves (hi + lo, 2^-16 relative): P V then
-// runs by key half, the halves' hi and lo in the P buffer one after the other, S(t + 1) cut in
-// two between them.  For bf16 results one bf16 weight is enough: its rounding (2^-8 of a weight,
+// For fp32 results the weights are carried as two bf16 halves (hi + lo, 2^-16 relative).  Beside
+// 576-wide Q there is room for one key half's only: P V then runs by key half, the halves' hi and
+// lo in the P buffer one after the other, S(t + 1) cut in two between them.  For bf16 results one bf16 weight is enough: its rounding (2^-8 of a weight,
 // either sign) averages out below the result's own rounding.
 //
 // The running maximum moves only when a tile raises it by more than 2^8: weights up to 256 keep
@@ -47,15 +47,18 @@ constexpr int kSlab = 64 * 128;     // bytes of 64 rows x 64 dims
 constexpr int kWideThreads = 416;
 constexpr int kSlots = 8;           // operands of two slabs
 
-template <int DKQ>
+template <int DKQ, bool HL>
 struct Wide {
     static constexpr int kNSK = DKQ / 64;
     static constexpr bool kRope = kNSK > 8;
+    // hi + lo weights of both key halves fit beside 512-wide Q only; else a half's at a time
+    static constexpr bool kSplit = HL && kRope;
+    static constexpr int kPSlabs = HL && !kRope ? 4 : 2;
     static constexpr int kOffQ = 0;
     static constexpr int kOffBuf = kNSK * kSlab;               // [kSlots][2] slabs
     static constexpr int kOffRope = kOffBuf + 2 * kSlots * kSlab;
     static constexpr int kOffP = kOffRope + (kRope ? kSlab : 0);
-    static constexpr int kOffMax = kOffP + 2 * kSlab;          // float [2][256]
+    static constexpr int kOffMax = kOffP + kPSlabs * kSlab;    // float [2][256]
     static constexpr int kOffItem = kOffMax + 2 * 256 * 4;     // Item, padded
     static constexpr int kOffBar = kOffItem + 64;
     static constexpr int kBars = 1 + 2 * kSlots + 2 + 2 + 2 + 2 + 1;
@@ -111,7 +114,8 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
 template <int DKQ, bool VK, bool HL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     chunk_wide_kernel(const __grid_constant__ WideMaps maps, const Params p, int bxs, int qpc, int n_cells) {
-    using L = Wide<DKQ>;
+    using L = Wide<DKQ, HL>;
+    constexpr bool SPLIT = L::kSplit;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
     Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
@@ -343,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 there = false;
             };
             auto pv_ops = [&](int t, int half) {
-                if (HL || half == 0) wait(b_p + half * 8, t & 1);
+                if (SPLIT || half == 0) wait(b_p + half * 8, t & 1);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const int i = 2 * half + n;
@@ -354,21 +358,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                     for (int x = 0; x < (HL ? 2 : 1); ++x)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma2(tO + n * 128, dP + (uint64_t)(((HL ? x : half) * kSlab + kk * 32) >> 4),
+                            mma2(tO + n * 128, dP + (uint64_t)(((SPLIT ? x : HL ? 2 * half + x : half) * kSlab + kk * 32) >> 4),
                                  dV + (uint64_t)((2 * i * kSlab + kk * 2048) >> 4), idPV,
                                  (t > 0 || half > 0 || x > 0 || kk > 0) ? 1u : 0u);
                     commit2(b_empty + (4 + i) * 8);
                 }
-                if (HL || half == 1) commit2(b_pv + half * 8);
+                if (SPLIT || half == 1) commit2(b_pv + half * 8);
             };
             wait(b_q, 0);
             for (int t = -1; t < n_tiles && ok; ++t) {
                 const bool more = t + 1 < n_tiles;
-                if (more) s_ops(t + 1, 0, HL ? 2 : 4);
-                if (!HL && more && ok) s_end(t + 1);
-                if (HL) there = false;
+                if (more) s_ops(t + 1, 0, SPLIT ? 2 : 4);
+                if (!SPLIT && more && ok) s_end(t + 1);
+                if (SPLIT) there = false;
                 if (t >= 0 && ok) pv_ops(t, 0);
-                if (HL && more && ok) {
+                if (SPLIT && more && ok) {
                     s_ops(t + 1, 2, 4);
                     if (ok) s_end(t + 1);
                 }
@@ -469,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                                  "r"(w[4 * x]), "r"(w[4 * x + 1]), "r"(w[4 * x + 2]), "r"(w[4 * x + 3])
                                  : "memory");
             };
-            if constexpr (HL) {
+            if constexpr (SPLIT) {
                 if (hh == 1) {   // O is rescaled; then P's second half, when the first is used up
                     __syncwarp();
                     if (lane == 0) arrive_cluster(p_ready0);
@@ -481,7 +485,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 __syncwarp();
                 if (lane == 0) arrive_cluster(hh == 1 ? p_ready1 : p_ready0);
             } else {
-                write(hi, sP + hh * kSlab);
+                write(hi, sP + (HL ? 2 * hh : hh) * kSlab);
+                if constexpr (HL) write(lo, sP + (2 * hh + 1) * kSlab);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(p_ready0);
@@ -536,7 +541,7 @@ template <int DKQ, bool VK, bool HL>
 int launch_wide_t(const Params &p, const WideMaps &maps, int bxs, int qpc, int64_t n_cells, cudaStream_t st) {
     if (!ensure_max_dynamic_smem(chunk_wide_kernel<DKQ, VK, HL>)) return SFA_ERR_CUDA;
     if (launch_pdl(chunk_wide_kernel<DKQ, VK, HL>, dim3(2 * p.items, p.h_kv, p.n_split), dim3(kWideThreads),
-                   (size_t)Wide<DKQ>::kBytes, st, maps, p, bxs, qpc, (int)n_cells) != cudaSuccess) {
+                   (size_t)Wide<DKQ, HL>::kBytes, st, maps, p, bxs, qpc, (int)n_cells) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
