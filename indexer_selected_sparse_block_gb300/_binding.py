@@ -753,7 +753,7 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
         ws_bytes = _chunk_workspace(dev, code, n_seq, n_q, h_q, h_kv, dkq, dv, V is not None, n_new_max,
                                     n_kv_max, o_code)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=_U8, device=Q.device)
+            workspace = torch.empty(ws_bytes, dtype=_U8, device=dev)
             if stream is not None:   # freed on return: not before that stream is done
                 workspace.record_stream(stream)
     else:

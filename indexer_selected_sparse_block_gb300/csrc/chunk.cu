@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
         }
     }
     __syncthreads();
-    const int64_t part0 = (((int64_t)blockIdx.x * p.h_kv + g) * p.n_split + split) * kRows;
+    const int64_t part0 = (((int64_t)blockIdx.x * p.h_kv + g) * p.n_split + split) * p.part_rows;
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
         const int row = rg * RPT + r;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 #pragma unroll
         for (int y = 0; y < B; ++y) {
             const int at = where(c + y * WPR);
-            const float *src = p.part_o + ((int64_t)max(at, 0) * p.item_rows + row) * DV + lane * 4;
+            const float *src = p.part_o + ((int64_t)max(at, 0) * p.part_rows + row) * DV + lane * 4;
 #pragma unroll
             for (int k = 0; k < C; ++k)
                 v[y][k] = at >= 0 && k * 128 + lane * 4 < DV ? *reinterpret_cast<const float4 *>(src + k * 128)
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
     float m[W], w[W], M = -INFINITY, l = 0.f;
 #pragma unroll
     for (int x = 0; x < W; ++x) {
-        const float2 ml = part[x] >= 0 ? *reinterpret_cast<const float2 *>(p.part_ml + ((int64_t)part[x] * p.item_rows + row) * 2)
+        const float2 ml = part[x] >= 0 ? *reinterpret_cast<const float2 *>(p.part_ml + ((int64_t)part[x] * p.part_rows + row) * 2)
                                        : make_float2(-INFINITY, 0.f);
         m[x] = ml.x;
         w[x] = ml.y;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 enum Kernel { kSimt, kWide, kNarrow };
 struct Plan {
     Kernel kernel;
-    int item_rows, item_q, items;
+    int item_rows, item_q, items, part_rows;
     int slots;                 // > 0: the work dealt out evenly (Share)
     int n_split, split_keys;   // else: pieces of a list
 };
@@ -430,6 +430,8 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
     pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
+    const int64_t most = (int64_t)n_new_max * G;
+    pl.part_rows = most < pl.item_rows ? (int)most : pl.item_rows;
     const int tile = 128;
     const int64_t tiles = n_kv_max > 0 ? (n_kv_max + tile - 1) / tile : 1, units = items * h_kv;
     int64_t slots = wide ? device_sm_count() / 2 : device_sm_count();
@@ -437,13 +439,13 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     // us: a tile, a piece's start and end in a launch of its own and behind another one, the merge
     const double t_tile = wide ? (o_bf16 ? 1.35 : 2.) : tc ? (o_bf16 ? 1.8 : 2.4) : dv == 512 ? 30. : 8.;
     const double t_piece = 7., t_next = 4., t_merge = 6.;
-    const double part_us = (double)pl.item_rows * dv * 4 * 2 / 4e6;   // a partial, both ways
+    const double part_us = (double)pl.part_rows * dv * 4 * 2 / 4e6;   // a partial, both ways
     int64_t best = 1;
     double best_us = 0;
     for (int64_t ns = 1; ns <= tiles && ns <= 128; ++ns) {
         const int64_t per = (tiles + ns - 1) / ns;
         if (ns > 1 && (tiles + per - 1) / per != ns) continue;
-        if (ns > 1 && (double)units * ns * pl.item_rows * (dv + 2) * 4 > 1e9) break;
+        if (ns > 1 && (double)units * ns * pl.part_rows * (dv + 2) * 4 > 1e9) break;
         const int64_t waves = (units * ns + slots - 1) / slots;
         const double us = waves * (per * t_tile + t_piece) + (ns > 1 ? t_merge + units * ns * part_us : 0.);
         if (ns == 1 || us < best_us) {
@@ -472,7 +474,7 @@ size_t plan_parts(const Plan &pl, int h_kv) {
     return pl.slots > 0 ? 2 * (size_t)pl.slots : pl.n_split > 1 ? (size_t)pl.items * h_kv * pl.n_split : 0;
 }
 size_t plan_workspace(const Plan &pl, int h_kv, int dv) {
-    return plan_parts(pl, h_kv) * pl.item_rows * ((size_t)dv + 2) * sizeof(float) + 2 * (size_t)pl.slots * sizeof(int4);
+    return plan_parts(pl, h_kv) * pl.part_rows * ((size_t)dv + 2) * sizeof(float) + 2 * (size_t)pl.slots * sizeof(int4);
 }
 
 bool shape_ok(int dkq, int dv, bool has_v) {
@@ -494,7 +496,7 @@ int launch_simt(const Params &p, int dtype, cudaStream_t st) {
 template <int DV>
 int launch_combine(const Params &p, cudaStream_t st) {
     const bool many = p.slots == 0 && p.n_split >= kManyPieces;
-    const unsigned z = many ? p.item_rows : (p.item_rows + 31) / 32;
+    const unsigned z = many ? p.part_rows : (p.part_rows + 31) / 32;
     if (launch_pdl(many ? chunk_combine_kernel<DV, 8> : chunk_combine_kernel<DV, 1>,
                    p.slots > 0 ? dim3(p.slots, 1, z) : dim3(p.items, p.h_kv, z), dim3(256), 0, st,
                    p) != cudaSuccess) {
@@ -569,7 +571,7 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.lse = lse;
     p.part_o = reinterpret_cast<float *>(workspace);
     if (need > 0) {
-        const size_t rows = plan_parts(pl, h_kv) * pl.item_rows;
+        const size_t rows = plan_parts(pl, h_kv) * pl.part_rows;
         p.part_ml = p.part_o + rows * dv;
         p.slot_info = reinterpret_cast<int4 *>(p.part_ml + rows * 2);
     }
@@ -586,6 +588,7 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.o_bf16 = o_dtype == SFA_BF16;
     p.items = pl.items;
     p.item_rows = pl.item_rows;
+    p.part_rows = pl.part_rows;
     p.item_q = pl.item_q;
     p.slots = pl.slots;
     p.n_split = pl.n_split;

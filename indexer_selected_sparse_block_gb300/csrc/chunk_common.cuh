@@ -27,6 +27,7 @@ struct Params {
     int o_bf16;          // O is bf16 (else fp32)
     int items;           // row tiles of all sequences, at most
     int item_rows;       // rows of a tile
+    int part_rows;       // of those, the ones a tile of partial results has room for (no chunk has more)
     int item_q;          // queries of a tile, 0: tiles cut the flattened rows anywhere
     int slots;           // > 0: the work is dealt out evenly to this many CTAs, see Share;
                          // 0: a CTA (pair) for each item, KV head and piece of n_split

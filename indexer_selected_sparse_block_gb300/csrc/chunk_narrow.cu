@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
             const bool any = l > 0.f || l != l;
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
-            const int64_t part = (int64_t)pc.part * p.item_rows + (w * qpt + ql) * G + h;
+            const int64_t part = (int64_t)pc.part * p.part_rows + (w * qpt + ql) * G + h;
             store_tile<D / 2, D>(p, sK + warp * (D * 64), tO, inv, live, whole ? orow : part, whole, kg * (D / 2));
             if (live && kg == 0) {
                 if (!whole) {

@@ -505,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         if (ok) {
             const bool any = l > 0.f || l != l;
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
-            const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.item_rows +
+            const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.part_rows +
                                  (c * qpc + ql) * G + h;
             // columns 128 cg ..: dims 256 cg + 128 hh ..; every operand is used up
             store_tile<128, 512>(p, buf0 + warp * 16384, tO + cg * 128 + lane_addr, inv, live,
