@@ -99,6 +99,11 @@ __device__ __forceinline__ void tma1_load(uint32_t dst, const CUtensorMap *map, 
 }
 
 // ------------------------------------------------------------------------------- key rows
+// The next kernel's CTAs (the merge) may take what SMs are free and wait there for this grid's end:
+// asked for by each CTA when its last results are on their way out (1 us of a single token's 13; in
+// the narrow heads' kernel, whose slots end at different times, it did not pay).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A warp's 32 rows (its tensor memory lanes) x C value dims of O from column tcol, times each
 // row's inv, to the output (whole) or the partial results: rows of DV values at `row`, dims d0 ...
 // By way of shared memory (C * 128 bytes at `stage`): a row's values leave as one line.  (Each lane

@@ -499,6 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             named_barrier(1, 256);
             l = (l + lb[tid ^ 64]) + (lb[tid ^ 128] + lb[tid ^ 192]);
         }
+        if (tid == 0) let_next_start();
         wait(b_pv + 8, (n_tiles - 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
