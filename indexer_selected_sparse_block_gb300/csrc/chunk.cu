@@ -1,6 +1,8 @@
 // chunk.cu -- causal attention of each sequence's chunk of new tokens over its pages
 // (sfa_chunk_attend_paged): the SIMT kernel, the merge of split lists, the launch plan and the
 // C entry points.
+#include <type_traits>
+
 #include "chunk_common.cuh"
 
 namespace sfa {
@@ -12,7 +14,9 @@ namespace {
 // eight warps each score an eighth of the head dim (4 x TK / 4 products a lane from registers,
 // 16-byte shared loads), the eight sums and the softmax meet in shared memory, and the value
 // dims are split over all threads.  fp32 caches take it (the tensor cores have no fp32 kind),
-// and q8_0 ones.
+// and q8_0 ones.  It is bound by its multiplications where the loads hide behind them: the wide
+// heads' fp32 rows come by asynchronous copies into a second buffer while the tile before is
+// worked on, the narrow ones leave room for two CTAs an SM.
 constexpr int kRows = 32;
 constexpr int kThreads = 256;
 
@@ -20,9 +24,12 @@ template <int DKQ, int DV, bool VK>
 struct Simt {
     static constexpr int TK = DKQ > 128 ? 16 : 32;
     static constexpr int PK = DKQ + 4, PV = DV + 4;   // row pitches: conflict-free 16-byte reads
-    static constexpr int kFloats = kRows * PK + TK * PK + (VK ? 0 : TK * PV) + 8 * kRows * TK +
-                                   TK * kRows + 3 * kRows;
-    static constexpr size_t bytes() { return kFloats * 4 + TK * 8; }
+    static constexpr int kTile = TK * PK + (VK ? 0 : TK * PV);
+    // two tiles where they fit beside Q
+    static constexpr int kBase = kRows * PK + 8 * kRows * TK + TK * kRows + 3 * kRows;
+    static constexpr int kBufs = DKQ > 128 && (kBase + 2 * kTile) * 4 + 2 * TK * 8 <= 226 * 1024 ? 2 : 1;
+    static constexpr int kFloats = kBase + kBufs * kTile;
+    static constexpr size_t bytes() { return kFloats * 4 + kBufs * TK * 8; }
 };
 
 __device__ __forceinline__ float4 load4(const void *base, int64_t elem, int dtype) {
@@ -57,6 +64,19 @@ __device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype
     }
 }
 
+// The same of an fp32 cache by asynchronous copies.
+template <int D>
+__device__ __forceinline__ void copy_rows(float *dst, const void *src, const int64_t *cells, int n, int h_kv, int g) {
+    constexpr int C = D / 4;
+    const uint32_t to = smem_u32(dst);
+    for (int e = threadIdx.x; e < n * C; e += kThreads) {
+        const int r = e / C, c = e - r * C;
+        const int64_t cell = cells[r];
+        const float *row = reinterpret_cast<const float *>(src) + (cell < 0 ? 0 : cell * h_kv + g) * D;
+        cp_async16(to + (r * (D + 4) + 4 * c) * 4, row + 4 * c, cell < 0 ? 0u : 16u);
+    }
+}
+
 // Writes four value dims of one row: the result, or a partial one of a split list.
 __device__ __forceinline__ void store4(const Params &p, int64_t row, int dv, int d, float4 v) {
     if (p.o_bf16)
@@ -69,13 +89,13 @@ __device__ __forceinline__ void store4(const Params &p, int64_t row, int dv, int
 template <int DKQ, int DV, bool VK>
 __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, int dtype) {
     using L = Simt<DKQ, DV, VK>;
-    constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV;
+    constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV, BUFS = L::kBufs;
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sK = sQ + kRows * PK, *sV = VK ? sK : sK + TK * PK;
-    float *sRed = (VK ? sK + TK * PK : sV + TK * L::PV);
-    float *sP = sRed + 8 * kRows * TK;    // [key][row]
+    float *sQ = sm, *sTile = sQ + kRows * PK;    // [BUFS] x (K rows, V rows)
+    float *sRed = sTile + BUFS * L::kTile;
+    float *sP = sRed + 8 * kRows * TK;           // [key][row]
     float *sM = sP + TK * kRows, *sL = sM + kRows, *sA = sL + kRows;
-    int64_t *sCell = reinterpret_cast<int64_t *>(sA + kRows);
+    int64_t *sCells = reinterpret_cast<int64_t *>(sA + kRows);   // [BUFS][TK]
     __shared__ Item s_item;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = blockIdx.z, g = blockIdx.y;
@@ -122,12 +142,48 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
 
-    for (int t0 = k0; t0 < k1; t0 += TK) {
-        __syncthreads();   // the previous tile is done with shared memory
-        if (tid < TK) sCell[tid] = t0 + tid < k1 ? cell_of(p, it.seq, t0 + tid) : -1;
+    // the tile of keys t0 .. into buffer b: its cells, then its rows (ahead: by asynchronous copies)
+    const bool ahead = BUFS == 2 && dtype == SFA_F32;
+    auto find_cells = [&](int t0, int b) {
+        if (tid < TK) sCells[b * TK + tid] = t0 + tid < k1 ? cell_of(p, it.seq, t0 + tid) : -1;
+    };
+    auto fetch = [&](int b) {
+        float *k = sTile + b * L::kTile;
+        const int64_t *cells = sCells + b * TK;
+        if (ahead) {
+            copy_rows<DKQ>(k, p.K, cells, TK, p.h_kv, g);
+            if constexpr (!VK) copy_rows<DV>(k + TK * PK, p.V, cells, TK, p.h_kv, g);
+            cp_async_commit();
+        } else {
+            load_rows<DKQ>(k, p.K, dtype, cells, TK, p.h_kv, g);
+            if constexpr (!VK) load_rows<DV>(k + TK * PK, p.V, dtype, cells, TK, p.h_kv, g);
+        }
+    };
+    const int first_pos = pos0 + r0 / p.G;   // the rows' first position
+    if (ahead && k0 < k1) {
+        find_cells(k0, 0);
         __syncthreads();
-        load_rows<DKQ>(sK, p.K, dtype, sCell, TK, p.h_kv, g);
-        if constexpr (!VK) load_rows<DV>(sV, p.V, dtype, sCell, TK, p.h_kv, g);
+        fetch(0);
+    }
+    int buf = 0;
+    for (int t0 = k0; t0 < k1; t0 += TK) {
+        if (ahead) {
+            if (t0 + TK < k1) find_cells(t0 + TK, buf ^ 1);
+            __syncthreads();   // the previous tile is done with its buffer; the cells are there
+            if (t0 + TK < k1) {
+                fetch(buf ^ 1);
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
+        } else {
+            __syncthreads();   // the previous tile is done with shared memory
+            find_cells(t0, 0);
+            __syncthreads();
+            fetch(0);
+        }
+        const float *sK = sTile + buf * L::kTile, *sV = VK ? sK : sK + TK * PK;
+        const int64_t *sCell = sCells + buf * TK;
         __syncthreads();
         {   // scores: warp w takes dims [w DKQ / 8, (w + 1) DKQ / 8)
             constexpr int KPT = TK / 4;
@@ -191,26 +247,47 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
                 sA[r] = al;
             }
         }
-        __syncthreads();
+        // every key of the tile is attended by every row: no zero weight in front of a NaN
+        const bool plain = __syncthreads_and(t0 + TK <= min(k1, first_pos + 1) && (tid >= TK || sCell[tid] >= 0));
 #pragma unroll
         for (int r = 0; r < RPT; ++r) {
             const float al = sA[rg * RPT + r];
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[r][c] *= al;
         }
-#pragma unroll 4
-        for (int k = 0; k < TK; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(sV + k * PV + 4 * cg);
+        auto weighted = [&](auto guarded) {
+            constexpr bool GUARD = decltype(guarded)::value;
+#pragma unroll 2
+            for (int k = 0; k < TK; ++k) {
+                const float4 v = *reinterpret_cast<const float4 *>(sV + k * PV + 4 * cg);
+                const float *pe = sP + k * kRows + rg * RPT;
+                float e[RPT];
+                if constexpr (RPT % 4 == 0) {
 #pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                const float e = sP[k * kRows + rg * RPT + r];
-                if (e == 0.f) continue;   // a key this row does not attend may hold NaN
-                acc[r][0] = fmaf(e, v.x, acc[r][0]);
-                acc[r][1] = fmaf(e, v.y, acc[r][1]);
-                acc[r][2] = fmaf(e, v.z, acc[r][2]);
-                acc[r][3] = fmaf(e, v.w, acc[r][3]);
+                    for (int r = 0; r < RPT; r += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(pe + r);
+                        e[r] = x.x;
+                        e[r + 1] = x.y;
+                        e[r + 2] = x.z;
+                        e[r + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < RPT; ++r) e[r] = pe[r];
+                }
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+                    if (GUARD && e[r] == 0.f) continue;   // a key this row does not attend may hold NaN
+                    acc[r][0] = fmaf(e[r], v.x, acc[r][0]);
+                    acc[r][1] = fmaf(e[r], v.y, acc[r][1]);
+                    acc[r][2] = fmaf(e[r], v.z, acc[r][2]);
+                    acc[r][3] = fmaf(e[r], v.w, acc[r][3]);
+                }
             }
-        }
+        };
+        if (plain) weighted(std::false_type{});
+        else weighted(std::true_type{});
+        buf = ahead ? buf ^ 1 : 0;
     }
     __syncthreads();
     const int64_t part0 = (((int64_t)blockIdx.x * p.h_kv + g) * p.n_split + split) * p.part_rows;
