@@ -604,7 +604,7 @@ int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_t *slot, in
  * tensor-core time and not a gather per query (sfa_dense_attend_paged); a chunk of one token is
  * a decode step, its list split over the SMs.
  *
- *   Q    [n_q][h_q][dkq] bf16 (SFA_F32: fp32), the chunks packed; rows >= cu_new[n_seq] unread
+ *   Q    [n_q][h_q][dkq] bf16 (SFA_F32: fp32), the chunks packed; rows of no chunk do not matter
  *   K    [n_cells][h_kv][dkq], V [n_cells][h_kv][dv] of dtype, or V NULL: V = K[..., :dv];
  *        SFA_Q8_0: q8_0 rows, Q bf16
  *   O    [n_q][h_q][dv] of o_dtype (SFA_F32, or SFA_BF16: rounded once at the end);  lse
@@ -618,6 +618,10 @@ int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_t *slot, in
  * A page table entry outside [0, n_cells / page_size) sets SFA_DEV_BAD_CELL; its positions are
  * left out.  A query that attends nothing gives O = 0 and lse = -inf.  What unattended cells
  * hold does not matter where no query of the chunk attends them (unwritten cells may hold NaN).
+ * Precision: fp32 sums of exact bf16 products; the weights meet V as two bf16 halves (2^-16) for an
+ * fp32 O and as one bf16 value for a bf16 O; fp32 and q8_0 caches multiply in three tf32 products
+ * (2^-19 of a product) and keep the weights that way.  A value that is not finite makes what
+ * attends it not finite; an infinity of V may come out as NaN.
  * Limits: (dkq, dv) in {(576, 512) with V NULL, (512, 512), (128, 128), (64, 64)}, h_q/h_kv <= 64.
  * At most two launches.
  */

@@ -1,32 +1,33 @@
 // chunk.cu -- causal attention of each sequence's chunk of new tokens over its pages
-// (sfa_chunk_attend_paged): the SIMT kernel, the merge of split lists, the launch plan and the
-// C entry points.
-#include <type_traits>
-
+// (sfa_chunk_attend_paged): the kernel of fp32 and q8_0 caches, the merge of split lists, the launch
+// plan and the C entry points.
 #include "chunk_common.cuh"
 
 namespace sfa {
 namespace chunk {
 namespace {
 
-// ------------------------------------------------------------------------------ SIMT kernel
-// One CTA: 32 rows (query, head) of one KV head against TK keys at a time, everything in fp32:
-// eight warps each score an eighth of the head dim (4 x TK / 4 products a lane from registers,
-// 16-byte shared loads), the eight sums and the softmax meet in shared memory, and the value
-// dims are split over all threads.  fp32 caches take it (the tensor cores have no fp32 kind),
-// and q8_0 ones.  It is bound by its multiplications where the loads hide behind them: the wide
-// heads' fp32 rows come by asynchronous copies into a second buffer while the tile before is
-// worked on, the narrow ones leave room for two CTAs an SM.
+// ------------------------------------------------------------------------------ fp32 kernel
+// fp32 and q8_0 caches.  One CTA: 32 rows (query, head) of one KV head against TK keys at a time.
+// Both products run on the tensor cores as three tf32 ones (mma.sync): each operand is cut in
+// hi + lo of 11 bits each (hi = x rounded, lo = x - hi cut: at most 2^-21 of x is lost), and
+// hi hi + hi lo + lo hi, summed in fp32, leaves at most 2^-22 of the product out.  Eight warps each score an
+// eighth of the head dim, the eight sums and the softmax meet in shared memory in fp32, and each
+// warp has an eighth of the value dims.  The wide heads' fp32 rows come by asynchronous copies into
+// a second buffer while the tile before is worked on; the narrow ones leave room for two CTAs an SM.
+// (Plain fp32 multiplications in the same frame: 25 TFLOP/s at 300 tokens behind 4096, 576 wide;
+// 41 so.)
 constexpr int kRows = 32;
 constexpr int kThreads = 256;
 
 template <int DKQ, int DV, bool VK>
-struct Simt {
+struct F32 {
     static constexpr int TK = DKQ > 128 ? 16 : 32;
     static constexpr int PK = DKQ + 4, PV = DV + 4;   // row pitches: conflict-free 16-byte reads
     static constexpr int kTile = TK * PK + (VK ? 0 : TK * PV);
     // two tiles where they fit beside Q
-    static constexpr int kBase = kRows * PK + 8 * kRows * TK + TK * kRows + 3 * kRows;
+    static constexpr int kPP = TK + 4;                // pitch of the weights' rows
+    static constexpr int kBase = kRows * PK + 8 * kRows * TK + kRows * kPP + 3 * kRows;
     static constexpr int kBufs = DKQ > 128 && (kBase + 2 * kTile) * 4 + 2 * TK * 8 <= 226 * 1024 ? 2 : 1;
     static constexpr int kFloats = kBase + kBufs * kTile;
     static constexpr size_t bytes() { return kFloats * 4 + kBufs * TK * 8; }
@@ -86,22 +87,45 @@ __device__ __forceinline__ void store4(const Params &p, int64_t row, int dv, int
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + row * dv + d) = v;
 }
 
+// x as hi + lo, tf32 both, by two integer and two fp32 operations (with cvt.rna.tf32 the kernel took
+// 1308 us at 300 tokens behind 4096, 576 wide; 1083 so).  A NaN that the addition carries out of
+// the exponent is NaN in lo.
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          const uint32_t (&bh)[2], const uint32_t (&bl)[2]) {
+    mma_tf32(d, al, bh);
+    mma_tf32(d, ah, bl);
+    mma_tf32(d, ah, bh);
+}
+
 template <int DKQ, int DV, bool VK>
-__global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, int dtype) {
-    using L = Simt<DKQ, DV, VK>;
-    constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV, BUFS = L::kBufs;
+__global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int dtype) {
+    using L = F32<DKQ, DV, VK>;
+    constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV, BUFS = L::kBufs, PP = L::kPP;
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sTile = sQ + kRows * PK;    // [BUFS] x (K rows, V rows)
     float *sRed = sTile + BUFS * L::kTile;
-    float *sP = sRed + 8 * kRows * TK;           // [key][row]
-    float *sM = sP + TK * kRows, *sL = sM + kRows, *sA = sL + kRows;
+    float *sP = sRed + 8 * kRows * TK;           // [row][key slot]
+    float *sM = sP + kRows * PP, *sL = sM + kRows, *sA = sL + kRows;
     int64_t *sCells = reinterpret_cast<int64_t *>(sA + kRows);   // [BUFS][TK]
     __shared__ Item s_item;
+    __shared__ unsigned s_odd;   // keys of the tile with values that are not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int fr = lane >> 2, fc = lane & 3;   // a fragment's row and column of this lane
     const int split = blockIdx.z, g = blockIdx.y;
     pdl_wait();
     if (warp == 0) {
-        const Item it = find_item(p, blockIdx.x, blockIdx.x == 0 && g == 0 && split == 0);
+        const Item it = find_item(p, blockIdx.x, g == 0 && split == 0);
         if (lane == 0) s_item = it;
     }
     __syncthreads();
@@ -132,15 +156,14 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
         sM[tid] = -INFINITY;
         sL[tid] = 0.f;
     }
-    constexpr int CG = DV / 4;                  // column groups of 4 value dims
-    constexpr int RPT = kRows * CG / kThreads;  // rows of a thread's tile
-    static_assert(RPT >= 1 && kRows * CG % kThreads == 0, "the value dims split evenly");
-    const int cg = tid % CG, rg = tid / CG;
-    float acc[RPT][4];
+    constexpr int NT = DV / 64;   // 8-wide column tiles of a warp's value dims
+    float acc[2][NT][4];
 #pragma unroll
-    for (int r = 0; r < RPT; ++r)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.f;
 
     // the tile of keys t0 .. into buffer b: its cells, then its rows (ahead: by asynchronous copies)
     const bool ahead = BUFS == 2 && dtype == SFA_F32;
@@ -186,32 +209,42 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
         const int64_t *sCell = sCells + buf * TK;
         __syncthreads();
         {   // scores: warp w takes dims [w DKQ / 8, (w + 1) DKQ / 8)
-            constexpr int KPT = TK / 4;
-            float s[4][KPT];
+            constexpr int KN = TK / 8;
+            float sc[2][KN][4];
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int b = 0; b < KPT; ++b) s[a][b] = 0.f;
-            const float *q = sQ + (lane & 7) * PK, *k = sK + (lane >> 3) * PK;
-            for (int d = warp * (DKQ / 8); d < (warp + 1) * (DKQ / 8); d += 4) {
-                float4 x[4], y[KPT];
+                for (int n = 0; n < KN; ++n)
 #pragma unroll
-                for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4 *>(q + 8 * a * PK + d);
+                    for (int c = 0; c < 4; ++c) sc[i][n][c] = 0.f;
+            const float *q = sQ + fr * PK + warp * (DKQ / 8) + fc, *k = sK + fr * PK + warp * (DKQ / 8) + fc;
 #pragma unroll
-                for (int b = 0; b < KPT; ++b) y[b] = *reinterpret_cast<const float4 *>(k + 4 * b * PK + d);
+            for (int d = 0; d < DKQ / 8; d += 8) {
+                uint32_t ah[2][4], al[2][4], bh[KN][2], bl[KN][2];
 #pragma unroll
-                for (int a = 0; a < 4; ++a)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int b = 0; b < KPT; ++b)
-                        s[a][b] = fmaf(x[a].w, y[b].w, fmaf(x[a].z, y[b].z,
-                                  fmaf(x[a].y, y[b].y, fmaf(x[a].x, y[b].x, s[a][b]))));
+                    for (int c = 0; c < 4; ++c)
+                        split_tf32(q[(16 * i + 8 * (c & 1)) * PK + d + 4 * (c >> 1)], ah[i][c], al[i][c]);
+#pragma unroll
+                for (int n = 0; n < KN; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) split_tf32(k[8 * n * PK + d + 4 * c], bh[n][c], bl[n][c]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < KN; ++n) mma_split(sc[i][n], ah[i], al[i], bh[n], bl[n]);
             }
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int b = 0; b < KPT; ++b)
-                    sRed[(warp * kRows + 8 * a + (lane & 7)) * TK + 4 * b + (lane >> 3)] = s[a][b];
+                for (int n = 0; n < KN; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<float2 *>(sRed + (warp * kRows + 16 * i + 8 * c + fr) * TK + 8 * n + 2 * fc) =
+                            make_float2(sc[i][n][2 * c], sc[i][n][2 * c + 1]);
         }
+        if (tid == 0) s_odd = 0;
         __syncthreads();
         {   // softmax of row tid / 8: TK / 8 keys a thread
             constexpr int KPT = TK / 8;
@@ -224,6 +257,10 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) v += sRed[(w * kRows + r) * TK + k];
+                if (v - v != 0.f) {   // halves of an infinity cancel to NaN: the plain product instead
+                    v = 0.f;
+                    for (int d = 0; d < DKQ; ++d) v += sQ[r * PK + d] * sK[k * PK + d];
+                }
                 s[b] = sCell[k] >= 0 && t0 + k <= pos ? v * p.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[b]);
             }
@@ -234,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
 #pragma unroll
             for (int b = 0; b < KPT; ++b) {
                 const float e = s[b] == -INFINITY ? 0.f : exp2f(s[b] - mn);
-                sP[(kk + 8 * b) * kRows + r] = e;
+                sP[r * PP + 8 * b + (kk & 1) * 4 + (kk >> 1)] = e;   // key slots: see below
                 sum += e;
             }
 #pragma unroll
@@ -250,63 +287,95 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const Params p, in
         // every key of the tile is attended by every row: no zero weight in front of a NaN
         const bool plain = __syncthreads_and(t0 + TK <= min(k1, first_pos + 1) && (tid >= TK || sCell[tid] >= 0));
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-            const float al = sA[rg * RPT + r];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[r][c] *= al;
-        }
-        auto weighted = [&](auto guarded) {
-            constexpr bool GUARD = decltype(guarded)::value;
-#pragma unroll 2
-            for (int k = 0; k < TK; ++k) {
-                const float4 v = *reinterpret_cast<const float4 *>(sV + k * PV + 4 * cg);
-                const float *pe = sP + k * kRows + rg * RPT;
-                float e[RPT];
-                if constexpr (RPT % 4 == 0) {
+            for (int c = 0; c < 4; ++c) {
+                const float al = sA[16 * i + 8 * (c >> 1) + fr];
 #pragma unroll
-                    for (int r = 0; r < RPT; r += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(pe + r);
-                        e[r] = x.x;
-                        e[r + 1] = x.y;
-                        e[r + 2] = x.z;
-                        e[r + 3] = x.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < RPT; ++r) e[r] = pe[r];
-                }
-#pragma unroll
-                for (int r = 0; r < RPT; ++r) {
-                    if (GUARD && e[r] == 0.f) continue;   // a key this row does not attend may hold NaN
-                    acc[r][0] = fmaf(e[r], v.x, acc[r][0]);
-                    acc[r][1] = fmaf(e[r], v.y, acc[r][1]);
-                    acc[r][2] = fmaf(e[r], v.z, acc[r][2]);
-                    acc[r][3] = fmaf(e[r], v.w, acc[r][3]);
-                }
+                for (int n = 0; n < NT; ++n) acc[i][n][c] *= al;
             }
-        };
-        if (plain) weighted(std::false_type{});
-        else weighted(std::true_type{});
+        const int d0 = warp * (DV / 8);   // the warp's value dims
+        if (!plain) {
+            // Keys that some rows do not attend may hold NaN and infinities there, which a zero
+            // weight does not cancel: such values are taken out of the tile, and added one by one to
+            // the rows that attend them.
+            float *v = sTile + buf * L::kTile + (VK ? 0 : TK * PK);
+            for (int e = tid; e < TK * DV; e += kThreads) {
+                const float x = v[(e / DV) * PV + e % DV];
+                if (x - x != 0.f) atomicOr(&s_odd, 1u << (e / DV));
+            }
+            __syncthreads();
+            const unsigned odd = s_odd;
+            if (odd) {
+                for (int k = 0; k < TK; ++k) {
+                    if (!((odd >> k) & 1)) continue;
+                    const int at = (k & ~7) + (k & 1) * 4 + ((k & 7) >> 1);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float x = v[k * PV + d0 + 8 * n + 2 * fc + (c & 1)];
+                                const float e = sP[(16 * i + 8 * (c >> 1) + fr) * PP + at];
+                                if (x - x != 0.f && e != 0.f) acc[i][n][c] += e * x;
+                            }
+                }
+                __syncthreads();
+                for (int e = tid; e < TK * DV; e += kThreads) {
+                    float &x = v[(e / DV) * PV + e % DV];
+                    if (x - x != 0.f) x = 0.f;
+                }
+                __syncthreads();
+            }
+        }
+        // Slot j < 4 of eight keys is key 2 j, slot j + 4 key 2 j + 1: the lanes' reads of V then fall
+        // in different banks.
+#pragma unroll
+        for (int k = 0; k < TK; k += 8) {
+            uint32_t ah[2][4], al[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    split_tf32(sP[(16 * i + 8 * (c & 1) + fr) * PP + k + fc + 4 * (c >> 1)], ah[i][c], al[i][c]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint32_t bh[2], bl[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) split_tf32(sV[(k + 2 * fc + c) * PV + d0 + 8 * n + fr], bh[c], bl[c]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mma_split(acc[i][n], ah[i], al[i], bh, bl);
+            }
+        }
         buf = ahead ? buf ^ 1 : 0;
     }
     __syncthreads();
     const int64_t part0 = (((int64_t)blockIdx.x * p.h_kv + g) * p.n_split + split) * p.part_rows;
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-        const int row = rg * RPT + r;
-        if (row >= rows) break;
+    for (int i = 0; i < 4; ++i) {   // the lane's rows
+        const int row = 16 * (i >> 1) + 8 * (i & 1) + fr;
+        if (row >= rows) continue;
         const float l = sL[row], m = sM[row];
-        if (whole) {
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // no key: zeros; NaN stays
-            const int64_t o = (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
-            store4(p, o, DV, 4 * cg, make_float4(acc[r][0] * inv, acc[r][1] * inv, acc[r][2] * inv, acc[r][3] * inv));
-            if (cg == 0 && p.lse) p.lse[o] = l > 0.f || l != l ? (m + log2f(l)) / kLog2e : -INFINITY;
-        } else {
-            *reinterpret_cast<float4 *>(p.part_o + (part0 + row) * DV + 4 * cg) =
-                make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
-            if (cg == 0) {
+        const bool any = l > 0.f || l != l;   // no key: zeros; NaN stays
+        const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
+        const int64_t o = (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int d = warp * (DV / 8) + 8 * n + 2 * fc;
+            const float x = acc[i >> 1][n][2 * (i & 1)] * inv, y = acc[i >> 1][n][2 * (i & 1) + 1] * inv;
+            if (whole && p.o_bf16)
+                *reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + o * DV + d) = pack_bf16(x, y);
+            else
+                *reinterpret_cast<float2 *>((whole ? reinterpret_cast<float *>(p.O) + o * DV : p.part_o + (part0 + row) * DV) + d) =
+                    make_float2(x, y);
+        }
+        if (warp == 0 && fc == 0) {
+            if (!whole) {
                 p.part_ml[(part0 + row) * 2] = m;
                 p.part_ml[(part0 + row) * 2 + 1] = l;
+            } else if (p.lse) {
+                p.lse[o] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
             }
         }
     }
@@ -474,7 +543,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 }
 
 // --------------------------------------------------------------------------------- the plan
-enum Kernel { kSimt, kWide, kNarrow };
+enum Kernel { kF32, kWide, kNarrow };
 struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, part_rows;
@@ -502,7 +571,7 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
                int64_t n_cells, bool o_bf16) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
-    pl.kernel = wide ? kWide : tc ? kNarrow : kSimt;
+    pl.kernel = wide ? kWide : tc ? kNarrow : kF32;
     pl.item_rows = wide ? 128 : tc ? 256 : kRows;
     pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
@@ -560,10 +629,10 @@ bool shape_ok(int dkq, int dv, bool has_v) {
 }
 
 template <int DKQ, int DV, bool VK>
-int launch_simt(const Params &p, int dtype, cudaStream_t st) {
-    if (!ensure_max_dynamic_smem(chunk_simt_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_simt_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
-                   Simt<DKQ, DV, VK>::bytes(), st, p, dtype) != cudaSuccess) {
+int launch_f32(const Params &p, int dtype, cudaStream_t st) {
+    if (!ensure_max_dynamic_smem(chunk_f32_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+                   F32<DKQ, DV, VK>::bytes(), st, p, dtype) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
@@ -677,10 +746,10 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     int r;
     if (pl.kernel == kWide) r = launch_wide(p, dkq, n_cells, st);
     else if (pl.kernel == kNarrow) r = launch_narrow(p, dkq, n_cells, st);
-    else if (dkq == 576) r = launch_simt<576, 512, true>(p, dtype, st);
-    else if (dkq == 512) r = V ? launch_simt<512, 512, false>(p, dtype, st) : launch_simt<512, 512, true>(p, dtype, st);
-    else if (dkq == 128) r = V ? launch_simt<128, 128, false>(p, dtype, st) : launch_simt<128, 128, true>(p, dtype, st);
-    else r = V ? launch_simt<64, 64, false>(p, dtype, st) : launch_simt<64, 64, true>(p, dtype, st);
+    else if (dkq == 576) r = launch_f32<576, 512, true>(p, dtype, st);
+    else if (dkq == 512) r = V ? launch_f32<512, 512, false>(p, dtype, st) : launch_f32<512, 512, true>(p, dtype, st);
+    else if (dkq == 128) r = V ? launch_f32<128, 128, false>(p, dtype, st) : launch_f32<128, 128, true>(p, dtype, st);
+    else r = V ? launch_f32<64, 64, false>(p, dtype, st) : launch_f32<64, 64, true>(p, dtype, st);
     if (r != SFA_OK || need == 0 || pl.slots == 1) return r;
     return dv == 512 ? launch_combine<512>(p, st) : dv == 128 ? launch_combine<128>(p, st) : launch_combine<64>(p, st);
 }

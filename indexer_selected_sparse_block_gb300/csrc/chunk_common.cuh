@@ -1,5 +1,5 @@
-// chunk_common.cuh -- what the chunk attention kernels share (chunk.cu: the SIMT kernel, the
-// merge of split lists, the launch plan and the C entry points).
+// chunk_common.cuh -- what the chunk attention kernels share (chunk.cu: the kernel of fp32
+// and q8_0 caches, the merge of split lists, the launch plan and the C entry points).
 //
 // A chunk is the new tokens of one sequence: rows cu[s] .. cu[s + 1] of the packed Q, at the
 // last positions of the sequence's total[s] cached tokens.  The rows of one KV head are (query,
@@ -44,11 +44,10 @@ struct Params {
 struct Seq {
     int c0, n, total;
 };
-__device__ __forceinline__ Seq load_seq(const Params &p, int s, bool flag) {
+__device__ __forceinline__ Seq make_seq(const Params &p, int c0, int c1, int total, bool flag) {
     Seq q;
-    q.c0 = p.cu[s];
-    const int c1 = p.cu[s + 1];
-    q.total = p.total[s];
+    q.c0 = c0;
+    q.total = total;
     bool bad = q.c0 < 0 || c1 < q.c0 || c1 > p.n_q;
     q.n = bad ? 0 : c1 - q.c0;
     // the positions follow from the true length: a clipped chunk keeps its first queries
@@ -57,6 +56,9 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int s, bool flag) {
         bad = true;
     if (bad && flag) set_status(p.status, SFA_DEV_BAD_QUERY);
     return q;
+}
+__device__ __forceinline__ Seq load_seq(const Params &p, int s, bool flag) {
+    return make_seq(p, p.cu[s], p.cu[s + 1], p.total[s], flag);
 }
 
 // Row tiles of a chunk of n queries.
@@ -71,13 +73,22 @@ struct Item {
     int seq, tile;
     Seq q;
 };
-// By one whole warp: the row tiles of the sequences are counted 32 sequences at a time.
-__device__ __forceinline__ Item find_item(const Params &p, int item, bool flag) {
+// By one whole warp: the row tiles of the sequences are counted 32 sequences at a time.  Where no
+// chunk has more than one tile, item s is sequence s (2048 decode steps, 576 wide, lists of up to
+// 500 keys: 837 us with the count, 388 so).
+// lead: one caller per item, which flags lengths and offsets that cannot be.
+__device__ __forceinline__ Item find_item(const Params &p, int item, bool lead) {
     const int lane = threadIdx.x & 31;
     Item it;
     it.seq = -1;
     it.tile = 0;
     it.q = Seq{0, 0, 0};
+    if (n_items(p, p.n_new_max) <= 1) {
+        if (item < p.n_seq) it.q = load_seq(p, item, lead && lane == 0);
+        if (it.q.n > 0) it.seq = item;
+        return it;
+    }
+    const bool flag = lead && item == 0;
     int base = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
         const int s = s0 + lane;
@@ -151,10 +162,10 @@ __device__ __forceinline__ void piece_rows(const Params &p, const Seq &q, int ti
     w.len = max(0, min(key_limit(p, q), w.pos0 + w.nq));
 }
 // One piece a CTA: `split` of item and KV head g; by a whole warp.
-__device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int split, bool flag) {
+__device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int split) {
     Piece w;
     w.state = kEnd;
-    const Item it = find_item(p, item, flag);
+    const Item it = find_item(p, item, g == 0 && split == 0);
     if (it.seq < 0) return w;
     w.seq = it.seq;
     w.g = g;
@@ -168,8 +179,8 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
 
 // The work dealt out evenly.  Every row tile and KV head weighs as many keys as its list has, and
 // kPieceKeys more for the start and end of a piece (about 6 us; without them slots with ten short
-// lists took 156 us where the others took 100); in a line, sequence by sequence, KV head by KV head, row tile by row tile, the weights sum up to W, and
-// slot c takes the keys from c W / slots to (c + 1) W / slots: whole lists, and at each end perhaps
+// lists took 156 us where the others took 100); in a line, sequence by sequence, KV head by KV head,
+// row tile by row tile, the weights sum up to W, and slot c takes the keys from c W / slots to (c + 1) W / slots: whole lists, and at each end perhaps
 // a part of one, cut on tile borders.  A slot then has at most two partial results, one that starts
 // inside a list (2 c) and one that ends inside one (2 c + 1), however long the lists are.
 // Of a border among those last keys the list is whole before it.
@@ -192,9 +203,10 @@ struct SeqWork {
     int64_t a, head, upto;   // head: the weights of one KV head; upto: all of the group's, to this lane
 };
 struct Share {
-    int64_t W, per, rem;     // all of the work, W / slots and what is left over
-    int64_t at, end;         // of this slot
-    SeqWork group;           // of the first 32 sequences
+    int64_t per, rem;        // W / slots and what is left over
+    int64_t at, end;         // of this slot: what is left of its part of the line
+    int64_t before;          // the weights of the sequences before s0, the group that `at` is in
+    int s0;
 };
 // Where slot c begins: the first rem slots have a key more than the others.
 __device__ __forceinline__ int64_t share_border(const Share &h, int c) {
@@ -207,11 +219,11 @@ __device__ __forceinline__ int64_t tile_weights(const Params &p, int64_t a, int 
     return full * a + p.item_q * (full * (full + 1) / 2) + (j < tiles ? 0 : a + n) + j * kPieceKeys;
 }
 // By one whole warp, as all of the following.
-__device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) {
+__device__ __forceinline__ SeqWork seq_work(const Params &p, int s0) {
     const int lane = threadIdx.x & 31, s = s0 + lane;
     SeqWork v;
     v.q = Seq{0, 0, 0};
-    if (s < p.n_seq) v.q = load_seq(p, s, flag);
+    if (s < p.n_seq) v.q = load_seq(p, s, false);
     v.n = min(v.q.n, p.n_new_max);
     v.tiles = n_items(p, v.q.n);
     v.a = max(v.q.total - v.q.n, 0);
@@ -224,40 +236,58 @@ __device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) 
     }
     return v;
 }
-__device__ __forceinline__ Share share_of(const Params &p, bool flag) {
-    Share h;
-    h.group = seq_work(p, 0, flag);
-    h.W = __shfl_sync(0xFFFFFFFFu, h.group.upto, 31);
-    for (int s0 = 32; s0 < p.n_seq; s0 += 32) {
-        const SeqWork v = seq_work(p, s0, flag);
-        h.W += __shfl_sync(0xFFFFFFFFu, v.upto, 31);
+__device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
+    const int lane = threadIdx.x & 31;
+    int64_t W = 0;
+    for (int s0 = 0; s0 < p.n_seq; s0 += 128) {   // four sequences a lane: their loads at once
+        int c0[4], c1[4], total[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int s = s0 + 32 * k + lane;
+            c0[k] = c1[k] = total[k] = 0;
+            if (s < p.n_seq) {
+                c0[k] = p.cu[s];
+                c1[k] = p.cu[s + 1];
+                total[k] = p.total[s];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const Seq q = make_seq(p, c0[k], c1[k], total[k], flag);
+            const int n = min(q.n, p.n_new_max), tiles = n_items(p, n);
+            if (n > 0) W += tile_weights(p, max(q.total - q.n, 0), n, tiles, tiles) * p.h_kv;
+        }
     }
-    h.per = h.W / p.slots;
-    h.rem = h.W - h.per * p.slots;
-    h.at = h.end = 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, o);
+    Share h;
+    h.per = W / p.slots;
+    h.rem = W - h.per * p.slots;
+    h.at = share_border(h, c);
+    h.end = share_border(h, c + 1);
+    h.before = 0;
+    h.s0 = 0;
     return h;
 }
-// The unit at place x < W of the line.
-__device__ __forceinline__ Unit share_unit(const Params &p, const Share &h, int64_t x) {
-    int64_t before = 0;
-    SeqWork v = h.group;
-    int s0 = 0;
-    unsigned in = __ballot_sync(0xFFFFFFFFu, x < v.upto);
-    while (!in && s0 + 32 < p.n_seq) {
-        before += __shfl_sync(0xFFFFFFFFu, v.upto, 31);
-        s0 += 32;
-        v = seq_work(p, s0, false);
-        in = __ballot_sync(0xFFFFFFFFu, x < before + v.upto);
+// The unit at place x < W of the line, no place before an earlier call's.
+__device__ __forceinline__ Unit share_unit(const Params &p, Share &h, int64_t x) {
+    SeqWork v = seq_work(p, h.s0);
+    unsigned in = __ballot_sync(0xFFFFFFFFu, x < h.before + v.upto);
+    while (!in && h.s0 + 32 < p.n_seq) {
+        h.before += __shfl_sync(0xFFFFFFFFu, v.upto, 31);
+        h.s0 += 32;
+        v = seq_work(p, h.s0);
+        in = __ballot_sync(0xFFFFFFFFu, x < h.before + v.upto);
     }
     const int l = in ? __ffs(in) - 1 : 31;
     Unit u;
-    u.seq = s0 + l;
+    u.seq = h.s0 + l;
     u.q.c0 = __shfl_sync(0xFFFFFFFFu, v.q.c0, l);
     u.q.n = __shfl_sync(0xFFFFFFFFu, v.q.n, l);
     u.q.total = __shfl_sync(0xFFFFFFFFu, v.q.total, l);
     const int64_t head = __shfl_sync(0xFFFFFFFFu, v.head, l), a = __shfl_sync(0xFFFFFFFFu, v.a, l);
     const int n = __shfl_sync(0xFFFFFFFFu, v.n, l), tiles = __shfl_sync(0xFFFFFFFFu, v.tiles, l);
-    int64_t r = x - before - __shfl_sync(0xFFFFFFFFu, v.upto - v.head * p.h_kv, l);
+    int64_t r = x - h.before - __shfl_sync(0xFFFFFFFFu, v.upto - v.head * p.h_kv, l);
     u.g = 0;
     if (p.h_kv > 1) {
         u.g = (int)(r / head);
@@ -300,25 +330,23 @@ __device__ __forceinline__ Piece share_next(const Params &p, int c, Share &h) {
     h.at = min(h.end, u.u0 + u.w);
     return w;
 }
-// Slot c's piece from place `at` of the line on (at < 0: its first), and the place behind it.  The
-// sequences' sums are made anew each time: a warp that does nothing else has the time, and the
-// kernel's other warps keep the registers.
-static __device__ __noinline__ Piece share_piece(const Params &p, int c, int64_t &at, bool flag) {
+// Slot c's next piece (first: its first one).  The group's sums are made anew each time: a warp that
+// does nothing else has the time, and the kernel's other warps keep the registers.
+static __device__ __noinline__ Piece share_piece(const Params &p, int c, Share &h, bool first) {
     const bool lead = (threadIdx.x & 31) == 0;
-    Share h = share_of(p, flag);
-    if (at < 0 && lead) {
-        p.slot_info[2 * c] = make_int4(0, 1, 0, 0);
-        p.slot_info[2 * c + 1] = make_int4(0, 0, 0, 0);
+    if (first) {
+        h = share_of(p, c, c == 0);
+        if (lead) {
+            p.slot_info[2 * c] = make_int4(0, 1, 0, 0);
+            p.slot_info[2 * c + 1] = make_int4(0, 0, 0, 0);
+        }
     }
-    h.at = at < 0 ? share_border(h, c) : at;
-    h.end = share_border(h, c + 1);
     const Piece w = share_next(p, c, h);
     if (w.state != kEnd && lead) {
         if (w.head) p.slot_info[2 * c] = make_int4(w.state == kRun && w.part == 2 * c, w.ends, 0, 0);
         if (w.state == kRun && w.part == 2 * c + 1)
             p.slot_info[2 * c + 1] = make_int4(1, w.c0 + w.q0, w.nq, w.g);
     }
-    at = h.at;
     return w;
 }
 

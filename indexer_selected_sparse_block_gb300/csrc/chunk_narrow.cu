@@ -101,13 +101,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();
-    int64_t share_at = -1;   // warp 19's place in the line of all work
+    Share share;   // warp 19's place in the line of all work
     if (warp == 19) {
         Piece f;
         if (p.slots > 0) {
-            f = share_piece(p, blockIdx.x, share_at, blockIdx.x == 0);
+            f = share_piece(p, blockIdx.x, share, true);
         } else {
-            f = piece_of(p, blockIdx.x, blockIdx.y, blockIdx.z, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
+            f = piece_of(p, blockIdx.x, blockIdx.y, blockIdx.z);
         }
         if (lane == 0) *reinterpret_cast<Piece *>(sPiece) = f;
     }
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 19) {
         Piece f;
         f.state = kEnd;
-        if (p.slots > 0) f = share_piece(p, blockIdx.x, share_at, false);
+        if (p.slots > 0) f = share_piece(p, blockIdx.x, share, false);
         if (lane == 0) *reinterpret_cast<Piece *>(sPiece + ((i_piece + 1) & 1) * 64) = f;
         __syncwarp();
     } else if (n_tiles == 0) {

@@ -150,7 +150,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     }
     pdl_wait();
     if (warp == 0) {
-        const Item it = find_item(p, item, blockIdx.x == 0 && g == 0 && split == 0);
+        const Item it = find_item(p, item, (blockIdx.x & 1) == 0 && g == 0 && split == 0);
         if (lane == 0) *sItem = it;
     }
     __syncwarp();

@@ -296,3 +296,142 @@ def test_agrees_with_the_dense_call(dev):
         ref, _, tol, _ = attend_reference(c.Q, c.K, c.V, c.table, 16, c.cu, c.total, c.scale, c.dv,
                                           p_round=UBF ** 2)
         check_close(c.O, O.double().cpu(), 2 * tol, "chunk against dense")
+
+
+def dealt_out(need, part_rows, dv):
+    """The workspace of work dealt out to s CTAs: two row tiles of partial results and notes each."""
+    return any(need == 2 * s * part_rows * (dv + 2) * 4 + 32 * s for s in range(1, 161))
+
+
+def many_lens(n, seed, longest=400):
+    r = random.Random(seed)
+    return [(r.choice([0, 1, 15, 16, 127, 128, r.randrange(longest)]), r.choice([0, 1, 1, 1, 2, 5])) for _ in range(n)]
+
+
+@pytest.mark.parametrize("shape,dtype", [(WIDE, "bf16"), (W512, "bf16"), (N128, "bf16"), (N64, "bf16"), (N64K, "bf16"),
+                                         (N128, "f32"), (WIDE, "q8")])
+@pytest.mark.parametrize("n_seq", [32, 33, 100])
+def test_many_sequences(dev, shape, dtype, n_seq):
+    """More sequences than lanes, empty chunks and lists among them, the last ones too."""
+    c = Case(dev, many_lens(n_seq - 2, n_seq) + [(40, 2), (3, 0)], 16, shape, dtype, "bf16", seed=n_seq)
+    assert c.call() == 0
+    c.check()
+
+
+DEALT = [(3000, 3), (0, 0), (0, 90), (700, 1), (2300, 60), (5, 0), (1, 1), (1500, 2), (0, 3), (2900, 100)]
+
+
+@pytest.mark.parametrize("shape", [N128, N64, N64K, N128K])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_dealt_out(dev, shape, out):
+    """Narrow heads with ragged lists: slots that hold several lists, lists that take several
+    slots, empty ones between; the same bits on every run, whatever the workspace held; bad pages."""
+    c = Case(dev, DEALT, 32, shape, "bf16", out, seed=shape[0])
+    need = sfa.sfa_chunk_attend_workspace_bytes(sfa.SFA_BF16, len(DEALT), c.cu[-1], shape[3], shape[4], shape[0], shape[1],
+                                                shape[2], 100, 3003, sfa.SFA_BF16 if out == "bf16" else sfa.SFA_F32)
+    assert dealt_out(need, min(100 * shape[3] // shape[4], 256), shape[1])
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=dev)
+    assert c.call(workspace=ws) == 0
+    c.check()
+    O, lse = c.O, c.lse
+    assert c.call(workspace=ws) == 0                    # what the first call left in it
+    assert torch.equal(c.O, O) and torch.equal(c.lse, lse)
+    t = [list(r) for r in c.table]
+    t[0][40], t[4][0], t[9][70] = -1, len(c.K) // 32, 2 ** 31 - 1
+    assert c.call(table=t, workspace=ws) == sfa.SFA_DEV_BAD_CELL
+    c.check(table=t)
+
+
+@pytest.mark.parametrize("shape,dtype", [(WIDE, "bf16"), (N128, "bf16"), (N64, "bf16"), (N128, "f32")])
+def test_captured_and_replayed(dev, shape, dtype):
+    """One captured call, replayed with other lengths (within the host bounds) and other queries."""
+    c = Case(dev, [(900, 20), (300, 33), (64, 1), (0, 10)], 16, shape, dtype, seed=5)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    Q, cu, total, table = c.Q.to(dev), i32(c.cu), i32(c.total), i32(c.table)
+    c.O = torch.full((c.cu[-1], c.h_q, c.dv), 7.0, device=dev)
+    c.lse = torch.full((c.cu[-1], c.h_q), 7.0, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    need = sfa.sfa_chunk_attend_workspace_bytes({"bf16": sfa.SFA_BF16, "f32": sfa.SFA_F32}[dtype], 4, c.cu[-1], c.h_q,
+                                                c.h_kv, c.dkq, c.dv, c.sep, 40, 950)
+    ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device=dev)
+    run = lambda: sfa.sfa_chunk_attend_paged(Q, c.Kc, c.Vc, table, 16, cu, total, 40, 950, c.scale, c.O, lse=c.lse,
+                                             workspace=ws, dev_status=status)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for new_cu, new_total in ((c.cu, c.total), ([0, 1, 41, 54, 64], [40, 333, 65, 10]), ([0, 20, 20, 60, 64], [920, 7, 65, 9])):
+        cu.copy_(i32(new_cu))
+        total.copy_(i32(new_total))
+        c.Q = torch.randn(c.Q.shape, generator=torch.Generator().manual_seed(new_cu[1])).to(torch.bfloat16).to(c.Q.dtype)
+        Q.copy_(c.Q)
+        c.O.fill_(7.0)
+        c.lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert sfa.sfa_read_device_status(status) == 0
+        c.check(cu=new_cu, total=new_total)
+
+
+def test_two_calls_at_once(dev):
+    """Two streams, a workspace each: calls that overlap do not meet."""
+    cases = [Case(dev, [(4000, 1), (2500, 1)], 32, s, seed=i) for i, s in enumerate((WIDE, N128, N64, W512))]
+    alone = []
+    for c in cases:
+        assert c.call() == 0
+        alone.append((c.O, c.lse))
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    streams = [torch.cuda.Stream() for _ in cases]
+    runs = []
+    for c in cases:
+        runs.append((c.Q.to(dev), i32(c.table), i32(c.cu), i32(c.total), torch.empty_like(c.O), torch.empty_like(c.lse),
+                     torch.zeros(1 << 24, dtype=torch.uint8, device=dev)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, st, (Q, table, cu, total, O, lse, ws) in zip(cases, streams, runs):
+            sfa.sfa_chunk_attend_paged(Q, c.Kc, c.Vc, table, 32, cu, total, 1, 4001, c.scale, O, lse=lse,
+                                       workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for (O, lse), run in zip(alone, runs):
+        assert torch.equal(O, run[4]) and torch.equal(lse, run[5])
+
+
+@pytest.mark.parametrize("shape,dtype", [(WIDE, "bf16"), (N128, "bf16"), (N64, "f32")])
+def test_caches_past_32_bit_offsets(dev, shape, dtype):
+    """Pages whose elements lie more than 2^32 into the cache."""
+    c = Case(dev, [(300, 5), (0, 40)], 64, shape, dtype, seed=7)
+    row = c.h_kv * min(c.dkq, c.dv)
+    shift = (2 ** 32 // row) // 64 + 3                 # pages
+    n = len(c.K)
+    if torch.cuda.mem_get_info()[0] < 3 * (shift * 64 + n) * c.h_kv * c.dkq * c.Kc.element_size():
+        pytest.skip("not enough device memory")
+
+    def far(x):
+        big = torch.empty((shift * 64 + n,) + x.shape[1:], dtype=x.dtype, device=dev)
+        big[shift * 64:] = x
+        return big
+
+    c.Kc, c.Vc = far(c.Kc), None if c.Vc is None else far(c.Vc)
+    assert c.call(table=[[e if e < 0 else e + shift for e in r] for r in c.table]) == 0
+    c.check()
+
+
+def test_infinite_keys(dev):
+    """A key with an infinity scores +-inf: -inf is no weight at all, as the formula has it."""
+    for shape, dtype in ((N128, "f32"), (N128, "bf16"), (W512, "bf16")):
+        c = Case(dev, [(100, 30)], 16, shape, dtype, seed=11)
+        c.Q[..., 3] = c.Q[..., 3].abs() + 0.5
+        cell = c.table[0][50 // 16] * 16 + 50 % 16
+        c.K[cell, :, 3] = -math.inf
+        c.Kc = c.K.to(dev)
+        assert c.call() == 0
+        t = c.table
+        c.K[cell, :, 3] = -1e4                         # a weight of zero in 64 bits too
+        ref, _, _, _ = attend_reference(c.Q, c.K, c.V, t, 16, c.cu, c.total, c.scale, c.dv)
+        c.K[cell, :, 3] = 0.0                          # the bound, without the far score
+        _, _, tol, _ = attend_reference(c.Q, c.K, c.V, t, 16, c.cu, c.total, c.scale, c.dv, p_round=P_ROUND[dtype, "f32"])
+        check_close(c.O, ref, tol, "O")
