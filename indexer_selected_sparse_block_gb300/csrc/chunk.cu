@@ -330,23 +330,35 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
             }
         }
         // Slot j < 4 of eight keys is key 2 j, slot j + 4 key 2 j + 1: the lanes' reads of V then fall
-        // in different banks.
+        // in different banks.  A tile's sum is added to acc with rounding: the tensor cores cut towards
+        // zero what they add to an accumulator, which a long list would show.
+        uint32_t ah[TK / 8][2][4], al[TK / 8][2][4];
 #pragma unroll
-        for (int k = 0; k < TK; k += 8) {
-            uint32_t ah[2][4], al[2][4];
+        for (int k = 0; k < TK / 8; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    split_tf32(sP[(16 * i + 8 * (c & 1) + fr) * PP + k + fc + 4 * (c >> 1)], ah[i][c], al[i][c]);
+                    split_tf32(sP[(16 * i + 8 * (c & 1) + fr) * PP + 8 * k + fc + 4 * (c >> 1)], ah[k][i][c], al[k][i][c]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
+            float add[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) add[i][c] = 0.f;
+#pragma unroll
+            for (int k = 0; k < TK / 8; ++k) {
                 uint32_t bh[2], bl[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) split_tf32(sV[(k + 2 * fc + c) * PV + d0 + 8 * n + fr], bh[c], bl[c]);
+                for (int c = 0; c < 2; ++c) split_tf32(sV[(8 * k + 2 * fc + c) * PV + d0 + 8 * n + fr], bh[c], bl[c]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) mma_split(acc[i][n], ah[i], al[i], bh, bl);
+                for (int i = 0; i < 2; ++i) mma_split(add[i], ah[k][i], al[k][i], bh, bl);
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][n][c] += add[i][c];
         }
         buf = ahead ? buf ^ 1 : 0;
     }

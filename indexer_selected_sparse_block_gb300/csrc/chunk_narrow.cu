@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(b_p + 8 * i, ((i ? u1 : u0) + t) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    pv_op(i, vs, t == 0);
+                    pv_op(i, vs, HL ? t % kDrain == 0 : t == 0);
                     if (more) {
                         if (i == 0) wait(b_kFull + 8 * ks, kp);
                         if (!ok) break;
@@ -286,6 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);  // a zero scale: weights of 1 to 1e-28
         const float sgn = neg ? -sc : sc;
         float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
+        float m_sum = -INFINITY;                              // m of the sums that have moved on
+        auto part_row = [&]() { return (int64_t)pc.part * p.part_rows + (w * qpt + ql) * G + h; };
+        auto drain = [&](bool first, bool back) {
+            drain_tile<D / 2, D>(whole ? reinterpret_cast<float *>(p.O) : p.part_o, tO, whole ? orow : part_row(), live,
+                                 kg * (D / 2), drain_keep(m_sum, m), first, back);
+        };
         float *mine = sMax + tid, *other = sMax + (tid ^ 128);
         const int kq = k0 + kg * 64;                          // the thread's first key
         auto read_entry = [&](int key) { return key < k1 ? __ldg(table + p.page_div.div(key)) : 0; };
@@ -304,6 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool masked = last < 63 || (cells[0] & cells[1]) != 0xFFFFFFFFu;
             wait(b_s + 8 * w, ((w ? u1 : u0) + t) & 1);
             tc_fence_after();
+            if (HL && t > 0 && t % kDrain == 0) {   // behind P V (t - 1); few registers are in use here
+                drain(t == kDrain, false);
+                m_sum = m;
+            }
             uint32_t r[2][32];
             tmem_ld32(tS, r[0]);
             tmem_ld32(tS + 32, r[1]);
@@ -389,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
             const bool any = l > 0.f || l != l;
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
-            const int64_t part = (int64_t)pc.part * p.part_rows + (w * qpt + ql) * G + h;
+            if (HL && n_tiles > kDrain) drain(false, true);
+            const int64_t part = part_row();
             store_tile<D / 2, D>(p, sK + warp * (D * 64), tO, inv, live, whole ? orow : part, whole, kg * (D / 2));
             if (live && kg == 0) {
                 if (!whole) {

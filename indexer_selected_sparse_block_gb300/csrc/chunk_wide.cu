@@ -360,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                         for (int kk = 0; kk < 4; ++kk)
                             mma2(tO + n * 128, dP + (uint64_t)(((SPLIT ? x : HL ? 2 * half + x : half) * kSlab + kk * 32) >> 4),
                                  dV + (uint64_t)((2 * i * kSlab + kk * 2048) >> 4), idPV,
-                                 (t > 0 || half > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                                 ((HL ? t % kDrain : t) > 0 || half > 0 || x > 0 || kk > 0) ? 1u : 0u);
                     commit2(b_empty + (4 + i) * 8);
                 }
                 if (SPLIT || half == 1) commit2(b_pv + half * 8);
@@ -393,6 +393,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
         const uint32_t p_ready0 = in_leader(b_p), p_ready1 = p_ready0 + 8;
         float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
+        float m_sum = -INFINITY;                              // m of the sums that have moved on
+        auto part_row = [&]() {
+            return (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.part_rows + (c * qpc + ql) * G + h;
+        };
+        auto drain = [&](bool first, bool back) {   // columns 128 cg ..: dims 256 cg + 128 hh ..
+            drain_tile<128, 512>(whole ? reinterpret_cast<float *>(p.O) : p.part_o, tO + cg * 128 + lane_addr,
+                                 whole ? orow : part_row(), live, cg * 256 + hh * 128, drain_keep(m_sum, m), first, back);
+        };
         const int kq = k0 + hh * 64 + cg * 32;                // the thread's first key
         auto read_entry = [&](int key) { return key < k1 ? __ldg(table + p.page_div.div(key)) : 0; };
         int entry = read_entry(kq + lane);
@@ -405,6 +413,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             const uint32_t cells = __ballot_sync(0xFFFFFFFFu, cell);
             entry = read_entry(kb + kT + lane);
             const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
+            if (HL && t > 0 && t % kDrain == 0) {   // here, where few registers are in use
+                wait(b_pv + 8, (t - 1) & 1);
+                tc_fence_after();
+                drain(t == kDrain, false);
+                m_sum = m;
+            }
             wait(b_s + b * 8, par);
             tc_fence_after();
             uint32_t r[32];
@@ -506,8 +520,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         if (ok) {
             const bool any = l > 0.f || l != l;
             const float inv = whole ? (any ? 1.f / l : 0.f) : 1.f;
-            const int64_t part = (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.part_rows +
-                                 (c * qpc + ql) * G + h;
+            if (HL && n_tiles > kDrain) drain(false, true);
+            const int64_t part = part_row();
             // columns 128 cg ..: dims 256 cg + 128 hh ..; every operand is used up
             store_tile<128, 512>(p, buf0 + warp * 16384, tO + cg * 128 + lane_addr, inv, live,
                                  whole ? orow : part, whole, cg * 256 + hh * 128);

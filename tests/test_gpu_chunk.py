@@ -435,3 +435,34 @@ def test_infinite_keys(dev):
         c.K[cell, :, 3] = 0.0                          # the bound, without the far score
         _, _, tol, _ = attend_reference(c.Q, c.K, c.V, t, 16, c.cu, c.total, c.scale, c.dv, p_round=P_ROUND[dtype, "f32"])
         check_close(c.O, ref, tol, "O")
+
+
+@pytest.mark.parametrize("shape,dtype,n_seq,length", [(N128, "bf16", 40, 30000), (N64, "bf16", 160, 30000),
+                                                      (WIDE, "bf16", 80, 20000), (W512, "bf16", 40, 20000),
+                                                      (W512K, "bf16", 80, 2100), (N128, "f32", 40, 20000)])
+def test_long_sums_keep_fp32(dev, shape, dtype, n_seq, length):
+    """fp32 results of long lists: hi + lo weights lose at most 2^-17, and a sum that is cut at each of
+    its additions half a step a time on average, 2^-24 of a running sum that is two thirds of its end
+    on average: 384 of them between sums that are rounded, so 256 2^-24.  (Sequences that share their pages, so that every list is long and whole.)"""
+    dkq, dv, sep, h_q, h_kv = shape
+    g = torch.Generator(device=dev).manual_seed(length)
+    n_pages = -(-length // 64)
+    randn = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16).to(TYPES[dtype])
+    K, V, Q = randn(n_pages * 64, h_kv, dkq), randn(n_pages * 64, h_kv, dv) if sep else None, randn(n_seq + 1, h_q, dkq)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    table = torch.arange(n_pages, dtype=torch.int32, device=dev).repeat(n_seq, 1)
+    O = torch.empty((n_seq + 1, h_q, dv), device=dev)
+    # the last sequence has two new tokens
+    sfa.sfa_chunk_attend_paged(Q, K, V, table, 64, i32(list(range(n_seq)) + [n_seq + 1]), i32([length] * n_seq), 2, length,
+                               1 / math.sqrt(dkq), O)
+    G = h_q // h_kv
+    for rows, keys in ((slice(0, n_seq - 1), length), (slice(n_seq - 1, n_seq), length - 1), (slice(n_seq, None), length)):
+        k = K[:keys].double()
+        v = k[..., :dv] if V is None else V[:keys].double()
+        q = Q[rows].double().view(-1, h_kv, G, dkq)
+        ref = torch.empty_like(O[rows], dtype=torch.float64)
+        for i in range(h_kv):
+            p = torch.softmax(q[:, i].reshape(-1, dkq) @ k[:, i].T / math.sqrt(dkq), -1)
+            ref[:, i * G:(i + 1) * G] = (p @ v[:, i]).view(-1, G, dv)
+        err = float((O[rows].double() - ref).norm() / ref.norm())
+        assert err <= 256 * 2.0 ** -24 + 2.0 ** -17, f"{err:.3g}"
