@@ -748,6 +748,7 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.item_rows = pl.item_rows;
     p.part_rows = pl.part_rows;
     p.item_q = pl.item_q;
+    p.one_tile = pl.item_q > 0 ? n_new_max <= pl.item_q : (int64_t)n_new_max * p.G <= pl.item_rows;
     p.slots = pl.slots;
     p.n_split = pl.n_split;
     p.split_keys = pl.split_keys;

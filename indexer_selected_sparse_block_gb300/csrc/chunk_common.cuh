@@ -29,6 +29,7 @@ struct Params {
     int item_rows;       // rows of a tile
     int part_rows;       // of those, the ones a tile of partial results has room for (no chunk has more)
     int item_q;          // queries of a tile, 0: tiles cut the flattened rows anywhere
+    int one_tile;        // no chunk has more than one row tile
     int slots;           // > 0: the work is dealt out evenly to this many CTAs, see Share;
                          // 0: a CTA (pair) for each item, KV head and piece of n_split
     int n_split;         // pieces a list is cut into, at most
@@ -83,7 +84,7 @@ __device__ __forceinline__ Item find_item(const Params &p, int item, bool lead) 
     it.seq = -1;
     it.tile = 0;
     it.q = Seq{0, 0, 0};
-    if (n_items(p, p.n_new_max) <= 1) {
+    if (p.one_tile) {
         if (item < p.n_seq) it.q = load_seq(p, item, lead && lane == 0);
         if (it.q.n > 0) it.seq = item;
         return it;
@@ -207,6 +208,7 @@ struct Share {
     int64_t at, end;         // of this slot: what is left of its part of the line
     int64_t before;          // the weights of the sequences before s0, the group that `at` is in
     int s0;
+    SeqWork group;           // of s0
 };
 // Where slot c begins: the first rem slots have a key more than the others.
 __device__ __forceinline__ int64_t share_border(const Share &h, int c) {
@@ -219,11 +221,11 @@ __device__ __forceinline__ int64_t tile_weights(const Params &p, int64_t a, int 
     return full * a + p.item_q * (full * (full + 1) / 2) + (j < tiles ? 0 : a + n) + j * kPieceKeys;
 }
 // By one whole warp, as all of the following.
-__device__ __forceinline__ SeqWork seq_work(const Params &p, int s0) {
+__device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) {
     const int lane = threadIdx.x & 31, s = s0 + lane;
     SeqWork v;
     v.q = Seq{0, 0, 0};
-    if (s < p.n_seq) v.q = load_seq(p, s, false);
+    if (s < p.n_seq) v.q = load_seq(p, s, flag);
     v.n = min(v.q.n, p.n_new_max);
     v.tiles = n_items(p, v.q.n);
     v.a = max(v.q.total - v.q.n, 0);
@@ -238,8 +240,10 @@ __device__ __forceinline__ SeqWork seq_work(const Params &p, int s0) {
 }
 __device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
     const int lane = threadIdx.x & 31;
-    int64_t W = 0;
-    for (int s0 = 0; s0 < p.n_seq; s0 += 128) {   // four sequences a lane: their loads at once
+    Share h;
+    h.group = seq_work(p, 0, flag);
+    int64_t W = lane == 31 ? h.group.upto : 0;
+    for (int s0 = 32; s0 < p.n_seq; s0 += 128) {   // four sequences a lane: their loads at once
         int c0[4], c1[4], total[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -260,7 +264,6 @@ __device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, o);
-    Share h;
     h.per = W / p.slots;
     h.rem = W - h.per * p.slots;
     h.at = share_border(h, c);
@@ -271,14 +274,14 @@ __device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
 }
 // The unit at place x < W of the line, no place before an earlier call's.
 __device__ __forceinline__ Unit share_unit(const Params &p, Share &h, int64_t x) {
-    SeqWork v = seq_work(p, h.s0);
-    unsigned in = __ballot_sync(0xFFFFFFFFu, x < h.before + v.upto);
+    unsigned in = __ballot_sync(0xFFFFFFFFu, x < h.before + h.group.upto);
     while (!in && h.s0 + 32 < p.n_seq) {
-        h.before += __shfl_sync(0xFFFFFFFFu, v.upto, 31);
+        h.before += __shfl_sync(0xFFFFFFFFu, h.group.upto, 31);
         h.s0 += 32;
-        v = seq_work(p, h.s0);
-        in = __ballot_sync(0xFFFFFFFFu, x < h.before + v.upto);
+        h.group = seq_work(p, h.s0, false);
+        in = __ballot_sync(0xFFFFFFFFu, x < h.before + h.group.upto);
     }
+    const SeqWork &v = h.group;
     const int l = in ? __ffs(in) - 1 : 31;
     Unit u;
     u.seq = h.s0 + l;
@@ -330,8 +333,7 @@ __device__ __forceinline__ Piece share_next(const Params &p, int c, Share &h) {
     h.at = min(h.end, u.u0 + u.w);
     return w;
 }
-// Slot c's next piece (first: its first one).  The group's sums are made anew each time: a warp that
-// does nothing else has the time, and the kernel's other warps keep the registers.
+// Slot c's next piece (first: its first one).  Not inlined: the kernel's other warps keep their registers.
 static __device__ __noinline__ Piece share_piece(const Params &p, int c, Share &h, bool first) {
     const bool lead = (threadIdx.x & 31) == 0;
     if (first) {
