@@ -480,77 +480,77 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
     };
 #pragma unroll 1
     for (int row = row0; row < min(rows, (int)(blockIdx.z + 1) * ROWS); row += 8) {
-    float4 v[B][C];
-    load(row, first, v);
-    float m[W], w[W], M = -INFINITY, l = 0.f;
+        float4 v[B][C];
+        load(row, first, v);
+        float m[W], w[W], M = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int x = 0; x < W; ++x) {
-        const float2 ml = part[x] >= 0 ? *reinterpret_cast<const float2 *>(p.part_ml + ((int64_t)part[x] * p.part_rows + row) * 2)
-                                       : make_float2(-INFINITY, 0.f);
-        m[x] = ml.x;
-        w[x] = ml.y;
-        M = fmaxf(M, m[x]);
-    }
+        for (int x = 0; x < W; ++x) {
+            const float2 ml = part[x] >= 0 ? *reinterpret_cast<const float2 *>(p.part_ml + ((int64_t)part[x] * p.part_rows + row) * 2)
+                                           : make_float2(-INFINITY, 0.f);
+            m[x] = ml.x;
+            w[x] = ml.y;
+            M = fmaxf(M, m[x]);
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
 #pragma unroll
-    for (int x = 0; x < W; ++x) {   // the piece's share of the sum, then its weight
-        const float e = m[x] == -INFINITY ? 0.f : exp2f(m[x] - M);
-        l += w[x] == 0.f ? 0.f : (m[x] == -INFINITY ? w[x] : e * w[x]);
-        w[x] = e;
-    }
+        for (int x = 0; x < W; ++x) {   // the piece's share of the sum, then its weight
+            const float e = m[x] == -INFINITY ? 0.f : exp2f(m[x] - M);
+            l += w[x] == 0.f ? 0.f : (m[x] == -INFINITY ? w[x] : e * w[x]);
+            w[x] = e;
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    float4 acc[C];
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        float4 acc[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = first; c < n_pieces; c += B * WPR) {
-        if (c != first) load(row, c, v);
+        for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = first; c < n_pieces; c += B * WPR) {
+            if (c != first) load(row, c, v);
 #pragma unroll
-        for (int y = 0; y < B; ++y) {
-            const int cy = c + y * WPR;
-            float e = 0.f;
+            for (int y = 0; y < B; ++y) {
+                const int cy = c + y * WPR;
+                float e = 0.f;
 #pragma unroll
-            for (int x = 0; x < W; ++x) {
-                const float f = __shfl_sync(0xFFFFFFFFu, w[x], cy & 31);
-                if (cy >> 5 == x) e = f;
-            }
+                for (int x = 0; x < W; ++x) {
+                    const float f = __shfl_sync(0xFFFFFFFFu, w[x], cy & 31);
+                    if (cy >> 5 == x) e = f;
+                }
 #pragma unroll
-            for (int k = 0; k < C; ++k) {
-                acc[k].x = fmaf(e, v[y][k].x, acc[k].x);
-                acc[k].y = fmaf(e, v[y][k].y, acc[k].y);
-                acc[k].z = fmaf(e, v[y][k].z, acc[k].z);
-                acc[k].w = fmaf(e, v[y][k].w, acc[k].w);
+                for (int k = 0; k < C; ++k) {
+                    acc[k].x = fmaf(e, v[y][k].x, acc[k].x);
+                    acc[k].y = fmaf(e, v[y][k].y, acc[k].y);
+                    acc[k].z = fmaf(e, v[y][k].z, acc[k].z);
+                    acc[k].w = fmaf(e, v[y][k].w, acc[k].w);
+                }
             }
         }
-    }
-    const bool any = l > 0.f || l != l;
-    const float inv = any ? 1.f / l : 0.f;
-    const int64_t o = (int64_t)(c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
-    if (lane == 0 && first == 0 && p.lse) p.lse[o] = any ? (M + log2f(l)) / kLog2e : -INFINITY;
-    if constexpr (WPR == 8) {
+        const bool any = l > 0.f || l != l;
+        const float inv = any ? 1.f / l : 0.f;
+        const int64_t o = (int64_t)(c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
+        if (lane == 0 && first == 0 && p.lse) p.lse[o] = any ? (M + log2f(l)) / kLog2e : -INFINITY;
+        if constexpr (WPR == 8) {
 #pragma unroll
-        for (int k = 0; k < C; ++k)
-            if (k * 128 + lane * 4 < DV) *reinterpret_cast<float4 *>(&s_acc[warp][k * 128 + lane * 4]) = acc[k];
-        __syncthreads();
-        for (int d = 4 * threadIdx.x; d < DV; d += 4 * 256) {
-            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < C; ++k)
+                if (k * 128 + lane * 4 < DV) *reinterpret_cast<float4 *>(&s_acc[warp][k * 128 + lane * 4]) = acc[k];
+            __syncthreads();
+            for (int d = 4 * threadIdx.x; d < DV; d += 4 * 256) {
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const float4 q = *reinterpret_cast<const float4 *>(&s_acc[y][d]);
-                t.x += q.x;
-                t.y += q.y;
-                t.z += q.z;
-                t.w += q.w;
+                for (int y = 0; y < 8; ++y) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&s_acc[y][d]);
+                    t.x += q.x;
+                    t.y += q.y;
+                    t.z += q.z;
+                    t.w += q.w;
+                }
+                store4(p, o, DV, d, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
             }
-            store4(p, o, DV, d, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int k = 0; k < C; ++k)
-            if (k * 128 + lane * 4 < DV)
-                store4(p, o, DV, k * 128 + lane * 4, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
-    }
+            for (int k = 0; k < C; ++k)
+                if (k * 128 + lane * 4 < DV)
+                    store4(p, o, DV, k * 128 + lane * 4, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+        }
     }
 }
 

@@ -181,10 +181,11 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
 // The work dealt out evenly.  Every row tile and KV head weighs as many keys as its list has, and
 // kPieceKeys more for the start and end of a piece (about 6 us; without them slots with ten short
 // lists took 156 us where the others took 100); in a line, sequence by sequence, KV head by KV head,
-// row tile by row tile, the weights sum up to W, and slot c takes the keys from c W / slots to (c + 1) W / slots: whole lists, and at each end perhaps
-// a part of one, cut on tile borders.  A slot then has at most two partial results, one that starts
-// inside a list (2 c) and one that ends inside one (2 c + 1), however long the lists are.
-// Of a border among those last keys the list is whole before it.
+// row tile by row tile, the weights sum up to W, and slot c takes the keys from c W / slots to
+// (c + 1) W / slots: whole lists, and at each end perhaps a part of one, cut on tile borders (a
+// border among the added keys leaves the list whole before it).  A slot then has at most two partial
+// results, one that starts inside a list (2 c) and one that ends inside one (2 c + 1), however long
+// the lists are.
 // For the merge a slot says in slot_info of its partial results, [c][0] = (written, the list ends
 // here) for the one that starts inside a list, [c][1] = (written, first query, queries, KV head) for
 // the one that is a list's start: the pieces of that list are it and the following slots' [0], up to

@@ -49,8 +49,8 @@ __device__ __forceinline__ int64_t map_taken(const MapParams &p, int64_t a, int6
 // list, their cells; the first token of a page that is taken also writes the table's entry.
 // Integer sums in a fixed order: the maps are the same on every run.
 // A decode step is one CTA and latency (3.3 us); whole prompts are 16 bytes of stores per token:
-// 4.2 M tokens in 44 us with one token a thread and 64-bit divisions, PROMPT_US with four a thread,
-// 16-byte stores and one 32-bit division (a product) for the four.
+// 4.2 M tokens in 44 us with one token a thread and 64-bit divisions, 19 us (3.5 TB/s of stores) with
+// four a thread, 16-byte stores and one 32-bit division (a product) for the four.
 template <int N>
 __global__ void __launch_bounds__(kMapThreads, N == 4 ? 3 : 4) page_maps_kernel(const MapParams p) {
     extern __shared__ int32_t s_map[];
@@ -246,7 +246,8 @@ struct CellWrites {
 
 // The rows' pieces in one line, four a thread in flight: their slots, their loads, their stores.
 // A row's neighbours in the line are its neighbours in memory on both sides.  With a warp to a row
-// a row of 72 pieces left a third of the lanes idle (65536 rows of 1408 bytes: 39 us, WRITE_US now).
+// a row of 72 pieces left a third of the lanes idle (65536 rows of 1408 bytes: 39 us; 29 so,
+// 6.3 TB/s).
 template <int KIND>
 __device__ __forceinline__ void write_pieces(const sfa_cell_write &w, int units, const FastDiv &div,
                                              const int32_t *__restrict__ slot, int64_t n_rows,
