@@ -257,11 +257,12 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) v += sRed[(w * kRows + r) * TK + k];
-                if (v - v != 0.f) {   // halves of an infinity cancel to NaN: the plain product instead
+                const bool on = sCell[k] >= 0 && t0 + k <= pos;
+                if (on && v - v != 0.f) {   // halves of an infinity cancel to NaN: the plain product instead
                     v = 0.f;
                     for (int d = 0; d < DKQ; ++d) v += sQ[r * PK + d] * sK[k * PK + d];
                 }
-                s[b] = sCell[k] >= 0 && t0 + k <= pos ? v * p.scale_log2 : -INFINITY;
+                s[b] = on ? v * p.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[b]);
             }
 #pragma unroll

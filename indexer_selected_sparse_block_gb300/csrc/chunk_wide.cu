@@ -518,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             named_barrier(1, 256);
             l = (l + lb[tid ^ 64]) + (lb[tid ^ 128] + lb[tid ^ 192]);
         }
-        if (tid == 0) let_next_start();
+        if (tid == 0 && p.n_split > 1) let_next_start();   // the merge: what else may follow is not known
         wait(b_pv + 8, (n_tiles - 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();

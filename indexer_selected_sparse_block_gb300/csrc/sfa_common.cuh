@@ -125,7 +125,7 @@ __device__ __forceinline__ void set_status(int32_t *status, int32_t bits) {
 
 // Programmatic dependent launch, device side: pdl_wait() blocks until the previous kernel in
 // the stream has completed (its writes visible).  No kernel here signals its dependents early
-// (griddepcontrol.launch_dependents): the next kernel's launch is then prepared while this one
+// (griddepcontrol.launch_dependents; chunk_wide_kernel alone, for its own merge): the next kernel's launch is then prepared while this one
 // runs and its CTAs start as this one's leave.  Measured on GB300, early signals let the next
 // kernel's CTAs occupy SMs and wait there while this one still ran, and every step was slower
 // for it (decode_32x131072: 112 -> 98 us per step without them).
