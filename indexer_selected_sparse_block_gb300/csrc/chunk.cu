@@ -11,18 +11,21 @@ namespace {
 // fp32 and q8_0 caches.  One CTA: 32 rows (query, head) of one KV head against TK keys at a time.
 // Both products run on the tensor cores as three tf32 ones (mma.sync): each operand is cut in
 // hi + lo of 11 bits each (hi = x rounded, lo = x - hi cut: at most 2^-21 of x is lost), and
-// hi hi + hi lo + lo hi, summed in fp32, leaves at most 2^-22 of the product out.  Eight warps each score an
-// eighth of the head dim, the eight sums and the softmax meet in shared memory in fp32, and each
-// warp has an eighth of the value dims.  The wide heads' fp32 rows come by asynchronous copies into
-// a second buffer while the tile before is worked on; the narrow ones leave room for two CTAs an SM.
-// (Plain fp32 multiplications in the same frame: 25 TFLOP/s at 300 tokens behind 4096, 576 wide;
-// 41 so.)
+// hi hi + hi lo + lo hi, summed in fp32, leaves at most 2^-22 of the product out.  Eight warps (wide
+// heads: two times eight, a half of the rows each) score an eighth of the head dim, the eight sums
+// and the softmax meet in shared memory in fp32, and each warp has its part of the value dims.  The
+// wide heads' fp32 rows come by asynchronous copies into a second buffer while the tile before is
+// worked on; the narrow ones leave room for two CTAs an SM.
+// The rate of mma.sync bounds it (the warps wait for that pipe most): 300 tokens behind 4096, 576
+// wide, 40 TFLOP/s, 120 of tf32; plain fp32 multiplications in the same frame made 25.  512 wide with
+// V apart 1158 us with 16 warps, 1243 with eight; 576 wide the same with either.
 constexpr int kRows = 32;
-constexpr int kThreads = 256;
 
 template <int DKQ, int DV, bool VK>
 struct F32 {
     static constexpr int TK = DKQ > 128 ? 16 : 32;
+    static constexpr int kSides = DKQ > 128 ? 2 : 1;          // the scores' warps: 8 dim groups x row halves
+    static constexpr int kThreads = 256 * kSides;
     static constexpr int PK = DKQ + 4, PV = DV + 4;   // row pitches: conflict-free 16-byte reads
     static constexpr int kTile = TK * PK + (VK ? 0 : TK * PV);
     // two tiles where they fit beside Q
@@ -42,11 +45,11 @@ __device__ __forceinline__ float4 load4(const void *base, int64_t elem, int dtyp
 
 // Rows (cell, g) of a cache into shared memory as fp32: D elements at pitch D + 4, zeros where
 // the cell is -1.
-template <int D>
+template <int D, int THREADS>
 __device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype, const int64_t *cells,
                                           int n, int h_kv, int g) {
     constexpr int C = D / 4;
-    for (int e = threadIdx.x; e < n * C; e += kThreads) {
+    for (int e = threadIdx.x; e < n * C; e += THREADS) {
         const int r = e / C, c = e - r * C;
         const int64_t cell = cells[r];
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -66,11 +69,11 @@ __device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype
 }
 
 // The same of an fp32 cache by asynchronous copies.
-template <int D>
+template <int D, int THREADS>
 __device__ __forceinline__ void copy_rows(float *dst, const void *src, const int64_t *cells, int n, int h_kv, int g) {
     constexpr int C = D / 4;
     const uint32_t to = smem_u32(dst);
-    for (int e = threadIdx.x; e < n * C; e += kThreads) {
+    for (int e = threadIdx.x; e < n * C; e += THREADS) {
         const int r = e / C, c = e - r * C;
         const int64_t cell = cells[r];
         const float *row = reinterpret_cast<const float *>(src) + (cell < 0 ? 0 : cell * h_kv + g) * D;
@@ -88,7 +91,7 @@ __device__ __forceinline__ void store4(const Params &p, int64_t row, int dv, int
 }
 
 // x as hi + lo, tf32 both, by two integer and two fp32 operations (with cvt.rna.tf32 the kernel took
-// 1308 us at 300 tokens behind 4096, 576 wide; 1083 so).  A NaN that the addition carries out of
+// 1308 us at 300 tokens behind 4096, 576 wide, when it took 1083 so).  A NaN that the addition carries out of
 // the exponent is NaN in lo.
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
@@ -109,9 +112,10 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4]
 }
 
 template <int DKQ, int DV, bool VK>
-__global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int dtype) {
+__global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(const Params p, int dtype) {
     using L = F32<DKQ, DV, VK>;
     constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV, BUFS = L::kBufs, PP = L::kPP;
+    constexpr int kThreads = L::kThreads, SIDES = L::kSides, RT = 2 / SIDES;   // RT: 16-row tiles of a scoring warp
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sTile = sQ + kRows * PK;    // [BUFS] x (K rows, V rows)
     float *sRed = sTile + BUFS * L::kTile;
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
         sM[tid] = -INFINITY;
         sL[tid] = 0.f;
     }
-    constexpr int NT = DV / 64;   // 8-wide column tiles of a warp's value dims
+    constexpr int NT = DV / (kThreads / 4);   // 8-wide column tiles of a warp's value dims
     float acc[2][NT][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -174,12 +178,12 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
         float *k = sTile + b * L::kTile;
         const int64_t *cells = sCells + b * TK;
         if (ahead) {
-            copy_rows<DKQ>(k, p.K, cells, TK, p.h_kv, g);
-            if constexpr (!VK) copy_rows<DV>(k + TK * PK, p.V, cells, TK, p.h_kv, g);
+            copy_rows<DKQ, kThreads>(k, p.K, cells, TK, p.h_kv, g);
+            if constexpr (!VK) copy_rows<DV, kThreads>(k + TK * PK, p.V, cells, TK, p.h_kv, g);
             cp_async_commit();
         } else {
-            load_rows<DKQ>(k, p.K, dtype, cells, TK, p.h_kv, g);
-            if constexpr (!VK) load_rows<DV>(k + TK * PK, p.V, dtype, cells, TK, p.h_kv, g);
+            load_rows<DKQ, kThreads>(k, p.K, dtype, cells, TK, p.h_kv, g);
+            if constexpr (!VK) load_rows<DV, kThreads>(k + TK * PK, p.V, dtype, cells, TK, p.h_kv, g);
         }
     };
     const int first_pos = pos0 + r0 / p.G;   // the rows' first position
@@ -208,21 +212,22 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
         const float *sK = sTile + buf * L::kTile, *sV = VK ? sK : sK + TK * PK;
         const int64_t *sCell = sCells + buf * TK;
         __syncthreads();
-        {   // scores: warp w takes dims [w DKQ / 8, (w + 1) DKQ / 8)
+        {   // scores: warp w takes dims [x DKQ / 8, (x + 1) DKQ / 8), x = w mod 8, of its rows
             constexpr int KN = TK / 8;
-            float sc[2][KN][4];
+            const int x = warp & 7, row0 = (warp >> 3) * 16;
+            float sc[RT][KN][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int n = 0; n < KN; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sc[i][n][c] = 0.f;
-            const float *q = sQ + fr * PK + warp * (DKQ / 8) + fc, *k = sK + fr * PK + warp * (DKQ / 8) + fc;
+            const float *q = sQ + (row0 + fr) * PK + x * (DKQ / 8) + fc, *k = sK + fr * PK + x * (DKQ / 8) + fc;
 #pragma unroll
             for (int d = 0; d < DKQ / 8; d += 8) {
-                uint32_t ah[2][4], al[2][4], bh[KN][2], bl[KN][2];
+                uint32_t ah[RT][4], al[RT][4], bh[KN][2], bl[KN][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < RT; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         split_tf32(q[(16 * i + 8 * (c & 1)) * PK + d + 4 * (c >> 1)], ah[i][c], al[i][c]);
@@ -231,29 +236,29 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
 #pragma unroll
                     for (int c = 0; c < 2; ++c) split_tf32(k[8 * n * PK + d + 4 * c], bh[n][c], bl[n][c]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < RT; ++i)
 #pragma unroll
                     for (int n = 0; n < KN; ++n) mma_split(sc[i][n], ah[i], al[i], bh[n], bl[n]);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int n = 0; n < KN; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<float2 *>(sRed + (warp * kRows + 16 * i + 8 * c + fr) * TK + 8 * n + 2 * fc) =
+                        *reinterpret_cast<float2 *>(sRed + (x * kRows + row0 + 16 * i + 8 * c + fr) * TK + 8 * n + 2 * fc) =
                             make_float2(sc[i][n][2 * c], sc[i][n][2 * c + 1]);
         }
         if (tid == 0) s_odd = 0;
         __syncthreads();
-        {   // softmax of row tid / 8: TK / 8 keys a thread
-            constexpr int KPT = TK / 8;
-            const int r = tid >> 3, kk = tid & 7;
+        {   // softmax of row tid / TPR, KPT keys a thread
+            constexpr int TPR = kThreads / kRows, KPT = TK / TPR;
+            const int r = tid / TPR, kk = tid % TPR;
             const int pos = pos0 + (r0 + r) / p.G;
             float s[KPT], mx = -INFINITY;
 #pragma unroll
             for (int b = 0; b < KPT; ++b) {
-                const int k = kk + 8 * b;
+                const int k = kk + TPR * b;
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) v += sRed[(w * kRows + r) * TK + k];
@@ -266,17 +271,18 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
                 mx = fmaxf(mx, s[b]);
             }
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            for (int o = TPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
             const float mo = sM[r], mn = fmaxf(mo, mx);
             float sum = 0.f;
 #pragma unroll
             for (int b = 0; b < KPT; ++b) {
                 const float e = s[b] == -INFINITY ? 0.f : exp2f(s[b] - mn);
-                sP[r * PP + 8 * b + (kk & 1) * 4 + (kk >> 1)] = e;   // key slots: see below
+                const int k = kk + TPR * b;   // key slots: see below
+                sP[r * PP + (k & ~7) + (k & 1) * 4 + ((k & 7) >> 1)] = e;
                 sum += e;
             }
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            for (int o = TPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
             const float al = mn == -INFINITY ? 1.f : exp2f(mo - mn);
             __syncwarp();
             if (kk == 0) {
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[i][n][c] *= al;
             }
-        const int d0 = warp * (DV / 8);   // the warp's value dims
+        const int d0 = warp * (NT * 8);   // the warp's value dims
         if (!plain) {
             // Keys that some rows do not attend may hold NaN and infinities there, which a zero
             // weight does not cancel: such values are taken out of the tile, and added one by one to
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) chunk_f32_kernel(const Params p, int
         const int64_t o = (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.h_q + g * p.G + (r0 + row) % p.G;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int d = warp * (DV / 8) + 8 * n + 2 * fc;
+            const int d = warp * (NT * 8) + 8 * n + 2 * fc;
             const float x = acc[i >> 1][n][2 * (i & 1)] * inv, y = acc[i >> 1][n][2 * (i & 1) + 1] * inv;
             if (whole && p.o_bf16)
                 *reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + o * DV + d) = pack_bf16(x, y);
@@ -644,7 +650,7 @@ bool shape_ok(int dkq, int dv, bool has_v) {
 template <int DKQ, int DV, bool VK>
 int launch_f32(const Params &p, int dtype, cudaStream_t st) {
     if (!ensure_max_dynamic_smem(chunk_f32_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(F32<DKQ, DV, VK>::kThreads),
                    F32<DKQ, DV, VK>::bytes(), st, p, dtype) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
