@@ -466,3 +466,74 @@ def test_long_sums_keep_fp32(dev, shape, dtype, n_seq, length):
             ref[:, i * G:(i + 1) * G] = (p @ v[:, i]).view(-1, G, dv)
         err = float((O[rows].double() - ref).norm() / ref.norm())
         assert err <= 256 * 2.0 ** -24 + 2.0 ** -17, f"{err:.3g}"
+
+
+@pytest.mark.parametrize("shape,n_seq", [(N128, 40), (N64, 160), (WIDE, 80), (W512, 40)])
+@pytest.mark.parametrize("bad_pages", [0, 56])
+def test_long_sums_with_moving_maxima(dev, shape, n_seq, bad_pages):
+    """Long whole lists whose scores rise and fall by tens, by other amounts in other heads, so that
+    sums that were set aside are scaled again; and lists whose first 28 tiles hold no key at all.
+    Bound: weights off by twice the scores' error (dkq / 16 additions cut by at most a step, 2^-23 of
+    the score), and what test_long_sums_keep_fp32 allows."""
+    dkq, dv, sep, h_q, h_kv = shape
+    length, page = 9000, 64
+    g = torch.Generator(device=dev).manual_seed(dkq + bad_pages)
+    n_pages = -(-length // page)
+    randn = lambda *s: torch.randn(s, generator=g, device=dev)
+    # a walk of the scores, a step every 100 keys: about +-30 over the list
+    steps = torch.randn(-(-n_pages * page // 100), generator=g, device=dev) * 4
+    walk = steps.cumsum(0).repeat_interleave(100)[:n_pages * page]
+    u = torch.sign(randn(h_kv, dkq))
+    K = (randn(n_pages * page, h_kv, dkq) * 0.1 + walk.view(-1, 1, 1) * u / dkq ** 0.5).to(torch.bfloat16)
+    V = randn(n_pages * page, h_kv, dv).to(torch.bfloat16) if sep else None
+    G = h_q // h_kv
+    gain = torch.linspace(-1, 1, G, device=dev).view(1, 1, G, 1)
+    Q = (u.view(1, h_kv, 1, dkq) * gain + randn(n_seq, h_kv, G, dkq) * 0.05).reshape(n_seq, h_q, dkq).to(torch.bfloat16)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    table = torch.arange(n_pages, dtype=torch.int32, device=dev).repeat(n_seq, 1)
+    table[:, :bad_pages] = -1
+    O = torch.empty((n_seq, h_q, dv), device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    sfa.sfa_chunk_attend_paged(Q, K, V, table, page, i32(list(range(n_seq + 1))), i32([length] * n_seq), 1, length,
+                               1 / math.sqrt(dkq), O, dev_status=status)
+    assert sfa.sfa_read_device_status(status) == (sfa.SFA_DEV_BAD_CELL if bad_pages else 0)
+    k = K[bad_pages * page:length].double()
+    v = k[..., :dv] if V is None else V[bad_pages * page:length].double()
+    q = Q.double().view(n_seq, h_kv, G, dkq)
+    ref = torch.empty_like(O, dtype=torch.float64)
+    most = 0.0
+    for i in range(h_kv):
+        x = q[:, i].reshape(-1, dkq) @ k[:, i].T / math.sqrt(dkq)
+        most = max(most, float(x.abs().max()))
+        ref[:, i * G:(i + 1) * G] = (torch.softmax(x, -1) @ v[:, i]).view(n_seq, G, dv)
+    assert most > 10
+    err = float((O.double() - ref).norm() / ref.norm())
+    assert err <= 2 * dkq / 16 * 2.0 ** -23 * most + 256 * 2.0 ** -24 + 2.0 ** -17, f"{err:.3g}"
+
+
+@pytest.mark.parametrize("shape", [N128, N64, WIDE, W512, (128, 128, True, 12, 4), (576, 512, False, 12, 1)])
+def test_long_chunks_keep_fp32(dev, shape):
+    """The same with chunks: tiles full of rows and ones that are not (203 queries; 12 heads)."""
+    dkq, dv, sep, h_q, h_kv = shape
+    n_seq, new, length, page = 6, 203, 9000, 64
+    g = torch.Generator(device=dev).manual_seed(h_q + dkq)
+    n_pages = -(-length // page)
+    randn = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16)
+    K, V, Q = randn(n_pages * page, h_kv, dkq), randn(n_pages * page, h_kv, dv) if sep else None, randn(n_seq * new, h_q, dkq)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    table = torch.arange(n_pages, dtype=torch.int32, device=dev).repeat(n_seq, 1)
+    O = torch.empty((n_seq * new, h_q, dv), device=dev)
+    sfa.sfa_chunk_attend_paged(Q, K, V, table, page, i32([s * new for s in range(n_seq + 1)]), i32([length] * n_seq), new,
+                               length, 1 / math.sqrt(dkq), O)
+    G = h_q // h_kv
+    k = K[:length].double()
+    v = k[..., :dv] if V is None else V[:length].double()
+    hidden = torch.arange(length, device=dev)[None, :] > torch.arange(length - new, length, device=dev)[:, None]
+    for s in range(n_seq):
+        rows = slice(s * new, (s + 1) * new)
+        ref = torch.empty_like(O[rows], dtype=torch.float64)
+        for h in range(h_q):
+            x = (Q[rows, h].double() @ k[:, h // G].T / math.sqrt(dkq)).masked_fill(hidden, -math.inf)
+            ref[:, h] = torch.softmax(x, -1) @ v[:, h // G]
+        err = float((O[rows].double() - ref).norm() / ref.norm())
+        assert err <= 256 * 2.0 ** -24 + 2.0 ** -17, f"{err:.3g}"
