@@ -7,7 +7,7 @@ namespace sfa {
 namespace {
 
 // ------------------------------------------------------------------------ page tables, slots
-constexpr int kMapThreads = 512;
+constexpr int kMapThreads = 256;
 constexpr int64_t kMapFourFrom = 1 << 18;
 constexpr int kMapMaxSeq = 16384;   // offsets and page bases of every sequence fit shared memory
 
@@ -48,11 +48,12 @@ __device__ __forceinline__ int64_t map_taken(const MapParams &p, int64_t a, int6
 // by bisection in cu, their page from the table (the partly filled last page) or from the free
 // list, their cells; the first token of a page that is taken also writes the table's entry.
 // Integer sums in a fixed order: the maps are the same on every run.
-// A decode step is one CTA and latency (3.3 us); whole prompts are 16 bytes of stores per token:
-// 4.2 M tokens in 44 us with one token a thread and 64-bit divisions, 19 us (3.5 TB/s of stores) with
-// four a thread, 16-byte stores and one 32-bit division (a product) for the four.
+// A decode step is one CTA and latency (2.8 us); whole prompts are 16 bytes of stores per token:
+// 4.2 M tokens in 44 us with one token a thread and 64-bit divisions, 18 us (3.8 TB/s of stores) with
+// four a thread, 16-byte stores and one 32-bit division (a product) for the four.  (Eight a thread:
+// 25 us, a warp's stores no longer whole lines; CTAs of 512 threads and stores that stay in L2: 19.3.)
 template <int N>
-__global__ void __launch_bounds__(kMapThreads, N == 4 ? 3 : 4) page_maps_kernel(const MapParams p) {
+__global__ void __launch_bounds__(kMapThreads, 6) page_maps_kernel(const MapParams p) {
     extern __shared__ int32_t s_map[];
     int32_t *s_cu = s_map;                    // [n_seq + 1], clipped to n_tok_cap
     int32_t *s_base = s_map + p.n_seq + 1;    // [n_seq]
@@ -204,10 +205,10 @@ __global__ void __launch_bounds__(kMapThreads, N == 4 ? 3 : 4) page_maps_kernel(
             poss[k] = (int32_t)(pos < 0x7FFFFFFF ? pos : 0x7FFFFFFF);
         }
         auto vec = [](const int *v) { return make_int4(v[0], v[1 % N], v[2 % N], v[3 % N]); };
-        if (N == 4 && p.vec && 4 * q + 4 <= p.n_tok_cap) {
+        if (N == 4 && p.vec && 4 * q + 4 <= p.n_tok_cap) {   // slot is read next: it may stay in L2
             reinterpret_cast<int4 *>(p.slot)[q] = vec(cells);
-            reinterpret_cast<int4 *>(p.q_seq)[q] = vec(seqs);
-            reinterpret_cast<int4 *>(p.q_pos)[q] = vec(poss);
+            __stcs(reinterpret_cast<int4 *>(p.q_seq) + q, vec(seqs));
+            __stcs(reinterpret_cast<int4 *>(p.q_pos) + q, vec(poss));
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k)
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kMapThreads, N == 4 ? 3 : 4) page_maps_kernel(
             int32_t *row = p.cell_of + (int64_t)seqs[0] * p.n_pos_cap + poss[0];
             if (N == 4 && seqs[0] >= 0 && seqs[N - 1] == seqs[0] && (int64_t)poss[0] + 4 <= p.n_pos_cap &&
                 (reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
-                *reinterpret_cast<int4 *>(row) = vec(cells);
+                __stcs(reinterpret_cast<int4 *>(row), vec(cells));
             } else {
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
@@ -420,7 +421,7 @@ extern "C" int sfa_build_page_maps(const int32_t *len_old, const int32_t *len_ne
     const bool four = n_tok_cap > (int64_t)kMapFourFrom;
     const int per_block = (four ? 4 : 1) * kMapThreads;
     int64_t blocks = (n_tok_cap + per_block - 1) / per_block;
-    const int64_t most = (four ? 3 : 4) * (int64_t)device_sm_count();   // resident at once
+    const int64_t most = 6 * (int64_t)device_sm_count();   // resident at once
     blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
     auto kernel = four ? page_maps_kernel<4> : page_maps_kernel<1>;
     if (smem > 48 * 1024 && !ensure_max_dynamic_smem(kernel)) return SFA_ERR_CUDA;
