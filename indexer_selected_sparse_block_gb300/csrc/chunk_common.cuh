@@ -48,11 +48,11 @@ struct Seq {
 __device__ __forceinline__ Seq make_seq(const Params &p, int c0, int c1, int total, bool flag) {
     Seq q;
     q.c0 = c0;
-    q.total = total;
+    q.total = max(total, 0);   // negative: positions below 0 all the same, and no overflow
     bool bad = q.c0 < 0 || c1 < q.c0 || c1 > p.n_q;
     q.n = bad ? 0 : c1 - q.c0;
     // the positions follow from the true length: a clipped chunk keeps its first queries
-    if (q.n > p.n_new_max || q.total < q.n || q.total > p.n_kv_max ||
+    if (q.n > p.n_new_max || total < q.n || q.total > p.n_kv_max ||
         (int64_t)q.total > p.table_stride * p.page)
         bad = true;
     if (bad && flag) set_status(p.status, SFA_DEV_BAD_QUERY);
@@ -194,8 +194,8 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
 // closed form and a place in the line is found without a pass over the tiles.
 constexpr int kPieceKeys = 448;
 struct Unit {
-    int seq, tile, g, w;
-    int64_t u0;           // its place in the line
+    int seq, tile, g;
+    int64_t w, u0;        // its weight, its place in the line
     Seq q;
 };
 // One sequence's part of the line, a lane's of a group of 32.
@@ -304,7 +304,7 @@ __device__ __forceinline__ Unit share_unit(const Params &p, Share &h, int64_t x)
         else hi = m - 1;
     }
     u.tile = lo;
-    u.w = (int)(a + min((int64_t)(lo + 1) * p.item_q, (int64_t)n)) + kPieceKeys;
+    u.w = a + min((int64_t)(lo + 1) * p.item_q, (int64_t)n) + kPieceKeys;
     u.u0 = x - r + tile_weights(p, a, n, tiles, lo);
     return u;
 }

@@ -537,3 +537,17 @@ def test_long_chunks_keep_fp32(dev, shape):
             ref[:, h] = torch.softmax(x, -1) @ v[:, h // G]
         err = float((O[rows].double() - ref).norm() / ref.norm())
         assert err <= 256 * 2.0 ** -24 + 2.0 ** -17, f"{err:.3g}"
+
+
+@pytest.mark.parametrize("shape,dtype", [(N128, "bf16"), (N64, "bf16"), (WIDE, "bf16"), (N128, "f32")])
+def test_lengths_at_the_ends_of_int32(dev, shape, dtype):
+    """Device lengths that cannot be, the largest and smallest ones: flagged; the largest attends what
+    its pages hold, the smallest and negative ones nothing, the others are right."""
+    lens = [(3000, 3), (0, 90), (1566, 2), (2300, 60), (100, 7), (64, 1), (1500, 2), (0, 3)]   # the third: whole pages
+    c = Case(dev, lens, 32, shape, dtype, seed=3)
+    total = list(c.total)
+    total[2], total[4], total[5] = 2 ** 31 - 1, -2 ** 31, -1
+    assert c.call(total=total) == sfa.SFA_DEV_BAD_QUERY | sfa.SFA_DEV_BAD_CELL
+    c.check(total=total, kv_max=max(c.total))
+    for s in (4, 5):
+        assert bool((c.O[c.cu[s]:c.cu[s + 1]] == 0).all())
