@@ -615,6 +615,8 @@ int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_t *slot, in
  *        ascend within [0, n_q] (an empty chunk) and for len_total[s] < n_s (positions below 0
  *        attend nothing).
  *   workspace: sfa_chunk_attend_workspace_bytes(...) bytes for the same arguments.
+ *        No other call, a captured one included, may use it while this one runs; what it holds
+ *        before a call does not matter.  An fp32 O may hold sums while the call runs.
  * A page table entry outside [0, n_cells / page_size) sets SFA_DEV_BAD_CELL; its positions are
  * left out.  A query that attends nothing gives O = 0 and lse = -inf.  What unattended cells
  * hold does not matter where no query of the chunk attends them (unwritten cells may hold NaN).
