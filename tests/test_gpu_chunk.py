@@ -551,3 +551,31 @@ def test_lengths_at_the_ends_of_int32(dev, shape, dtype):
     c.check(total=total, kv_max=max(c.total))
     for s in (4, 5):
         assert bool((c.O[c.cu[s]:c.cu[s + 1]] == 0).all())
+
+
+def test_two_graphs_share_a_workspace(dev):
+    """Captured calls of two shapes on one workspace, replayed in turn on one stream."""
+    cases = [Case(dev, lens, 32, s, seed=i) for i, (s, lens) in enumerate(((WIDE, [(4000, 1), (2500, 1)]), (N128, DEALT)))]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=dev)
+    graphs, kept = [], []
+    for c in cases:
+        assert c.call() == 0
+        Q, table, cu, total = c.Q.to(dev), i32(c.table), i32(c.cu), i32(c.total)
+        O, lse = torch.empty_like(c.O), torch.empty_like(c.lse)
+        most = max(n for _, n in c.lens)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            sfa.sfa_chunk_attend_paged(Q, c.Kc, c.Vc, table, 32, cu, total, most, max(c.total), c.scale, O, lse=lse, workspace=ws)
+        graphs.append(graph)
+        kept.append((Q, table, cu, total, O, lse))
+    for _ in range(3):
+        for c, graph, (_, _, _, _, O, lse) in zip(cases, graphs, kept):
+            O.fill_(5.0)
+            graph.replay()
+    torch.cuda.synchronize()
+    for c, (_, _, _, _, O, lse) in zip(cases, kept):
+        n = c.cu[-1]
+        assert torch.equal(O[:n], c.O[:n]) and torch.equal(lse[:n], c.lse[:n])
