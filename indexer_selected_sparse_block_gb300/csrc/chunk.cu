@@ -428,13 +428,15 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
         rows = start.z * p.G;
         if (!start.x || row0 >= rows) return;
         n_pieces = 0;
+        bool ended = false;   // a list may end in the last of 32 slots: their number does not say
 #pragma unroll
         for (int x = 0; x < W; ++x) {   // lane 0: the start; lane l: the slot l behind it
-            if (n_pieces != 32 * x) break;   // ended
+            if (ended) break;
             const int d = c + lane + 32 * x;
             const int4 head = d > c && d < p.slots ? p.slot_info[2 * d] : make_int4(0, d >= p.slots, 0, 0);
             const unsigned ends = __ballot_sync(0xFFFFFFFFu, head.y != 0);
-            n_pieces += ends ? __ffs(ends) : 32;
+            ended = ends != 0;
+            n_pieces += ended ? __ffs(ends) : 32;
             if (d == c) part[x] = 2 * c + 1;
             else if (head.x && lane + 32 * x < n_pieces) part[x] = 2 * d;
         }

@@ -100,3 +100,8 @@ def check_close(got, ref, tol, what):
     assert not bool(bad.any()), (f"{what}: {int(bad.sum())} of {bad.numel()} beyond the bound, worst "
                                  f"{float(ratio[~torch.isnan(ratio)].max()) if (~torch.isnan(ratio)).any() else math.nan:.3g} x, "
                                  f"first at {torch.nonzero(bad)[0].tolist()}, {int(torch.isnan(got).sum())} NaN")
+
+
+def g_sum(n):
+    """The bound of attend_reference on a sum of n terms in fp32, relative to its terms' sizes."""
+    return 6 * math.sqrt(max(n, 1)) * 2 * U32
