@@ -164,6 +164,16 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _scratch(n_bytes, device, stream):
+    """A workspace for one call on `stream` (None: the current one).  It comes from that stream's
+    own pool: a block of another stream's may still be in use there, by work that this stream does
+    not wait for, and this one could be handed out there while the call still runs."""
+    if stream is None:
+        return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+
+
 def _check(fn: str, rc: int):
     if rc != SFA_OK:
         raise SfaError(fn, rc)
@@ -283,7 +293,7 @@ def sfa_topk_blocks_refine(lower, upper, q_idx, w, q_seq, q_pos, Kbar, compress_
     n_q, h_idx, d_idx = q_idx.shape
     need = sfa_topk_refine_workspace_bytes(n_q, n_blk_max)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q_pos.device)
+        workspace = _scratch(max(need, 16), q_pos.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     rc = lib().sfa_topk_blocks_refine(_p(lower), _p(upper), lower.stride(0), _p(q_idx), _p(w),
                                       _p(q_seq), _p(q_pos), n_q, h_idx, d_idx, _p(Kbar),
@@ -306,7 +316,7 @@ def sfa_topk_blocks(scores, q_pos, compress_ratio: int, top_k: int, n_blk_max: i
     n_q = q_pos.shape[0]
     need = sfa_topk_workspace_bytes(n_q, n_blk_max, top_k)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_pos.device)
+        workspace = _scratch(need, q_pos.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().sfa_topk_blocks(_p(scores, strided=True), scores.stride(0), _p(q_pos), n_q,
                                compress_ratio,
@@ -355,7 +365,7 @@ def sfa_gather_attend(Q, K, V, q_seq, q_pos, blk_idx, n_sel, top_k: int, compres
     n_kv_max = top_k * compress_ratio + compress_ratio - 1
     need = sfa_attend_workspace_bytes(n_q, h_q, h_kv, dv, n_kv_max)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _scratch(need, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().sfa_gather_attend(_p(Q), _p(K), _p(V), _dtype_code(K), n_seq, n_tok_cap, n_q, h_q,
                                  h_kv, dkq, dv, float(scale), _p(q_seq), _p(q_pos), _p(blk_idx),
@@ -378,7 +388,7 @@ def sfa_gather_attend_window(Q, K, V, q_seq, q_pos, blk_idx, n_sel, top_k: int,
     n_kv_max = sfa_window_kv_max(top_k, compress_ratio, window, part)
     need = sfa_attend_workspace_bytes(n_q, h_q, h_kv, dv, n_kv_max)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _scratch(need, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().sfa_gather_attend_window(_p(Q), _p(K), _p(V), _dtype_code(K), n_seq, n_tok_cap,
                                         n_q, h_q, h_kv, dkq, dv, float(scale), _p(q_seq),
@@ -438,7 +448,7 @@ def sfa_dense_attend(Q, K, V, q_seq, q_pos, n_kv_max: int, scale: float, O, lse=
     n_q, h_q, dkq, n_seq, n_tok_cap, h_kv, dv = _attn_dims(Q, K, V, O)
     need = sfa_attend_workspace_bytes(n_q, h_q, h_kv, dv, n_kv_max)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _scratch(need, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().sfa_dense_attend(_p(Q), _p(K), _p(V), _dtype_code(K), n_seq, n_tok_cap, n_q, h_q,
                                 h_kv, dkq, dv, float(scale), _p(q_seq), _p(q_pos), n_kv_max,
@@ -487,7 +497,7 @@ def sfa_gather_attend_paged(Q, K, V, cell_of, q_seq, q_pos, blk_idx, n_sel, top_
     n_kv_max = top_k * compress_ratio + compress_ratio - 1
     need = sfa_attend_workspace_bytes(n_q, h_q, h_kv, dv, n_kv_max)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _scratch(need, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().sfa_gather_attend_paged(_p(Q), _p(K), _p(V), _dtype_code(K), n_cells, _p(cell_of),
                                        n_seq, n_pos_cap, n_q, h_q, h_kv, dkq, dv, float(scale),
@@ -503,7 +513,7 @@ def sfa_dense_attend_paged(Q, K, V, cell_of, q_seq, q_pos, n_kv_max: int, scale:
     n_q, h_q, dkq, n_cells, n_seq, n_pos_cap, h_kv, dv = _paged_attn_dims(Q, K, V, O, cell_of)
     need = sfa_attend_workspace_bytes(n_q, h_q, h_kv, dv, n_kv_max)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _scratch(need, Q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().sfa_dense_attend_paged(_p(Q), _p(K), _p(V), _dtype_code(K), n_cells, _p(cell_of),
                                       n_seq, n_pos_cap, n_q, h_q, h_kv, dkq, dv, float(scale),
@@ -753,9 +763,7 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
         ws_bytes = _chunk_workspace(dev, code, n_seq, n_q, h_q, h_kv, dkq, dv, V is not None, n_new_max,
                                     n_kv_max, o_code)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=_U8, device=dev)
-            if stream is not None:   # freed on return: not before that stream is done
-                workspace.record_stream(stream)
+            workspace = _scratch(ws_bytes, dev, stream)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     _call(lib().sfa_chunk_attend_paged, dev, stream, Q.data_ptr(), K.data_ptr(),
