@@ -560,14 +560,16 @@ def _row_copy(dst, src):
 
 
 def sfa_copy_cache_rows_multi(pairs, stream=None) -> None:
-    """Several (dst, src) row copies as sfa_copy_cache_rows makes them, in one kernel launch."""
+    """Several (dst, src) row copies as sfa_copy_cache_rows makes them, in one kernel launch on the
+    device of the first tensor that is on one."""
     pairs = list(pairs)
     if len(pairs) > SFA_MAX_ROW_COPIES:
         raise ValueError(f"at most {SFA_MAX_ROW_COPIES} copies per call")
     arr = (_RowCopy * max(len(pairs), 1))(*[_row_copy(d, s) for d, s in pairs])
-    rc = lib().sfa_copy_cache_rows_multi(len(pairs), ctypes.cast(arr, ctypes.c_void_p),
-                                         _stream(stream))
-    _check("sfa_copy_cache_rows_multi", rc)
+    dev = next((t.get_device() for pair in pairs for t in pair if t.is_cuda), None)
+    if dev is None:
+        dev = torch.cuda.current_device()
+    _call(lib().sfa_copy_cache_rows_multi, dev, stream, len(pairs), ctypes.cast(arr, ctypes.c_void_p))
 
 
 def sfa_copy_cache_rows(dst, src, stream=None) -> None:

@@ -32,7 +32,9 @@ class Fake:
     def element_size(self):
         return self.dtype.itemsize
 
-    def stride(self, i=0):
+    def stride(self, i=None):
+        if i is None:
+            return tuple(self.stride(k) for k in range(len(self.shape)))
         n = 1
         for s in self.shape[i % len(self.shape) + 1:]:
             n *= s
