@@ -315,18 +315,20 @@ class SfaPagedCache:
                                  workspace=workspace, dev_status=self.status, stream=stream)
         return O
 
-    def release(self, seq: int):
-        """Empties sequence seq: its pages go to the end of the free list (reads its length and
-        the list's head on the host, so it is not for capture)."""
-        n = -(-int(self.length[seq]) // self.page_size)
-        pages = self.page_table[seq, :n]
-        pages = pages[pages >= 0]
-        head = int(self.free_head)
-        free = torch.cat([self.free_pages[head:], pages])
-        # in place: a captured step keeps reading these buffers
-        self.free_pages[self.n_pages - free.numel():] = free
-        self.free_head.fill_(self.n_pages - free.numel())
-        self.page_table[seq].fill_(-1)
-        if self.cell_of is not None:
-            self.cell_of[seq].fill_(-1)
-        self.length[seq] = 0
+    def release(self, seq: int, stream=None):
+        """Empties sequence seq: its pages go to the end of the free list.  On `stream`, behind what
+        it holds: the one that the steps run on.  (Reads the sequence's length and the list's head
+        on the host, so it is not for capture.)"""
+        with torch.cuda.stream(stream):
+            n = -(-int(self.length[seq]) // self.page_size)
+            pages = self.page_table[seq, :n]
+            pages = pages[pages >= 0]
+            head = int(self.free_head)
+            free = torch.cat([self.free_pages[head:], pages])
+            # in place: a captured step keeps reading these buffers
+            self.free_pages[self.n_pages - free.numel():] = free
+            self.free_head.fill_(self.n_pages - free.numel())
+            self.page_table[seq].fill_(-1)
+            if self.cell_of is not None:
+                self.cell_of[seq].fill_(-1)
+            self.length[seq] = 0
