@@ -297,11 +297,15 @@ class SfaPagedCache:
     def step(self, len_new, K=None, V=None, X=None, stream=None):
         """Pages and cells for len_new [n_seq] int32 new tokens a sequence (n_tok_cap in all, at
         most) and their rows K, V, X [n_tok_cap][...], packed sequence by sequence, into them."""
+        given = (("key", K, self.K), ("value", V, self.V), ("index key", X, self.X))
+        for name, rows, cells in given:
+            if rows is not None and cells is None:
+                raise ValueError(f"{name} rows for a cache that holds none (separate_v, d_idx)")
         B.sfa_build_page_maps(self.length, len_new, self.page_size, self.free_pages, self.free_head,
                               self.n_pages, self.page_table, self.cu_new, self.len_total,
                               self.q_seq, self.q_pos, self.slot, self._head_out,
                               cell_of=self.cell_of, dev_status=self.status, stream=stream)
-        pairs = [(r, c) for r, c in ((K, self.K), (V, self.V), (X, self.X)) if r is not None]
+        pairs = [(rows, cells) for _, rows, cells in given if rows is not None]
         B.sfa_write_cells(pairs, self.slot, dev_status=self.status, stream=stream)
         copies = [(self.length.unsqueeze(0), self.len_total.unsqueeze(0)),
                   (self.free_head, self._head_out)]
