@@ -264,7 +264,12 @@ class SfaPagedCache:
     graph (SfaStep.graphed), whose replays advance the lengths.  Rows past the step's last token
     are padding.  cell_of is the position -> cell map the other paged entry points and SfaStep
     take (pass the cache's X, K, V to them); q_seq and q_pos are the new tokens' sequences and
-    positions."""
+    positions.
+
+    A token that finds no page (SFA_DEV_NO_PAGES in status; SFA_DEV_BAD_LENGTH beyond max_pages)
+    counts in its sequence's length all the same, has no cell, and is left out of this attention
+    and every later one (SFA_DEV_BAD_CELL), also when pages come free: release that sequence and
+    feed it again."""
 
     def __init__(self, *, n_seq: int, n_pages: int, page_size: int, max_pages: int, n_tok_cap: int,
                  h_kv: int, dkq: int, dv: int, separate_v: bool = False, d_idx: int = 0,

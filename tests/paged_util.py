@@ -105,3 +105,39 @@ def check_close(got, ref, tol, what):
 def g_sum(n):
     """The bound of attend_reference on a sum of n terms in fp32, relative to its terms' sizes."""
     return 6 * math.sqrt(max(n, 1)) * 2 * U32
+
+
+def attend_exact(Q, K, V, cells, cu, total, scale, dv, product=0.0, p_round=0.0, o_round=0.0):
+    """What attend_reference gives, for long lists: on the tensors' device, a KV head at a time, from
+    each sequence's cells of its positions (a list or tensor; below 0: left out).  product: how far
+    one product of a score or a value may be off, relative, at worst and all one way; it moves a
+    score by product sum_d |q_d k_d|, and so a result by twice that A and by product A itself."""
+    dev, h_q, h_kv = Q.device, Q.shape[1], K.shape[1]
+    G = h_q // h_kv
+    O = torch.zeros((Q.shape[0], h_q, dv), dtype=torch.float64, device=dev)
+    L = torch.full((Q.shape[0], h_q), -math.inf, dtype=torch.float64, device=dev)
+    tol_o, tol_l = torch.zeros_like(O), torch.zeros((Q.shape[0], h_q), dtype=torch.float64, device=dev)
+    for s in range(len(total)):
+        n = cu[s + 1] - cu[s]
+        cell = torch.as_tensor(cells[s], dtype=torch.long, device=dev)
+        pos = torch.nonzero(cell >= 0)[:, 0]
+        cell = cell[pos]
+        if n == 0 or pos.numel() == 0:
+            continue
+        seen = pos[None, :] <= total[s] - n + torch.arange(n, device=dev)[:, None]
+        any_, cnt = seen.any(1)[:, None, None], seen.sum(1)
+        g_keys = torch.tensor([g_sum(int(c)) for c in cnt], dtype=torch.float64, device=dev)[:, None]
+        for i in range(h_kv):
+            rows, heads = slice(cu[s], cu[s + 1]), slice(i * G, (i + 1) * G)
+            k = K[cell, i].double()
+            v = k[:, :dv] if V is None else V[cell, i].double()
+            q = Q[rows, heads].double()
+            x = (torch.einsum("ngd,td->ngt", q, k) * scale).masked_fill(~seen[:, None], -math.inf)
+            p = torch.where(any_, torch.softmax(x, -1), torch.zeros_like(x))
+            O[rows, heads], L[rows, heads] = p @ v, torch.logsumexp(x, -1)
+            size = torch.einsum("ngd,td->ngt", q.abs(), k.abs()).masked_fill(~seen[:, None], 0.0).amax(-1) * abs(scale)
+            d = size * (g_sum(q.shape[-1]) + product) + 2.0 ** -20 * (1 + size)
+            tol_o[rows, heads] = ((2 * d + 2 * p_round + product + g_keys)[..., None] * (p @ v.abs())
+                                  + o_round * O[rows, heads].abs() + 1e-30)
+            tol_l[rows, heads] = d + g_keys + 4 * U32 * torch.where(any_[..., 0], L[rows, heads], 0.0).abs()
+    return O.cpu(), L.cpu(), tol_o.cpu(), tol_l.cpu()
