@@ -504,9 +504,10 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
 #pragma unroll
         for (int x = 0; x < W; ++x) {   // the piece's share of the sum, then its weight
+            const bool none = m[x] == -INFINITY && w[x] == 0.f;   // the row attends no key of it
             const float e = m[x] == -INFINITY ? 0.f : exp2f(m[x] - M);
             l += w[x] == 0.f ? 0.f : (m[x] == -INFINITY ? w[x] : e * w[x]);
-            w[x] = e;
+            w[x] = none ? -1.f : e;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
@@ -524,6 +525,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
                     const float f = __shfl_sync(0xFFFFFFFFu, w[x], cy & 31);
                     if (cy >> 5 == x) e = f;
                 }
+                if (e < 0.f) continue;   // what its sums hold there may be NaN
 #pragma unroll
                 for (int k = 0; k < C; ++k) {
                     acc[k].x = fmaf(e, v[y][k].x, acc[k].x);
