@@ -149,6 +149,7 @@ __device__ __forceinline__ int64_t cell_of(const Params &p, int s, int t) {
 // queries from q0 on, the first at position pos0) and KV head.  n_tiles 0 with whole: a list of no key.
 struct Piece {
     int seq, c0, q0, nq, pos0, g, len, k0, k1;
+    int r0;      // queries of the row tile before q0: 0, but for a piece that is done again
     int part;    // where its partial results go, in row tiles; -1: the piece is the whole list
     int state;   // kRun, kSkip (nothing to do), kEnd (no further piece)
     int head, ends;   // of a slot's share: the list began in an earlier slot; it ends in this one
@@ -157,6 +158,7 @@ enum { kRun, kSkip, kEnd };
 
 __device__ __forceinline__ void piece_rows(const Params &p, const Seq &q, int tile, Piece &w) {
     w.c0 = q.c0;
+    w.r0 = 0;
     w.q0 = tile * p.item_q;
     w.nq = min(p.item_q, min(q.n, p.n_new_max) - w.q0);
     w.pos0 = q.total - q.n + w.q0;
@@ -351,6 +353,50 @@ static __device__ __noinline__ Piece share_piece(const Params &p, int c, Share &
             p.slot_info[2 * c + 1] = make_int4(1, w.c0 + w.q0, w.nq, w.g);
     }
     return w;
+}
+
+// Values that are not finite.  A product gives a key that a query does not attend a weight of zero, and
+// zero times such a value is NaN: a NaN in a chunk's token would reach the queries before it that share
+// its row tile.  The kernels on tcgen05 look at their results: where one is NaN, they look for such
+// values among the keys that some query of the tile does not attend, and do the queries up to the
+// first of them (a group; then those up to the next one) again, over the keys before it.
+//
+// The first key in [a, b) of sequence seq whose values of KV head g are not all finite, b if there is
+// none; by one whole warp.  Positions without a cell read as zeros.
+template <int DV>
+__device__ __forceinline__ int first_odd(const Params &p, const void *rows, int stride, int seq, int g, int a, int b) {
+    for (int t0 = a; t0 < b; t0 += 32) {
+        const int t = t0 + (threadIdx.x & 31);
+        bool odd = false;
+        if (t < b) {
+            const int64_t cell = cell_of(p, seq, t);
+            if (cell >= 0) {
+                const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(rows) +
+                                                                 (cell * p.h_kv + g) * stride);
+                auto bad = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+                for (int i = 0; i < DV / 8; ++i) {
+                    const uint4 x = v[i];
+                    odd = odd || bad(x.x) || bad(x.y) || bad(x.z) || bad(x.w);
+                }
+            }
+        }
+        const unsigned any = __ballot_sync(0xFFFFFFFFu, odd);
+        if (any) return t0 + __ffs(any) - 1;
+    }
+    return b;
+}
+// The next group of piece w, whose queries before `from` are done: kEnd if its results are right.
+template <int DV>
+__device__ __forceinline__ Piece odd_group(const Params &p, const Piece &w, int from, int stride) {
+    Piece f = w;
+    const int a = max(max(w.k0, 0), w.pos0 + from + 1), t = first_odd<DV>(p, p.V ? p.V : p.K, stride, w.seq, w.g, a, w.k1);
+    f.r0 = from;
+    f.q0 += from;
+    f.pos0 += from;
+    f.nq = t - f.pos0;
+    f.k1 = t;
+    f.state = t >= w.k1 ? kEnd : w.part < 0 || f.k0 < f.k1 ? kRun : kSkip;   // a part without a key: nothing is read of it
+    return f;
 }
 
 // The kernel for 512 value dims on tcgen05 CTA pairs (chunk_wide.cu): queries of one CTA's 64

@@ -109,10 +109,13 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 // By way of shared memory (C * 128 bytes at `stage`): a row's values leave as one line.  (Each lane
 // storing its own row's 16 bytes took 5.8 us for 64 rows of 512 fp32 values and 32 sectors a
 // store.)  16-byte pieces are exchanged by the row's number, so neither side meets bank conflicts.
+// Returns look and whether the lane's row has a NaN here (the maximum of three with NaN: two values an
+// instruction, which costs nothing that can be measured).
 template <int C, int DV>
-__device__ __forceinline__ void store_tile(const Params &p, uint32_t stage, uint32_t tcol, float inv,
-                                           bool live, int64_t row, bool whole, int d0) {
+__device__ __forceinline__ bool store_tile(const Params &p, uint32_t stage, uint32_t tcol, float inv,
+                                           bool live, int64_t row, bool whole, int d0, bool look) {
     constexpr int PIECES = C / 4;   // of a row
+    float most = -INFINITY;         // NaN once a value is
     const int lane = threadIdx.x & 31;
     const uint32_t mine = stage + lane * (C * 4);
 #pragma unroll 1
@@ -125,6 +128,8 @@ __device__ __forceinline__ void store_tile(const Params &p, uint32_t stage, uint
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(r[4 * j + k]) * inv;
+            asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(most) : "f"(v[0]), "f"(v[1]));
+            asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(most) : "f"(v[2]), "f"(v[3]));
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
                              mine + (((x * 8 + j) ^ (lane & (PIECES - 1))) << 4)),
                          "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
@@ -151,6 +156,7 @@ __device__ __forceinline__ void store_tile(const Params &p, uint32_t stage, uint
         else
             *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + to) = v;
     }
+    return look && most != most;
 }
 
 // fp32 results: tensor memory sums kDrain tiles only, then the sums move on.  The tensor cores cut

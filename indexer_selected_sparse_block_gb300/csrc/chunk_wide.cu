@@ -64,11 +64,24 @@ struct Wide {
     static constexpr int kOffRope = kOffBuf + 2 * kSlots * kSlab;
     static constexpr int kOffP = kOffRope + (kRope ? kSlab : 0);
     static constexpr int kOffMax = kOffP + kPSlabs * kSlab;    // float [2][256]
-    static constexpr int kOffItem = kOffMax + 2 * 256 * 4;     // Item, padded
+    static constexpr int kOffItem = kOffMax + 2 * 256 * 4;     // Item and Group, 32 bytes each
     static constexpr int kOffBar = kOffItem + 64;
     static constexpr int kBars = 1 + 2 * kSlots + 2 + 2 + 2 + 2 + 1;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
     static_assert(kBytes <= 227 * 1024, "fits one CTA per SM");
+};
+
+// What a pass works on: nq queries of a row tile, from its query r0 on (at position pos0 of q0), and keys k0 .. k1.
+struct Work {
+    Item it;
+    int item, g, split, q0, pos0, len, k0;
+    int r0, nq, k1, n_tiles;
+    int tb, np;        // tiles and passes before: the barriers' phases go on
+    uint32_t tmem;
+};
+// Queries that are done again (odd_group).
+struct Group {
+    int state, r0, nq, k1;
 };
 
 struct WideMaps {
@@ -95,6 +108,15 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
 }
+// A word into this shared address of the pair's CTA `rank`.
+__device__ __forceinline__ void store_in(uint32_t saddr, uint32_t rank, int v) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(saddr),
+        "r"(rank), "r"(v)
+        : "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -116,90 +138,53 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
         : "memory");
 }
 // --------------------------------------------------------------------------------- the kernel
+// The words behind the barriers: tensor memory's address; a wait ran out; a result of either CTA is not
+// finite; in the first CTA: a wait of the other one's ran out.
+enum { kWordTmem, kWordAbort, kWordOdd, kWordOtherAbort };
+
+// Where a list has no key: zeros.
+__device__ __forceinline__ void wide_zeros(const Params &p, const Work &wk, int qpc) {
+    const int warp = threadIdx.x >> 5, c = (int)cluster_rank(), G = p.G;
+    const int row = (warp & 1) * 32 + (threadIdx.x & 31), part = 2 * ((warp >> 1) & 1) + (warp >> 2);
+    const int ql = row / G, h = row - ql * G;
+    if (warp >= 8 || ql >= qpc || c * qpc + ql >= wk.nq) return;
+    const int64_t orow = (int64_t)(wk.it.q.c0 + wk.q0 + wk.r0 + c * qpc + ql) * p.h_q + wk.g * G + h;
+    for (int d = part * 128; d < (part + 1) * 128; d += 4) {
+        if (p.o_bf16)
+            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d) = make_uint2(0, 0);
+        else
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * 512 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (part == 0 && p.lse) p.lse[orow] = -INFINITY;
+}
+
 template <int DKQ, bool VK, bool HL>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
-    chunk_wide_kernel(const __grid_constant__ WideMaps maps, const Params p, int bxs, int qpc, int n_cells) {
+__device__ __forceinline__ void wide_pass(const WideMaps &maps, const Params &p, int bxs, int qpc, int n_cells,
+                                          uint8_t *smem, const Work &wk) {
     using L = Wide<DKQ, HL>;
     constexpr bool SPLIT = L::kSplit;
-    extern __shared__ __align__(1024) uint8_t smem[];
     float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
-    Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kBars);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *words = reinterpret_cast<volatile int *>(bars + L::kBars), *abort_flag = words + kWordAbort;
     const uint32_t bar0 = smem_u32(bars);
     // barriers, as shared addresses
     const uint32_t b_q = bar0, b_full = bar0 + 8, b_empty = b_full + 8 * kSlots, b_rope = b_empty + 8 * kSlots,
                    b_ropeDone = b_rope + 8, b_s = b_ropeDone + 8, b_p = b_s + 16, b_pv = b_p + 16,
                    b_drain = b_pv + 16;
-
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = (int)cluster_rank();
-    const int item = blockIdx.x >> 1, g = blockIdx.y, split = blockIdx.z;
-    // the barriers, tensor memory and the pair's meeting need nothing from global memory: they
-    // overlap the search for the item
-    if (tid == 0) {
-        const int ip = (int)(b_p - bar0) / 8;
-        // P (half 0) ready: eight warps of each CTA; P half 1: four of each
-        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 16 : i == ip + 1 ? 8 : 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                         smem_u32(tmem_slot))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
-    pdl_wait();
-    if (warp == 0) {
-        const Item it = find_item(p, item, (blockIdx.x & 1) == 0 && g == 0 && split == 0);
-        if (lane == 0) *sItem = it;
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    auto leave = [&]() {   // both CTAs of the pair, with nothing in flight
-        if (warp == 12)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-    };
-    const Item it = *sItem;
-    if (it.seq < 0) return leave();
-    const int q0 = it.tile * p.item_q;                        // first query of the tile
-    const int nq = min(p.item_q, min(it.q.n, p.n_new_max) - q0);
-    const int pos0 = it.q.total - it.q.n + q0;                // its position
-    const int len = max(0, min(key_limit(p, it.q), pos0 + nq));
-    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
-    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
-    if (split > 0 && k0 >= k1) return leave();                // no such piece
-    const bool whole = len <= p.split_keys;
-    const int n_tiles = (k1 - k0 + kT - 1) / kT;
-    const int G = p.G;
+    const Item &it = wk.it;
+    const int item = wk.item, g = wk.g, split = wk.split, q0 = wk.q0, r0 = wk.r0, nq = wk.nq, pos0 = wk.pos0;
+    const int k0 = wk.k0, k1 = wk.k1, n_tiles = wk.n_tiles, tb = wk.tb, np = wk.np, G = p.G;
+    const bool whole = wk.len <= p.split_keys;
+    const uint32_t tmem = wk.tmem;
 
     // a softmax thread's row: query ql of this CTA's qpc, head h.  Both halves hh of the tensor
     // memory lanes have every row, and two warps (cg) share a lane's columns.
     const int row = (warp & 1) * 32 + lane, hh = (warp >> 1) & 1, cg = warp >> 2;
     const int ql = row / G, h = row - ql * G;
     const bool live = warp < 8 && ql < qpc && c * qpc + ql < nq;
-    const int64_t orow = (int64_t)(it.q.c0 + q0 + c * qpc + ql) * p.h_q + g * G + h;
-
-    if (n_tiles == 0) {   // nothing to attend: zeros
-        if (live) {
-            for (int d = (2 * hh + cg) * 128; d < (2 * hh + cg + 1) * 128; d += 4) {
-                if (p.o_bf16)
-                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + orow * 512 + d) = make_uint2(0, 0);
-                else
-                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + orow * 512 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            if (hh == 0 && cg == 0 && p.lse) p.lse[orow] = -INFINITY;
-        }
-        return leave();
-    }
+    const int64_t orow = (int64_t)(it.q.c0 + q0 + r0 + c * qpc + ql) * p.h_q + g * G + h;
 
     const uint32_t tS = tmem, tO = tmem + 128;   // S: 2 x 64 columns, O: 2 x 128
     const uint32_t buf0 = smem_u32(smem + L::kOffBuf), sQ = smem_u32(smem + L::kOffQ),
@@ -222,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         if (j == 0 && elect_one()) {
             if (c == 0) mbar_arrive_expect_tx(bars, 2u * L::kNSK * 128u * (uint32_t)(qpc * G));
             for (int d = 0; d < L::kNSK; ++d)
-                tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + c * qpc, lead);
+                tma2_load(sQ + d * kSlab, &maps.q, d * 64, g * G, it.q.c0 + q0 + r0 + c * qpc, lead);
         }
         __syncwarp();
         const uint32_t s_full = b_full + j * 8, s_empty = b_empty + j * 8, v_full = s_full + 32, v_empty = s_empty + 32;
@@ -243,17 +228,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 };
                 int ps = k0 + c * 64, pv = k0 + half * 64;
                 int es = entry(ps), ev = entry(pv);
-                bool there = true;
+                bool there = tb == 0;
                 for (int t = -1; t < n_tiles && ok; ++t) {
+                    const int T = tb + t;
                     if (t + 1 < n_tiles) {
                         const int r = row(es, ps), v = rows_in(r, ps);
                         es = entry(ps + kT);
-                        if (!there) wait(s_empty, t & 1);
+                        if (!there) wait(s_empty, T & 1);
                         if (!ok) break;
                         expect(s_full, 4u * kSlab);
                         load_slabs_one<2, kSlab, true>(r, v, s_at, maps.kv.k, 128 * j, g, n_cells, lead + (s_full - bar0));
                         if (L::kRope && j == 3) {
-                            wait(b_ropeDone, t & 1);
+                            wait(b_ropeDone, T & 1);
                             if (!ok) break;
                             expect(b_rope, 2u * kSlab);
                             load_slabs_one<1, kSlab, true>(r, v, sRope, maps.kv.k, 512, g, n_cells, lead + (b_rope - bar0));
@@ -261,17 +247,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                         ps += kT;
                     }
                     if (t >= 0) {
-                        there = mbar_test_wait(v_empty, (t & 1) ^ 1);
+                        there = mbar_test_wait(v_empty, (T & 1) ^ 1);
                         const int r = row(ev, pv), v = rows_in(r, pv);
                         ev = entry(pv + kT);
-                        if (!there) wait(v_empty, (t & 1) ^ 1);
+                        if (!there) wait(v_empty, (T & 1) ^ 1);
                         if (!ok) break;
-                        there = t + 2 < n_tiles && mbar_test_wait(s_empty, (t + 1) & 1);
+                        there = t + 2 < n_tiles && mbar_test_wait(s_empty, (T + 1) & 1);
                         expect(v_full, 4u * kSlab);
                         load_slabs_one<2, kSlab, true>(r, v, v_at, vm, vx, g, n_cells, lead + (v_full - bar0));
                         pv += kT;
                     } else {
-                        there = n_tiles > 1 && mbar_test_wait(s_empty, 0);
+                        there = n_tiles > 1 && mbar_test_wait(s_empty, (T + 1) & 1);
                     }
                 }
             }
@@ -287,13 +273,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 __syncwarp();
             };
             for (int t = -1; t < n_tiles && ok; ++t) {
+                const int T = tb + t;
                 if (t + 1 < n_tiles) {
                     find_rows(hs, p, n_cells);
-                    slot_free(s_full, s_empty, (t & 1), 4u * kSlab);
+                    slot_free(s_full, s_empty, (T & 1), 4u * kSlab);
                     if (!ok) break;
                     load_slabs<2, kSlab, true>(hs, s_at, maps.kv.k, 128 * j, g, bxs, lead + (s_full - bar0));
                     if (L::kRope && j == 3) {
-                        slot_free(b_rope, b_ropeDone, (t & 1), 2u * kSlab);
+                        slot_free(b_rope, b_ropeDone, (T & 1), 2u * kSlab);
                         if (!ok) break;
                         load_slabs<1, kSlab, true>(hs, sRope, maps.kv.k, 512, g, bxs, lead + (b_rope - bar0));
                     }
@@ -301,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 }
                 if (t >= 0) {
                     find_rows(hv, p, n_cells);
-                    slot_free(v_full, v_empty, (t & 1) ^ 1, 4u * kSlab);
+                    slot_free(v_full, v_empty, (T & 1) ^ 1, 4u * kSlab);
                     if (!ok) break;
                     load_slabs<2, kSlab, true>(hv, v_at, vm, vx, g, bxs, lead + (v_full - bar0));
                     read_entries(hv, p, table, k0 + (t + 1) * kT + half * 64, k1, bxs);
@@ -322,43 +309,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 if (!there) wait(bar, parity);
                 tc_fence_after();
             };
-            auto s_ops = [&](int t, int i0, int i1) {
+            auto s_ops = [&](int T, int i0, int i1) {
                 for (int i = i0; i < i1; ++i) {
-                    take(b_full + i * 8, t & 1);
+                    take(b_full + i * 8, T & 1);
                     if (!ok) return;
-                    there = i < 3 ? mbar_test_wait(b_full + (i + 1) * 8, t & 1)
-                                  : L::kRope && mbar_test_wait(b_rope, t & 1);
+                    there = i < 3 ? mbar_test_wait(b_full + (i + 1) * 8, T & 1)
+                                  : L::kRope && mbar_test_wait(b_rope, T & 1);
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma2(tS + (t & 1) * 64, dQ + (uint64_t)(((2 * i + s) * kSlab + kk * 32) >> 4),
+                            mma2(tS + (T & 1) * 64, dQ + (uint64_t)(((2 * i + s) * kSlab + kk * 32) >> 4),
                                  dBuf + (uint64_t)(((2 * i + s) * kSlab + kk * 32) >> 4), idS,
                                  (i > 0 || s > 0 || kk > 0) ? 1u : 0u);
                     commit2(b_empty + i * 8);
                 }
             };
-            auto s_end = [&](int t) {
+            auto s_end = [&](int T) {
                 if (L::kRope) {
-                    take(b_rope, t & 1);
+                    take(b_rope, T & 1);
                     if (!ok) return;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma2(tS + (t & 1) * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
+                        mma2(tS + (T & 1) * 64, dQ + (uint64_t)((8 * kSlab + kk * 32) >> 4),
                              dRope + (uint64_t)((kk * 32) >> 4), idS, 1u);
                     commit2(b_ropeDone);
                 }
-                commit2(b_s + (t & 1) * 8);
+                commit2(b_s + (T & 1) * 8);
                 there = false;
             };
             auto pv_ops = [&](int t, int half) {
-                if (SPLIT || half == 0) wait(b_p + half * 8, t & 1);
+                const int T = tb + t;
+                if (SPLIT || half == 0) wait(b_p + half * 8, T & 1);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const int i = 2 * half + n;
-                    take(b_full + (4 + i) * 8, t & 1);
+                    take(b_full + (4 + i) * 8, T & 1);
                     if (!ok) return;
-                    there = n == 0 ? mbar_test_wait(b_full + (5 + i) * 8, t & 1) : false;
+                    there = n == 0 ? mbar_test_wait(b_full + (5 + i) * 8, T & 1) : false;
 #pragma unroll
                     for (int x = 0; x < (HL ? 2 : 1); ++x)
 #pragma unroll
@@ -370,16 +358,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 }
                 if (SPLIT || half == 1) commit2(b_pv + half * 8);
             };
-            wait(b_q, 0);
+            wait(b_q, np & 1);
             for (int t = -1; t < n_tiles && ok; ++t) {
                 const bool more = t + 1 < n_tiles;
-                if (more) s_ops(t + 1, 0, SPLIT ? 2 : 4);
-                if (!SPLIT && more && ok) s_end(t + 1);
+                if (more) s_ops(tb + t + 1, 0, SPLIT ? 2 : 4);
+                if (!SPLIT && more && ok) s_end(tb + t + 1);
                 if (SPLIT) there = false;
                 if (t >= 0 && ok) pv_ops(t, 0);
                 if (SPLIT && more && ok) {
-                    s_ops(t + 1, 2, 4);
-                    if (ok) s_end(t + 1);
+                    s_ops(tb + t + 1, 2, 4);
+                    if (ok) s_end(tb + t + 1);
                 }
                 if (t >= 0 && ok) pv_ops(t, 1);
             }
@@ -391,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         __syncwarp();
     } else if (warp < 8) {
         // ------------------------------------------------------------------------------ softmax
-        const int pos = pos0 + c * qpc + ql;                  // the row's last key
+        const int pos = pos0 + r0 + c * qpc + ql;             // the row's last key
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const bool neg = p.scale_log2 < 0.f;
         // a zero scale: weights of 1 to 1e-28
@@ -400,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
         float m_sum = -INFINITY;                              // m of the sums that have moved on
         auto part_row = [&]() {
-            return (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.part_rows + (c * qpc + ql) * G + h;
+            return (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.part_rows + (r0 + c * qpc + ql) * G + h;
         };
         auto drain = [&](bool first, bool back) {   // columns 128 cg ..: dims 256 cg + 128 hh ..
             drain_tile<128, 512>(whole ? reinterpret_cast<float *>(p.O) : p.part_o, tO + cg * 128 + lane_addr,
@@ -410,7 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         auto read_entry = [&](int key) { return key < k1 ? __ldg(table + p.page_div.div(key)) : 0; };
         int entry = read_entry(kq + lane);
         for (int t = 0; t < n_tiles; ++t) {
-            const uint32_t b = t & 1, par = (t >> 1) & 1;
+            const int T = tb + t;
+            const uint32_t b = T & 1, par = (T >> 1) & 1;
             const int kb = kq + t * kT;
             // bit j: key kb + j has a cell (its entry was read a tile ago)
             const bool cell = kb + lane >= k1 || (entry >= 0 && entry < p.n_pages);
@@ -419,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             entry = read_entry(kb + kT + lane);
             const int last = min(pos, k1 - 1) - kb;           // the last key attended, from kb
             if (HL && t > 0 && t % kDrain == 0) {   // here, where few registers are in use
-                wait(b_pv + 8, (t - 1) & 1);
+                wait(b_pv + 8, (T - 1) & 1);
                 tc_fence_after();
                 drain(t == kDrain, false);
                 m_sum = m;
@@ -470,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             }
             l = l * alpha + (sum[0] + sum[1]);
             // the products of the tile before are done with P and O
-            if (t > 0) wait(b_pv + 8, (t - 1) & 1);
+            if (t > 0) wait(b_pv + 8, (T - 1) & 1);
             if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
                 tc_fence_after();
 #pragma unroll 1
@@ -496,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 if (hh == 1) {   // O is rescaled; then P's second half, when the first is used up
                     __syncwarp();
                     if (lane == 0) arrive_cluster(p_ready0);
-                    wait(b_pv, t & 1);
+                    wait(b_pv, T & 1);
                 }
                 write(hi, sP);
                 write(lo, sP + kSlab);
@@ -513,13 +502,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
         // -------------------------------------------------------------------------------- result
         {   // the buffer that the last tile's maxima did not use
-            float *lb = sMax + (n_tiles & 1) * 256;
+            float *lb = sMax + ((tb + n_tiles) & 1) * 256;
             lb[tid] = l;
             named_barrier(1, 256);
             l = (l + lb[tid ^ 64]) + (lb[tid ^ 128] + lb[tid ^ 192]);
         }
         if (tid == 0 && p.n_split > 1) let_next_start();   // the merge: what else may follow is not known
-        wait(b_pv + 8, (n_tiles - 1) & 1);
+        wait(b_pv + 8, (tb + n_tiles - 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         if (ok) {
@@ -528,8 +517,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             if (HL && n_tiles > kDrain) drain(false, true);
             const int64_t part = part_row();
             // columns 128 cg ..: dims 256 cg + 128 hh ..; every operand is used up
-            store_tile<128, 512>(p, buf0 + warp * 16384, tO + cg * 128 + lane_addr, inv, live,
-                                 whole ? orow : part, whole, cg * 256 + hh * 128);
+            // NaN counts where there are keys that some query does not attend
+            if (store_tile<128, 512>(p, buf0 + warp * 16384, tO + cg * 128 + lane_addr, inv, live, whole ? orow : part,
+                                     whole, cg * 256 + hh * 128, live && k1 > pos0 + 1)) {
+                store_in(smem_u32(bars + L::kBars) + 4 * kWordOdd, 0, 1);
+                store_in(smem_u32(bars + L::kBars) + 4 * kWordOdd, 1, 1);
+            }
             if (live && hh == 0 && cg == 0) {
                 if (!whole) {
                     p.part_ml[part * 2] = m;
@@ -541,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
     }
 
-    // -------------------------------------------------------------------------------- teardown
+    // ------------------------------------------------------------------------- the pass's end
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -553,8 +546,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     __syncwarp();
     cluster_sync_all();   // neither CTA leaves while the other's products or arrivals need it
     tc_fence_after();
-    if (warp == 12)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// The groups of queries that are done again (odd_group), until there is none: the pair's first CTA says
+// which.  Inlined, with a pass of its own: a call that is not, or one loop over passes, takes the kernel's
+// products and copies out of uniform registers (512 tokens behind 8192 took 103 to 107 us, and 100; 98 so,
+// 97 without groups; one token at 4096 13.4, 13.0 without).
+template <int DKQ, bool VK, bool HL>
+__device__ __forceinline__ void wide_again(const WideMaps &maps, const Params &p, int bxs, int qpc, int n_cells, Work wk) {
+    using L = Wide<DKQ, HL>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, c = (int)cluster_rank();
+    volatile int *words = reinterpret_cast<volatile int *>(smem + L::kOffBar + 8 * L::kBars);
+    const Group *group = reinterpret_cast<const Group *>(smem + L::kOffItem + 32);
+    const int end = wk.k1;
+    int done = 0;
+    for (;;) {
+        wk.tb += wk.n_tiles;
+        wk.np += wk.n_tiles > 0;
+        if (c == 1 && tid == 0)
+            store_in(smem_u32(smem + L::kOffBar + 8 * L::kBars) + 4 * kWordOtherAbort, 0, words[kWordAbort]);
+        fence_proxy_async_smem();   // the next pass's loads land where the results passed
+        __syncwarp();
+        cluster_sync_all();
+        if (c == 0 && warp == 0) {
+            Piece w;
+            w.seq = wk.it.seq;
+            w.g = wk.g;
+            w.q0 = wk.q0;
+            w.pos0 = wk.pos0;
+            w.k0 = wk.k0;
+            w.k1 = end;
+            w.part = wk.len <= p.split_keys ? -1 : 0;
+            const Piece f = odd_group<512>(p, w, done, VK ? DKQ : 512);
+            if ((tid & 31) == 0) {
+                const int v[4] = {words[kWordAbort] || words[kWordOtherAbort] ? (int)kEnd : f.state, f.r0, f.nq, f.k1};
+                for (int i = 0; i < 8; ++i) store_in(smem_u32(group) + 4 * (i & 3), i >> 2, v[i & 3]);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+        if (group->state == kEnd) return;
+        wk.r0 = group->r0;
+        wk.nq = group->nq;
+        wk.k1 = group->k1;
+        done = wk.r0 + wk.nq;
+        wk.n_tiles = max(0, (wk.k1 - wk.k0 + kT - 1) / kT);
+        if (wk.n_tiles > 0) wide_pass<DKQ, VK, HL>(maps, p, bxs, qpc, n_cells, smem, wk);
+        else if (group->state == kRun) wide_zeros(p, wk, qpc);
+    }
+}
+
+template <int DKQ, bool VK, bool HL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    chunk_wide_kernel(const __grid_constant__ WideMaps maps, const Params p, int bxs, int qpc, int n_cells) {
+    using L = Wide<DKQ, HL>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Item *sItem = reinterpret_cast<Item *>(smem + L::kOffItem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+    volatile int *words = reinterpret_cast<volatile int *>(bars + L::kBars);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Work wk;
+    wk.item = blockIdx.x >> 1;
+    wk.g = blockIdx.y;
+    wk.split = blockIdx.z;
+    // the barriers, tensor memory and the pair's meeting need nothing from global memory: they
+    // overlap the search for the item
+    if (tid == 0) {
+        const int ip = 1 + 2 * kSlots + 2 + 2;   // b_p
+        // P (half 0) ready: eight warps of each CTA; P half 1: four of each
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bars + i, i == ip ? 16 : i == ip + 1 ? 8 : 1);
+        words[kWordAbort] = words[kWordOdd] = words[kWordOtherAbort] = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(bars + L::kBars))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    if (warp == 0) {
+        const Item it = find_item(p, wk.item, (blockIdx.x & 1) == 0 && wk.g == 0 && wk.split == 0);
+        if (lane == 0) *sItem = it;
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    tc_fence_after();
+    wk.tmem = (uint32_t)words[kWordTmem];
+    auto leave = [&]() {   // both CTAs of the pair, with nothing in flight
+        if (warp == 12)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(wk.tmem) : "memory");
+    };
+    wk.it = *sItem;
+    if (wk.it.seq < 0) return leave();
+    wk.q0 = wk.it.tile * p.item_q;                            // first query of the tile
+    wk.r0 = 0;
+    wk.nq = min(p.item_q, min(wk.it.q.n, p.n_new_max) - wk.q0);
+    wk.pos0 = wk.it.q.total - wk.it.q.n + wk.q0;              // its position
+    wk.len = max(0, min(key_limit(p, wk.it.q), wk.pos0 + wk.nq));
+    wk.k0 = (int)min((int64_t)wk.len, (int64_t)wk.split * p.split_keys);
+    wk.k1 = (int)min((int64_t)wk.len, (int64_t)wk.k0 + p.split_keys);
+    if (wk.split > 0 && wk.k0 >= wk.k1) return leave();       // no such piece
+    wk.n_tiles = (wk.k1 - wk.k0 + kT - 1) / kT;
+    wk.tb = wk.np = 0;
+    if (wk.n_tiles == 0) {   // nothing to attend
+        wide_zeros(p, wk, qpc);
+        return leave();
+    }
+    wide_pass<DKQ, VK, HL>(maps, p, bxs, qpc, n_cells, smem, wk);
+    if (words[kWordOdd]) wide_again<DKQ, VK, HL>(maps, p, bxs, qpc, n_cells, wk);
+    leave();
 }
 
 template <int DKQ, bool VK, bool HL>

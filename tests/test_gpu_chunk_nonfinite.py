@@ -113,3 +113,79 @@ def test_pieces_that_a_row_does_not_attend(dev, shape, out, many):
     c = Chunks(dev, shape, [(total - 3, 3)], odd, out=out, seed=dkq)
     assert c.call() == need
     c.check()
+
+
+N128K, N64K, G1 = (128, 128, False, 4, 4), (64, 64, False, 8, 2), (512, 512, True, 2, 2)
+SHAPES = [WIDE, W512, W512K, G1, N128, N128K, N64, N64K]
+NAN, INF = math.nan, math.inf
+
+
+def odd_tokens(shape, lens):
+    """In every sequence's chunk: its second token, one in the middle and the last, other values and KV
+    heads each; in the first sequence every token from the sixth on."""
+    odd = []
+    for s, (a, n) in enumerate(lens):
+        for k, pos in enumerate(sorted({a + min(1, n - 1), a + n // 2, a + n - 1})):
+            odd.append((s, pos, (s + k) % shape[4], (7 * k + s) % shape[1], (NAN, INF, -INF)[k % 3]))
+    odd += [(0, lens[0][0] + j, 0, j % shape[1], NAN) for j in range(5, lens[0][1])]
+    return odd
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+def test_later_tokens(dev, shape, dtype, out):
+    """Chunks of one to 150 tokens behind none to 700, odd tokens all over them."""
+    lens = [(100, 30), (5, 3), (0, 40), (127, 2), (700, 150), (64, 1), (0, 1), (300, 129)]
+    c = Chunks(dev, shape, lens, odd_tokens(shape, lens), out=out, dtype=dtype, seed=shape[0])
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_later_tokens_of_cut_lists(dev, shape, out):
+    """Long lists in pieces, each looked at for itself; a chunk that lies across two of them."""
+    lens = [(6000, 5), (4090, 12), (37, 8)]
+    c = Chunks(dev, shape, lens, odd_tokens(shape, lens), out=out, page=32, seed=shape[0] + 1)
+    assert c.call() > 0
+    c.check()
+
+
+@pytest.mark.parametrize("shape,n_seq", [(WIDE, 80), (W512, 40), (N128, 40), (N64, 160)])
+def test_later_tokens_behind_moved_sums(dev, shape, n_seq):
+    """Whole lists of more than 24 tiles with fp32 results, whose sums were set aside on the way."""
+    lens = [(4000, 4)] * n_seq
+    odd = [(s, 4000 + s % 4, s % shape[4], s % shape[1], NAN) for s in range(0, n_seq, 3)]
+    c = Chunks(dev, shape, lens, odd, page=64, seed=shape[0] + 2)
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64, N64K])
+def test_positions_below_zero(dev, shape):
+    """More new tokens than cached ones: queries below position 0 attend nothing, whatever the tokens
+    from 0 on hold."""
+    c = Chunks(dev, shape, [(0, 12)], [(0, 0, 0, 3, NAN), (0, 5, 0, 4, NAN)], seed=3)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    O = torch.full((12, c.h_q, c.dv), 7.0, device=dev)
+    lse = torch.full((12, c.h_q), 7.0, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    sfa.sfa_chunk_attend_paged(c.Q, c.K, c.V, c.table, 16, i32([0, 12]), i32([8]), 12, 12, c.scale, O, lse=lse,
+                               dev_status=status)
+    assert sfa.sfa_read_device_status(status) == sfa.SFA_DEV_BAD_QUERY
+    G = c.h_q // c.h_kv
+    assert bool((O[:4] == 0).all()) and bool(torch.isneginf(lse[:4]).all())
+    # queries 4 to 8 are at positions 0 to 4: the odd token at 5 is not theirs
+    if c.sep:
+        assert bool(torch.isfinite(O[4:9, :G, 4]).all()) and not bool(torch.isfinite(O[9:, :G, 4]).any())
+        assert not bool(torch.isfinite(O[4:, :G, 3]).any())
+    assert bool(torch.isfinite(O[:, G:]).all())
+
+
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+def test_old_odd_values(dev, shape):
+    """Odd values in cached tokens, which every query attends: nothing is done again, all are odd."""
+    lens = [(300, 20), (50, 9)]
+    c = Chunks(dev, shape, lens, [(0, 250, 0, 3, NAN), (1, 3, 0, 5, NAN)], seed=5)
+    c.call()
+    c.check()
