@@ -622,9 +622,13 @@ int sfa_write_cells(int n, const sfa_cell_write *writes, const int32_t *slot, in
  * hold does not matter where no query of the chunk attends them (unwritten cells may hold NaN).
  * Precision: fp32 sums of exact bf16 products; the weights meet V as two bf16 halves (2^-16) for an
  * fp32 O (some 7e-6 of a result in all, however long the list) and as one bf16 value for a bf16
- * O; fp32 and q8_0 caches multiply in three tf32 products (2^-19 of a product), weights and all.  A value that is not finite makes what
- * attends it not finite (an infinity of V may come out as NaN), and no query that does not; queries of a
- * bf16 cache that share a tile with a later token that is not finite take a second run.
+ * O (2^-8 of a weight at most: about as much again as the rounding of O, and up to 2^-8 of O where
+ * one key has nearly all the weight); fp32 and q8_0 caches multiply in three tf32 products (2^-19
+ * of a product), weights and all.
+ * A value that is not finite makes what attends it not finite (an infinity of V may come out as
+ * NaN), and no query that does not; queries of a bf16 cache that share a tile with a later token
+ * that is not finite take a second run.  fp32 values within 2^-12 of the type's largest count as
+ * infinite.
  * Limits: (dkq, dv) in {(576, 512) with V NULL, (512, 512), (128, 128), (64, 64)}, h_q/h_kv <= 64.
  * At most two launches.
  */

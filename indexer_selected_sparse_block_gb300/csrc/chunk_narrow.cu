@@ -10,8 +10,8 @@
 // Tensor memory: two S / P tiles of 128 columns, two O tiles of D.
 //
 // For fp32 results the weights are two bf16 halves (hi + lo, 2^-16 relative) and P V runs twice; for
-// bf16 results one bf16 weight is enough.  The running maximum moves only when a tile raises it by
-// more than 2^8, and O in tensor memory is rescaled only then.
+// bf16 results a weight is one bf16 value, off by 2^-8 of itself at most (see chunk_wide.cu).  The running
+// maximum moves only when a tile raises it by more than 2^8, and O in tensor memory is rescaled only then.
 //
 // The chains are what bounds it: in a ragged batch (24 sequences, 128 wide) the tensor pipe is busy
 // 41% of the time, the schedulers 44%, the exponentials' unit 20%.  With one row a thread (four warps a

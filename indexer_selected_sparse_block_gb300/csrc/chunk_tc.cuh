@@ -165,7 +165,7 @@ __device__ __forceinline__ bool store_tile(const Params &p, uint32_t stage, uint
 // the list).  The sums wait where the result will be (O, or the partial results, fp32 both), in no
 // order of their own: a full warp's lanes write whole lines, another warp's live lanes their own
 // rows.  It costs about 8% of a long list: with 16 tiles 12%; leaving the addition to L2 (red) made
-// wide heads 2% faster, narrow ones 1% slower.  bf16 results are rounded by 2^-9: not for them.
+// wide heads 2% faster, narrow ones 1% slower.  bf16 results are rounded by 2^-8: not for them.
 constexpr int kDrain = 24;
 
 // A warp's 32 rows x C value dims of tensor memory from column tcol: added to keep times the sums at

@@ -22,8 +22,11 @@
 // For fp32 results the weights are carried as two bf16 halves (hi + lo, 2^-16 relative).  Beside
 // 576-wide Q there is room for one key half's only: P V then runs by key half, the halves' hi and
 // lo in the P buffer one after the other, S(t + 1) cut in two between them (beside 512-wide Q with
-// both halves in place 512 tokens behind 1000 take 30 us, 36 so).  For bf16 results one bf16 weight is
-// enough: its rounding (2^-9 of a weight, either sign) averages out below the result's own rounding.
+// both halves in place 512 tokens behind 1000 take 30 us, 36 so).  For bf16 results a weight is one bf16
+// value: off by 2^-8 of itself at most, either sign, which leaves the result off by about as much as its
+// own rounding does (1.7e-3 of its size each, at 64 keys as at 16384: the sum and its error shrink
+// alike), and by up to 2^-8 where one key has nearly all the weight (the sum of the weights is of the
+// unrounded ones).  A choice for speed: the second half doubles the products of P V.
 //
 // The running maximum moves only when a tile raises it by more than 2^8: weights up to 256 keep
 // their relative precision in bf16 and fp32, and O in tensor memory is rescaled seldom.

@@ -26,7 +26,7 @@ class Chunks:
     """lens: (cached before, new) of each sequence, on random pages; `odd` of them, (sequence,
     position, KV head, value dim, value), are set in V (or K, where it is V)."""
 
-    def __init__(self, dev, shape, lens, odd, out="f32", dtype="bf16", page=16, seed=0):
+    def __init__(self, dev, shape, lens, odd, out="f32", dtype="bf16", page=16, seed=0, full=False):
         self.dkq, self.dv, self.sep, self.h_q, self.h_kv = shape
         self.lens, self.page, self.out, self.odd = lens, page, out, odd
         g = torch.Generator(device=dev).manual_seed(seed)
@@ -42,7 +42,8 @@ class Chunks:
             at += k
             self.cu.append(self.cu[-1] + lens[s][1])
         self.dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
-        randn = lambda n, h, d: torch.randn((n, h, d), generator=g, device=dev).to(torch.bfloat16).to(self.dt)
+        held = torch.float32 if full else torch.bfloat16      # full: fp32 values with all their bits
+        randn = lambda n, h, d: torch.randn((n, h, d), generator=g, device=dev).to(held).to(self.dt)
         n_cells = order.numel() * page
         self.Q = randn(self.cu[-1], self.h_q, self.dkq)
         self.K, self.V = randn(n_cells, self.h_kv, self.dkq), randn(n_cells, self.h_kv, self.dv) if self.sep else None
