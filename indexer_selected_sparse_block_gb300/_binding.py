@@ -739,7 +739,7 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
     """Causal attention of each sequence's chunk of new tokens (rows cu_new[s] .. cu_new[s + 1] of
     Q [n_q][h_q][dkq]) over its len_total[s] cached tokens, the chunk's own included: K
     [n_cells][h_kv][dkq] and V [n_cells][h_kv][dv] or None, through page_table [n_seq][pages].
-    O [n_q][h_q][dv] fp32 or bf16, lse [n_q][h_q] fp32."""
+    O [n_q][h_q][dv] fp32 or bf16, lse [n_q][h_q] fp32; either may be in page-locked host memory."""
     dev = Q.get_device()
     n_q, h_q, dkq = Q.shape
     n_cells, h_kv, k_row = K.shape
@@ -755,9 +755,12 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
         raise ValueError("O must be an fp32 or bf16 [n_q][h_q][dv] tensor")
     if lse is not None and (lse.shape != (n_q, h_q) or lse.dtype is not _F32):
         raise ValueError("lse must be an fp32 [n_q][h_q] tensor")
-    for t in (Q, K, V, O, lse, workspace):
+    for t in (Q, K, V, workspace):
         if t is not None and (t.get_device() != dev or not t.is_contiguous() or dev < 0):
             _no_tensor("every tensor", t, dev, "contiguous")
+    for t in (O, lse):   # on the device, or in page-locked host memory
+        if t is not None and (not t.is_contiguous() or t.get_device() != dev and (t.is_cuda or not t.is_pinned())):
+            _no_tensor("an output", t, dev, "contiguous")
     table, cu = _int_rows("page_table", page_table, n_seq, dev), _ints("cu_new", cu_new, n_seq + 1, dev)
     total = _ints("len_total", len_total, n_seq, dev)
     ws_bytes = 0

@@ -41,3 +41,31 @@ def test_own_workspaces_of_overlapping_calls(dev):
     for c, _, _, _, _, O, lse in runs:
         n = c.cu[-1]
         assert torch.equal(O[:n], c.O[:n]) and torch.equal(lse[:n], c.lse[:n])
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_outputs_in_host_memory(dev, out):
+    """O and lse in page-locked host memory, of whole and cut lists and of lists whose sums are set
+    aside on the way: what the call gives on the device."""
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    for shape, lens in ((WIDE, [(4000, 1), (70, 9)]), (N128, DEALT), (N128, [(5000, 1)] * 40), (WIDE, [(4000, 2)] * 80)):
+        c = Case(dev, lens, 32, shape, out=out, seed=len(lens))
+        assert c.call() == 0
+        O, lse = torch.full(c.O.shape, 7.0, dtype=c.O.dtype).pin_memory(), torch.full(c.lse.shape, 7.0).pin_memory()
+        Q = c.Q.to(dev)
+        sfa.sfa_chunk_attend_paged(Q, c.Kc, c.Vc, i32(c.table), 32, i32(c.cu), i32(c.total), max(n for _, n in lens),
+                                   max(c.total), c.scale, O, lse=lse)
+        torch.cuda.synchronize()
+        assert torch.equal(O, c.O.cpu()) and torch.equal(lse, c.lse.cpu())
+        with pytest.raises(ValueError):
+            sfa.sfa_chunk_attend_paged(Q, c.Kc, c.Vc, i32(c.table), 32, i32(c.cu), i32(c.total), max(n for _, n in lens),
+                                       max(c.total), c.scale, torch.empty(O.shape, dtype=O.dtype), lse=lse)
+
+
+@pytest.mark.parametrize("shape", [WIDE, N128])
+def test_a_cache_smaller_than_a_page(dev, shape):
+    """No cell of any page: every position is left out, and the call says so."""
+    c = Case(dev, [(30, 3)], 64, shape, seed=1)
+    c.Kc, c.Vc = c.Kc[:40].contiguous(), None if c.Vc is None else c.Vc[:40].contiguous()
+    assert c.call(table=[[0, 1]]) == sfa.SFA_DEV_BAD_CELL
+    assert bool((c.O == 0).all()) and bool(torch.isneginf(c.lse).all())
