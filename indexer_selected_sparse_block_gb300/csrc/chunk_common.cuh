@@ -333,7 +333,8 @@ __device__ __forceinline__ Piece share_next(const Params &p, int c, Share &h) {
     w.state = w.k0 < w.k1 || (all && first) ? kRun : kSkip;
     w.head = !first;
     w.ends = u.u0 + u.w <= share_border(h, c + 1);
-    h.at = min(h.end, u.u0 + u.w);
+    // lengths that change while the call runs can put the list's end behind this place: the slot then ends
+    h.at = u.u0 + u.w > h.at ? min(h.end, u.u0 + u.w) : h.end;
     return w;
 }
 // Slot c's next piece (first: its first one).  Not inlined: the kernel's other warps keep their registers.
