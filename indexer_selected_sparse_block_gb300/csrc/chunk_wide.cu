@@ -37,7 +37,7 @@
 //
 // Measured (576 wide, 16 heads): 512 tokens behind 8192 in 96 us, 1570 TFLOP/s, the tensor pipe 78%
 // busy; 2048 behind 131072 in 5.5 ms, 1720 TFLOP/s, where the card's power is what holds it; 32 single
-// tokens at 131072 in 0.89 ms, 5.4 TB/s; one at 4096 in 13 us, a chain of latencies.
+// tokens at 131072 in 0.89 ms, 5.4 TB/s; one at 4096 in 13.3 us, a chain of latencies.
 //
 // Warps 0-7: softmax, correction, result: a thread has one row, a quarter of its keys and a
 // quarter of its value dims; warps 8-11: loads, one S and one P V operand of a tile each (a
