@@ -29,7 +29,7 @@ def listed():
         dict(name="rope decode 32", op="rope", rows=32, pad=0, far=131072, h_q=16, h_kv=1, d=576,
              rot=64, split=True, pairs=True, factor=1.0, orig=0, src="bf16", dst="bf16", page=64),
         # a prefill chunk deep in a context four times as long as the trained one
-        dict(name="rope chunk 2048, scaled", op="rope", rows=2048, pad=37, far=131072, h_q=16, h_kv=1,
+        dict(name="rope chunk 2048 scaled", op="rope", rows=2048, pad=37, far=131072, h_q=16, h_kv=1,
              d=576, rot=64, split=False, pairs=False, factor=4.0, orig=32768, src="f32", dst="bf16",
              page=64),
         # whole prompts of grouped heads of 128, all dims rotated: the memory
@@ -40,16 +40,16 @@ def listed():
         # trees of many sequences, some short, a padded capacity
         dict(name="maps ragged 256 x 64", op="maps", n_seq=256, old=4096, new=64, spread=1.0, pad=100),
         # one sequence's small tree: latency
-        dict(name="attend 1x4096, 16 nodes", op="attend", n_seq=1, old=4096, new=16, spread=0.0, page=64,
+        dict(name="attend 1x4096 16 nodes", op="attend", n_seq=1, old=4096, new=16, spread=0.0, page=64,
              h_q=16, h_kv=1, dkq=576, dv=512, sep_v=False, dtype="bf16", out="bf16", part="all"),
         # a full batch's trees over a latent cache
-        dict(name="attend 32x32768, 16 nodes", op="attend", n_seq=32, old=32768, new=16, spread=0.0,
+        dict(name="attend 32x32768 16 nodes", op="attend", n_seq=32, old=32768, new=16, spread=0.0,
              page=64, h_q=16, h_kv=1, dkq=576, dv=512, sep_v=False, dtype="bf16", out="bf16", part="all"),
         # large trees deep in long contexts: the tensor cores
-        dict(name="attend 8x131072, 63 nodes", op="attend", n_seq=8, old=131072, new=63, spread=0.0,
+        dict(name="attend 8x131072 63 nodes", op="attend", n_seq=8, old=131072, new=63, spread=0.0,
              page=64, h_q=16, h_kv=1, dkq=576, dv=512, sep_v=False, dtype="bf16", out="bf16", part="all"),
         # a mixed batch with grouped heads of 128, small pages
-        dict(name="attend ragged 24, 128 wide", op="attend", n_seq=24, old=8192, new=61, spread=1.0,
+        dict(name="attend ragged 24 128 wide", op="attend", n_seq=24, old=8192, new=61, spread=1.0,
              page=16, h_q=16, h_kv=4, dkq=128, dv=128, sep_v=True, dtype="bf16", out="bf16", part="all"),
         # the drafted tokens alone, fp32 results to be merged with the sparse attention's of the cache
         dict(name="attend drafted 32 x 64", op="attend", n_seq=32, old=16411, new=64, spread=0.0,
