@@ -642,6 +642,69 @@ int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtyp
                            int64_t n_kv_max, void *O, int o_dtype, float *lse, void *workspace,
                            size_t workspace_bytes, int32_t *dev_status, sfa_stream_t stream);
 
+/*
+ * Rotary positions.  sfa_rope holds what a rotation needs beside the rows: n_rot dims of a head are
+ * turned in pairs, pair j by the angle pos * f_j,
+ *   (u, v) -> magnitude * (u cos - v sin, u sin + v cos),
+ * pairs 0: pair j is dims (j, j + n_rot/2);  pairs 1: dims (2j, 2j + 1).
+ * turns[j] is f_j / 2 pi in units of 2^-64 turns, rounded: the low 64 bits of pos * turns[j] are the
+ * angle's fraction of a turn to 2^-34, however far the position, with no 64-bit floating-point
+ * arithmetic on the device.  A plain struct of the caller's: it is read when a call is made.
+ *
+ * sfa_rope_frequencies -- n_rot/2 frequencies f_j = base^(-2j / n_rot) (radians a position, double),
+ * scaled for contexts `factor` times as long as the trained ones:
+ *   original_len 0:  f_j / factor, every position brought back into the trained range;
+ *   else by parts (YaRN, Peng et al. 2023, section 3.2): with r = original_len f_j / 2 pi, the turns
+ *        that pair j makes over the trained length, and k = (r - beta_slow) / (beta_fast - beta_slow)
+ *        within [0, 1]:  k f_j + (1 - k) f_j / factor.
+ * sfa_rope_init -- fills *rope from any such frequencies.
+ * Host only.  Limits: n_rot even, 2 .. SFA_MAX_ROT; base > 0, factor > 0, original_len >= 0,
+ * beta_fast > beta_slow; frequencies and magnitude finite.  SFA_ERR_INVALID_ARG otherwise.
+ */
+#define SFA_MAX_ROT 512
+typedef struct {
+    int32_t n_rot, pairs;
+    float magnitude;
+    int32_t reserved;
+    uint64_t turns[SFA_MAX_ROT / 2];
+} sfa_rope;
+int sfa_rope_frequencies(int n_rot, double base, double factor, double original_len,
+                         double beta_fast, double beta_slow, double *freq);
+int sfa_rope_init(sfa_rope *rope, int n_rot, int pairs, const double *freq, double magnitude);
+
+/*
+ * sfa_rotate_rows -- for n (<= SFA_MAX_ROTATIONS) sets of rows at once (a step's queries, its keys on
+ * their way into the cache): dims rot_begin .. rot_begin + n_rot of every head of row i turned by its
+ * position pos[i], the head's other dims as they are, i < n_rows.
+ *   src  heads h of row i at src + i * src_stride + h * src_head_stride, d elements each
+ *   dst  the same with its own strides; to_cells: row slot[i] of a cache of n_cells rows instead of
+ *        row i (slot as sfa_build_page_maps gives it; else slot may be NULL)
+ *   src_dtype, dst_dtype: SFA_BF16 or SFA_F32, not SFA_BF16 into SFA_F32; fp32 arithmetic, rounded
+ *        once (dims that do not turn are copied bit for bit, or rounded, likewise)
+ *   dst == src with the same strides and type, not to_cells: in place; the other dims are not touched
+ *   pos[i] < 0 (padding): row i is left out
+ *   inverse 1: every angle the other way.  Since the map is magnitude times a rotation, this is also
+ *        its gradient's: the gradient of the unrotated rows from that of the rotated ones.
+ * One rotation may write what another one does not read or write; one's dst may not overlap its own src
+ * but in place.  A negative slot is left out; one >= n_cells too, flagged SFA_DEV_BAD_CELL.
+ * One launch.  Rows at any stride, aligned to their type; 16 bytes a load where everything is aligned
+ * so (d, rot_begin and n_rot / 2 multiples of 8, strides of 16 bytes), else an element or a pair.
+ * Limits: rot_begin >= 0, rot_begin + n_rot <= d, n_heads * d <= 2^24; no two heads of dst overlap
+ * (heads within rows or rows within heads).  SFA_ERR_INVALID_ARG otherwise.
+ */
+#define SFA_MAX_ROTATIONS 4
+typedef struct {
+    const void *src;
+    int64_t src_stride, src_head_stride;
+    void *dst;
+    int64_t dst_stride, dst_head_stride;
+    int src_dtype, dst_dtype;
+    int n_heads, d, rot_begin, to_cells;
+} sfa_row_rotation;
+int sfa_rotate_rows(int n, const sfa_row_rotation *rotations, const sfa_rope *rope, int inverse,
+                    const int32_t *pos, int64_t n_rows, const int32_t *slot, int64_t n_cells,
+                    int32_t *dev_status, sfa_stream_t stream);
+
 /* Copies *dev_status to *host_out after the work already enqueued on `stream` (this call
  * synchronises the stream). */
 int sfa_read_device_status(const int32_t *dev_status, int32_t *host_out, sfa_stream_t stream);

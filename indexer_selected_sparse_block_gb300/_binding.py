@@ -29,6 +29,7 @@ SFA_REFINE_MAX_BLOCKS = 131072  # longest row sfa_topk_blocks_refine takes
 _lib = None
 _vp, _i64, _int, _f32, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                               ctypes.c_size_t)
+_f64 = ctypes.c_double
 
 class _RowCopy(ctypes.Structure):
     """sfa_row_copy of include/sfa.h."""
@@ -46,6 +47,8 @@ class _CellWrite(ctypes.Structure):
 
 SFA_MAX_ROW_COPIES = 8
 SFA_MAX_CELL_WRITES = 4
+SFA_MAX_ROT = 512
+SFA_MAX_ROTATIONS = 4
 
 # name -> (restype, argtypes); mirrors include/sfa.h
 SIGNATURES = {
@@ -106,6 +109,9 @@ SIGNATURES = {
     "sfa_chunk_attend_paged": (_int, [_vp, _vp, _vp, _int, _i64, _vp, _i64, _int, _int, _int,
                                       _int, _int, _int, _int, _f32, _vp, _vp, _int, _i64, _vp,
                                       _int, _vp, _vp, _sz, _vp, _vp]),
+    "sfa_rope_frequencies": (_int, [_int, _f64, _f64, _f64, _f64, _f64, _vp]),
+    "sfa_rope_init": (_int, [_vp, _int, _int, _vp, _f64]),
+    "sfa_rotate_rows": (_int, [_int, _vp, _vp, _int, _vp, _i64, _vp, _i64, _vp, _vp]),
     "sfa_read_device_status": (_int, [_vp, _vp, _vp]),
     "sfa_status_string": (ctypes.c_char_p, [_int]),
 }
@@ -776,6 +782,92 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
           n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu, total, n_new_max, n_kv_max, O.data_ptr(), o_code,
           None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
           ws_bytes, None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
+
+
+class _Rope(ctypes.Structure):
+    """sfa_rope of include/sfa.h."""
+    _fields_ = [("n_rot", ctypes.c_int32), ("pairs", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * (SFA_MAX_ROT // 2))]
+
+
+class SfaRope:
+    """A rotation by position for sfa_rotate_rows, made once: n_rot dims of a head turned in pairs, halves
+    (j, j + n_rot/2) or, with pairs, adjacent dims (2j, 2j + 1), pair j by base ** (-2 j / n_rot) radians a
+    position.  For contexts `factor` times the trained length: every frequency divided by it, or, given
+    the trained length original_len, by parts (sfa_rope_frequencies); freqs gives any n_rot/2 others
+    instead.  magnitude multiplies the turned dims.  freqs (a list of floats) holds what it turns by."""
+
+    def __init__(self, n_rot: int, base: float = 10000.0, pairs: bool = False, factor: float = 1.0,
+                 original_len: float = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 magnitude: float = 1.0, freqs=None):
+        if n_rot < 2 or n_rot > SFA_MAX_ROT or n_rot % 2:
+            raise ValueError(f"n_rot must be even, 2 to {SFA_MAX_ROT}")
+        f = (ctypes.c_double * (n_rot // 2))()
+        if freqs is None:
+            _check("sfa_rope_frequencies", lib().sfa_rope_frequencies(n_rot, base, factor, original_len,
+                                                                      beta_fast, beta_slow, f))
+        else:
+            freqs = [float(x) for x in freqs]
+            if len(freqs) != n_rot // 2:
+                raise ValueError(f"freqs must hold n_rot / 2 = {n_rot // 2} values")
+            f[:] = freqs
+        self._rope = _Rope()
+        _check("sfa_rope_init", lib().sfa_rope_init(ctypes.addressof(self._rope), n_rot, int(bool(pairs)), f,
+                                                    magnitude))
+        self.n_rot, self.pairs, self.magnitude = n_rot, bool(pairs), float(self._rope.magnitude)
+        self.freqs = list(f)
+
+
+_ROTATION = struct.Struct("@QqqQqqiiiiii")     # sfa_row_rotation of include/sfa.h
+
+
+def _rotation(src, dst, begin, n_rows, n_dst, to_cells, dev):
+    """src [>= n_rows][d] or [..][h][d] into dst of the same heads, any strides but the last."""
+    if src.dim() == 2:
+        h, d, sh = 1, src.size(1), 0
+    elif src.dim() == 3:
+        h, d, sh = src.size(1), src.size(2), src.stride(1)
+    else:
+        h, d, sh = 0, 0, 0
+    if (h < 1 or d < 1 or src.size(0) < n_rows or src.dtype not in (_BF16, _F32) or src.get_device() != dev
+            or (src.stride(-1) != 1 and d > 1)):
+        _no_tensor("rows to rotate", src, dev, f"bf16 or fp32, [>= {n_rows}][d] or [>= {n_rows}][h][d], each "
+                   "head contiguous")
+    if (dst.dim() != src.dim() or dst.size(0) < n_dst or dst.shape[1:] != src.shape[1:]
+            or dst.dtype not in (_BF16, _F32) or dst.get_device() != dev or (dst.stride(-1) != 1 and d > 1)):
+        _no_tensor("rotated rows", dst, dev, f"bf16 or fp32, of their rows' heads, at least {n_dst} of them")
+    return _ROTATION.pack(src.data_ptr(), src.stride(0), sh, dst.data_ptr(), dst.stride(0),
+                          dst.stride(1) if dst.dim() == 3 else 0, _CODES[src.dtype], _CODES[dst.dtype], h, d,
+                          begin, to_cells)
+
+
+def sfa_rotate_rows(rows, pos, rope: SfaRope, cells=(), slot=None, inverse: bool = False, dev_status=None,
+                    stream=None):
+    """Rows turned by their positions pos [n] int32 (negative: left out), in one launch: for every (x, out,
+    begin) of rows, dims begin .. begin + n_rot of each head of x [n][d] or [n][h][d] into out (x itself:
+    in place; views of any stride but the last's); for every (x, cache, begin) of cells, row i into row
+    slot[i] of cache [n_cells][..].  fp32 rows may become bf16.  inverse turns the other way, which is
+    also the way of gradients.  At most SFA_MAX_ROTATIONS of both."""
+    rows, cells = list(rows), list(cells)
+    if len(rows) + len(cells) > SFA_MAX_ROTATIONS:
+        raise ValueError(f"at most {SFA_MAX_ROTATIONS} sets of rows per call")
+    if cells and slot is None:
+        raise ValueError("rows for cells need their slots")
+    dev = _device_of(pos)
+    n = pos.numel()
+    at = _ints("pos", pos, n, dev)
+    to = None if slot is None else _ints("slot", slot, n, dev)
+    n_cells = cells[0][1].size(0) if cells else 0
+    for _, cache, _ in cells:
+        if cache.size(0) != n_cells:
+            raise ValueError("caches of one call must have the same cells")
+    packed = b"".join([_rotation(x, y, b, n, n, 0, dev) for x, y, b in rows]
+                      + [_rotation(x, y, b, n, n_cells, 1, dev) for x, y, b in cells])
+    if not packed:
+        return
+    _call(lib().sfa_rotate_rows, dev, stream, len(rows) + len(cells), packed, ctypes.addressof(rope._rope),
+          int(bool(inverse)), at, n, to, n_cells,
+          None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
 
 
 def sfa_read_device_status(dev_status, stream=None) -> int:
