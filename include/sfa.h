@@ -81,6 +81,10 @@ enum sfa_dtype { SFA_BF16 = 0, SFA_F32 = 1, SFA_Q8_0 = 2 };
                                    its cell map (those tokens get no cell)               */
 #define SFA_DEV_NO_PAGES 0x80   /* sfa_build_page_maps: the free list ran out: the pages
                                    that it lacks are -1 in the page table                */
+#define SFA_DEV_BAD_TREE 0x100  /* a drafted node whose parent is neither -1 nor an earlier
+                                   node of its tree, a tree of more nodes than its mask has
+                                   bits, or an accepted path that does not ascend within its
+                                   tree                                                   */
 
 /*
  * sfa_pool_index_keys -- one mean-pooled index key per block of compress_ratio tokens, taken
@@ -337,7 +341,12 @@ int sfa_gather_attend(const void *Q, const void *K, const void *V, int dtype, in
  *               sfa_window_kv_max(top_k, compress_ratio, window, part)) bytes.
  * Arguments otherwise, limits and kernels as sfa_gather_attend; window >= 0.
  */
-enum sfa_part { SFA_PART_ALL = 0, SFA_PART_SELECTED = 1, SFA_PART_WINDOW = 2 };
+enum sfa_part {
+    SFA_PART_ALL = 0,
+    SFA_PART_SELECTED = 1,
+    SFA_PART_WINDOW = 2,
+    SFA_PART_DRAFTED = 3 /* of sfa_tree_attend_paged */
+};
 int64_t sfa_window_kv_max(int top_k, int compress_ratio, int64_t window, int part);
 int sfa_gather_attend_window(const void *Q, const void *K, const void *V, int dtype, int n_seq,
                              int64_t n_tok_cap, int n_q, int h_q, int h_kv, int dkq, int dv,
@@ -704,6 +713,111 @@ typedef struct {
 int sfa_rotate_rows(int n, const sfa_row_rotation *rotations, const sfa_rope *rope, int inverse,
                     const int32_t *pos, int64_t n_rows, const int32_t *slot, int64_t n_cells,
                     int32_t *dev_status, sfa_stream_t stream);
+
+/*
+ * Drafted trees: one step that verifies, for every sequence, a tree of drafted tokens.  The nodes of
+ * sequence s are new tokens cu_new[s] .. cu_new[s + 1] of a step (sfa_build_page_maps), in any order in
+ * which parents come before their children; parent [n_rows] int32 is a node's parent as an index
+ * within its own tree, -1 for a root (a node right behind the cached tokens; there may be several).
+ * Node j sits in the cell of position a_s + j, a_s = len_total[s] - (cu_new[s+1] - cu_new[s]), but its
+ * position in the text is a_s + its depth.  A step is
+ *   sfa_build_page_maps, sfa_build_tree_maps   cells; masks and positions
+ *   sfa_rotate_rows, sfa_write_cells           the nodes' rows, by their positions, into their cells
+ *   sfa_tree_attend_paged                      every node over the cached tokens and its ancestors
+ *   sfa_tree_accept, sfa_tree_commit           the path that the model agrees with stays, the rest goes
+ * and no call reads a length on the host.  A tree has at most SFA_MAX_TREE nodes.
+ *
+ * sfa_build_tree_maps -- from the parents of the n_rows rows:
+ *   mask [n_rows][mask_words] uint32: bit x of row i (word x / 32, bit x % 32) is set where node x of its
+ *        tree is node i itself or an ancestor.  Rows behind cu_new[n_seq] get 0.
+ *   q_pos [n_rows] int32: a_s + the node's depth (0 for a root); rows behind the last node -1.
+ *   cached_pos [n_rows] int32, nullable: a_s - 1, the position as which the sparse calls see a node
+ *        (their kept blocks and tail then end with the cached tokens), -1 likewise.
+ * A node whose parent is none (SFA_DEV_BAD_TREE) is taken for a root.  Nodes past 32 * mask_words get an
+ * empty mask and position -1 (SFA_DEV_BAD_TREE).  Offsets that do not ascend within [0, n_rows] give an
+ * empty tree, and len_total[s] below its nodes' number a_s = 0 (SFA_DEV_BAD_QUERY).
+ * Limits: 1 <= mask_words <= SFA_MAX_TREE / 32.  One launch.
+ */
+#define SFA_MAX_TREE 1024
+int sfa_build_tree_maps(const int32_t *parent, const int32_t *cu_new, const int32_t *len_total,
+                        int n_seq, int64_t n_rows, uint32_t *mask, int mask_words, int32_t *q_pos,
+                        int32_t *cached_pos, int32_t *dev_status, sfa_stream_t stream);
+
+/*
+ * sfa_tree_attend_paged -- attention of every drafted node of a step over its sequence's cached tokens and
+ * the nodes that its mask names, through the page table: row i = cu_new[s] + j of Q attends
+ *   t < a_s, and t = a_s + x for every x < n_s with bit x of mask row i set
+ *   (n_s = cu_new[s+1] - cu_new[s], a_s = len_total[s] - n_s),
+ * O_ih and lse as sfa_chunk_attend_paged defines them over those keys.  The rows of a tree and the heads
+ * of a KV head share every K/V tile.
+ *   mask  [n_q][mask_words] uint32, as sfa_build_tree_maps writes it, or any other: bits of nodes of the
+ *         sequence, in any pattern (a row need not attend itself); bits past n_s do not matter
+ *   part  SFA_PART_ALL; or SFA_PART_DRAFTED: the nodes alone, not the cached tokens.  Beside it the cached
+ *         ones may be attended by what the indexer selects (sfa_gather_attend_paged of the same rows with
+ *         cached_pos for q_pos) and both merged by sfa_combine_attention: a sparse verification step.
+ * A tree of more than n_new_max nodes is cut to the first n_new_max, as rows and as keys (SFA_DEV_BAD_QUERY).
+ * A row that attends nothing gives O = 0 and lse = -inf.  A value of a node that is not finite makes what
+ * attends it not finite, and nothing else: rows of a bf16 cache that share a tile with one are done a
+ * second time, their bf16 results then rounded twice.
+ * Arguments otherwise, precision, limits and workspace as sfa_chunk_attend_paged;
+ * n_new_max <= 32 * mask_words <= SFA_MAX_TREE.
+ */
+size_t sfa_tree_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv,
+                                       int has_v, int part, int n_new_max, int64_t n_kv_max, int o_dtype);
+int sfa_tree_attend_paged(const void *Q, const void *K, const void *V, int dtype, int64_t n_cells,
+                          const int32_t *page_table, int64_t table_stride, int page_size, int n_seq,
+                          int n_q, int h_q, int h_kv, int dkq, int dv, float scale,
+                          const int32_t *cu_new, const int32_t *len_total, const uint32_t *mask,
+                          int mask_words, int part, int n_new_max, int64_t n_kv_max, void *O, int o_dtype,
+                          float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                          sfa_stream_t stream);
+
+/*
+ * sfa_tree_accept -- the longest path of each tree that the model agrees with: from the sequence's end,
+ * the child whose token is the one that the model chose behind its parent, and so on.
+ *   token, target [n_rows] int32: a node's drafted token, and the one that the model chose (its most
+ *        probable, or one drawn from its distribution: the accepted tokens then follow that distribution
+ *        whatever was drafted) behind the node
+ *   root_target [n_seq] int32, or NULL: the token that a root has to be; NULL: the first root is accepted
+ *        as it is (the token that the step before chose)
+ *   path [n_seq][path_stride] int32: the accepted nodes from the root on, then -1; n_acc [n_seq]: their number
+ *   next_token [n_seq]: the model's token behind the last of them; with none accepted root_target[s], or
+ *        -1 where that is NULL
+ * Of several children with that token the first is taken.  A path ends at path_stride nodes.  Nodes whose
+ * parent is none (SFA_DEV_BAD_TREE) are never accepted, nor those past SFA_MAX_TREE; offsets as above.
+ * Limits: path_stride >= 1.  One launch.
+ */
+int sfa_tree_accept(const int32_t *parent, const int32_t *token, const int32_t *target,
+                    const int32_t *root_target, const int32_t *cu_new, int n_seq, int64_t n_rows,
+                    int32_t *path, int64_t path_stride, int32_t *n_acc, int32_t *next_token,
+                    int32_t *dev_status, sfa_stream_t stream);
+
+/*
+ * sfa_tree_commit -- the accepted nodes stay: for n (<= SFA_MAX_CELL_WRITES) caches at once, the row of
+ * cell slot[cu_new[s] + path[s][k]] becomes that of cell slot[cu_new[s] + k], k < n_acc[s], so that
+ * position a_s + k holds the path's k-th token; and the sequences and the free list go on from there:
+ *   len_out[s] = a_s + n_acc[s] (may be len_total, or the lengths the step began with)
+ *   the pages behind position len_out[s] - 1 that the step had taken go back: into free_pages [n_free],
+ *   sequence by sequence, in their table's order, up to entry *free_head, the first entry not taken
+ *   before; *free_head_out is it afterwards (may be free_head).  Their entries of page_table stay as they
+ *   are, behind the sequence's end, until a later step takes pages for them.
+ *   caches: base and row bytes (even) of [n_cells][...] arrays, rows of any kind, q8_0 ones included
+ *   path, path_stride, n_acc: as sfa_tree_accept writes them, or any nodes of the tree in ascending
+ *        order; it ends where they do not ascend or leave the tree, or at path_stride (SFA_DEV_BAD_TREE)
+ * A node without a cell (slot -1: the pages had run out) counts, and its row is not moved: its position
+ * then holds another node's (SFA_DEV_BAD_CELL); as after any lack of pages, empty that sequence and feed
+ * it again.  One launch.
+ */
+typedef struct {
+    void *rows;
+    int64_t row_bytes;
+} sfa_cell_rows;
+int sfa_tree_commit(int n, const sfa_cell_rows *caches, int64_t n_cells, const int32_t *slot,
+                    const int32_t *cu_new, const int32_t *len_total, int n_seq, int64_t n_rows,
+                    const int32_t *path, int64_t path_stride, const int32_t *n_acc, int page_size,
+                    const int32_t *page_table, int64_t table_stride, int32_t *free_pages,
+                    int64_t n_free, const int32_t *free_head, int32_t *len_out,
+                    int32_t *free_head_out, int32_t *dev_status, sfa_stream_t stream);
 
 /* Copies *dev_status to *host_out after the work already enqueued on `stream` (this call
  * synchronises the stream). */

@@ -22,8 +22,8 @@ SFA_OK, SFA_ERR_INVALID_ARG, SFA_ERR_UNSUPPORTED, SFA_ERR_CUDA, SFA_ERR_WORKSPAC
 SFA_BF16, SFA_F32, SFA_Q8_0 = 0, 1, 2
 SFA_DEV_BAD_BLOCK, SFA_DEV_BAD_NSEL, SFA_DEV_BAD_QUERY, SFA_DEV_TIMEOUT = 1, 2, 4, 8
 SFA_DEV_BAD_CELL, SFA_DEV_FP16_RANGE = 16, 32
-SFA_DEV_BAD_LENGTH, SFA_DEV_NO_PAGES = 64, 128
-SFA_PART_ALL, SFA_PART_SELECTED, SFA_PART_WINDOW = 0, 1, 2
+SFA_DEV_BAD_LENGTH, SFA_DEV_NO_PAGES, SFA_DEV_BAD_TREE = 64, 128, 256
+SFA_PART_ALL, SFA_PART_SELECTED, SFA_PART_WINDOW, SFA_PART_DRAFTED = 0, 1, 2, 3
 SFA_REFINE_MAX_BLOCKS = 131072  # longest row sfa_topk_blocks_refine takes
 
 _lib = None
@@ -49,6 +49,7 @@ SFA_MAX_ROW_COPIES = 8
 SFA_MAX_CELL_WRITES = 4
 SFA_MAX_ROT = 512
 SFA_MAX_ROTATIONS = 4
+SFA_MAX_TREE = 1024
 
 # name -> (restype, argtypes); mirrors include/sfa.h
 SIGNATURES = {
@@ -112,6 +113,15 @@ SIGNATURES = {
     "sfa_rope_frequencies": (_int, [_int, _f64, _f64, _f64, _f64, _f64, _vp]),
     "sfa_rope_init": (_int, [_vp, _int, _int, _vp, _f64]),
     "sfa_rotate_rows": (_int, [_int, _vp, _vp, _int, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "sfa_tree_attend_workspace_bytes": (_sz, [_int, _int, _int, _int, _int, _int, _int, _int, _int,
+                                              _int, _i64, _int]),
+    "sfa_tree_attend_paged": (_int, [_vp, _vp, _vp, _int, _i64, _vp, _i64, _int, _int, _int, _int, _int,
+                                     _int, _int, _f32, _vp, _vp, _vp, _int, _int, _int, _i64, _vp, _int,
+                                     _vp, _vp, _sz, _vp, _vp]),
+    "sfa_build_tree_maps": (_int, [_vp, _vp, _vp, _int, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
+    "sfa_tree_accept": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "sfa_tree_commit": (_int, [_int, _vp, _i64, _vp, _vp, _vp, _int, _i64, _vp, _i64, _vp, _int, _vp,
+                               _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
     "sfa_read_device_status": (_int, [_vp, _vp, _vp]),
     "sfa_status_string": (ctypes.c_char_p, [_int]),
 }
@@ -739,6 +749,20 @@ def _chunk_workspace(dev, *sizes):
         return int(lib().sfa_chunk_attend_workspace_bytes(*sizes))
 
 
+def sfa_tree_attend_workspace_bytes(dtype_code: int, n_seq: int, n_q: int, h_q: int, h_kv: int, dkq: int,
+                                    dv: int, has_v: bool, n_new_max: int, n_kv_max: int,
+                                    o_dtype: int = SFA_F32, part: int = SFA_PART_ALL) -> int:
+    return int(lib().sfa_tree_attend_workspace_bytes(dtype_code, n_seq, n_q, h_q, h_kv, dkq, dv, int(has_v),
+                                                     part, n_new_max, n_kv_max, o_dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(dev, part, *sizes):
+    """sfa_tree_attend_workspace_bytes on device dev: sizes in, a size out."""
+    with torch.cuda.device(dev):
+        return int(lib().sfa_tree_attend_workspace_bytes(*sizes[:8], part, *sizes[8:]))
+
+
 def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_total, n_new_max: int,
                            n_kv_max: int, scale: float, O, lse=None, workspace=None,
                            dev_status=None, stream=None):
@@ -746,6 +770,23 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
     Q [n_q][h_q][dkq]) over its len_total[s] cached tokens, the chunk's own included: K
     [n_cells][h_kv][dkq] and V [n_cells][h_kv][dv] or None, through page_table [n_seq][pages].
     O [n_q][h_q][dv] fp32 or bf16, lse [n_q][h_q] fp32; either may be in page-locked host memory."""
+    _attend_pages(None, 0, Q, K, V, page_table, page_size, cu_new, len_total, n_new_max, n_kv_max, scale, O,
+                  lse, workspace, dev_status, stream)
+
+
+def sfa_tree_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_total, tree_mask, n_new_max: int,
+                          n_kv_max: int, scale: float, O, lse=None, part: int = SFA_PART_ALL, workspace=None,
+                          dev_status=None, stream=None):
+    """Attention of the drafted nodes of each sequence (rows cu_new[s] .. cu_new[s + 1] of Q) over its cached
+    tokens and the nodes that their rows of tree_mask [n_q][words] int32 name (sfa_build_tree_maps), or,
+    with part SFA_PART_DRAFTED, over those nodes alone.  Otherwise as sfa_chunk_attend_paged."""
+    _attend_pages(tree_mask, part, Q, K, V, page_table, page_size, cu_new, len_total, n_new_max, n_kv_max,
+                  scale, O, lse, workspace, dev_status, stream)
+
+
+def _attend_pages(mask, part, Q, K, V, page_table, page_size, cu_new, len_total, n_new_max, n_kv_max, scale, O,
+                  lse, workspace, dev_status, stream):
+    """sfa_chunk_attend_paged, or with a mask sfa_tree_attend_paged."""
     dev = Q.get_device()
     n_q, h_q, dkq = Q.shape
     n_cells, h_kv, k_row = K.shape
@@ -769,17 +810,19 @@ def sfa_chunk_attend_paged(Q, K, V, page_table, page_size: int, cu_new, len_tota
             _no_tensor("an output", t, dev, "contiguous")
     table, cu = _int_rows("page_table", page_table, n_seq, dev), _ints("cu_new", cu_new, n_seq + 1, dev)
     total = _ints("len_total", len_total, n_seq, dev)
+    tree = () if mask is None else (_int_rows("tree_mask", mask, n_q, dev), mask.size(1), part)
     ws_bytes = 0
     if workspace is None:
-        ws_bytes = _chunk_workspace(dev, code, n_seq, n_q, h_q, h_kv, dkq, dv, V is not None, n_new_max,
-                                    n_kv_max, o_code)
+        sizes = (code, n_seq, n_q, h_q, h_kv, dkq, dv, V is not None, n_new_max, n_kv_max, o_code)
+        ws_bytes = _chunk_workspace(dev, *sizes) if mask is None else _tree_workspace(dev, part, *sizes)
         if ws_bytes:
             workspace = _scratch(ws_bytes, dev, stream)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
-    _call(lib().sfa_chunk_attend_paged, dev, stream, Q.data_ptr(), K.data_ptr(),
+    _call(lib().sfa_chunk_attend_paged if mask is None else lib().sfa_tree_attend_paged, dev, stream,
+          Q.data_ptr(), K.data_ptr(),
           None if V is None else V.data_ptr(), code, n_cells, table, page_table.size(1), page_size,
-          n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu, total, n_new_max, n_kv_max, O.data_ptr(), o_code,
+          n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu, total, *tree, n_new_max, n_kv_max, O.data_ptr(), o_code,
           None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
           ws_bytes, None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
 
@@ -867,6 +910,71 @@ def sfa_rotate_rows(rows, pos, rope: SfaRope, cells=(), slot=None, inverse: bool
         return
     _call(lib().sfa_rotate_rows, dev, stream, len(rows) + len(cells), packed, ctypes.addressof(rope._rope),
           int(bool(inverse)), at, n, to, n_cells,
+          None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
+
+
+def sfa_build_tree_maps(parent, cu_new, len_total, mask, q_pos, cached_pos=None, dev_status=None,
+                        stream=None):
+    """Drafted trees from their nodes' parents (parent [n] int32, indices within the node's own tree, -1:
+    a root; the trees packed at cu_new [n_seq + 1], their ends at len_total): mask [n][words] int32 of
+    the node itself and its ancestors, q_pos [n] (the cached tokens plus the node's depth) and, when
+    given, cached_pos [n] (the last cached position).  Rows past the last node: 0 and -1."""
+    dev = _device_of(parent)
+    n, n_seq = parent.numel(), len_total.numel()
+    rows = _int_rows("mask", mask, n, dev)
+    _call(lib().sfa_build_tree_maps, dev, stream, _ints("parent", parent, n, dev),
+          _ints("cu_new", cu_new, n_seq + 1, dev), _ints("len_total", len_total, n_seq, dev), n_seq, n, rows,
+          mask.size(1), _ints("q_pos", q_pos, n, dev),
+          None if cached_pos is None else _ints("cached_pos", cached_pos, n, dev),
+          None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
+
+
+def sfa_tree_accept(parent, token, target, cu_new, path, n_acc, next_token, root_target=None,
+                    dev_status=None, stream=None):
+    """The path of each tree that the model agrees with: from a root (the first one, or the one whose token
+    is root_target [n_seq]) to the child whose token is target of its parent, and so on.  token, target
+    [n]: the nodes' drafted tokens, the model's choice behind each.  path [n_seq][most] gets the nodes,
+    then -1, n_acc [n_seq] their number, next_token [n_seq] the model's choice behind the last."""
+    dev = _device_of(parent)
+    n, n_seq = parent.numel(), n_acc.numel()
+    rows = _int_rows("path", path, n_seq, dev)
+    _call(lib().sfa_tree_accept, dev, stream, _ints("parent", parent, n, dev), _ints("token", token, n, dev),
+          _ints("target", target, n, dev),
+          None if root_target is None else _ints("root_target", root_target, n_seq, dev),
+          _ints("cu_new", cu_new, n_seq + 1, dev), n_seq, n, rows, path.size(1),
+          _ints("n_acc", n_acc, n_seq, dev), _ints("next_token", next_token, n_seq, dev),
+          None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
+
+
+_CELL_ROWS = struct.Struct("@Qq")     # sfa_cell_rows of include/sfa.h
+
+
+def sfa_tree_commit(caches, slot, cu_new, path, n_acc, len_total, page_size: int, page_table, free_pages,
+                    free_head, len_out, free_head_out, dev_status=None, stream=None):
+    """The accepted nodes of each tree stay: in every cache ([n_cells][..], at most SFA_MAX_CELL_WRITES) the
+    rows of path's first n_acc nodes move to the first cells of their step, len_out [n_seq] is where the
+    sequences end then, and the pages behind go back to free_pages before entry free_head, which
+    free_head_out replaces (either may be the tensor it follows from)."""
+    caches = list(caches)
+    if len(caches) > SFA_MAX_CELL_WRITES:
+        raise ValueError(f"at most {SFA_MAX_CELL_WRITES} caches per call")
+    dev = _device_of(slot)
+    n, n_seq = slot.numel(), n_acc.numel()
+    n_cells = caches[0].size(0) if caches else 0x7FFFFFFF
+    packed = []
+    for c in caches:
+        if c.get_device() != dev or not c.is_contiguous() or c.size(0) != n_cells or c.dim() < 2:
+            _no_tensor("a cache", c, dev, f"a contiguous [{n_cells}][..] tensor")
+        packed.append(_CELL_ROWS.pack(c.data_ptr(), c.stride(0) * c.element_size()))
+    rows = _int_rows("path", path, n_seq, dev)
+    table = _int_rows("page_table", page_table, n_seq, dev)
+    n_free = free_pages.numel()
+    _call(lib().sfa_tree_commit, dev, stream, len(caches) if n_cells else 0, b"".join(packed), n_cells,
+          _ints("slot", slot, n, dev), _ints("cu_new", cu_new, n_seq + 1, dev),
+          _ints("len_total", len_total, n_seq, dev), n_seq, n, rows, path.size(1),
+          _ints("n_acc", n_acc, n_seq, dev), page_size, table, page_table.size(1),
+          _ints("free_pages", free_pages, n_free, dev), n_free, _ints("free_head", free_head, 1, dev),
+          _ints("len_out", len_out, n_seq, dev), _ints("free_head_out", free_head_out, 1, dev),
           None if dev_status is None else _ints("dev_status", dev_status, 1, dev))
 
 

@@ -1,6 +1,6 @@
 // chunk.cu -- causal attention of each sequence's chunk of new tokens over its pages
-// (sfa_chunk_attend_paged): the kernel of fp32 and q8_0 caches, the merge of split lists, the launch
-// plan and the C entry points.
+// (sfa_chunk_attend_paged), and the attention of its drafted tree (sfa_tree_attend_paged): the kernel
+// of fp32 and q8_0 caches, the merge of split lists, the launch plan and the C entry points.
 #include "chunk_common.cuh"
 
 namespace sfa {
@@ -111,7 +111,7 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4]
     mma_tf32(d, ah, bh);
 }
 
-template <int DKQ, int DV, bool VK>
+template <int DKQ, int DV, bool VK, bool TREE>
 __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(const Params p, int dtype) {
     using L = F32<DKQ, DV, VK>;
     constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV, BUFS = L::kBufs, PP = L::kPP;
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
     const int rows = min(kRows, (int)((int64_t)n * p.G - r0));
     const int pos0 = it.q.total - it.q.n;                  // position of the chunk's first query
     const int p_last = pos0 + (r0 + rows - 1) / p.G;
-    const int len = max(0, min(key_limit(p, it.q), p_last + 1));
-    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
+    const int len = list_end(p, it.q, p_last + 1), begin = TREE ? list_begin(p, it.q, len) : 0;
+    const int k0 = (int)min((int64_t)len, begin + (int64_t)split * p.split_keys);
     const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
-    const bool whole = len <= p.split_keys;                // this piece is the whole list
+    const bool whole = len - begin <= p.split_keys;        // this piece is the whole list
     if (split > 0 && k0 >= k1) return;                     // no such piece
 
     for (int e = tid; e < kRows * (DKQ / 4); e += kThreads) {
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
             if constexpr (!VK) load_rows<DV, kThreads>(k + TK * PK, p.V, dtype, cells, TK, p.h_kv, g);
         }
     };
-    const int first_pos = pos0 + r0 / p.G;   // the rows' first position
+    // the last key that every row attends
+    const int first_pos = !TREE ? pos0 + r0 / p.G : p.tree == kDrafted ? -1 : pos0 - 1;
     if (ahead && k0 < k1) {
         find_cells(k0, 0);
         __syncthreads();
@@ -254,7 +255,10 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
         {   // softmax of row tid / TPR, KPT keys a thread
             constexpr int TPR = kThreads / kRows, KPT = TK / TPR;
             const int r = tid / TPR, kk = tid % TPR;
-            const int pos = pos0 + (r0 + r) / p.G;
+            const int pos = TREE ? k1 : pos0 + (r0 + r) / p.G;
+            uint32_t node = ~0u;   // TREE: bit j: key t0 + j is attended
+            if constexpr (TREE)
+                node = tree_bits(p, r < rows ? p.mask + (int64_t)(it.q.c0 + (r0 + r) / p.G) * p.mask_words : nullptr, pos0, t0);
             float s[KPT], mx = -INFINITY;
 #pragma unroll
             for (int b = 0; b < KPT; ++b) {
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) v += sRed[(w * kRows + r) * TK + k];
-                const bool on = sCell[k] >= 0 && t0 + k <= pos;
+                const bool on = sCell[k] >= 0 && t0 + k <= pos && (!TREE || ((node >> k) & 1));
                 if (on && v - v != 0.f) {   // halves of an infinity cancel to NaN: the plain product instead
                     v = 0.f;
                     for (int d = 0; d < DKQ; ++d) v += sQ[r * PK + d] * sK[k * PK + d];
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
         }
         if (row0 >= rows) return;
         const int p_last = it.q.total - it.q.n + (r0 + rows - 1) / p.G;
-        const int len = max(0, min(key_limit(p, it.q), p_last + 1));
+        const int end = list_end(p, it.q, p_last + 1), len = end - list_begin(p, it.q, end);
         if (len <= p.split_keys) return;
         n_pieces = (len + p.split_keys - 1) / p.split_keys;
 #pragma unroll
@@ -591,7 +595,7 @@ int64_t items_bound(int n_seq, int n_q, int G, int n_new_max, int item_rows, int
 // each: more than DRAM has where row tiles share a cache larger than L2.  As one loop over pieces it
 // also ran 6% slower at 2048 tokens behind 131072.)
 Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new_max, int64_t n_kv_max,
-               int64_t n_cells, bool o_bf16) {
+               int64_t n_cells, bool o_bf16, int tree) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
     pl.kernel = wide ? kWide : tc ? kNarrow : kF32;
@@ -626,7 +630,7 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     pl.split_keys = best > 1 ? (int)(per * tile) : 0x7FFFFF80;
     pl.n_split = (int)best;
     pl.slots = 0;
-    if (pl.kernel == kNarrow && units > 0) {
+    if (pl.kernel == kNarrow && units > 0 && tree != kDrafted) {
         // four tiles a slot at least: shorter pieces cost the merge more than they gain
         const int64_t few = (units * tiles + 3) / 4, ss = few < slots ? few : slots;
         // lists shorter than their bound leave whole ones' SMs idle, dealt out ones' not
@@ -651,15 +655,20 @@ bool shape_ok(int dkq, int dv, bool has_v) {
            (dkq == 128 && dv == 128) || (dkq == 64 && dv == 64);
 }
 
-template <int DKQ, int DV, bool VK>
-int launch_f32(const Params &p, int dtype, cudaStream_t st) {
-    if (!ensure_max_dynamic_smem(chunk_f32_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(F32<DKQ, DV, VK>::kThreads),
+template <int DKQ, int DV, bool VK, bool TREE>
+int launch_f32_any(const Params &p, int dtype, cudaStream_t st) {
+    if (!ensure_max_dynamic_smem(chunk_f32_kernel<DKQ, DV, VK, TREE>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK, TREE>, dim3(p.items, p.h_kv, p.n_split), dim3(F32<DKQ, DV, VK>::kThreads),
                    F32<DKQ, DV, VK>::bytes(), st, p, dtype) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
     return SFA_OK;
+}
+
+template <int DKQ, int DV, bool VK>
+int launch_f32(const Params &p, int dtype, cudaStream_t st) {
+    return p.tree ? launch_f32_any<DKQ, DV, VK, true>(p, dtype, st) : launch_f32_any<DKQ, DV, VK, false>(p, dtype, st);
 }
 
 template <int DV>
@@ -687,46 +696,46 @@ int check_sizes(int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv, bool has
     return SFA_OK;
 }
 
-}  // namespace
-}  // namespace chunk
-}  // namespace sfa
-
-extern "C" size_t sfa_chunk_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv,
-                                                   int dkq, int dv, int has_v, int n_new_max,
-                                                   int64_t n_kv_max, int o_dtype) {
-    using namespace sfa::chunk;
-    if (check_sizes(n_seq, n_q, h_q, h_kv, dkq, dv, has_v != 0, n_new_max, n_kv_max) != SFA_OK) return 0;
-    if (n_seq == 0 || n_q == 0 || n_new_max == 0) return 0;
-    return plan_workspace(make_plan(dtype, n_seq, n_q, h_q / h_kv, h_kv, dv, n_new_max, n_kv_max, 1,
-                                    o_dtype == SFA_BF16), h_kv, dv);
+// The keys that a list has at most: of the drafted part, the nodes and up to 127 keys before them.
+int64_t plan_keys(int tree, int n_new_max, int64_t n_kv_max) {
+    const int64_t few = (int64_t)n_new_max + 127;
+    return tree == kDrafted && few < n_kv_max ? few : n_kv_max;
 }
 
-extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtype,
-                                      int64_t n_cells, const int32_t *page_table,
-                                      int64_t table_stride, int page_size, int n_seq, int n_q,
-                                      int h_q, int h_kv, int dkq, int dv, float scale,
-                                      const int32_t *cu_new, const int32_t *len_total,
-                                      int n_new_max, int64_t n_kv_max, void *O, int o_dtype,
-                                      float *lse, void *workspace, size_t workspace_bytes,
-                                      int32_t *dev_status, sfa_stream_t stream) {
-    using namespace sfa;
-    using namespace sfa::chunk;
+size_t attend_workspace(int dtype, int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv, bool has_v, int n_new_max,
+                        int64_t n_kv_max, int o_dtype, int tree) {
+    if (check_sizes(n_seq, n_q, h_q, h_kv, dkq, dv, has_v, n_new_max, n_kv_max) != SFA_OK) return 0;
+    if (n_seq == 0 || n_q == 0 || n_new_max == 0) return 0;
+    return plan_workspace(make_plan(dtype, n_seq, n_q, h_q / h_kv, h_kv, dv, n_new_max,
+                                    plan_keys(tree, n_new_max, n_kv_max), 1, o_dtype == SFA_BF16, tree), h_kv, dv);
+}
+
+int attend(const void *Q, const void *K, const void *V, int dtype, int64_t n_cells, const int32_t *page_table,
+           int64_t table_stride, int page_size, int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv, float scale,
+           const int32_t *cu_new, const int32_t *len_total, int tree, const uint32_t *mask, int mask_words,
+           int n_new_max, int64_t n_kv_max, void *O, int o_dtype, float *lse, void *workspace, size_t workspace_bytes,
+           int32_t *dev_status, sfa_stream_t stream) {
     if (dtype != SFA_BF16 && dtype != SFA_F32 && dtype != SFA_Q8_0) return SFA_ERR_INVALID_ARG;
     if (o_dtype != SFA_BF16 && o_dtype != SFA_F32) return SFA_ERR_INVALID_ARG;
     const int rc = check_sizes(n_seq, n_q, h_q, h_kv, dkq, dv, V != nullptr, n_new_max, n_kv_max);
     if (rc != SFA_OK) return rc;
+    if (tree) {
+        if (mask_words < 1 || (int64_t)mask_words * 32 < n_new_max) return SFA_ERR_INVALID_ARG;
+        if (mask_words > SFA_MAX_TREE / 32) return SFA_ERR_UNSUPPORTED;
+    }
     if (page_size < 1 || table_stride < 0 || table_stride > 0x7FFFFFFF ||
         table_stride * page_size > 0x7FFFFFFF || n_cells < 0 || n_cells > 0x7FFFFFFF)
         return SFA_ERR_INVALID_ARG;
     if (!(scale == scale) || scale - scale != 0.f) return SFA_ERR_INVALID_ARG;
     if (n_seq == 0 || n_q == 0 || n_new_max == 0) return SFA_OK;
-    if (!Q || !K || !page_table || !cu_new || !len_total || !O) return SFA_ERR_INVALID_ARG;
+    if (!Q || !K || !page_table || !cu_new || !len_total || !O || (tree && !mask)) return SFA_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(lse) ||
         !aligned16(workspace))
         return SFA_ERR_INVALID_ARG;
     // a cache of no cell: every page is a bad one, and any kernel's plan fits the workspace
-    const Plan pl = make_plan(dtype, n_seq, n_q, h_q / h_kv, h_kv, dv, n_new_max, n_cells > 0 ? n_kv_max : 0,
-                              n_cells, o_dtype == SFA_BF16);
+    const Plan pl = make_plan(dtype, n_seq, n_q, h_q / h_kv, h_kv, dv, n_new_max,
+                              n_cells > 0 ? plan_keys(tree, n_new_max, n_kv_max) : 0,
+                              n_cells, o_dtype == SFA_BF16, tree);
     const size_t need = plan_workspace(pl, h_kv, dv);
     if (need > 0 && (!workspace || workspace_bytes < need)) return SFA_ERR_WORKSPACE;
     Params p{};
@@ -738,6 +747,9 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.total = len_total;
     p.O = O;
     p.lse = lse;
+    p.tree = tree;
+    p.mask = mask;
+    p.mask_words = mask_words;
     p.part_o = reinterpret_cast<float *>(workspace);
     if (need > 0) {
         const size_t rows = plan_parts(pl, h_kv) * pl.part_rows;
@@ -768,12 +780,55 @@ extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *
     p.scale_log2 = scale * kLog2e;
     cudaStream_t st = (cudaStream_t)stream;
     int r;
-    if (pl.kernel == kWide) r = launch_wide(p, dkq, n_cells, st);
-    else if (pl.kernel == kNarrow) r = launch_narrow(p, dkq, n_cells, st);
+    if (pl.kernel == kWide) r = tree ? launch_wide_tree(p, dkq, n_cells, st) : launch_wide(p, dkq, n_cells, st);
+    else if (pl.kernel == kNarrow) r = tree ? launch_narrow_tree(p, dkq, n_cells, st) : launch_narrow(p, dkq, n_cells, st);
     else if (dkq == 576) r = launch_f32<576, 512, true>(p, dtype, st);
     else if (dkq == 512) r = V ? launch_f32<512, 512, false>(p, dtype, st) : launch_f32<512, 512, true>(p, dtype, st);
     else if (dkq == 128) r = V ? launch_f32<128, 128, false>(p, dtype, st) : launch_f32<128, 128, true>(p, dtype, st);
     else r = V ? launch_f32<64, 64, false>(p, dtype, st) : launch_f32<64, 64, true>(p, dtype, st);
     if (r != SFA_OK || need == 0 || pl.slots == 1) return r;
     return dv == 512 ? launch_combine<512>(p, st) : dv == 128 ? launch_combine<128>(p, st) : launch_combine<64>(p, st);
+}
+
+}  // namespace
+}  // namespace chunk
+}  // namespace sfa
+
+extern "C" size_t sfa_chunk_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv,
+                                                   int has_v, int n_new_max, int64_t n_kv_max, int o_dtype) {
+    using namespace sfa::chunk;
+    return attend_workspace(dtype, n_seq, n_q, h_q, h_kv, dkq, dv, has_v != 0, n_new_max, n_kv_max, o_dtype, kCausal);
+}
+
+extern "C" int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtype, int64_t n_cells,
+                                      const int32_t *page_table, int64_t table_stride, int page_size, int n_seq, int n_q,
+                                      int h_q, int h_kv, int dkq, int dv, float scale, const int32_t *cu_new,
+                                      const int32_t *len_total, int n_new_max, int64_t n_kv_max, void *O, int o_dtype,
+                                      float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                      sfa_stream_t stream) {
+    using namespace sfa::chunk;
+    return attend(Q, K, V, dtype, n_cells, page_table, table_stride, page_size, n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu_new,
+                  len_total, kCausal, nullptr, 0, n_new_max, n_kv_max, O, o_dtype, lse, workspace, workspace_bytes,
+                  dev_status, stream);
+}
+
+extern "C" size_t sfa_tree_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv, int has_v,
+                                                  int part, int n_new_max, int64_t n_kv_max, int o_dtype) {
+    using namespace sfa::chunk;
+    if (part != SFA_PART_ALL && part != SFA_PART_DRAFTED) return 0;
+    return attend_workspace(dtype, n_seq, n_q, h_q, h_kv, dkq, dv, has_v != 0, n_new_max, n_kv_max, o_dtype,
+                            part == SFA_PART_ALL ? kTree : kDrafted);
+}
+
+extern "C" int sfa_tree_attend_paged(const void *Q, const void *K, const void *V, int dtype, int64_t n_cells,
+                                     const int32_t *page_table, int64_t table_stride, int page_size, int n_seq, int n_q,
+                                     int h_q, int h_kv, int dkq, int dv, float scale, const int32_t *cu_new,
+                                     const int32_t *len_total, const uint32_t *mask, int mask_words, int part, int n_new_max,
+                                     int64_t n_kv_max, void *O, int o_dtype, float *lse, void *workspace,
+                                     size_t workspace_bytes, int32_t *dev_status, sfa_stream_t stream) {
+    using namespace sfa::chunk;
+    if (part != SFA_PART_ALL && part != SFA_PART_DRAFTED) return SFA_ERR_INVALID_ARG;
+    return attend(Q, K, V, dtype, n_cells, page_table, table_stride, page_size, n_seq, n_q, h_q, h_kv, dkq, dv, scale, cu_new,
+                  len_total, part == SFA_PART_ALL ? kTree : kDrafted, mask, mask_words, n_new_max, n_kv_max, O, o_dtype, lse,
+                  workspace, workspace_bytes, dev_status, stream);
 }

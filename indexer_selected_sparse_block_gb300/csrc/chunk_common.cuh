@@ -5,6 +5,10 @@
 // last positions of the sequence's total[s] cached tokens.  The rows of one KV head are (query,
 // head of the group) pairs, flattened query-major; a work item is a tile of such rows of one
 // sequence and KV head, and a piece of its keys 0 .. p_last.
+//
+// A chunk may be a drafted tree instead (sfa_tree_attend_paged): its rows attend the a = total[s] - n
+// cached tokens and, of the n drafted ones, those whose bits their mask rows have.  Every tile's keys
+// then go up to the last node; or, of the drafted part alone, from the tile border before the first.
 #pragma once
 
 #include "sfa_common.cuh"
@@ -14,8 +18,12 @@ namespace chunk {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+enum { kCausal, kTree, kDrafted };   // Params::tree
+
 struct Params {
     const void *Q, *K, *V;
+    const uint32_t *mask;   // of a tree's nodes, mask_words words a row
+    int tree, mask_words;
     const int32_t *table, *cu, *total;
     void *O;
     float *lse, *part_o, *part_ml;
@@ -134,6 +142,28 @@ __device__ __forceinline__ int key_limit(const Params &p, const Seq &q) {
     return (int)(t > 0 ? t : 0);
 }
 
+// The keys [list_begin, list_end) that a row tile attends between its rows; after: the position behind
+// the tile's last query.
+__device__ __forceinline__ int list_end(const Params &p, const Seq &q, int after) {
+    return max(0, min(key_limit(p, q), p.tree ? q.total - q.n + min(q.n, p.n_new_max) : after));
+}
+__device__ __forceinline__ int list_begin(const Params &p, const Seq &q, int end) {
+    return p.tree == kDrafted ? min(max(q.total - q.n, 0) & ~127, end) : 0;
+}
+
+// Of keys kb .. kb + 31, those that a tree's row attends: bit j for key kb + j.  row: its mask's words,
+// null for a row that is none; a: the cached tokens.  Keys behind the last node are the caller's to
+// leave out.
+__device__ __forceinline__ uint32_t tree_bits(const Params &p, const uint32_t *row, int a, int kb) {
+    const int x = kb - a;   // the first key as a node
+    if (x <= -32) return p.tree == kTree ? 0xFFFFFFFFu : 0u;
+    const int w = x >> 5;
+    auto word = [&](int i) { return row && i >= 0 && i < p.mask_words ? __ldg(row + i) : 0u; };
+    uint32_t bits = __funnelshift_r(word(w), word(w + 1), x & 31);
+    if (x < 0 && p.tree == kTree) bits |= (1u << -x) - 1u;
+    return bits;
+}
+
 // Cell of position t of sequence s, or -1 (flagged) when the page table's entry is no page.
 __device__ __forceinline__ int64_t cell_of(const Params &p, int s, int t) {
     const int pg = p.page_div.div(t);
@@ -162,7 +192,7 @@ __device__ __forceinline__ void piece_rows(const Params &p, const Seq &q, int ti
     w.q0 = tile * p.item_q;
     w.nq = min(p.item_q, min(q.n, p.n_new_max) - w.q0);
     w.pos0 = q.total - q.n + w.q0;
-    w.len = max(0, min(key_limit(p, q), w.pos0 + w.nq));
+    w.len = list_end(p, q, w.pos0 + w.nq);
 }
 // One piece a CTA: `split` of item and KV head g; by a whole warp.
 __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int split) {
@@ -173,9 +203,10 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
     w.seq = it.seq;
     w.g = g;
     piece_rows(p, it.q, it.tile, w);
-    w.k0 = (int)min((int64_t)w.len, (int64_t)split * p.split_keys);
+    const int kb = list_begin(p, it.q, w.len);
+    w.k0 = (int)min((int64_t)w.len, kb + (int64_t)split * p.split_keys);
     w.k1 = (int)min((int64_t)w.len, (int64_t)w.k0 + p.split_keys);
-    w.part = w.len <= p.split_keys ? -1 : ((item * p.h_kv + g) * p.n_split + split);
+    w.part = w.len - kb <= p.split_keys ? -1 : ((item * p.h_kv + g) * p.n_split + split);
     w.state = split > 0 && w.k0 >= w.k1 ? kEnd : kRun;
     return w;
 }
@@ -192,8 +223,8 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
 // here) for the one that starts inside a list, [c][1] = (written, first query, queries, KV head) for
 // the one that is a list's start: the pieces of that list are it and the following slots' [0], up to
 // the one where the list ends.
-// The weights of a sequence's row tiles grow by item_q from one to the next, so their sums have a
-// closed form and a place in the line is found without a pass over the tiles.
+// The weights of a sequence's row tiles grow by item_q from one to the next (a tree's are all the same),
+// so their sums have a closed form and a place in the line is found without a pass over the tiles.
 constexpr int kPieceKeys = 448;
 struct Unit {
     int seq, tile, g;
@@ -220,6 +251,7 @@ __device__ __forceinline__ int64_t share_border(const Share &h, int c) {
 // Sum of the weights of the first j row tiles of a sequence with n new tokens behind a cached ones
 // (j at most their number; the last one may be short).
 __device__ __forceinline__ int64_t tile_weights(const Params &p, int64_t a, int n, int tiles, int64_t j) {
+    if (p.tree) return j * (a + n + kPieceKeys);
     const int64_t full = j < tiles ? j : tiles - 1;
     return full * a + p.item_q * (full * (full + 1) / 2) + (j < tiles ? 0 : a + n) + j * kPieceKeys;
 }
@@ -306,7 +338,7 @@ __device__ __forceinline__ Unit share_unit(const Params &p, Share &h, int64_t x)
         else hi = m - 1;
     }
     u.tile = lo;
-    u.w = a + min((int64_t)(lo + 1) * p.item_q, (int64_t)n) + kPieceKeys;
+    u.w = a + (p.tree ? (int64_t)n : min((int64_t)(lo + 1) * p.item_q, (int64_t)n)) + kPieceKeys;
     u.u0 = x - r + tile_weights(p, a, n, tiles, lo);
     return u;
 }
@@ -400,14 +432,114 @@ __device__ __forceinline__ Piece odd_group(const Params &p, const Piece &w, int 
     return f;
 }
 
-// The kernel for 512 value dims on tcgen05 CTA pairs (chunk_wide.cu): queries of one CTA's 64
-// rows, and the launch (p.item_q = twice that, p.item_rows = 128).
+// A tree's rows do not attend a prefix of its nodes each, so there are no groups of them.  Where a result
+// is NaN and such a value is there (odd_nodes), the tile is done again over the cached tokens of its
+// piece, which every row attends, and the nodes that a row attends are added to it one by one, by a warp
+// (add_nodes): a bf16 result is then rounded twice.
+//
+// The nodes' keys [t0, t1) of a piece; fresh: it has no cached token, or is of the drafted part.
+struct Nodes {
+    int a, t0, t1, k1;   // the cached tokens; k1: where the cached tokens of the piece end
+};
+__device__ __forceinline__ Nodes piece_nodes(const Params &p, int a, int k0, int k1) {
+    Nodes v;
+    v.a = a;
+    v.t0 = max(k0, min(a, k1));
+    v.t1 = k1;
+    v.k1 = p.tree == kDrafted ? k0 : v.t0;
+    return v;
+}
+// Whether a key that some row of the piece does not attend has values that are not finite; by one whole warp.
+template <int DV>
+__device__ __forceinline__ bool odd_nodes(const Params &p, const Nodes &v, int stride, int seq, int g, int k0) {
+    const int from = p.tree == kDrafted ? k0 : v.t0;
+    return first_odd<DV>(p, p.V ? p.V : p.K, stride, seq, g, from, v.t1) < v.t1;
+}
+// The nodes that row `q_row` (of Q, head h) attends, added to its result, or with part >= 0 to its partial
+// one there; lse2: the base-2 log-sum-exp of a result.  fresh: there is none yet.  By one whole warp.
+template <int DKQ, int DV, bool VK>
+__device__ __noinline__ void add_nodes(const Params &p, const Nodes &v, int seq, int g, int q_row, int h, int64_t part,
+                                       float lse2, bool fresh) {
+    constexpr int NQ = DKQ / 64, NV = DV / 64;   // pairs of dims 64 i + 2 lane
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)q_row * p.h_q + h;
+    const uint32_t *mask = p.mask + (int64_t)q_row * p.mask_words;
+    auto pair = [](const void *base, int64_t e) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const __nv_bfloat16 *>(base) + e);
+        return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+    };
+    float2 q[NQ], acc[NV];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) q[i] = pair(p.Q, row * DKQ + 64 * i + 2 * lane);
+    float m = -INFINITY, l = 0.f;
+    if (!fresh) {
+        m = part >= 0 ? p.part_ml[2 * part] : lse2;
+        l = part >= 0 ? p.part_ml[2 * part + 1] : m == -INFINITY ? 0.f : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int d = 64 * i + 2 * lane;
+        if (fresh) acc[i] = make_float2(0.f, 0.f);
+        else if (part >= 0) acc[i] = *reinterpret_cast<const float2 *>(p.part_o + part * DV + d);
+        else if (p.o_bf16) acc[i] = pair(p.O, row * DV + d);
+        else acc[i] = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(p.O) + row * DV + d);
+    }
+    for (int t = v.t0; t < v.t1; ++t) {
+        const int x = t - v.a;
+        if ((x >> 5) >= p.mask_words || !((mask[x >> 5] >> (x & 31)) & 1)) continue;
+        const int64_t cell = cell_of(p, seq, t);
+        if (cell < 0) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const float2 k = pair(p.K, (cell * p.h_kv + g) * DKQ + 64 * i + 2 * lane);
+            s = fmaf(q[i].x, k.x, fmaf(q[i].y, k.y, s));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        s *= p.scale_log2;
+        if (s == -INFINITY) continue;
+        const float mn = fmaxf(m, s), al = m == -INFINITY ? 0.f : exp2f(m - mn), e = exp2f(s - mn);
+        m = mn;
+        l = l * al + e;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float2 y = pair(VK ? p.K : p.V, (cell * p.h_kv + g) * (VK ? DKQ : DV) + 64 * i + 2 * lane);
+            acc[i].x = fmaf(e, y.x, acc[i].x * al);
+            acc[i].y = fmaf(e, y.y, acc[i].y * al);
+        }
+    }
+    const bool any = l > 0.f || l != l;
+    const float inv = part >= 0 ? 1.f : any ? 1.f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int d = 64 * i + 2 * lane;
+        const float2 y = make_float2(acc[i].x * inv, acc[i].y * inv);
+        if (part >= 0) *reinterpret_cast<float2 *>(p.part_o + part * DV + d) = y;
+        else if (p.o_bf16)
+            *reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + row * DV + d) = pack_bf16(y.x, y.y);
+        else *reinterpret_cast<float2 *>(reinterpret_cast<float *>(p.O) + row * DV + d) = y;
+    }
+    if (lane == 0) {
+        if (part >= 0) {
+            p.part_ml[2 * part] = m;
+            p.part_ml[2 * part + 1] = l;
+        } else if (p.lse) {
+            p.lse[row] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
+        }
+    }
+}
+
+// The kernel for 512 value dims on tcgen05 CTA pairs (chunk_wide.cuh): queries of one CTA's 64
+// rows, and the launch (p.item_q = twice that, p.item_rows = 128), of chunks and of trees.
 inline int wide_qpc(int G) { return 64 / G; }
 int launch_wide(const Params &p, int dkq, int64_t n_cells, cudaStream_t st);
-// The kernel for 128- and 64-wide heads on tcgen05 (chunk_narrow.cu): queries of one 128-row tile,
-// and the launch (p.item_q = twice that, p.item_rows = 256).
+int launch_wide_tree(const Params &p, int dkq, int64_t n_cells, cudaStream_t st);
+// The kernel for 128- and 64-wide heads on tcgen05 (chunk_narrow.cuh): queries of one 128-row tile,
+// and the launch (p.item_q = twice that, p.item_rows = 256), of chunks and of trees.
 inline int narrow_qpt(int G) { return 128 / G; }
 int launch_narrow(const Params &p, int d, int64_t n_cells, cudaStream_t st);
+int launch_narrow_tree(const Params &p, int d, int64_t n_cells, cudaStream_t st);
 
 }  // namespace chunk
 }  // namespace sfa

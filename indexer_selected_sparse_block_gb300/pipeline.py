@@ -259,8 +259,21 @@ class SfaPagedCache:
                                (sfa_chunk_attend_paged)
       release(seq)             a finished sequence's pages return to the free list
 
+    or, for drafted trees of tokens, of which the model's own choice decides what stays,
+
+      draft(len_new, parent, K, V, X)   the nodes get cells, masks and positions (sfa_build_tree_maps),
+                               their rows are written; the lengths stay as they are
+      attend_tree(Q, ...)      every node over the cached tokens and its ancestors
+                               (sfa_tree_attend_paged)
+      commit(token, target)    the accepted path stays (sfa_tree_accept, sfa_tree_commit): the lengths
+                               go on by it, the other nodes' pages return to the free list
+
+    (another step or draft instead of commit drops the tree.)  With a rope (SfaRope) step and draft turn
+    the last n_rot dims of the key rows on their way into their cells, and of queries given with them in
+    place, by the positions q_pos (sfa_rotate_rows).
+
     Neither step nor attend reads a length on the host, allocates (given a workspace) or
-    synchronises: with len_new, the rows and Q in fixed buffers they can be captured in a CUDA
+    synchronises, nor do draft, attend_tree and commit: with len_new, the rows and Q in fixed buffers they can be captured in a CUDA
     graph (SfaStep.graphed), whose replays advance the lengths.  Rows past the step's last token
     are padding.  cell_of is the position -> cell map the other paged entry points and SfaStep
     take (pass the cache's X, K, V to them); q_seq and q_pos are the new tokens' sequences and
@@ -273,7 +286,8 @@ class SfaPagedCache:
 
     def __init__(self, *, n_seq: int, n_pages: int, page_size: int, max_pages: int, n_tok_cap: int,
                  h_kv: int, dkq: int, dv: int, separate_v: bool = False, d_idx: int = 0,
-                 dtype=torch.bfloat16, q8_0: bool = False, cell_map: bool = True, device="cuda"):
+                 dtype=torch.bfloat16, q8_0: bool = False, cell_map: bool = True, device="cuda",
+                 n_draft_max: int = 0):
         self.__dict__.update(n_seq=n_seq, n_pages=n_pages, page_size=page_size, dv=dv)
         dev = torch.device(device)
         n_cells = n_pages * page_size
@@ -298,20 +312,43 @@ class SfaPagedCache:
         self.cu_new = i32(n_seq + 1)
         self.q_seq, self.q_pos, self.slot = (i32(n_tok_cap, fill=-1) for _ in range(3))
         self.status = i32(1)
+        self.tree_mask = self._parent = None
+        if n_draft_max:
+            self._tree_buffers(n_draft_max)
 
-    def step(self, len_new, K=None, V=None, X=None, stream=None):
-        """Pages and cells for len_new [n_seq] int32 new tokens a sequence (n_tok_cap in all, at
-        most) and their rows K, V, X [n_tok_cap][...], packed sequence by sequence, into them."""
+    def _place(self, len_new, K, V, X, rope, Q, stream, tree=None):
+        """The cells of a step's tokens and their rows in them; tree: of drafted nodes."""
         given = (("key", K, self.K), ("value", V, self.V), ("index key", X, self.X))
         for name, rows, cells in given:
             if rows is not None and cells is None:
                 raise ValueError(f"{name} rows for a cache that holds none (separate_v, d_idx)")
+        if Q is not None and rope is None:
+            raise ValueError("queries are given to be turned by a rope")
+        if rope is not None and self.K.dtype == torch.uint8:
+            raise ValueError("rows are turned into bf16 or fp32 cells, not q8_0 ones")
         B.sfa_build_page_maps(self.length, len_new, self.page_size, self.free_pages, self.free_head,
                               self.n_pages, self.page_table, self.cu_new, self.len_total,
                               self.q_seq, self.q_pos, self.slot, self._head_out,
                               cell_of=self.cell_of, dev_status=self.status, stream=stream)
+        if tree is not None:
+            B.sfa_build_tree_maps(tree, self.cu_new, self.len_total, self.tree_mask, self.q_pos,
+                                  cached_pos=self.cached_pos, dev_status=self.status, stream=stream)
+        if rope is not None:
+            turned = [(x, x, x.size(-1) - rope.n_rot) for x in (Q,) if x is not None]
+            keys = [(K, self.K, K.size(-1) - rope.n_rot)] if K is not None else []
+            B.sfa_rotate_rows(turned, self.q_pos, rope, cells=keys, slot=self.slot, dev_status=self.status,
+                              stream=stream)
+            given = given[1:]
         pairs = [(rows, cells) for _, rows, cells in given if rows is not None]
-        B.sfa_write_cells(pairs, self.slot, dev_status=self.status, stream=stream)
+        if pairs or rope is None:
+            B.sfa_write_cells(pairs, self.slot, dev_status=self.status, stream=stream)
+
+    def step(self, len_new, K=None, V=None, X=None, stream=None, rope=None, Q=None):
+        """Pages and cells for len_new [n_seq] int32 new tokens a sequence (n_tok_cap in all, at
+        most) and their rows K, V, X [n_tok_cap][...], packed sequence by sequence, into them.  rope: the
+        last n_rot dims of K's rows are turned on the way, and of Q's [n_tok_cap][h_q][dkq] in place."""
+        self._place(len_new, K, V, X, rope, Q, stream)
+        self._parent = None
         copies = [(self.length.unsqueeze(0), self.len_total.unsqueeze(0)),
                   (self.free_head, self._head_out)]
         B.sfa_copy_cache_rows_multi(copies, stream=stream)
@@ -323,6 +360,50 @@ class SfaPagedCache:
                                  self.len_total, n_new_max, n_kv_max, scale, O, lse=lse,
                                  workspace=workspace, dev_status=self.status, stream=stream)
         return O
+
+    def _tree_buffers(self, n_nodes_max: int):
+        """The buffers of drafted trees of at most n_nodes_max nodes each."""
+        words, n, dev = max(1, (n_nodes_max + 31) // 32), self.slot.numel(), self.slot.device
+        if words > B.SFA_MAX_TREE // 32:
+            raise ValueError(f"a drafted tree has at most {B.SFA_MAX_TREE} nodes")
+        i32 = lambda *shape: torch.full(shape, -1, dtype=torch.int32, device=dev)
+        self.tree_mask, self.cached_pos = i32(n, words).zero_(), i32(n)
+        self.path, self.n_acc, self.next_token = i32(self.n_seq, n_nodes_max), i32(self.n_seq), i32(self.n_seq)
+
+    def draft(self, len_new, parent, K=None, V=None, X=None, stream=None, rope=None, Q=None):
+        """Cells, masks and positions (tree_mask, q_pos, cached_pos) for the nodes of a drafted tree a
+        sequence: len_new [n_seq] nodes, parent [n_tok_cap] their parents within it (-1: a root, parents
+        before children), packed like their rows K, V, X.  Needs n_draft_max of the constructor.  rope, Q
+        as in step."""
+        if self.tree_mask is None:
+            raise ValueError("a cache for drafted trees is made with n_draft_max")
+        self._place(len_new, K, V, X, rope, Q, stream, tree=parent)
+        self._parent = parent
+
+    def attend_tree(self, Q, n_new_max: int, n_kv_max: int, scale: float, O, lse=None,
+                    part: int = B.SFA_PART_ALL, workspace=None, stream=None):
+        """O (and lse) of the drafted nodes over the cached tokens and their ancestors, or (part
+        SFA_PART_DRAFTED) over their ancestors alone."""
+        B.sfa_tree_attend_paged(Q, self.K, self.V, self.page_table, self.page_size, self.cu_new,
+                                self.len_total, self.tree_mask, n_new_max, n_kv_max, scale, O, lse=lse,
+                                part=part, workspace=workspace, dev_status=self.status, stream=stream)
+        return O
+
+    def commit(self, token, target, root_target=None, stream=None):
+        """Of the last draft the path that the model agrees with stays: token [n_tok_cap] the nodes' tokens,
+        target [n_tok_cap] the model's choice behind each, root_target [n_seq] behind the cached tokens (None:
+        the first root is taken).  path, n_acc and next_token say which, how many and what comes next.  Once a
+        draft."""
+        if self._parent is None:
+            raise ValueError("no drafted tree to commit")
+        B.sfa_tree_accept(self._parent, token, target, self.cu_new, self.path, self.n_acc, self.next_token,
+                          root_target=root_target, dev_status=self.status, stream=stream)
+        B.sfa_tree_commit([c for c in (self.K, self.V, self.X) if c is not None], self.slot, self.cu_new,
+                          self.path, self.n_acc, self.len_total, self.page_size, self.page_table,
+                          self.free_pages, self._head_out, self.length, self.free_head,
+                          dev_status=self.status, stream=stream)
+        self._parent = None
+        return self.next_token
 
     def release(self, seq: int, stream=None):
         """Empties sequence seq: its pages go to the end of the free list.  On `stream`, behind what
