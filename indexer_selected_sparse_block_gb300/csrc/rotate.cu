@@ -7,8 +7,7 @@ namespace sfa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 8;        // rows of a CTA
-constexpr int kTableBytes = kMaxRows * (SFA_MAX_ROT / 2) * (int)sizeof(float2);
+constexpr int kTurns = 2048;       // of a block without 16-byte accesses: its rows times n_rot / 2
 
 enum Kind { kBf16, kRound, kF32 };   // bf16 rows, fp32 into bf16, fp32 rows
 
@@ -16,20 +15,23 @@ struct Rotation {
     const void *src;
     void *dst;
     int64_t src_stride, src_head, dst_stride, dst_head;
-    FastDiv by_row, by_head;   // units of a row, of a head
-    int row_units, head_units;
-    int kind, vec, to_cells;
-    int lo, rot;               // a head's units: lo copied ones, rot turned ones, copied ones
-    int begin;                 // first dim that turns
-    int skip;                  // in place: the copied ones are left out; lo = 0
+    int kind, to_cells;
+    int heads, begin;          // begin: first dim that turns
+    int stay, lo;              // a head's units that stay, those before the turning ones (0: in place)
+    FastDiv by_head, by_row;   // by stay, by heads * stay
+    // 16-byte accesses: a row's `groups` threads have eight dims of the first half (or eight adjacent ones)
+    // each, `subs` such teams every subs-th head; a block has `rows` rows
+    int subs, rows;
+    FastDiv by_team;           // by groups * subs
 };
 struct Params {
     Rotation r[SFA_MAX_ROTATIONS];
     const int32_t *pos, *slot;
     int32_t *status;
     int64_t n_rows, n_cells;
-    int n, rows;               // rows of a CTA
     int half;                  // pairs: n_rot / 2
+    int groups;
+    FastDiv by_groups;
     int pairs, inverse;
     float magnitude;
     uint64_t turns[SFA_MAX_ROT / 2];
@@ -47,6 +49,17 @@ __device__ __forceinline__ float2 turn(const Params &p, int pos, int j) {
     c = (((q + 1) & 2) ? -cc : cc) * p.magnitude;
     s = ((q & 2) ? -ss : ss) * p.magnitude;
     return make_float2(c, p.inverse ? -s : s);
+}
+// Where row i of a set goes, or -1: it is left out.
+__device__ __forceinline__ int64_t target(const Params &p, const Rotation &r, int64_t i, int pos) {
+    if (pos < 0) return -1;
+    if (!r.to_cells) return i;
+    const int c = p.slot[i];
+    if (c >= p.n_cells) {
+        set_status(p.status, SFA_DEV_BAD_CELL);
+        return -1;
+    }
+    return c < 0 ? -1 : c;
 }
 
 // Eight elements of a row in registers, as they were loaded.
@@ -101,72 +114,114 @@ struct Eight {
     }
 };
 
-// A unit is eight elements that stay, eight that turn among themselves (adjacent pairs), or eight of the
-// first half and their eight partners.  U of a thread's units are in flight at a time.
-template <int KIND, bool PAIRS>
-__device__ __forceinline__ void rotate_vec(const Params &p, const Rotation &r, int64_t row0, int rows, const int *sPos,
-                                           const int64_t *sDst, const float2 *sTurn) {
-    constexpr int U = (KIND == kBf16 ? 4 : 2) / (PAIRS ? 1 : 2);
-    const int total = rows * r.row_units;
-    for (int e0 = threadIdx.x; e0 < total; e0 += kThreads * U) {
-        Eight<KIND> a[U], b[PAIRS ? 1 : U];
-        int64_t to[U];
-        int row[U], x[U];   // x: the unit's place among the turning ones, -1: it stays, -2: nothing to do
+// The rows of a block, where everything is aligned to 16 bytes.  A thread has the cosines and sines of its
+// eight pairs (adjacent pairs: four) in registers and takes one head after the other, U of their loads in
+// flight, the first ones before it makes the cosines: no thread waits for another.  Then the block's
+// threads copy the dims that stay.
+// The memory bounds it: 65536 rows of 20 heads of 128, bf16, 102 us (6.6 TB/s), 162 with the cosines of a
+// block's rows in shared memory, made by all before any loads; 2048 rows of 17 heads, 64 of 576 dims turned,
+// fp32 into bf16, 16.8 us, 30.4 so; 32 rows are latency, 2.5 us.
+template <int KIND, bool PAIRS, int U>
+__device__ __forceinline__ void rotate_vec(const Params &p, const Rotation &r, int64_t row0) {
+    constexpr int NP = PAIRS ? 4 : 8;
+    const int rows = (int)min((int64_t)r.rows, p.n_rows - row0), team = p.groups * r.subs;
+    const int row = r.by_team.div(threadIdx.x), in = threadIdx.x - row * team;
+    const int sub = p.by_groups.div(in), g = in - sub * p.groups;
+    if (row < rows) {
+        const int64_t i = row0 + row;
+        const int pos = p.pos[i];
+        const int64_t to = target(p, r, i, pos);
+        const int dim = r.begin + g * 8;
+        const int64_t from = i * r.src_stride + dim, at = to * r.dst_stride + dim;
+        if (to >= 0) {
+            float c[NP], s[NP];
+            for (int h0 = sub; h0 < r.heads; h0 += U * r.subs) {
+                Eight<KIND> a[U], b[PAIRS ? 1 : U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int e = e0 + k * kThreads;
-            x[k] = -2;
-            row[k] = 0;
-            to[k] = 0;
-            if (e >= total) continue;
-            row[k] = r.by_row.div(e);
-            const int in_row = e - row[k] * r.row_units, h = r.by_head.div(in_row);
-            const int u = in_row - h * r.head_units, y = u - r.lo;
-            const int64_t d0 = sDst[row[k]];
-            if (sPos[row[k]] < 0 || d0 < 0) continue;
-            x[k] = y >= 0 && y < r.rot ? y : -1;
-            const int dim = y < 0 ? u * 8 : y < r.rot ? r.begin + y * 8 : r.begin + 2 * p.half + (y - r.rot) * 8;
-            const int64_t from = (row0 + row[k]) * r.src_stride + h * r.src_head + dim;
-            to[k] = d0 * r.dst_stride + h * r.dst_head + dim;
-            a[k].load(r.src, from);
-            if constexpr (!PAIRS)
-                if (x[k] >= 0) b[k].load(r.src, from + p.half);
-        }
+                for (int k = 0; k < U; ++k) {
+                    const int h = h0 + k * r.subs;
+                    if (h >= r.heads) continue;
+                    a[k].load(r.src, from + h * r.src_head);
+                    if constexpr (!PAIRS) b[k].load(r.src, from + h * r.src_head + p.half);
+                }
+                if (h0 == sub) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (x[k] == -2) continue;
-            if (KIND == kRound || x[k] >= 0) {
-                float f[8];
-                a[k].get(f);
-                if (x[k] >= 0) {
-                    const float2 *t = sTurn + row[k] * p.half + x[k] * (PAIRS ? 4 : 8);
-                    if constexpr (PAIRS) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 cs = t[i];
-                            const float u = f[2 * i], v = f[2 * i + 1];
-                            f[2 * i] = u * cs.x - v * cs.y;
-                            f[2 * i + 1] = u * cs.y + v * cs.x;
-                        }
-                    } else {
-                        float g[8];
-                        b[k].get(g);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 cs = t[i];
-                            const float u = f[i], v = g[i];
-                            f[i] = u * cs.x - v * cs.y;
-                            g[i] = u * cs.y + v * cs.x;
-                        }
-                        b[k].put(g);
-                        b[k].store(r.dst, to[k] + p.half);
+                    for (int x = 0; x < NP; ++x) {
+                        const float2 cs = turn(p, pos, g * NP + x);
+                        c[x] = cs.x;
+                        s[x] = cs.y;
                     }
                 }
-                a[k].put(f);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int h = h0 + k * r.subs;
+                    if (h >= r.heads) continue;
+                    float f[8];
+                    a[k].get(f);
+                    if constexpr (PAIRS) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float u = f[2 * x], v = f[2 * x + 1];
+                            f[2 * x] = u * c[x] - v * s[x];
+                            f[2 * x + 1] = u * s[x] + v * c[x];
+                        }
+                    } else {
+                        float e[8];
+                        b[k].get(e);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const float u = f[x], v = e[x];
+                            f[x] = u * c[x] - v * s[x];
+                            e[x] = u * s[x] + v * c[x];
+                        }
+                        b[k].put(e);
+                        b[k].store(r.dst, at + h * r.dst_head + p.half);
+                    }
+                    a[k].put(f);
+                    a[k].store(r.dst, at + h * r.dst_head);
+                }
             }
-            a[k].store(r.dst, to[k]);
         }
     }
+    constexpr int C = 4;
+    const int total = rows * r.heads * r.stay;
+    for (int e0 = threadIdx.x; e0 < total; e0 += kThreads * C) {
+        Eight<KIND> a[C];
+        int64_t at[C];
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int e = e0 + k * kThreads;
+            at[k] = -1;
+            if (e >= total) continue;
+            const int x = r.by_row.div(e), y = e - x * r.heads * r.stay, h = r.by_head.div(y), u = y - h * r.stay;
+            const int64_t i = row0 + x, to = target(p, r, i, p.pos[i]);
+            if (to < 0) continue;
+            const int dim = 8 * u + (u < r.lo ? 0 : 2 * p.half);
+            a[k].load(r.src, i * r.src_stride + h * r.src_head + dim);
+            at[k] = to * r.dst_stride + h * r.dst_head + dim;
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            if (at[k] < 0) continue;
+            if constexpr (KIND == kRound) {
+                float f[8];
+                a[k].get(f);
+                a[k].put(f);
+            }
+            a[k].store(r.dst, at[k]);
+        }
+    }
+}
+
+template <bool PAIRS, int U>
+__global__ void __launch_bounds__(kThreads) rotate_rows_kernel(const __grid_constant__ Params p) {
+    pdl_wait();
+    const Rotation &r = p.r[blockIdx.y];
+    const int64_t row0 = (int64_t)blockIdx.x * r.rows;
+    if (row0 >= p.n_rows) return;
+    if (r.kind == kBf16) rotate_vec<kBf16, PAIRS, U>(p, r, row0);
+    else if (r.kind == kRound) rotate_vec<kRound, PAIRS, (U + 1) / 2>(p, r, row0);
+    else rotate_vec<kF32, PAIRS, (U + 1) / 2>(p, r, row0);
 }
 
 __device__ __forceinline__ float load1(const void *base, int64_t e, int kind) {
@@ -177,66 +232,39 @@ __device__ __forceinline__ void store1(void *base, int64_t e, int kind, float v)
     if (kind == kF32) reinterpret_cast<float *>(base)[e] = v;
     else reinterpret_cast<__nv_bfloat16 *>(base)[e] = __float2bfloat16_rn(v);
 }
-// Rows of any alignment: a unit is an element that stays, or a pair.
-__device__ __forceinline__ void rotate_any(const Params &p, const Rotation &r, int64_t row0, int rows, const int *sPos,
-                                           const int64_t *sDst, const float2 *sTurn) {
-    const int total = rows * r.row_units;
-    for (int e = threadIdx.x; e < total; e += kThreads) {
-        const int row = r.by_row.div(e);
-        const int in_row = e - row * r.row_units, h = r.by_head.div(in_row);
-        const int u = in_row - h * r.head_units, y = u - r.lo;
-        const int64_t d0 = sDst[row];
-        if (sPos[row] < 0 || d0 < 0) continue;
-        const int64_t from = (row0 + row) * r.src_stride + h * r.src_head, to = d0 * r.dst_stride + h * r.dst_head;
-        if (y >= 0 && y < r.rot) {
-            const int a = r.begin + (p.pairs ? 2 * y : y), b = p.pairs ? a + 1 : a + p.half;
-            const float2 cs = sTurn[row * p.half + y];
-            const float f = load1(r.src, from + a, r.kind), g = load1(r.src, from + b, r.kind);
-            store1(r.dst, to + a, r.kind, f * cs.x - g * cs.y);
-            store1(r.dst, to + b, r.kind, f * cs.y + g * cs.x);
-        } else {
-            const int a = y < 0 ? u : r.begin + 2 * p.half + (y - r.rot);
-            if (r.kind == kBf16)   // bit for bit: a conversion would quiet a NaN
-                reinterpret_cast<uint16_t *>(r.dst)[to + a] = reinterpret_cast<const uint16_t *>(r.src)[from + a];
-            else store1(r.dst, to + a, r.kind, reinterpret_cast<const float *>(r.src)[from + a]);
-        }
-    }
-}
-
-// A CTA has up to eight rows of every set: their cosines and sines, once for all heads and sets, then the
-// rows themselves.
-template <bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 3) rotate_rows_kernel(const __grid_constant__ Params p) {
-    extern __shared__ float2 sTurn[];   // [rows][half]
-    __shared__ int sPos[kMaxRows];
-    __shared__ int64_t sRow[kMaxRows], sCell[kMaxRows];
+// Rows of any alignment: a block has a few of them, their cosines and sines in shared memory, and then an
+// element that stays or a pair at a time.
+__global__ void __launch_bounds__(kThreads) rotate_any_kernel(const __grid_constant__ Params p) {
+    __shared__ float2 sTurn[kTurns];   // [rows][half]
     pdl_wait();
-    const int64_t row0 = (int64_t)blockIdx.x * p.rows;
-    const int rows = (int)min((int64_t)p.rows, p.n_rows - row0);
-    if (threadIdx.x < rows) {
-        const int64_t i = row0 + threadIdx.x;
-        sPos[threadIdx.x] = p.pos[i];
-        sRow[threadIdx.x] = i;
-        int64_t c = p.slot ? p.slot[i] : -1;
-        if (p.slot && c >= p.n_cells) {
-            set_status(p.status, SFA_DEV_BAD_CELL);
-            c = -1;
-        }
-        sCell[threadIdx.x] = c;
-    }
-    __syncthreads();
+    const Rotation &r = p.r[blockIdx.y];
+    const int64_t row0 = (int64_t)blockIdx.x * r.rows;
+    const int rows = (int)min((int64_t)r.rows, p.n_rows - row0);
     for (int e = threadIdx.x; e < rows * p.half; e += kThreads) {
-        const int row = e / p.half;
-        sTurn[e] = turn(p, sPos[row], e - row * p.half);
+        const int row = p.by_groups.div(e);
+        sTurn[e] = turn(p, p.pos[row0 + row], e - row * p.half);
     }
     __syncthreads();
-    for (int k = 0; k < p.n; ++k) {
-        const Rotation &r = p.r[k];
-        const int64_t *to = r.to_cells ? sCell : sRow;
-        if (!r.vec) rotate_any(p, r, row0, rows, sPos, to, sTurn);
-        else if (r.kind == kBf16) rotate_vec<kBf16, PAIRS>(p, r, row0, rows, sPos, to, sTurn);
-        else if (r.kind == kRound) rotate_vec<kRound, PAIRS>(p, r, row0, rows, sPos, to, sTurn);
-        else rotate_vec<kF32, PAIRS>(p, r, row0, rows, sPos, to, sTurn);
+    const int units = p.half + r.stay;
+    for (int row = 0; row < rows; ++row) {
+        const int64_t i = row0 + row, d0 = target(p, r, i, p.pos[i]);
+        if (d0 < 0) continue;
+        for (int e = threadIdx.x; e < r.heads * units; e += kThreads) {
+            const int h = r.by_head.div(e), y = e - h * units;
+            const int64_t from = i * r.src_stride + h * r.src_head, to = d0 * r.dst_stride + h * r.dst_head;
+            if (y < p.half) {
+                const int a = r.begin + (p.pairs ? 2 * y : y), b = p.pairs ? a + 1 : a + p.half;
+                const float2 cs = sTurn[row * p.half + y];
+                const float f = load1(r.src, from + a, r.kind), g = load1(r.src, from + b, r.kind);
+                store1(r.dst, to + a, r.kind, f * cs.x - g * cs.y);
+                store1(r.dst, to + b, r.kind, f * cs.y + g * cs.x);
+            } else {
+                const int u = y - p.half, a = u + (u < r.lo ? 0 : 2 * p.half);
+                if (r.kind == kBf16)   // bit for bit: a conversion would quiet a NaN
+                    reinterpret_cast<uint16_t *>(r.dst)[to + a] = reinterpret_cast<const uint16_t *>(r.src)[from + a];
+                else store1(r.dst, to + a, r.kind, reinterpret_cast<const float *>(r.src)[from + a]);
+            }
+        }
     }
 }
 
@@ -303,7 +331,7 @@ extern "C" int sfa_rotate_rows(int n, const sfa_row_rotation *rotations, const s
     Params p{};
     const int rot = rope->n_rot;
     constexpr int64_t kFar = (int64_t)1 << 40;
-    bool cells = false;
+    bool cells = false, vec = rot % (rope->pairs ? 8 : 16) == 0;
     for (int k = 0; k < n; ++k) {
         const sfa_row_rotation &w = rotations[k];
         if ((w.src_dtype != SFA_BF16 && w.src_dtype != SFA_F32) || (w.dst_dtype != SFA_BF16 && w.dst_dtype != SFA_F32))
@@ -339,18 +367,13 @@ extern "C" int sfa_rotate_rows(int n, const sfa_row_rotation *rotations, const s
         }
         // strides of a single row or head do not count
         auto far16 = [](int64_t count, int64_t stride, int size) { return count <= 1 || stride * size % 16 == 0; };
-        r.vec = aligned16(w.src) && aligned16(w.dst) && w.d % 8 == 0 && w.rot_begin % 8 == 0 &&
-                rot % (rope->pairs ? 8 : 16) == 0 && far16(n_rows, w.src_stride, ss) &&
-                far16(w.to_cells ? n_cells : n_rows, w.dst_stride, ds) && far16(w.n_heads, w.src_head_stride, ss) &&
-                far16(w.n_heads, w.dst_head_stride, ds);
-        const int v = r.vec ? 8 : 1;
+        vec = vec && aligned16(w.src) && aligned16(w.dst) && w.d % 8 == 0 && w.rot_begin % 8 == 0 &&
+              far16(n_rows, w.src_stride, ss) && far16(w.to_cells ? n_cells : n_rows, w.dst_stride, ds) &&
+              far16(w.n_heads, w.src_head_stride, ss) && far16(w.n_heads, w.dst_head_stride, ds);
+        r.heads = w.n_heads;
         r.begin = w.rot_begin;
-        r.lo = same ? 0 : w.rot_begin / v;
-        r.rot = r.vec && rope->pairs ? rot / v : rot / 2 / v;
-        r.head_units = r.lo + r.rot + (same ? 0 : (w.d - w.rot_begin - rot) / v);
-        r.row_units = w.n_heads * r.head_units;
-        r.by_head.set(r.head_units);
-        r.by_row.set(r.row_units);
+        r.lo = same ? 0 : w.rot_begin;
+        r.stay = same ? 0 : w.d - rot;
     }
     if (n == 0 || n_rows == 0) return SFA_OK;
     if (!pos || (cells && !slot)) return SFA_ERR_INVALID_ARG;
@@ -359,20 +382,44 @@ extern "C" int sfa_rotate_rows(int n, const sfa_row_rotation *rotations, const s
     p.status = dev_status;
     p.n_rows = n_rows;
     p.n_cells = n_cells;
-    p.n = n;
     p.half = rot / 2;
     p.pairs = rope->pairs;
     p.inverse = inverse;
     p.magnitude = rope->magnitude;
     for (int j = 0; j < rot / 2; ++j) p.turns[j] = rope->turns[j];
-    // a row a CTA until every SM has several; then up to eight, which share a pass over the parameters
-    int64_t rows = n_rows / (8 * (int64_t)device_sm_count());
-    rows = rows < 1 ? 1 : rows > kMaxRows ? kMaxRows : rows;
-    p.rows = (int)rows;
-    const size_t smem = (size_t)rows * p.half * sizeof(float2);
-    static_assert(kTableBytes <= 40 * 1024, "fits without a raised limit");
-    if (launch_pdl(p.pairs ? rotate_rows_kernel<true> : rotate_rows_kernel<false>,
-                   dim3((unsigned)((n_rows + rows - 1) / rows)), dim3(kThreads), smem, (cudaStream_t)stream, p) !=
+    p.groups = vec ? (p.pairs ? rot / 8 : rot / 16) : p.half;
+    p.by_groups.set(p.groups);
+    // Four heads a thread, or one where that would leave threads of the device without any.
+    int64_t threads = 0, blocks = 1;
+    for (int k = 0; k < n; ++k) threads += n_rows * p.groups * p.r[k].heads;
+    const int per = threads > 4 * 2048 * (int64_t)device_sm_count() ? 4 : 1;
+    // few rows: a block on every SM before it has a second one
+    const int few = n_rows >= kThreads * (int64_t)device_sm_count() ? kThreads
+                    : n_rows > device_sm_count() ? (int)(n_rows / device_sm_count()) : 1;
+    for (int k = 0; k < n; ++k) {
+        Rotation &r = p.r[k];
+        if (vec) {
+            r.lo /= 8;
+            r.stay /= 8;
+            const int most = kThreads / p.groups;
+            r.subs = (r.heads + per - 1) / per;
+            if (r.subs > most) r.subs = most;
+            r.rows = kThreads / (p.groups * r.subs);
+            if (r.rows > few) r.rows = few;
+            r.by_team.set(p.groups * r.subs);
+            r.by_head.set(r.stay > 0 ? r.stay : 1);
+            r.by_row.set(r.stay > 0 ? r.heads * r.stay : 1);
+        } else {
+            r.rows = kTurns / p.half < 8 ? kTurns / p.half : 8;
+            r.by_head.set(p.half + r.stay);
+        }
+        const int64_t b = (n_rows + r.rows - 1) / r.rows;
+        if (b > blocks) blocks = b;
+    }
+    auto kernel = !vec ? rotate_any_kernel
+                  : per == 4 ? (p.pairs ? rotate_rows_kernel<true, 4> : rotate_rows_kernel<false, 4>)
+                             : (p.pairs ? rotate_rows_kernel<true, 1> : rotate_rows_kernel<false, 1>);
+    if (launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)n), dim3(kThreads), 0, (cudaStream_t)stream, p) !=
         cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
