@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
     const int pos0 = it.q.total - it.q.n;                  // position of the chunk's first query
     const int p_last = pos0 + (r0 + rows - 1) / p.G;
     const int len = list_end(p, it.q, p_last + 1), begin = TREE ? list_begin(p, it.q, len) : 0;
-    const int k0 = (int)min((int64_t)len, begin + (int64_t)split * p.split_keys);
-    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
-    const bool whole = len - begin <= p.split_keys;        // this piece is the whole list
+    int k0, k1;
+    piece_keys(p, blockIdx.x, g, split, begin, len, k0, k1);
+    const bool whole = one_piece(p, blockIdx.x, g, len - begin);   // this piece is the whole list
     if (split > 0 && k0 >= k1) return;                     // no such piece
 
     for (int e = tid; e < kRows * (DKQ / 4); e += kThreads) {
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
         buf = ahead ? buf ^ 1 : 0;
     }
     __syncthreads();
-    const int64_t part0 = (((int64_t)blockIdx.x * p.h_kv + g) * p.n_split + split) * p.part_rows;
+    const int64_t part0 = (int64_t)piece_part(p, blockIdx.x, g, split) * p.part_rows;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {   // the lane's rows
         const int row = 16 * (i >> 1) + 8 * (i & 1) + fr;
@@ -463,11 +463,11 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
         if (row0 >= rows) return;
         const int p_last = it.q.total - it.q.n + (r0 + rows - 1) / p.G;
         const int end = list_end(p, it.q, p_last + 1), len = end - list_begin(p, it.q, end);
-        if (len <= p.split_keys) return;
-        n_pieces = (len + p.split_keys - 1) / p.split_keys;
+        n_pieces = sfa::chunk::n_pieces(p, blockIdx.x, g, len);
+        if (n_pieces == 1) return;
 #pragma unroll
         for (int x = 0; x < W; ++x)
-            if (lane + 32 * x < n_pieces) part[x] = (blockIdx.x * p.h_kv + g) * p.n_split + lane + 32 * x;
+            if (lane + 32 * x < n_pieces) part[x] = piece_part(p, blockIdx.x, g, lane + 32 * x);
         c0 = it.q.c0;
     }
     // B of this warp's pieces from piece c on
@@ -575,7 +575,7 @@ struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, part_rows;
     int slots;                 // > 0: the work dealt out evenly (Share)
-    int n_split, split_keys;   // else: pieces of a list
+    int n_split, first_keys, split_keys, whole_lists;   // else: pieces of a list
 };
 
 // Row tiles of n_q queries in n_seq chunks of at most n_new_max, at most.
@@ -584,6 +584,43 @@ int64_t items_bound(int n_seq, int n_q, int G, int n_new_max, int item_rows, int
                                    : ((int64_t)n_new_max * G + item_rows - 1) / item_rows;
     const int64_t all = (item_q > 0 ? n_q / item_q : (int64_t)n_q * G / item_rows) + n_seq;
     return per * n_seq < all ? per * n_seq : all;
+}
+
+// A tree's row tiles all have lists as long as its sequence: those that are left after the whole waves keep
+// few SMs busy for as long as a wave.  Only they are cut: into equal pieces, or, where they are nearly a
+// wave themselves, a long first piece each and the rest in m pieces, of which `rounds` follow one another
+// on the `spare` places while the long ones run.  Chunks, whose row tiles are many, keep their equal cuts.
+// 576 wide, bf16 results: 56 lists of 30000 keys on 76 pairs 283 us whole, 270 so; 80 of 20000 329, 308; 160 of
+// 8192 278, 257; 256 of 16384 745, 715.  With every SM busy the card's power lowers its clock by about a
+// tenth, which a cut has to gain first (64 lists of 32768 369 us either way, 60 of 16384 186 and 191).
+void plan_last_wave(Plan &pl, int64_t units, int64_t tiles, int64_t slots, double t_tile, double t_piece, double t_merge,
+                    double part_us, double best_us) {
+    const int64_t whole = units / slots * slots, left = units - whole;
+    if (left == 0) return;
+    const double before = units / slots * (tiles * t_tile + t_piece), t_exit = 1.;   // t_exit: a piece that is none
+    auto take = [&](double us, int64_t n, int64_t first, int64_t other) {
+        us = before + 1.1 * us + t_merge + left * n * part_us + (double)whole * (n - 1) / slots * t_exit;
+        if (us >= best_us || (double)left * n * pl.part_rows * 514 * 4 > 1e9) return;
+        best_us = us;
+        pl.n_split = (int)n;
+        pl.first_keys = (int)(first * 128);
+        pl.split_keys = (int)(other * 128);
+        pl.whole_lists = (int)whole;
+    };
+    for (int64_t n = 2; n <= tiles && n <= 64; ++n) {
+        const int64_t per = (tiles + n - 1) / n;
+        if ((tiles + per - 1) / per == n) take((left * n + slots - 1) / slots * (per * t_tile + t_piece), n, per, per);
+    }
+    const int64_t spare = slots - left;
+    for (int64_t m = 1; m <= 4; ++m) {
+        // first * t_tile + t_piece = rounds * (rest / m * t_tile + t_piece), first + rest = tiles
+        const int64_t rounds = (left * m + spare - 1) / spare;
+        const double rest = (tiles * t_tile - (rounds - 1) * t_piece) / (t_tile * (1. + (double)rounds / m));
+        const int64_t cut = (int64_t)(rest / m + 0.5), first = tiles - cut * m;   // cut: tiles of a short piece
+        if (cut < 4 || first < cut) continue;
+        const double a = first * t_tile + t_piece, b = rounds * (cut * t_tile + t_piece);
+        take(a > b ? a : b, 1 + m, first, cut);
+    }
 }
 
 // The kernel, and how the lists are spread over the SMs: each whole or in equal pieces, a CTA
@@ -629,7 +666,10 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     const int64_t per = (tiles + best - 1) / best;
     pl.split_keys = best > 1 ? (int)(per * tile) : 0x7FFFFF80;
     pl.n_split = (int)best;
+    pl.first_keys = pl.split_keys;
     pl.slots = 0;
+    pl.whole_lists = 0;
+    if (tree == kTree && wide) plan_last_wave(pl, units, tiles, slots, t_tile, t_piece, t_merge, part_us, best_us);
     if (pl.kernel == kNarrow && units > 0 && tree != kDrafted) {
         // four tiles a slot at least: shorter pieces cost the merge more than they gain
         const int64_t few = (units * tiles + 3) / 4, ss = few < slots ? few : slots;
@@ -644,7 +684,8 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
 
 // Row tiles of partial results: each DV values and (m, l) a row; behind them the slots' own notes.
 size_t plan_parts(const Plan &pl, int h_kv) {
-    return pl.slots > 0 ? 2 * (size_t)pl.slots : pl.n_split > 1 ? (size_t)pl.items * h_kv * pl.n_split : 0;
+    return pl.slots > 0 ? 2 * (size_t)pl.slots
+                        : pl.n_split > 1 ? ((size_t)pl.items * h_kv - pl.whole_lists) * pl.n_split : 0;
 }
 size_t plan_workspace(const Plan &pl, int h_kv, int dv) {
     return plan_parts(pl, h_kv) * pl.part_rows * ((size_t)dv + 2) * sizeof(float) + 2 * (size_t)pl.slots * sizeof(int4);
@@ -774,6 +815,8 @@ int attend(const void *Q, const void *K, const void *V, int dtype, int64_t n_cel
     p.one_tile = pl.item_q > 0 ? n_new_max <= pl.item_q : (int64_t)n_new_max * p.G <= pl.item_rows;
     p.slots = pl.slots;
     p.n_split = pl.n_split;
+    p.whole_lists = pl.whole_lists;
+    p.first_keys = pl.first_keys;
     p.split_keys = pl.split_keys;
     p.n_new_max = n_new_max;
     p.n_kv_max = n_kv_max;

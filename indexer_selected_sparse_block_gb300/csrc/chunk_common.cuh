@@ -41,7 +41,9 @@ struct Params {
     int slots;           // > 0: the work is dealt out evenly to this many CTAs, see Share;
                          // 0: a CTA (pair) for each item, KV head and piece of n_split
     int n_split;         // pieces a list is cut into, at most
-    int split_keys;      // keys of a piece
+    int whole_lists;     // the lists of so many row tiles and KV heads, the first ones, are not cut
+    int first_keys;      // keys of a list's first piece
+    int split_keys;      // of the others
     int n_new_max;       // the caller's bound on a chunk's length
     int64_t n_kv_max;    // the caller's bound on total[s]
     float scale_log2;
@@ -151,6 +153,27 @@ __device__ __forceinline__ int list_begin(const Params &p, const Seq &q, int end
     return p.tree == kDrafted ? min(max(q.total - q.n, 0) & ~127, end) : 0;
 }
 
+// The list of row tile `item` and KV head g in the order in which they start, from the first cut one on.
+__device__ __forceinline__ int cut_list(const Params &p, int item, int g) { return g * p.items + item - p.whole_lists; }
+// Whether a list of len keys is one piece, and how many it is.
+__device__ __forceinline__ bool one_piece(const Params &p, int item, int g, int len) {
+    return cut_list(p, item, g) < 0 || len <= p.first_keys;
+}
+__device__ __forceinline__ int n_pieces(const Params &p, int item, int g, int len) {
+    return one_piece(p, item, g, len) ? 1 : 1 + (len - p.first_keys + p.split_keys - 1) / p.split_keys;
+}
+// Where piece `split` of the list [begin, end) starts and ends; one that is not there is empty.
+__device__ __forceinline__ void piece_keys(const Params &p, int item, int g, int split, int begin, int end, int &k0, int &k1) {
+    const bool cut = cut_list(p, item, g) >= 0;
+    const int64_t first = cut ? p.first_keys : 0x7FFFFF80, a = split > 0 ? first + (int64_t)(split - 1) * p.split_keys : 0;
+    k0 = (int)min((int64_t)end, begin + a);
+    k1 = (int)min((int64_t)end, k0 + (split > 0 ? (int64_t)p.split_keys : first));
+}
+// Row tile of a cut list's partial results.
+__device__ __forceinline__ int piece_part(const Params &p, int item, int g, int split) {
+    return cut_list(p, item, g) * p.n_split + split;
+}
+
 // Of keys kb .. kb + 31, those that a tree's row attends: bit j for key kb + j.  row: its mask's words,
 // null for a row that is none; a: the cached tokens.  Keys behind the last node are the caller's to
 // leave out.
@@ -204,9 +227,8 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
     w.g = g;
     piece_rows(p, it.q, it.tile, w);
     const int kb = list_begin(p, it.q, w.len);
-    w.k0 = (int)min((int64_t)w.len, kb + (int64_t)split * p.split_keys);
-    w.k1 = (int)min((int64_t)w.len, (int64_t)w.k0 + p.split_keys);
-    w.part = w.len - kb <= p.split_keys ? -1 : ((item * p.h_kv + g) * p.n_split + split);
+    piece_keys(p, item, g, split, kb, w.len, w.k0, w.k1);
+    w.part = one_piece(p, item, g, w.len - kb) ? -1 : piece_part(p, item, g, split);
     w.state = split > 0 && w.k0 >= w.k1 ? kEnd : kRun;
     return w;
 }

@@ -396,7 +396,7 @@ __device__ __forceinline__ void wide_pass(const WideMaps &maps, const Params &p,
         float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
         float m_sum = -INFINITY;                              // m of the sums that have moved on
         auto part_row = [&]() {
-            return (((int64_t)item * p.h_kv + g) * p.n_split + split) * p.part_rows + (r0 + c * qpc + ql) * G + h;
+            return (int64_t)piece_part(p, item, g, split) * p.part_rows + (r0 + c * qpc + ql) * G + h;
         };
         auto drain = [&](bool first, bool back) {   // columns 128 cg ..: dims 256 cg + 128 hh ..
             drain_tile<128, 512>(whole ? reinterpret_cast<float *>(p.O) : p.part_o, tO + cg * 128 + lane_addr,
@@ -644,7 +644,7 @@ __device__ __forceinline__ void wide_again_tree(const WideMaps &maps, const Para
     for (int row = warp; row < qpc * p.G; row += kWideThreads / 32) {
         const int ql = row / p.G, h = row - ql * p.G, q = c * qpc + ql;
         if (q >= wk.nq) break;
-        const int64_t part = (((int64_t)wk.item * p.h_kv + wk.g) * p.n_split + wk.split) * p.part_rows + (int64_t)q * p.G + h;
+        const int64_t part = (int64_t)piece_part(p, wk.item, wk.g, wk.split) * p.part_rows + (int64_t)q * p.G + h;
         add_nodes<DKQ, 512, VK>(p, v, wk.it.seq, wk.g, wk.it.q.c0 + wk.q0 + q, wk.g * p.G + h, wk.whole ? -1 : part,
                                 lse2[row], wk.n_tiles == 0);
     }
@@ -703,9 +703,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     wk.pos0 = wk.it.q.total - wk.it.q.n + wk.q0;              // its position
     wk.len = list_end(p, wk.it.q, wk.pos0 + wk.nq);
     const int begin = TREE ? list_begin(p, wk.it.q, wk.len) : 0;
-    wk.whole = wk.len - begin <= p.split_keys;
-    wk.k0 = (int)min((int64_t)wk.len, begin + (int64_t)wk.split * p.split_keys);
-    wk.k1 = (int)min((int64_t)wk.len, (int64_t)wk.k0 + p.split_keys);
+    wk.whole = one_piece(p, wk.item, wk.g, wk.len - begin);
+    piece_keys(p, wk.item, wk.g, wk.split, begin, wk.len, wk.k0, wk.k1);
     if (wk.split > 0 && wk.k0 >= wk.k1) return leave();       // no such piece
     wk.n_tiles = (wk.k1 - wk.k0 + kT - 1) / kT;
     wk.tb = wk.np = 0;

@@ -181,6 +181,23 @@ def test_split_lists(shape, out, lens):
     c.check()
 
 
+@pytest.mark.parametrize("shape,out,n_seq,old,n", [
+    (WIDE, "bf16", 7, 6000, 63),        # 56 lists on 76 pairs: long first pieces, the ends on the others
+    (WIDE, "f32", 10, 3000, 63),        # 80 lists: a wave of whole ones, the last few cut
+    (WIDE, "bf16", 20, 2000, 61),
+    (W512, "bf16", 12, 2500, 63)])      # two KV heads: lists in the order of both
+def test_last_waves(shape, out, n_seq, old, n):
+    lens = [(old - 17 * s, n - (s % 3 == 2)) for s in range(n_seq)]
+    odd = [(1, lens[1][0] + 5, 0, 3, math.nan), (n_seq - 1, old - 17 * (n_seq - 1), 0, 8, math.inf)]
+    c = Trees(lens, 64, shape, "bf16", out, seed=n_seq)
+    assert c.call() == 0 and c.need > 0
+    c.check()
+    if shape[2]:                         # V apart: an odd value is no odd score
+        c = Trees(lens, 64, shape, "bf16", out, seed=n_seq, odd=odd)
+        assert c.call() == 0
+        c.check_odd(odd)
+
+
 @pytest.mark.parametrize("shape", [WIDE, W512K, N128, N128K, N64])
 @pytest.mark.parametrize("n", [129, 500, 1024])
 def test_large_trees(shape, n):
