@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 }
 
 // --------------------------------------------------------------------------------- the plan
-enum Kernel { kF32, kWide, kNarrow };
+enum Kernel { kF32, kWide, kNarrow, kNodes };
+constexpr int kNodesMax = 256;   // nodes of a tree whose drafted part is done node by node
 struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, part_rows;
@@ -635,6 +636,13 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
                int64_t n_cells, bool o_bf16, int tree) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
+    if (tree == kDrafted && wide && n_new_max <= kNodesMax && (int64_t)n_seq * n_new_max <= 0x7FFFFFFF &&
+        h_kv * ((G + 15) / 16) <= 65535) {
+        pl = Plan{};
+        pl.kernel = kNodes;
+        pl.n_split = 1;
+        return pl;
+    }
     pl.kernel = wide ? kWide : tc ? kNarrow : kF32;
     pl.item_rows = wide ? 128 : tc ? 256 : kRows;
     pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
@@ -824,6 +832,7 @@ int attend(const void *Q, const void *K, const void *V, int dtype, int64_t n_cel
     cudaStream_t st = (cudaStream_t)stream;
     int r;
     if (pl.kernel == kWide) r = tree ? launch_wide_tree(p, dkq, n_cells, st) : launch_wide(p, dkq, n_cells, st);
+    else if (pl.kernel == kNodes) r = launch_nodes(p, dkq, st);
     else if (pl.kernel == kNarrow) r = tree ? launch_narrow_tree(p, dkq, n_cells, st) : launch_narrow(p, dkq, n_cells, st);
     else if (dkq == 576) r = launch_f32<576, 512, true>(p, dtype, st);
     else if (dkq == 512) r = V ? launch_f32<512, 512, false>(p, dtype, st) : launch_f32<512, 512, true>(p, dtype, st);
