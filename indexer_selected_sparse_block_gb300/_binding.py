@@ -866,22 +866,21 @@ _ROTATION = struct.Struct("@QqqQqqiiiiii")     # sfa_row_rotation of include/sfa
 
 def _rotation(src, dst, begin, n_rows, n_dst, to_cells, dev):
     """src [>= n_rows][d] or [..][h][d] into dst of the same heads, any strides but the last."""
-    if src.dim() == 2:
-        h, d, sh = 1, src.size(1), 0
-    elif src.dim() == 3:
-        h, d, sh = src.size(1), src.size(2), src.stride(1)
+    shape, to, st, dt = src.shape, dst.shape, src.stride(), dst.stride()
+    code, out = _CODES.get(src.dtype, SFA_Q8_0), _CODES.get(dst.dtype, SFA_Q8_0)
+    if len(shape) == 3:
+        n, h, d = shape
+        sh, dh = st[1], dt[1] if len(to) == 3 else 0
     else:
-        h, d, sh = 0, 0, 0
-    if (h < 1 or d < 1 or src.size(0) < n_rows or src.dtype not in (_BF16, _F32) or src.get_device() != dev
-            or (src.stride(-1) != 1 and d > 1)):
+        n, d = shape if len(shape) == 2 else (-1, 0)
+        h, sh, dh = 1, 0, 0
+    if (h < 1 or d < 1 or n < n_rows or code == SFA_Q8_0 or src.get_device() != dev or (st[-1] != 1 and d > 1)):
         _no_tensor("rows to rotate", src, dev, f"bf16 or fp32, [>= {n_rows}][d] or [>= {n_rows}][h][d], each "
                    "head contiguous")
-    if (dst.dim() != src.dim() or dst.size(0) < n_dst or dst.shape[1:] != src.shape[1:]
-            or dst.dtype not in (_BF16, _F32) or dst.get_device() != dev or (dst.stride(-1) != 1 and d > 1)):
+    if (to[1:] != shape[1:] or to[0] < n_dst or out == SFA_Q8_0 or dst.get_device() != dev
+            or (dt[-1] != 1 and d > 1)):
         _no_tensor("rotated rows", dst, dev, f"bf16 or fp32, of their rows' heads, at least {n_dst} of them")
-    return _ROTATION.pack(src.data_ptr(), src.stride(0), sh, dst.data_ptr(), dst.stride(0),
-                          dst.stride(1) if dst.dim() == 3 else 0, _CODES[src.dtype], _CODES[dst.dtype], h, d,
-                          begin, to_cells)
+    return _ROTATION.pack(src.data_ptr(), st[0], sh, dst.data_ptr(), dt[0], dh, code, out, h, d, begin, to_cells)
 
 
 def sfa_rotate_rows(rows, pos, rope: SfaRope, cells=(), slot=None, inverse: bool = False, dev_status=None,
