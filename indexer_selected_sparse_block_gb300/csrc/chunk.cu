@@ -655,7 +655,8 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     int64_t slots = wide ? device_sm_count() / 2 : device_sm_count();
     if (slots > kMaxPieces) slots = kMaxPieces;
     // us: a tile, a piece's start and end in a launch of its own and behind another one, the merge
-    const double t_tile = wide ? (o_bf16 ? 1.35 : 2.) : tc ? (o_bf16 ? 1.8 : 2.4) : dv == 512 ? 30. : 8.;
+    double t_tile = wide ? (o_bf16 ? 1.35 : 2.) : tc ? (o_bf16 ? 1.8 : 2.4) : dv == 512 ? 30. : 8.;
+    if (tree == kTree && pl.kernel == kNarrow && pl.part_rows <= 128) t_tile *= 0.7;   // one row tile
     const double t_piece = 7., t_next = 4., t_merge = 6.;
     const double part_us = (double)pl.part_rows * dv * 4 * 2 / 4e6;   // a partial, both ways
     int64_t best = 1;
@@ -683,8 +684,17 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
         const int64_t few = (units * tiles + 3) / 4, ss = few < slots ? few : slots;
         // lists shorter than their bound leave whole ones' SMs idle, dealt out ones' not
         const bool ragged = n_q < (int64_t)n_seq * n_new_max;
-        const double us = (double)units * tiles / ss * t_tile * (ragged ? 0.7 : 1.) + t_piece +
-                          (double)units / ss * t_next + (ss > 1 ? t_merge : 0.);
+        double us = (double)units * tiles / ss * t_tile * (ragged ? 0.7 : 1.) + t_piece +
+                    (double)units / ss * t_next + (ss > 1 ? t_merge : 0.);
+        // A tree's few rows leave a tile's time to the memory once every SM reads, and dealing out costs
+        // more than the model of chunks says: pieces and partial results.  (128 wide, 16 heads on 4: 24
+        // trees of 16 nodes behind 2048 whole 33 us, dealt out 41; behind 8192 92 and 89; 4 of 60 behind
+        // 8192, in equal pieces, 44 and 50; 24 of 1 to 61 behind up to 8192 97 and 79.)
+        if (tree == kTree) {
+            const double t_read = 128. * 4 * dv / 6.5e6 * ss;   // a tile of K and V
+            us += (double)units * tiles / ss * (ragged ? 0.7 : 1.) * (t_read > t_tile ? t_read - t_tile : 0.) + 10. +
+                  2. * ss * part_us;
+        }
         if (us < best_us) pl.slots = (int)ss;
     }
     return pl;
