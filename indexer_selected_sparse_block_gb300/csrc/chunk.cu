@@ -624,6 +624,18 @@ void plan_last_wave(Plan &pl, int64_t units, int64_t tiles, int64_t slots, doubl
     }
 }
 
+// Whether the drafted part is done node by node: what is faster by the waves of either, their times measured
+// on trees (a node's time grows with the nodes it attends, a tile's with the tree).  32 trees of 64 nodes, 576
+// wide, 16 heads, fp32 results: 31 us, 55 on tiles; one of 16: 5.2, 12.7; 128 wide, 16 heads on 4: one of 16 3.7,
+// 11.3, and 32 of 64 30, 14 on tiles.  (Masks that name every node: 32 of 64, 576 wide, 65 and 55.)
+bool use_nodes(int n_seq, int n_q, int G, int h_kv, bool wide, int n_new_max, int64_t items) {
+    const int64_t groups = (int64_t)h_kv * ((G + 15) / 16), grid = (int64_t)n_seq * n_new_max, sms = device_sm_count();
+    if (n_new_max > kNodesMax || grid > 0x7FFFFFFF || groups > 65535) return false;
+    const int64_t nodes = (grid < n_q ? grid : n_q) * groups, at_once = wide ? sms / 2 : sms;
+    const double one = wide ? 8.5 / (4. * sms) : 3.7 / (8. * sms), tiles = wide ? 13. : 11.;
+    return nodes * one < (items * h_kv + at_once - 1) / at_once * tiles;
+}
+
 // The kernel, and how the lists are spread over the SMs: each whole or in equal pieces, a CTA
 // (pair) for one, or, by the narrow heads' kernel, all of them dealt out evenly.  What the model
 // says takes least time:
@@ -636,18 +648,17 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
                int64_t n_cells, bool o_bf16, int tree) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
-    if (tree == kDrafted && wide && n_new_max <= kNodesMax && (int64_t)n_seq * n_new_max <= 0x7FFFFFFF &&
-        h_kv * ((G + 15) / 16) <= 65535) {
-        pl = Plan{};
-        pl.kernel = kNodes;
-        pl.n_split = 1;
-        return pl;
-    }
     pl.kernel = wide ? kWide : tc ? kNarrow : kF32;
     pl.item_rows = wide ? 128 : tc ? 256 : kRows;
     pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
     pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
+    if (tree == kDrafted && tc && use_nodes(n_seq, n_q, G, h_kv, wide, n_new_max, items)) {
+        pl = Plan{};
+        pl.kernel = kNodes;
+        pl.n_split = 1;
+        return pl;
+    }
     const int64_t most = (int64_t)n_new_max * G;
     pl.part_rows = most < pl.item_rows ? (int)most : pl.item_rows;
     const int tile = 128;

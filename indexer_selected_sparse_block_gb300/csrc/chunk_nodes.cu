@@ -1,5 +1,4 @@
-// chunk_nodes.cu -- attention of drafted nodes over each other alone (SFA_PART_DRAFTED), 512 value dims,
-// bf16 caches.
+// chunk_nodes.cu -- attention of drafted nodes over each other alone (SFA_PART_DRAFTED), bf16 caches.
 //
 // A node attends its ancestors: a handful of rows, where the tiles of chunk_wide.cuh would compute on every
 // node of the tree.  One CTA has one node and 16 heads of one KV head, and gathers the rows that the
@@ -15,12 +14,12 @@ namespace sfa {
 namespace chunk {
 namespace {
 
-constexpr int kThreads = 128, kKeys = 16, kHeads = 16, kDV = 512;
+constexpr int kThreads = 128, kKeys = 16, kHeads = 16;
 constexpr int kPP = 24;   // pitch of the weights' rows, in elements: 16-byte rows without bank conflicts
 
-template <int DKQ, bool VK>
+template <int DKQ, int DV, bool VK>
 struct Nodes16 {
-    static constexpr int kPQ = DKQ + 8, kPV = kDV + 8;   // pitches, as above
+    static constexpr int kPQ = DKQ + 8, kPV = DV + 8;   // pitches, as above
     static constexpr int kOffK = kHeads * kPQ * 2;
     static constexpr int kOffV = kOffK + kKeys * kPQ * 2;
     static constexpr int kOffRed = kOffV + (VK ? 0 : kKeys * kPV * 2);   // float [4][16][20]
@@ -44,9 +43,10 @@ __device__ __forceinline__ void gather(uint32_t to, const void *src, const int64
     }
 }
 
-template <int DKQ, bool VK>
-__global__ void __launch_bounds__(kThreads, 4) drafted_nodes_kernel(const Params p) {
-    using L = Nodes16<DKQ, VK>;
+template <int DKQ, int DV, bool VK>
+__global__ void __launch_bounds__(kThreads, DV == 512 ? 4 : 8) drafted_nodes_kernel(const Params p) {
+    using L = Nodes16<DKQ, DV, VK>;
+    constexpr int NT = DV / 32;   // 8-wide column tiles of a warp's value dims
     extern __shared__ __align__(16) uint8_t smem[];
     float *sRed = reinterpret_cast<float *>(smem + L::kOffRed);
     __nv_bfloat16 *sP = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffP);
@@ -90,9 +90,9 @@ __global__ void __launch_bounds__(kThreads, 4) drafted_nodes_kernel(const Params
         __syncwarp();
     }
     float m = -INFINITY, l = 0.f;   // of row tid / 8, base 2
-    float acc[16][4];               // value dims 128 warp + 8 x + ..
+    float acc[NT][4];               // value dims DV / 4 warp + 8 x + ..
 #pragma unroll
-    for (int x = 0; x < 16; ++x)
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[x][c] = 0.f;
     int count = 0;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 4) drafted_nodes_kernel(const Params
         count = s_count;
         if (k0 >= count) break;
         gather<DKQ, L::kPQ>(sK, p.K, sCell, p.h_kv, g);
-        if constexpr (!VK) gather<kDV, L::kPV>(sV, p.V, sCell, p.h_kv, g);
+        if constexpr (!VK) gather<DV, L::kPV>(sV, p.V, sCell, p.h_kv, g);
         cp_async_commit();
         cp_async_wait<0>();
         __syncthreads();
@@ -170,9 +170,9 @@ __global__ void __launch_bounds__(kThreads, 4) drafted_nodes_kernel(const Params
             const uint32_t pa = smem_u32(sP) + ((lane & 15) * kPP + 8 * (lane >> 4)) * 2;
 #pragma unroll
             for (int y = 0; y < 3; ++y) ldsm_x4(pa + y * 16 * kPP * 2, A[y][0], A[y][1], A[y][2], A[y][3]);
-            const uint32_t va = sV + (((lane & 7) + 8 * ((lane >> 3) & 1)) * PV + warp * 128 + 8 * (lane >> 4)) * 2;
+            const uint32_t va = sV + (((lane & 7) + 8 * ((lane >> 3) & 1)) * PV + warp * (DV / 4) + 8 * (lane >> 4)) * 2;
 #pragma unroll
-            for (int x = 0; x < 16; x += 2) {
+            for (int x = 0; x < NT; x += 2) {
                 uint32_t B[2][2];
                 ldsm_x4_t(va + 16 * x, B[0][0], B[0][1], B[1][0], B[1][1]);
 #pragma unroll
@@ -205,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 4) drafted_nodes_kernel(const Params
         const float inv = sAlpha[r];
         if (p.o_bf16) {
             // two lanes have a row's four neighbouring dims of two tiles: each takes one tile's
-            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.O) + (row0 + r) * kDV + warp * 128 + 4 * ((lane & 3) >> 1);
+            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.O) + (row0 + r) * DV + warp * (DV / 4) + 4 * ((lane & 3) >> 1);
             const bool odd = lane & 1;
 #pragma unroll
-            for (int x = 0; x < 16; x += 2) {
+            for (int x = 0; x < NT; x += 2) {
                 const uint32_t u = pack_bf16(acc[x][2 * c] * inv, acc[x][2 * c + 1] * inv),
                                v = pack_bf16(acc[x + 1][2 * c] * inv, acc[x + 1][2 * c + 1] * inv);
                 const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? u : v, 1);
@@ -216,21 +216,22 @@ __global__ void __launch_bounds__(kThreads, 4) drafted_nodes_kernel(const Params
                     *reinterpret_cast<uint2 *>(o + 8 * (x + odd)) = odd ? make_uint2(other, v) : make_uint2(u, other);
             }
         } else if (r < heads) {
-            float *o = reinterpret_cast<float *>(p.O) + (row0 + r) * kDV + warp * 128 + 2 * (lane & 3);
+            float *o = reinterpret_cast<float *>(p.O) + (row0 + r) * DV + warp * (DV / 4) + 2 * (lane & 3);
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
+            for (int x = 0; x < NT; ++x)
                 *reinterpret_cast<float2 *>(o + 8 * x) = make_float2(acc[x][2 * c] * inv, acc[x][2 * c + 1] * inv);
         }
     }
 }
 
-template <int DKQ, bool VK>
+template <int DKQ, int DV, bool VK>
 int launch(const Params &p, cudaStream_t st) {
-    if (!ensure_max_dynamic_smem(drafted_nodes_kernel<DKQ, VK>)) return SFA_ERR_CUDA;
+    using L = Nodes16<DKQ, DV, VK>;
+    if (L::kBytes > 48 * 1024 && !ensure_max_dynamic_smem(drafted_nodes_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
     const int64_t x = (int64_t)p.n_seq * p.n_new_max;
     const int y = p.h_kv * ((p.G + kHeads - 1) / kHeads);
-    if (launch_pdl(drafted_nodes_kernel<DKQ, VK>, dim3((unsigned)x, (unsigned)y), dim3(kThreads),
-                   (size_t)Nodes16<DKQ, VK>::kBytes, st, p) != cudaSuccess) {
+    if (launch_pdl(drafted_nodes_kernel<DKQ, DV, VK>, dim3((unsigned)x, (unsigned)y), dim3(kThreads), (size_t)L::kBytes, st,
+                   p) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
@@ -240,8 +241,12 @@ int launch(const Params &p, cudaStream_t st) {
 }  // namespace
 
 int launch_nodes(const Params &p, int dkq, cudaStream_t st) {
-    if (dkq == 576) return launch<576, true>(p, st);
-    return p.V ? launch<512, false>(p, st) : launch<512, true>(p, st);
+    switch (dkq) {
+        case 576: return launch<576, 512, true>(p, st);
+        case 512: return p.V ? launch<512, 512, false>(p, st) : launch<512, 512, true>(p, st);
+        case 128: return p.V ? launch<128, 128, false>(p, st) : launch<128, 128, true>(p, st);
+        default: return p.V ? launch<64, 64, false>(p, st) : launch<64, 64, true>(p, st);
+    }
 }
 
 }  // namespace chunk
