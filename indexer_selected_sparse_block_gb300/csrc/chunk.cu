@@ -571,7 +571,6 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 
 // --------------------------------------------------------------------------------- the plan
 enum Kernel { kF32, kWide, kNarrow, kNodes };
-constexpr int kNodesMax = 256;   // nodes of a tree whose drafted part is done node by node
 struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, part_rows;

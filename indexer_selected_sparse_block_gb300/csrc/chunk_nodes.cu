@@ -15,6 +15,7 @@ namespace chunk {
 namespace {
 
 constexpr int kThreads = 128, kKeys = 16, kHeads = 16;
+constexpr int kPR = 18;   // pitch of the scores' rows
 constexpr int kPP = 24;   // pitch of the weights' rows, in elements: 16-byte rows without bank conflicts
 
 template <int DKQ, int DV, bool VK>
@@ -22,12 +23,12 @@ struct Nodes16 {
     static constexpr int kPQ = DKQ + 8, kPV = DV + 8;   // pitches, as above
     static constexpr int kOffK = kHeads * kPQ * 2;
     static constexpr int kOffV = kOffK + kKeys * kPQ * 2;
-    static constexpr int kOffRed = kOffV + (VK ? 0 : kKeys * kPV * 2);   // float [4][16][20]
-    static constexpr int kOffP = kOffRed + 4 * 16 * 20 * 4;              // bf16 [3][16][kPP]
+    static constexpr int kOffRed = kOffV + (VK ? 0 : kKeys * kPV * 2);   // float [4][16][kPR]
+    static constexpr int kOffP = kOffRed + 4 * 16 * kPR * 4;              // bf16 [3][16][kPP]
     static constexpr int kOffCell = kOffP + 3 * 16 * kPP * 2;            // int64 [16]
     static constexpr int kOffAlpha = kOffCell + kKeys * 8;               // float [16]
-    static constexpr int kOffList = kOffAlpha + 16 * 4;                  // uint16 [SFA_MAX_TREE]
-    static constexpr int kBytes = kOffList + SFA_MAX_TREE * 2;
+    static constexpr int kOffList = kOffAlpha + 16 * 4;                  // uint16 [kNodesMax]
+    static constexpr int kBytes = kOffList + kNodesMax * 2;
 };
 
 // Rows of D elements at pitch P from the cells; zeros where there is none.
@@ -44,7 +45,7 @@ __device__ __forceinline__ void gather(uint32_t to, const void *src, const int64
 }
 
 template <int DKQ, int DV, bool VK>
-__global__ void __launch_bounds__(kThreads, DV == 512 ? 4 : 8) drafted_nodes_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_kernel(const Params p) {
     using L = Nodes16<DKQ, DV, VK>;
     constexpr int NT = DV / 32;   // 8-wide column tiles of a warp's value dims
     extern __shared__ __align__(16) uint8_t smem[];
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 4 : 8) drafted_nodes_ker
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    *reinterpret_cast<float2 *>(sRed + (warp * 16 + (lane >> 2) + 8 * c) * 20 + 8 * x + 2 * (lane & 3)) =
+                    *reinterpret_cast<float2 *>(sRed + (warp * 16 + (lane >> 2) + 8 * c) * kPR + 8 * x + 2 * (lane & 3)) =
                         make_float2(sc[x][2 * c], sc[x][2 * c + 1]);
         }
         __syncthreads();
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 4 : 8) drafted_nodes_ker
             float v[2], mx = -INFINITY;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float *f = sRed + r * 20 + k + 8 * x;
-                v[x] = (f[0] + f[16 * 20]) + (f[2 * 16 * 20] + f[3 * 16 * 20]);
+                const float *f = sRed + r * kPR + k + 8 * x;
+                v[x] = (f[0] + f[16 * kPR]) + (f[2 * 16 * kPR] + f[3 * 16 * kPR]);
                 v[x] = sCell[k + 8 * x] >= 0 ? v[x] * p.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, v[x]);
             }
