@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_ker
     float *sAlpha = reinterpret_cast<float *>(smem + L::kOffAlpha);
     uint16_t *sList = reinterpret_cast<uint16_t *>(smem + L::kOffList);
     __shared__ int s_count;
+    __shared__ float sInv[16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sQ = smem_u32(smem), sK = sQ + L::kOffK, sV = VK ? sK : sQ + L::kOffV;
     constexpr int PV = VK ? L::kPQ : L::kPV;
@@ -190,12 +191,13 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_ker
                 }
             }
         }
+        if (k0 + kKeys >= count) break;
     }
     // ------------------------------------------------------------------------------------ result
     const bool any = l > 0.f || l != l;
     if ((tid & 7) == 0) {
         const int r = tid >> 3;
-        sAlpha[r] = any ? 1.f / l : 0.f;
+        sInv[r] = any ? 1.f / l : 0.f;
         if (r < heads && p.lse) p.lse[row0 + r] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
     }
     cp_async_wait<0>();   // a node that attends nothing has its queries in flight still
@@ -203,24 +205,25 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_ker
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int r = (lane >> 2) + 8 * c;
-        const float inv = sAlpha[r];
-        if (p.o_bf16) {
-            // two lanes have a row's four neighbouring dims of two tiles: each takes one tile's
-            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.O) + (row0 + r) * DV + warp * (DV / 4) + 4 * ((lane & 3) >> 1);
-            const bool odd = lane & 1;
+        const float inv = sInv[r];
+        // two lanes have a row's four neighbouring dims of two tiles: each takes one tile's
+        const int64_t e = (row0 + r) * DV + warp * (DV / 4) + 4 * ((lane & 3) >> 1);
+        const bool odd = lane & 1;
 #pragma unroll
-            for (int x = 0; x < NT; x += 2) {
-                const uint32_t u = pack_bf16(acc[x][2 * c] * inv, acc[x][2 * c + 1] * inv),
-                               v = pack_bf16(acc[x + 1][2 * c] * inv, acc[x + 1][2 * c + 1] * inv);
-                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? u : v, 1);
+        for (int x = 0; x < NT; x += 2) {
+            const float u0 = acc[x][2 * c] * inv, u1 = acc[x][2 * c + 1] * inv, v0 = acc[x + 1][2 * c] * inv,
+                        v1 = acc[x + 1][2 * c + 1] * inv;
+            if (p.o_bf16) {
+                const uint32_t u = pack_bf16(u0, u1), v = pack_bf16(v0, v1), other = __shfl_xor_sync(0xFFFFFFFFu, odd ? u : v, 1);
                 if (r < heads)
-                    *reinterpret_cast<uint2 *>(o + 8 * (x + odd)) = odd ? make_uint2(other, v) : make_uint2(u, other);
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + e + 8 * (x + odd)) =
+                        odd ? make_uint2(other, v) : make_uint2(u, other);
+            } else {
+                const float o0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? u0 : v0, 1), o1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? u1 : v1, 1);
+                if (r < heads)
+                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.O) + e + 8 * (x + odd)) =
+                        odd ? make_float4(o0, o1, v0, v1) : make_float4(u0, u1, o0, o1);
             }
-        } else if (r < heads) {
-            float *o = reinterpret_cast<float *>(p.O) + (row0 + r) * DV + warp * (DV / 4) + 2 * (lane & 3);
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-                *reinterpret_cast<float2 *>(o + 8 * x) = make_float2(acc[x][2 * c] * inv, acc[x][2 * c + 1] * inv);
         }
     }
 }
