@@ -209,15 +209,17 @@ struct Piece {
 };
 enum { kRun, kSkip, kEnd };
 
+template <bool TREE>
 __device__ __forceinline__ void piece_rows(const Params &p, const Seq &q, int tile, Piece &w) {
     w.c0 = q.c0;
     w.r0 = 0;
     w.q0 = tile * p.item_q;
     w.nq = min(p.item_q, min(q.n, p.n_new_max) - w.q0);
     w.pos0 = q.total - q.n + w.q0;
-    w.len = list_end(p, q, w.pos0 + w.nq);
+    w.len = TREE ? list_end(p, q, 0) : max(0, min(key_limit(p, q), w.pos0 + w.nq));
 }
 // One piece a CTA: `split` of item and KV head g; by a whole warp.
+template <bool TREE>
 __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int split) {
     Piece w;
     w.state = kEnd;
@@ -225,8 +227,8 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item, int g, int 
     if (it.seq < 0) return w;
     w.seq = it.seq;
     w.g = g;
-    piece_rows(p, it.q, it.tile, w);
-    const int kb = list_begin(p, it.q, w.len);
+    piece_rows<TREE>(p, it.q, it.tile, w);
+    const int kb = TREE ? list_begin(p, it.q, w.len) : 0;
     piece_keys(p, item, g, split, kb, w.len, w.k0, w.k1);
     w.part = one_piece(p, item, g, w.len - kb) ? -1 : piece_part(p, item, g, split);
     w.state = split > 0 && w.k0 >= w.k1 ? kEnd : kRun;
@@ -272,12 +274,14 @@ __device__ __forceinline__ int64_t share_border(const Share &h, int c) {
 }
 // Sum of the weights of the first j row tiles of a sequence with n new tokens behind a cached ones
 // (j at most their number; the last one may be short).
+template <bool TREE>
 __device__ __forceinline__ int64_t tile_weights(const Params &p, int64_t a, int n, int tiles, int64_t j) {
-    if (p.tree) return j * (a + n + kPieceKeys);
+    if constexpr (TREE) return j * (a + n + kPieceKeys);
     const int64_t full = j < tiles ? j : tiles - 1;
     return full * a + p.item_q * (full * (full + 1) / 2) + (j < tiles ? 0 : a + n) + j * kPieceKeys;
 }
 // By one whole warp, as all of the following.
+template <bool TREE>
 __device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) {
     const int lane = threadIdx.x & 31, s = s0 + lane;
     SeqWork v;
@@ -286,7 +290,7 @@ __device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) 
     v.n = min(v.q.n, p.n_new_max);
     v.tiles = n_items(p, v.q.n);
     v.a = max(v.q.total - v.q.n, 0);
-    v.head = v.n > 0 ? tile_weights(p, v.a, v.n, v.tiles, v.tiles) : 0;
+    v.head = v.n > 0 ? tile_weights<TREE>(p, v.a, v.n, v.tiles, v.tiles) : 0;
     v.upto = v.head * p.h_kv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -295,10 +299,11 @@ __device__ __forceinline__ SeqWork seq_work(const Params &p, int s0, bool flag) 
     }
     return v;
 }
+template <bool TREE>
 __device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
     const int lane = threadIdx.x & 31;
     Share h;
-    h.group = seq_work(p, 0, flag);
+    h.group = seq_work<TREE>(p, 0, flag);
     int64_t W = lane == 31 ? h.group.upto : 0;
     for (int s0 = 32; s0 < p.n_seq; s0 += 128) {   // four sequences a lane: their loads at once
         int c0[4], c1[4], total[4];
@@ -316,7 +321,7 @@ __device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
         for (int k = 0; k < 4; ++k) {
             const Seq q = make_seq(p, c0[k], c1[k], total[k], flag);
             const int n = min(q.n, p.n_new_max), tiles = n_items(p, n);
-            if (n > 0) W += tile_weights(p, max(q.total - q.n, 0), n, tiles, tiles) * p.h_kv;
+            if (n > 0) W += tile_weights<TREE>(p, max(q.total - q.n, 0), n, tiles, tiles) * p.h_kv;
         }
     }
 #pragma unroll
@@ -330,12 +335,13 @@ __device__ __forceinline__ Share share_of(const Params &p, int c, bool flag) {
     return h;
 }
 // The unit at place x < W of the line, no place before an earlier call's.
+template <bool TREE>
 __device__ __forceinline__ Unit share_unit(const Params &p, Share &h, int64_t x) {
     unsigned in = __ballot_sync(0xFFFFFFFFu, x < h.before + h.group.upto);
     while (!in && h.s0 + 32 < p.n_seq) {
         h.before += __shfl_sync(0xFFFFFFFFu, h.group.upto, 31);
         h.s0 += 32;
-        h.group = seq_work(p, h.s0, false);
+        h.group = seq_work<TREE>(p, h.s0, false);
         in = __ballot_sync(0xFFFFFFFFu, x < h.before + h.group.upto);
     }
     const SeqWork &v = h.group;
@@ -356,12 +362,12 @@ __device__ __forceinline__ Unit share_unit(const Params &p, Share &h, int64_t x)
     int lo = 0, hi = tiles - 1;   // the last tile whose weights begin at or before r
     while (lo < hi) {
         const int m = (lo + hi + 1) >> 1;
-        if (tile_weights(p, a, n, tiles, m) <= r) lo = m;
+        if (tile_weights<TREE>(p, a, n, tiles, m) <= r) lo = m;
         else hi = m - 1;
     }
     u.tile = lo;
-    u.w = a + (p.tree ? (int64_t)n : min((int64_t)(lo + 1) * p.item_q, (int64_t)n)) + kPieceKeys;
-    u.u0 = x - r + tile_weights(p, a, n, tiles, lo);
+    u.w = a + (TREE ? (int64_t)n : min((int64_t)(lo + 1) * p.item_q, (int64_t)n)) + kPieceKeys;
+    u.u0 = x - r + tile_weights<TREE>(p, a, n, tiles, lo);
     return u;
 }
 // Keys [k0, k1) of a unit with a list of len that slot c has; by its borders alone, so that
@@ -372,14 +378,15 @@ __device__ __forceinline__ void share_keys(const Share &h, int c, const Unit &u,
     k1 = b >= u.w ? len : (int)min((b + 64) & ~(int64_t)127, (int64_t)len);
 }
 // Slot c's next piece.
+template <bool TREE>
 __device__ __forceinline__ Piece share_next(const Params &p, int c, Share &h) {
     Piece w;
     w.state = kEnd;
     if (h.at >= h.end) return w;
-    const Unit u = share_unit(p, h, h.at);
+    const Unit u = share_unit<TREE>(p, h, h.at);
     w.seq = u.seq;
     w.g = u.g;
-    piece_rows(p, u.q, u.tile, w);
+    piece_rows<TREE>(p, u.q, u.tile, w);
     share_keys(h, c, u, w.len, w.k0, w.k1);
     const bool first = u.u0 >= share_border(h, c);   // the list's start is this slot's
     const bool all = w.k0 == 0 && w.k1 == w.len;
@@ -392,16 +399,17 @@ __device__ __forceinline__ Piece share_next(const Params &p, int c, Share &h) {
     return w;
 }
 // Slot c's next piece (first: its first one).  Not inlined: the kernel's other warps keep their registers.
+template <bool TREE>
 static __device__ __noinline__ Piece share_piece(const Params &p, int c, Share &h, bool first) {
     const bool lead = (threadIdx.x & 31) == 0;
     if (first) {
-        h = share_of(p, c, c == 0);
+        h = share_of<TREE>(p, c, c == 0);
         if (lead) {
             p.slot_info[2 * c] = make_int4(0, 1, 0, 0);
             p.slot_info[2 * c + 1] = make_int4(0, 0, 0, 0);
         }
     }
-    const Piece w = share_next(p, c, h);
+    const Piece w = share_next<TREE>(p, c, h);
     if (w.state != kEnd && lead) {
         if (w.head) p.slot_info[2 * c] = make_int4(w.state == kRun && w.part == 2 * c, w.ends, 0, 0);
         if (w.state == kRun && w.part == 2 * c + 1)

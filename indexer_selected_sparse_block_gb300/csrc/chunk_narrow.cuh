@@ -512,9 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 19) {
         Piece f;
         if (p.slots > 0) {
-            f = share_piece(p, blockIdx.x, share, true);
+            f = share_piece<TREE>(p, blockIdx.x, share, true);
         } else {
-            f = piece_of(p, blockIdx.x, blockIdx.y, blockIdx.z);
+            f = piece_of<TREE>(p, blockIdx.x, blockIdx.y, blockIdx.z);
         }
         if (lane == 0) *reinterpret_cast<Piece *>(sPiece) = f;
     }
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 19) {
             Piece f;
             f.state = kEnd;
-            if (p.slots > 0) f = share_piece(p, blockIdx.x, share, false);
+            if (p.slots > 0) f = share_piece<TREE>(p, blockIdx.x, share, false);
             if (lane == 0) *reinterpret_cast<Piece *>(sPiece + ((i_piece + 1) & 1) * 64) = f;
         } else {
             narrow_piece<D, VK, HL, TREE>(maps, p, bxs, qpt, n_cells, smem, tmem, pc, ph);

@@ -396,7 +396,8 @@ __device__ __forceinline__ void wide_pass(const WideMaps &maps, const Params &p,
         float m = -INFINITY, l = 0.f;                         // base 2; l of this thread's keys only
         float m_sum = -INFINITY;                              // m of the sums that have moved on
         auto part_row = [&]() {
-            return (int64_t)piece_part(p, item, g, split) * p.part_rows + (r0 + c * qpc + ql) * G + h;
+            return (TREE ? (int64_t)piece_part(p, item, g, split) : ((int64_t)g * p.items + item) * p.n_split + split) * p.part_rows +
+                   (r0 + c * qpc + ql) * G + h;
         };
         auto drain = [&](bool first, bool back) {   // columns 128 cg ..: dims 256 cg + 128 hh ..
             drain_tile<128, 512>(whole ? reinterpret_cast<float *>(p.O) : p.part_o, tO + cg * 128 + lane_addr,
@@ -701,10 +702,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     wk.r0 = 0;
     wk.nq = min(p.item_q, min(wk.it.q.n, p.n_new_max) - wk.q0);
     wk.pos0 = wk.it.q.total - wk.it.q.n + wk.q0;              // its position
-    wk.len = list_end(p, wk.it.q, wk.pos0 + wk.nq);
-    const int begin = TREE ? list_begin(p, wk.it.q, wk.len) : 0;
-    wk.whole = one_piece(p, wk.item, wk.g, wk.len - begin);
-    piece_keys(p, wk.item, wk.g, wk.split, begin, wk.len, wk.k0, wk.k1);
+    if constexpr (TREE) {
+        wk.len = list_end(p, wk.it.q, 0);
+        const int begin = list_begin(p, wk.it.q, wk.len);
+        wk.whole = one_piece(p, wk.item, wk.g, wk.len - begin);
+        piece_keys(p, wk.item, wk.g, wk.split, begin, wk.len, wk.k0, wk.k1);
+    } else {   // equal pieces
+        wk.len = max(0, min(key_limit(p, wk.it.q), wk.pos0 + wk.nq));
+        wk.whole = wk.len <= p.split_keys;
+        wk.k0 = (int)min((int64_t)wk.len, (int64_t)wk.split * p.split_keys);
+        wk.k1 = (int)min((int64_t)wk.len, (int64_t)wk.k0 + p.split_keys);
+    }
     if (wk.split > 0 && wk.k0 >= wk.k1) return leave();       // no such piece
     wk.n_tiles = (wk.k1 - wk.k0 + kT - 1) / kT;
     wk.tb = wk.np = 0;
