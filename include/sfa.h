@@ -695,7 +695,7 @@ int sfa_rope_init(sfa_rope *rope, int n_rot, int pairs, const double *freq, doub
  *   inverse 1: every angle the other way.  Since the map is magnitude times a rotation, this is also
  *        its gradient's: the gradient of the unrotated rows from that of the rotated ones.
  * One rotation may write what another one does not read or write; one's dst may not overlap its own src
- * but in place.  A negative slot is left out; one >= n_cells too, flagged SFA_DEV_BAD_CELL.
+ * but in place.  A negative slot is left out; one >= n_cells too, flagged SFA_DEV_BAD_CELL; the others must differ.
  * One launch.  Rows at any stride, aligned to their type; 16 bytes a load where everything is aligned
  * so (d, rot_begin and n_rot / 2 multiples of 8, strides of 16 bytes), else an element or a pair.
  * Limits: rot_begin >= 0, rot_begin + n_rot <= d, n_heads * d <= 2^24; no two heads of dst overlap

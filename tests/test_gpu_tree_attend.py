@@ -210,6 +210,49 @@ def test_large_trees(shape, n):
     c.check()
 
 
+@pytest.mark.parametrize("shape", [(576, 512, False, 48, 1), (576, 512, False, 12, 4), (512, 512, True, 40, 2),
+                                   (512, 512, False, 64, 1), (128, 128, True, 64, 1), (128, 128, False, 15, 3),
+                                   (64, 64, True, 21, 3), (64, 64, True, 16, 16)])
+def test_groups_of_heads(shape):
+    """Groups that leave tiles with rows to spare, and more heads than a node's tile has."""
+    c = Trees([(300, 11), (0, 5), (77, 19)], 16, shape, "bf16", "f32", seed=shape[3])
+    assert c.call() == 0
+    c.check()
+    assert c.call(DRAFTED) == 0
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [WIDE, N128, N64])
+@pytest.mark.parametrize("n_seq", [33, 300])
+def test_many_sequences(shape, n_seq):
+    """More sequences than a warp counts at a time, of a few nodes each, some without any."""
+    r = random.Random(n_seq)
+    lens = [(r.choice([0, 3, 130, r.randrange(300)]), r.choice([0, 1, 2, 5, 9])) for _ in range(n_seq)]
+    c = Trees(lens, 8, shape, "bf16", "bf16", seed=n_seq, spare_q=3)
+    assert c.call() == 0
+    c.check()
+    assert c.call(DRAFTED) == 0
+    c.check()
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace from its stream's pool."""
+    a, b = Trees([(30000, 20)], 64, WIDE, seed=3), Trees([(20000, 31), (9000, 4)], 64, N128, seed=4)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args = [(c.Q, c.K, c.V, c.table, c.page, i32(c.cu), i32(c.total), c.mask, 31, 30031, c.scale) for c in (a, b)]
+    for c in (a, b):
+        c.part = sfa.SFA_PART_ALL
+        c.O = torch.full((c.Q.shape[0], c.h_q, c.dv), 7.0, device=DEV)
+        c.lse = torch.full((c.Q.shape[0], c.h_q), 7.0, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, x, s in zip((a, b), args, streams):
+            sfa.sfa_tree_attend_paged(*x, c.O, lse=c.lse, stream=s)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
 @pytest.mark.parametrize("shape,dtype", [(WIDE, "bf16"), (N128, "bf16"), (N64, "bf16"), (WIDE, "f32"), (N64, "q8")])
 def test_any_mask(shape, dtype):
     """Masks that are no tree's: rows that attend nothing, later nodes, not themselves; bits behind the last
