@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 }
 
 // --------------------------------------------------------------------------------- the plan
-enum Kernel { kF32, kWide, kNarrow, kNodes };
+enum Kernel { kF32, kWide, kNarrow, kNodes, kQ8Tree };
 struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, part_rows;
@@ -647,8 +647,9 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
                int64_t n_cells, bool o_bf16, int tree) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
-    pl.kernel = wide ? kWide : tc ? kNarrow : kF32;
-    pl.item_rows = wide ? 128 : tc ? 256 : kRows;
+    const bool q8_tree = dtype == SFA_Q8_0 && tree;
+    pl.kernel = wide ? kWide : tc ? kNarrow : q8_tree ? kQ8Tree : kF32;
+    pl.item_rows = wide ? 128 : tc ? 256 : q8_tree ? kQ8Rows : kRows;
     pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
     pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
@@ -667,6 +668,7 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     // us: a tile, a piece's start and end in a launch of its own and behind another one, the merge
     double t_tile = wide ? (o_bf16 ? 1.35 : 2.) : tc ? (o_bf16 ? 1.8 : 2.4) : dv == 512 ? 30. : 8.;
     if (tree == kTree && pl.kernel == kNarrow && pl.part_rows <= 128) t_tile *= 0.7;   // one row tile
+    if (q8_tree) t_tile = dv == 512 ? 17. : dv == 128 ? 5. : 3.;
     const double t_piece = 7., t_next = 4., t_merge = 6.;
     const double part_us = (double)pl.part_rows * dv * 4 * 2 / 4e6;   // a partial, both ways
     int64_t best = 1;
@@ -853,6 +855,7 @@ int attend(const void *Q, const void *K, const void *V, int dtype, int64_t n_cel
     int r;
     if (pl.kernel == kWide) r = tree ? launch_wide_tree(p, dkq, n_cells, st) : launch_wide(p, dkq, n_cells, st);
     else if (pl.kernel == kNodes) r = launch_nodes(p, dkq, st);
+    else if (pl.kernel == kQ8Tree) r = launch_q8_tree(p, dkq, st);
     else if (pl.kernel == kNarrow) r = tree ? launch_narrow_tree(p, dkq, n_cells, st) : launch_narrow(p, dkq, n_cells, st);
     else if (dkq == 576) r = launch_f32<576, 512, true>(p, dtype, st);
     else if (dkq == 512) r = V ? launch_f32<512, 512, false>(p, dtype, st) : launch_f32<512, 512, true>(p, dtype, st);
