@@ -4,8 +4,8 @@
 // binary16 and bf16, so the products run on them as they are and the scales come in around the products:
 //   s_ik  = sum_b scale_kb (sum_{j in b} q_ij code_kj)   a block's sum, two m16n8k16 steps, then one fp32
 //           multiply-add: exact products, fp32 sums;
-//   o_id += sum_k (p_ik scale_kb) code_kd                the weights take the scale of the key's block that d
-//           is in, as two bf16 parts (2^-17): a lane's are scaled and cut for 32 dims at a time.
+//   o_id += sum_k p_ik (scale_kb code_kd)                weights and values as two bf16 parts each (2^-17), the
+//           three larger products of the four; a lane expands the values where it needs them, in registers.
 // bf16 queries are binary16 times a power of two of their row (a value below 2^-35 of the row's largest
 // loses bits).  No value is ever expanded in memory: a tile is its raw rows.
 //
@@ -21,16 +21,22 @@ namespace chunk {
 namespace {
 
 constexpr int kThreads = 256, kKeys = 32, kBufs = 3;
-constexpr int kPS = kKeys + 4;   // pitch of the weights' rows
+constexpr int kPS = kKeys + 8;   // pitch of the weights' rows, in bf16: 16-byte rows without bank conflicts
+// Pitch of a raw row in shared memory: four rows' 32 bytes, a quarter of the bank line each.
+constexpr int raw_pitch(int bytes) { return bytes % 128 == 32 || bytes % 128 == 96 ? bytes : raw_pitch(bytes + 16); }
+// Where key k of sixteen stands in the contraction with the values: lane fc has those of 2 fc, 2 fc + 1, 2 fc + 8
+// and 2 fc + 9, which are the keys fc, fc + 4, fc + 8 and fc + 12.
+__device__ __forceinline__ int key_slot(int k) { return 2 * (k & 3) + ((k >> 2) & 1) + 8 * (k >> 3); }
 
 template <int DKQ, int DV, bool VK>
 struct Q8 {
     static constexpr int kRK = q8_row_bytes(DKQ), kRV = q8_row_bytes(DV);
-    static constexpr int kPQ = DKQ + 8;                               // pitch of the queries' rows
+    static constexpr int kPK = raw_pitch(kRK), kPV = VK ? kPK : raw_pitch(kRV);
+    static constexpr int kPQ = DKQ + 32;                              // pitch of the queries' rows
     static constexpr int kOffK = kQ8Rows * kPQ * 2;
-    static constexpr int kOffV = kOffK + kBufs * kKeys * kRK;
-    static constexpr int kOffP = kOffV + (VK ? 0 : kBufs * kKeys * kRV);
-    static constexpr int kOffOk = kOffP + kQ8Rows * kPS * 4;           // int [kBufs][kKeys]: the key has a cell
+    static constexpr int kOffV = kOffK + kBufs * kKeys * kPK;
+    static constexpr int kOffP = kOffV + (VK ? 0 : kBufs * kKeys * kPV);   // bf16 [2][64][kPS]
+    static constexpr int kOffOk = kOffP + 2 * kQ8Rows * kPS * 2;       // int [kBufs][kKeys]: the key has a cell
     static constexpr int kOffMax = kOffOk + kBufs * kKeys * 4;        // float [2][64]
     static constexpr int kOffAlpha = kOffMax + 2 * kQ8Rows * 4;
     static constexpr int kOffUnit = kOffAlpha + kQ8Rows * 4;           // a row's scores' unit
@@ -53,6 +59,19 @@ template <int I>
 __device__ __forceinline__ float code_f32(uint32_t w) {
     return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + I)) - 8388736.f;
 }
+// mma_f16_16816 onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Two values to bf16, and what is left of them.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16(x, y);
+    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+}
 __device__ __forceinline__ float scale_at(const uint8_t *row, int d, int block) {
     return __half2float(*reinterpret_cast<const __half *>(row + d + 2 * block));
 }
@@ -60,11 +79,12 @@ __device__ __forceinline__ float scale_at(const uint8_t *row, int d, int block) 
 template <int DKQ, int DV, bool VK>
 __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_kernel(const Params p) {
     using L = Q8<DKQ, DV, VK>;
-    constexpr int RK = L::kRK, RV = VK ? L::kRK : L::kRV, DVS = VK ? DKQ : DV;   // DVS: where a value row's scales are
+    constexpr int RK = L::kRK, RV = L::kRV, PK = L::kPK, PV = L::kPV, DVS = VK ? DKQ : DV;   // DVS: where a value row's scales are
     constexpr int BW = L::kBW, MW = L::kMW;
     extern __shared__ __align__(16) uint8_t smem[];
     __half *sQ = reinterpret_cast<__half *>(smem);
-    float *sP = reinterpret_cast<float *>(smem + L::kOffP), *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
+    __nv_bfloat16 *sP = reinterpret_cast<__nv_bfloat16 *>(smem + L::kOffP);
+    float *sMax = reinterpret_cast<float *>(smem + L::kOffMax);
     float *sAlpha = reinterpret_cast<float *>(smem + L::kOffAlpha), *sUnit = reinterpret_cast<float *>(smem + L::kOffUnit);
     int *sOk = reinterpret_cast<int *>(smem + L::kOffOk);
     __shared__ Item s_item;
@@ -98,11 +118,11 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
             const int64_t cell = __shfl_sync(0xFFFFFFFFu, mine, i);
             const int64_t row = (cell < 0 ? 0 : cell) * p.h_kv + g;
             const uint32_t on = cell < 0 ? 0u : 16u;
-            const uint32_t k = smem_u32(smem + L::kOffK + (b * kKeys + warp * 4 + i) * RK);
+            const uint32_t k = smem_u32(smem + L::kOffK + (b * kKeys + warp * 4 + i) * PK);
             for (int c = lane; c < RK / 16; c += 32)
                 cp_async16(k + 16 * c, reinterpret_cast<const uint8_t *>(p.K) + row * RK + 16 * c, on);
             if constexpr (!VK) {
-                const uint32_t v = smem_u32(smem + L::kOffV + (b * kKeys + warp * 4 + i) * RV);
+                const uint32_t v = smem_u32(smem + L::kOffV + (b * kKeys + warp * 4 + i) * PV);
                 for (int c = lane; c < RV / 16; c += 32)
                     cp_async16(v + 16 * c, reinterpret_cast<const uint8_t *>(p.V) + row * RV + 16 * c, on);
             }
@@ -166,31 +186,41 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
         __syncthreads();   // the tile is there, for all; the one before is done with
         if (t + kBufs - 1 < n_tiles) fetch(t0 + (kBufs - 1) * kKeys, buf == 0 ? kBufs - 1 : buf - 1);
         cp_async_commit();
-        const uint8_t *rK = smem + L::kOffK + buf * kKeys * RK;
-        const uint8_t *rV = VK ? rK : smem + L::kOffV + buf * kKeys * RV;
+        const uint8_t *rK = smem + L::kOffK + buf * kKeys * PK;
+        const uint8_t *rV = VK ? rK : smem + L::kOffV + buf * kKeys * PV;
         float s[2][4] = {};   // keys 16 kh + 8 nt + 2 fc, + 1 of both rows
         {
             const __half *qa = sQ + (16 * rg + fr) * L::kPQ + 8 * fc;
-#pragma unroll 2
-            for (int b = 0; b < DKQ / 32; ++b) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(qa + 32 * b),
-                            y = *reinterpret_cast<const uint4 *>(qa + 8 * L::kPQ + 32 * b);
-                const uint32_t A0[4] = {x.x, y.x, x.y, y.y}, A1[4] = {x.z, y.z, x.w, y.w};
+            const uint8_t *kc = rK + (16 * kh + fr) * PK + 8 * fc, *ks = rK + (16 * kh + 2 * fc) * PK + DKQ;
+#pragma unroll 1
+            for (int b0 = 0; b0 < DKQ / 32; b0 += 2) {
+                float2 c[2][2];   // scales of both blocks, of keys 8 nt + 2 fc and the next
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(rK + (16 * kh + 8 * nt + fr) * RK + 32 * b + 8 * fc);
-                    uint32_t h[4];
-                    codes_f16(w.x, h[0], h[1]);
-                    codes_f16(w.y, h[2], h[3]);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16_16816(d, A0, h[0], h[1]);
-                    mma_f16_16816(d, A1, h[2], h[3]);
-                    const uint8_t *key = rK + (16 * kh + 8 * nt + 2 * fc) * RK;
-                    const float c0 = scale_at(key, DKQ, b), c1 = scale_at(key + RK, DKQ, b);
-                    s[nt][0] = fmaf(d[0], c0, s[nt][0]);
-                    s[nt][1] = fmaf(d[1], c1, s[nt][1]);
-                    s[nt][2] = fmaf(d[2], c0, s[nt][2]);
-                    s[nt][3] = fmaf(d[3], c1, s[nt][3]);
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        c[nt][x] = __half22float2(*reinterpret_cast<const __half2 *>(ks + (8 * nt + x) * PK + 2 * b0));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int b = b0 + y;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(qa + 32 * b),
+                                v = *reinterpret_cast<const uint4 *>(qa + 8 * L::kPQ + 32 * b);
+                    const uint32_t A0[4] = {u.x, v.x, u.y, v.y}, A1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(kc + 8 * nt * PK + 32 * b);
+                        uint32_t h[4];
+                        codes_f16(w.x, h[0], h[1]);
+                        codes_f16(w.y, h[2], h[3]);
+                        float d[4];
+                        mma_f16_first(d, A0, h[0], h[1]);
+                        mma_f16_16816(d, A1, h[2], h[3]);
+                        const float c0 = y ? c[nt][0].y : c[nt][0].x, c1 = y ? c[nt][1].y : c[nt][1].x;
+                        s[nt][0] = fmaf(d[0], c0, s[nt][0]);
+                        s[nt][1] = fmaf(d[1], c1, s[nt][1]);
+                        s[nt][2] = fmaf(d[2], c0, s[nt][2]);
+                        s[nt][3] = fmaf(d[3], c1, s[nt][3]);
+                    }
                 }
             }
         }
@@ -223,14 +253,16 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
             float sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                float e[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float x = s[nt][2 * y + c];
-                    e[c] = x == -INFINITY ? 0.f : exp2f(x - mn);
-                    sum += e[c];
+                    const float e = x == -INFINITY ? 0.f : exp2f(x - mn);
+                    sum += e;
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(e);
+                    __nv_bfloat16 *to = sP + row * kPS + 16 * kh + key_slot(8 * nt + 2 * fc + c);
+                    to[0] = hi;
+                    to[kQ8Rows * kPS] = __float2bfloat16_rn(e - __bfloat162float(hi));
                 }
-                *reinterpret_cast<float2 *>(sP + row * kPS + 16 * kh + 8 * nt + 2 * fc) = make_float2(e[0], e[1]);
             }
             m[y] = mn;
             l[y] = l[y] * al + sum;
@@ -257,40 +289,60 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
 #pragma unroll
             for (int b = 0; b < BW; ++b) {
                 const int blk = BW * bw + b;
-                const uint8_t *v0 = rV + (16 * ks + 2 * fc) * RV;   // keys 2 fc, + 1, + 8, + 9
+                const uint8_t *v0 = rV + (16 * ks + fc) * PV;   // keys fc, + 4, + 8, + 12
                 uint32_t w[4];
                 float c[4];
+                bool odd = false;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint8_t *v = v0 + ((x & 1) + 8 * (x >> 1)) * RV;
+                    const uint8_t *v = v0 + 4 * x * PV;
                     w[x] = *reinterpret_cast<const uint32_t *>(v + 32 * blk + 4 * fr) ^ 0x80808080u;
                     c[x] = scale_at(v, DVS, blk);
+                    // a scale that is not finite: not in the products, where a zero weight would not cancel it
+                    if (c[x] - c[x] != 0.f) {
+                        c[x] = 0.f;
+                        odd = true;
+                    }
                 }
-                uint32_t B[4][2];   // of dims 4 fr + i
+                uint32_t hi[4][2], lo[4][2];   // of dims 4 fr + i
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    B[0][x] = pack_bf16(code_f32<0>(w[2 * x]), code_f32<0>(w[2 * x + 1]));
-                    B[1][x] = pack_bf16(code_f32<1>(w[2 * x]), code_f32<1>(w[2 * x + 1]));
-                    B[2][x] = pack_bf16(code_f32<2>(w[2 * x]), code_f32<2>(w[2 * x + 1]));
-                    B[3][x] = pack_bf16(code_f32<3>(w[2 * x]), code_f32<3>(w[2 * x + 1]));
+                    const uint32_t u = w[2 * x], v = w[2 * x + 1];
+                    const float cu = c[2 * x], cv = c[2 * x + 1];
+                    split_bf16(code_f32<0>(u) * cu, code_f32<0>(v) * cv, hi[0][x], lo[0][x]);
+                    split_bf16(code_f32<1>(u) * cu, code_f32<1>(v) * cv, hi[1][x], lo[1][x]);
+                    split_bf16(code_f32<2>(u) * cu, code_f32<2>(v) * cv, hi[2][x], lo[2][x]);
+                    split_bf16(code_f32<3>(u) * cu, code_f32<3>(v) * cv, hi[3][x], lo[3][x]);
                 }
 #pragma unroll
                 for (int x = 0; x < MW; ++x) {
-                    uint32_t hi[4], lo[4];
+                    uint32_t ph[4], pl[4];
+                    const uint32_t pa = smem_u32(sP + (16 * (MW * mw + x) + (lane & 15)) * kPS + 16 * ks + 8 * (lane >> 4));
+                    ldsm_x4(pa, ph[0], ph[1], ph[2], ph[3]);
+                    ldsm_x4(pa + kQ8Rows * kPS * 2, pl[0], pl[1], pl[2], pl[3]);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {   // rows fr, fr + 8; keys 2 fc .., 2 fc + 8 ..
-                        float2 e = *reinterpret_cast<const float2 *>(sP + (16 * (MW * mw + x) + fr + 8 * (y & 1)) * kPS + 16 * ks +
-                                                                     8 * (y >> 1) + 2 * fc);
-                        // what no weight meets has none, whatever its scale
-                        e.x = e.x == 0.f ? 0.f : e.x * c[2 * (y >> 1)];
-                        e.y = e.y == 0.f ? 0.f : e.y * c[2 * (y >> 1) + 1];
-                        hi[y] = pack_bf16(e.x, e.y);
-                        lo[y] = pack_bf16(e.x - __uint_as_float(hi[y] << 16), e.y - __uint_as_float(hi[y] & 0xFFFF0000u));
-                    }
+                    for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], pl, hi[i][0], hi[i][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma_bf16_16816(acc[b][x][i], lo, B[i][0], B[i][1]);
-                        mma_bf16_16816(acc[b][x][i], hi, B[i][0], B[i][1]);
+                    for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], ph, lo[i][0], lo[i][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], ph, hi[i][0], hi[i][1]);
+                }
+                if (__any_sync(0xFFFFFFFFu, odd)) {   // such keys one by one, to the rows that attend them
+                    for (int k = 0; k < 16; ++k) {
+                        const uint8_t *v = rV + (16 * ks + k) * PV;
+                        const float sc = scale_at(v, DVS, blk);
+                        if (sc - sc == 0.f) continue;
+#pragma unroll
+                        for (int x = 0; x < MW; ++x)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {   // row fr + 8 (y / 2), dim 8 fc + 4 (y % 2) + i
+                                    const int row = 16 * (MW * mw + x) + fr + 8 * (y >> 1);
+                                    const float e = __bfloat162float(sP[row * kPS + 16 * ks + key_slot(k)]);
+                                    const float code = (float)(int8_t)v[32 * blk + 8 * fc + 4 * (y & 1) + i];
+                                    if (e != 0.f) acc[b][x][i][y] += e * (sc * code);
+                                }
                     }
                 }
             }
