@@ -759,8 +759,13 @@ int sfa_build_tree_maps(const int32_t *parent, const int32_t *cu_new, const int3
  * A row that attends nothing gives O = 0 and lse = -inf.  A value of a node that is not finite makes what
  * attends it not finite, and nothing else: rows of a bf16 cache that share a tile with one are done a
  * second time, their bf16 results then rounded twice.
- * Arguments otherwise, precision, limits and workspace as sfa_chunk_attend_paged;
- * n_new_max <= 32 * mask_words <= SFA_MAX_TREE.
+ * Precision as sfa_chunk_attend_paged, but: the drafted part of bf16 caches, where it is done node by node
+ * (trees of up to 256 nodes, a rule on sizes), keeps the weights to 2^-27; q8_0 caches are multiplied as
+ * codes, the scores fp32 sums of exact products of a block each, weights and values as two bf16 halves
+ * (2^-16 of a product); a bf16 query is binary16 there, scaled by a power of two (what is below 2^-35 of
+ * its largest value loses bits).
+ * Arguments otherwise, limits and workspace as sfa_chunk_attend_paged; n_new_max <= 32 * mask_words <=
+ * SFA_MAX_TREE.
  */
 size_t sfa_tree_attend_workspace_bytes(int dtype, int n_seq, int n_q, int h_q, int h_kv, int dkq, int dv,
                                        int has_v, int part, int n_new_max, int64_t n_kv_max, int o_dtype);
