@@ -625,7 +625,7 @@ void plan_last_wave(Plan &pl, int64_t units, int64_t tiles, int64_t slots, doubl
 
 // Whether the drafted part is done node by node: what is faster by the waves of either, their times measured
 // on trees (a node's time grows with the nodes it attends, a tile's with the tree).  32 trees of 64 nodes, 576
-// wide, 16 heads, fp32 results: 31 us, 55 on tiles; one of 16: 5.2, 12.7; 128 wide, 16 heads on 4: one of 16 3.7,
+// wide, 16 heads, fp32 results: 28 us, 55 on tiles; one of 16: 5.2, 12.7; 128 wide, 16 heads on 4: one of 16 3.7,
 // 11.3, and 32 of 64 30, 14 on tiles.  (Masks that name every node: 32 of 64, 576 wide, 65 and 55.)
 bool use_nodes(int n_seq, int n_q, int G, int h_kv, bool wide, int n_new_max, int64_t items) {
     const int64_t groups = (int64_t)h_kv * ((G + 15) / 16), grid = (int64_t)n_seq * n_new_max, sms = device_sm_count();

@@ -6,8 +6,10 @@
 // products, and a value that is not finite reaches the nodes that attend it and no other.
 //   S = Q K^T: each of the four warps over a quarter of the head dims, summed in shared memory;
 //   O += P V:  each warp a quarter of the value dims, the weights as three bf16 parts (2^-27).
-// What it has to move is what bounds it, Q and O (32 trees of 64 nodes, 16 heads, 576 wide, fp32 results:
-// 105 MB, 16 us): the products are a quarter of what they are on whole tiles.
+// It is a chain of latencies a CTA (offsets, mask, page table, rows, scores, softmax, values) on the five CTAs that an
+// SM's shared memory and registers hold.  32 trees of 64 nodes, 16 heads, 576 wide, fp32 results: 28.5 us, 3.8 TB/s
+// of what has to move, Q and O (105 MB, 16 us); on tiles of all nodes 55.  Four CTAs 31.0; stores of 8 bytes a lane and
+// a barrier more 28.8; operands from global memory straight into registers, values by movmatrix, 38.
 #include "chunk_common.cuh"
 
 namespace sfa {
