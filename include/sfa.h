@@ -757,7 +757,7 @@ int sfa_build_tree_maps(const int32_t *parent, const int32_t *cu_new, const int3
  *         cached_pos for q_pos) and both merged by sfa_combine_attention: a sparse verification step.
  * A tree of more than n_new_max nodes is cut to the first n_new_max, as rows and as keys (SFA_DEV_BAD_QUERY).
  * A row that attends nothing gives O = 0 and lse = -inf.  A value of a node that is not finite makes what
- * attends it not finite, and nothing else: rows of a bf16 cache that share a tile with one are done a
+ * attends it (by a score above minus infinity) not finite, and nothing else: rows of a bf16 cache that share a tile with one are done a
  * second time, their bf16 results then rounded twice.
  * Precision as sfa_chunk_attend_paged, but: the drafted part of bf16 caches, where it is done node by node
  * (trees of up to 256 nodes, a rule on sizes), keeps the weights to 2^-27; q8_0 caches are multiplied as

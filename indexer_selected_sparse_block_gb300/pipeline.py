@@ -393,7 +393,7 @@ class SfaPagedCache:
         """Of the last draft the path that the model agrees with stays: token [n_tok_cap] the nodes' tokens,
         target [n_tok_cap] the model's choice behind each, root_target [n_seq] behind the cached tokens (None:
         the first root is taken).  path, n_acc and next_token say which, how many and what comes next.  Once a
-        draft."""
+        draft (a second time would move rows that have moved); the parents given to draft are read again."""
         if self._parent is None:
             raise ValueError("no drafted tree to commit")
         B.sfa_tree_accept(self._parent, token, target, self.cu_new, self.path, self.n_acc, self.next_token,
@@ -402,7 +402,6 @@ class SfaPagedCache:
                           self.path, self.n_acc, self.len_total, self.page_size, self.page_table,
                           self.free_pages, self._head_out, self.length, self.free_head,
                           dev_status=self.status, stream=stream)
-        self._parent = None
         return self.next_token
 
     def release(self, seq: int, stream=None):

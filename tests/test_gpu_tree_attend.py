@@ -316,6 +316,33 @@ def test_odd_values_stay_in_their_branch(shape, dtype, out):
     c.check_odd(odd)
 
 
+@pytest.mark.parametrize("scale", [b"\x00\x7c", b"\x01\x7e"])     # an infinity, a NaN
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+def test_odd_scales_of_q8_rows_stay_in_their_branch(shape, scale):
+    """A block's scale that is not finite: of the values (apart, its 32 dims; where V is K, whatever attends it, but
+    by a score of minus infinity, whose weight is zero)."""
+    a, n, node, blk = 70, 30, 4, 1
+    c = Trees([(a, n), (5, 9)], 16, shape, "q8", "f32", seed=9)
+    rows, d = (c.V, c.dv) if c.sep else (c.K, c.dkq)
+    rows[c.cells[0][a + node], 0, d + 2 * blk:d + 2 * blk + 2] = torch.tensor(list(scale), dtype=torch.uint8, device=DEV)
+    assert c.call() == 0
+    ref, ref_l, tol, tol_l = c.exact()
+    hit = torch.tensor([v[node] for v in c.seen[0]] + [False] * 9)
+    heads = torch.arange(c.h_q) < c.h_q // c.h_kv           # of KV head 0
+    odd = hit[:, None] & heads[None]
+    O, lse = c.O.double().cpu(), c.lse.double().cpu()
+    dims = torch.zeros(c.dv, dtype=torch.bool)
+    dims[32 * blk:32 * blk + 32] = True
+    if not c.sep:
+        dims[:] = True
+    bad = odd[..., None] & dims
+    assert bool(hit.any())
+    if c.sep or scale == b"\x01\x7e":
+        assert not bool(torch.isfinite(O[bad]).any())
+    check_close(torch.where(bad, ref, O), ref, tol, "O")
+    check_close(lse if c.sep else torch.where(odd, ref_l, lse), ref_l, tol_l, "lse")
+
+
 @pytest.mark.parametrize("shape", [WIDE, N128])
 def test_odd_values_of_the_cached_tokens_stay_out_of_the_drafted_part(shape):
     c = Trees([(130, 10)], 16, shape, "bf16", "f32", odd=[(0, 129, 0, 1, math.nan), (0, 128, 0, 2, math.inf)])

@@ -154,6 +154,34 @@ def test_steps(dkq, dv, h_q, h_kv, sep, rot, pairs, captured):
         check_cache()
 
 
+def test_draft_and_commit_in_graphs_of_their_own():
+    """The model's choices are made between them; replayed, they keep what a cache without graphs keeps."""
+    kw = dict(n_seq=2, n_pages=20, page_size=4, max_pages=8, n_tok_cap=12, h_kv=1, dkq=64, dv=64, n_draft_max=6)
+    a, b = sfa.SfaPagedCache(**kw), sfa.SfaPagedCache(**kw)
+    r = random.Random(5)
+    new, parent, token, target = i32([0, 0]), i32([0] * 12), i32([0] * 12), i32([0] * 12)
+    K = torch.zeros((12, 1, 64), dtype=torch.bfloat16, device=DEV)
+    draft = sfa.SfaStep.graphed(lambda: a.draft(new, parent, K))
+    commit = sfa.SfaStep.graphed(lambda: a.commit(token, target))
+    for _ in range(6):
+        n = [r.randint(0, 6), r.randint(0, 6)]
+        trees = [random_tree(k, r, chain=0.6) for k in n]
+        new.copy_(i32(n))
+        parent.copy_(i32(flat(trees, 12)))
+        token.copy_(torch.randint(0, 2, (12,), device=DEV))
+        target.copy_(torch.randint(0, 2, (12,), device=DEV))
+        K.copy_(torch.randn((12, 1, 64), device=DEV))
+        draft.replay()
+        commit.replay()
+        b.draft(new, parent, K)
+        b.commit(token, target)
+        torch.cuda.synchronize()
+        for x, y in ((a.length, b.length), (a.free_head, b.free_head), (a.free_pages, b.free_pages), (a.path, b.path),
+                     (a.next_token, b.next_token), (a.K, b.K)):
+            assert torch.equal(x, y)
+    assert int(a.length.sum()) > 0 and sfa.sfa_read_device_status(a.status) == 0
+
+
 def test_a_dropped_tree():
     """A draft that is not committed leaves nothing behind: the next step takes its place."""
     kw = dict(n_seq=2, n_pages=12, page_size=4, max_pages=5, n_tok_cap=12, h_kv=1, dkq=64, dv=64, n_draft_max=12)

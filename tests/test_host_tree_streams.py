@@ -73,6 +73,7 @@ def test_a_draft_launches_on_its_own_device(launches, given):
     assert all(dev == 1 and st == (77 if given else 101) for _, dev, st in seen), seen
     # the workspace: of the call's stream, not the current one's
     assert taken == [1 if given else 0]
+    c.step(i32(2), Far(6, 1, 64), stream=stream)           # drops the tree
     with pytest.raises(ValueError):
         c.commit(i32(6), i32(6))
 
