@@ -70,6 +70,14 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// mma_bf16_16816 onto zeros.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // Two values to bf16, and what is left of them.
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x, y);
@@ -79,7 +87,10 @@ __device__ __forceinline__ float scale_at(const uint8_t *row, int d, int block) 
     return __half2float(*reinterpret_cast<const __half *>(row + d + 2 * block));
 }
 
-template <int DKQ, int DV, bool VK>
+// ROUND, fp32 results: sixteen keys' sum is added to acc with rounding.  The tensor cores cut what they add to an
+// accumulator towards zero: 1.1e-9 of a result for a key of a piece's, which bf16 results do not show (3e-5 at 30000
+// keys; it costs 8%).
+template <int DKQ, int DV, bool VK, bool ROUND>
 __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_kernel(const Params p) {
     using L = Q8<DKQ, DV, VK>;
     constexpr int RK = L::kRK, RV = L::kRV, PK = L::kPK, PV = L::kPV, DVS = VK ? DKQ : DV;   // DVS: where a value row's scales are
@@ -323,12 +334,26 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
                     const uint32_t pa = smem_u32(sP + (16 * (MW * mw + x) + (lane & 15)) * kPS + 16 * ks + 8 * (lane >> 4));
                     ldsm_x4(pa, ph[0], ph[1], ph[2], ph[3]);
                     ldsm_x4(pa + kQ8Rows * kPS * 2, pl[0], pl[1], pl[2], pl[3]);
+                    if constexpr (ROUND) {
+                        float d[4][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], pl, hi[i][0], hi[i][1]);
+                        for (int i = 0; i < 4; ++i) mma_bf16_first(d[i], pl, hi[i][0], hi[i][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], ph, lo[i][0], lo[i][1]);
+                        for (int i = 0; i < 4; ++i) mma_bf16_16816(d[i], ph, lo[i][0], lo[i][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], ph, hi[i][0], hi[i][1]);
+                        for (int i = 0; i < 4; ++i) mma_bf16_16816(d[i], ph, hi[i][0], hi[i][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) acc[b][x][i][y] += d[i][y];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], pl, hi[i][0], hi[i][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], ph, lo[i][0], lo[i][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_bf16_16816(acc[b][x][i], ph, hi[i][0], hi[i][1]);
+                    }
                 }
                 if (__any_sync(0xFFFFFFFFu, odd)) {   // such keys one by one, to the rows that attend them
                     for (int k = 0; k < 16; ++k) {
@@ -413,15 +438,19 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
         }
 }
 
-template <int DKQ, int DV, bool VK>
+template <int DKQ, int DV, bool VK, bool ROUND>
 int launch(const Params &p, cudaStream_t st) {
-    if (!ensure_max_dynamic_smem(chunk_q8_tree_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_q8_tree_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+    if (!ensure_max_dynamic_smem(chunk_q8_tree_kernel<DKQ, DV, VK, ROUND>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_q8_tree_kernel<DKQ, DV, VK, ROUND>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
                    (size_t)Q8<DKQ, DV, VK>::kBytes, st, p) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
     return SFA_OK;
+}
+template <int DKQ, int DV, bool VK>
+int launch(const Params &p, cudaStream_t st) {
+    return p.o_bf16 ? launch<DKQ, DV, VK, false>(p, st) : launch<DKQ, DV, VK, true>(p, st);
 }
 
 }  // namespace

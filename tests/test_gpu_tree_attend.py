@@ -410,6 +410,36 @@ def test_another_stream_and_host_results():
     assert torch.equal(O, c.O.cpu())
 
 
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+@pytest.mark.parametrize("dtype", ["q8", "f32", "bf16"])
+def test_long_sums_are_rounded_not_cut(shape, dtype):
+    """Queries of zero: every weight is one, and the results are means of many positive values, to which a sum
+    cut towards zero at every step would be short by its steps.  Off by: the values' two parts, 2^-17 at most
+    each way (q8_0 ones; bf16 and fp32 ones less); sums of what tiles of at least 16 keys give, rounded or,
+    of bf16 caches, cut for 24 tiles of 128 keys at a time: 2.2e-7 a tile; the result's rounding."""
+    n_keys = 30000
+    c = Trees([(n_keys, 4)], 64, shape, dtype, "f32", seed=2)
+    c.Q.zero_()
+    for x, v in ((c.K, c.Kv), (c.V, c.Vv)):
+        if x is None:
+            continue
+        if dtype == "q8":                       # the codes' signs
+            d = v.shape[-1]
+            codes = x[..., :d].contiguous().view(torch.int8)
+            x[..., :d] = codes.abs().view(torch.uint8)
+            v.copy_(q8_values(x, d))
+        else:
+            x.abs_()
+            v.abs_()
+    assert c.call() == 0
+    ref, ref_l, _, _ = c.exact()
+    steps = n_keys / 16
+    off = 2.0 ** -16 + 6 * math.sqrt(steps) * 2.0 ** -24 + 24 * 2.2e-7 + 2.0 ** -22
+    err = (c.O.double().cpu() - ref).abs() / ref
+    assert float(err.max()) <= off, (float(err.max()), off)
+    assert float((c.lse.double().cpu() - ref_l).abs().max()) <= 6 * math.sqrt(n_keys) * 2.0 ** -24
+
+
 def test_results_do_not_change_from_run_to_run():
     for shape, lens in ((WIDE, [(9000, 16), (100, 30)]), (N128, [(9000, 16), (100, 61), (3000, 2)])):
         c = Trees(lens, 16, shape, "bf16", "f32")
