@@ -111,7 +111,7 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4]
     mma_tf32(d, ah, bh);
 }
 
-template <int DKQ, int DV, bool VK, bool TREE>
+template <int DKQ, int DV, bool VK>
 __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(const Params p, int dtype) {
     using L = F32<DKQ, DV, VK>;
     constexpr int TK = L::TK, PK = L::PK, PV = VK ? L::PK : L::PV, BUFS = L::kBufs, PP = L::kPP;
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
     const int rows = min(kRows, (int)((int64_t)n * p.G - r0));
     const int pos0 = it.q.total - it.q.n;                  // position of the chunk's first query
     const int p_last = pos0 + (r0 + rows - 1) / p.G;
-    const int len = list_end(p, it.q, p_last + 1), begin = TREE ? list_begin(p, it.q, len) : 0;
-    int k0, k1;
-    piece_keys(p, blockIdx.x, g, split, begin, len, k0, k1);
-    const bool whole = one_piece(p, blockIdx.x, g, len - begin);   // this piece is the whole list
+    const int len = max(0, min(key_limit(p, it.q), p_last + 1));
+    const int k0 = (int)min((int64_t)len, (int64_t)split * p.split_keys);
+    const int k1 = (int)min((int64_t)len, (int64_t)k0 + p.split_keys);
+    const bool whole = len <= p.split_keys;                // this piece is the whole list
     if (split > 0 && k0 >= k1) return;                     // no such piece
 
     for (int e = tid; e < kRows * (DKQ / 4); e += kThreads) {
@@ -186,8 +186,7 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
             if constexpr (!VK) load_rows<DV, kThreads>(k + TK * PK, p.V, dtype, cells, TK, p.h_kv, g);
         }
     };
-    // the last key that every row attends
-    const int first_pos = !TREE ? pos0 + r0 / p.G : p.tree == kDrafted ? -1 : pos0 - 1;
+    const int first_pos = pos0 + r0 / p.G;   // the rows' first position
     if (ahead && k0 < k1) {
         find_cells(k0, 0);
         __syncthreads();
@@ -255,10 +254,7 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
         {   // softmax of row tid / TPR, KPT keys a thread
             constexpr int TPR = kThreads / kRows, KPT = TK / TPR;
             const int r = tid / TPR, kk = tid % TPR;
-            const int pos = TREE ? k1 : pos0 + (r0 + r) / p.G;
-            uint32_t node = ~0u;   // TREE: bit j: key t0 + j is attended
-            if constexpr (TREE)
-                node = tree_bits(p, r < rows ? p.mask + (int64_t)(it.q.c0 + (r0 + r) / p.G) * p.mask_words : nullptr, pos0, t0);
+            const int pos = pos0 + (r0 + r) / p.G;
             float s[KPT], mx = -INFINITY;
 #pragma unroll
             for (int b = 0; b < KPT; ++b) {
@@ -266,7 +262,7 @@ __global__ void __launch_bounds__(F32<DKQ, DV, VK>::kThreads) chunk_f32_kernel(c
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) v += sRed[(w * kRows + r) * TK + k];
-                const bool on = sCell[k] >= 0 && t0 + k <= pos && (!TREE || ((node >> k) & 1));
+                const bool on = sCell[k] >= 0 && t0 + k <= pos;
                 if (on && v - v != 0.f) {   // halves of an infinity cancel to NaN: the plain product instead
                     v = 0.f;
                     for (int d = 0; d < DKQ; ++d) v += sQ[r * PK + d] * sK[k * PK + d];
@@ -570,7 +566,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p) {
 }
 
 // --------------------------------------------------------------------------------- the plan
-enum Kernel { kF32, kWide, kNarrow, kNodes, kQ8Tree };
+enum Kernel { kF32, kWide, kNarrow, kNodes, kQ8Tree, kF32Tree };
 struct Plan {
     Kernel kernel;
     int item_rows, item_q, items, part_rows;
@@ -647,9 +643,10 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
                int64_t n_cells, bool o_bf16, int tree) {
     Plan pl;
     const bool tc = dtype == SFA_BF16 && n_cells > 0, wide = tc && dv == 512;
-    const bool q8_tree = dtype == SFA_Q8_0 && tree;
-    pl.kernel = wide ? kWide : tc ? kNarrow : q8_tree ? kQ8Tree : kF32;
-    pl.item_rows = wide ? 128 : tc ? 256 : q8_tree ? kQ8Rows : kRows;
+    // (a tree of a bf16 cache of no cell attends nothing, like a chunk of it)
+    const bool q8_tree = dtype == SFA_Q8_0 && tree, f32_tree = dtype == SFA_F32 && tree;
+    pl.kernel = wide ? kWide : tc ? kNarrow : q8_tree ? kQ8Tree : f32_tree ? kF32Tree : kF32;
+    pl.item_rows = wide ? 128 : tc ? 256 : q8_tree ? kQ8Rows : f32_tree ? kF32Rows : kRows;
     pl.item_q = wide ? 2 * wide_qpc(G) : tc ? 2 * narrow_qpt(G) : 0;
     const int64_t items = items_bound(n_seq, n_q, G, n_new_max, pl.item_rows, pl.item_q);
     pl.items = (int)(items > 0x3FFFFFFF ? 0x3FFFFFFF : items);
@@ -669,6 +666,7 @@ Plan make_plan(int dtype, int n_seq, int n_q, int G, int h_kv, int dv, int n_new
     double t_tile = wide ? (o_bf16 ? 1.35 : 2.) : tc ? (o_bf16 ? 1.8 : 2.4) : dv == 512 ? 30. : 8.;
     if (tree == kTree && pl.kernel == kNarrow && pl.part_rows <= 128) t_tile *= 0.7;   // one row tile
     if (q8_tree) t_tile = dv == 512 ? 17. : dv == 128 ? 5. : 3.;
+    if (f32_tree) t_tile = dv == 512 ? 24. : dv == 128 ? 6. : 4.;
     const double t_piece = 7., t_next = 4., t_merge = 6.;
     const double part_us = (double)pl.part_rows * dv * 4 * 2 / 4e6;   // a partial, both ways
     int64_t best = 1;
@@ -726,20 +724,15 @@ bool shape_ok(int dkq, int dv, bool has_v) {
            (dkq == 128 && dv == 128) || (dkq == 64 && dv == 64);
 }
 
-template <int DKQ, int DV, bool VK, bool TREE>
-int launch_f32_any(const Params &p, int dtype, cudaStream_t st) {
-    if (!ensure_max_dynamic_smem(chunk_f32_kernel<DKQ, DV, VK, TREE>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK, TREE>, dim3(p.items, p.h_kv, p.n_split), dim3(F32<DKQ, DV, VK>::kThreads),
+template <int DKQ, int DV, bool VK>
+int launch_f32(const Params &p, int dtype, cudaStream_t st) {
+    if (!ensure_max_dynamic_smem(chunk_f32_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
+    if (launch_pdl(chunk_f32_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(F32<DKQ, DV, VK>::kThreads),
                    F32<DKQ, DV, VK>::bytes(), st, p, dtype) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
     }
     return SFA_OK;
-}
-
-template <int DKQ, int DV, bool VK>
-int launch_f32(const Params &p, int dtype, cudaStream_t st) {
-    return p.tree ? launch_f32_any<DKQ, DV, VK, true>(p, dtype, st) : launch_f32_any<DKQ, DV, VK, false>(p, dtype, st);
 }
 
 template <int DV>
@@ -856,6 +849,7 @@ int attend(const void *Q, const void *K, const void *V, int dtype, int64_t n_cel
     if (pl.kernel == kWide) r = tree ? launch_wide_tree(p, dkq, n_cells, st) : launch_wide(p, dkq, n_cells, st);
     else if (pl.kernel == kNodes) r = launch_nodes(p, dkq, st);
     else if (pl.kernel == kQ8Tree) r = launch_q8_tree(p, dkq, st);
+    else if (pl.kernel == kF32Tree) r = launch_f32_tree(p, dkq, st);
     else if (pl.kernel == kNarrow) r = tree ? launch_narrow_tree(p, dkq, n_cells, st) : launch_narrow(p, dkq, n_cells, st);
     else if (dkq == 576) r = launch_f32<576, 512, true>(p, dtype, st);
     else if (dkq == 512) r = V ? launch_f32<512, 512, false>(p, dtype, st) : launch_f32<512, 512, true>(p, dtype, st);

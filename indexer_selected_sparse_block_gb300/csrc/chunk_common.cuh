@@ -570,9 +570,10 @@ int launch_wide_tree(const Params &p, int dkq, int64_t n_cells, cudaStream_t st)
 inline int narrow_qpt(int G) { return 128 / G; }
 int launch_narrow(const Params &p, int d, int64_t n_cells, cudaStream_t st);
 int launch_narrow_tree(const Params &p, int d, int64_t n_cells, cudaStream_t st);
-// Trees over q8_0 caches (chunk_q8_tree.cu): tiles of kQ8Rows flattened rows.
-constexpr int kQ8Rows = 64;
+// Trees over q8_0 and fp32 caches (chunk_q8_tree.cu, chunk_f32_tree.cu): tiles of so many flattened rows.
+constexpr int kQ8Rows = 64, kF32Rows = 64;
 int launch_q8_tree(const Params &p, int dkq, cudaStream_t st);
+int launch_f32_tree(const Params &p, int dkq, cudaStream_t st);
 // The drafted part alone, a node at a time (chunk_nodes.cu): of trees of at most kNodesMax nodes.
 constexpr int kNodesMax = 256;
 int launch_nodes(const Params &p, int dkq, cudaStream_t st);
