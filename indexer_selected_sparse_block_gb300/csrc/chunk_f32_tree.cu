@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
             const uint32_t ka = smem_u32(sK + (NT == 1 ? (key0 + (lane & 7)) * PQ + 8 * (lane >> 3)
                                                        : (key0 + (lane & 7) + 8 * (lane >> 4)) * PQ + 8 * ((lane >> 3) & 1)));
 #pragma unroll 2
-            for (int i = 0; i < DKQ / 16; i += C) {
+            for (int i = 0; i < (16 * rg < rows ? DKQ / 16 : 0); i += C) {
                 uint32_t Bh[4], Bl[4];
                 ldsm_x4(ka + 32 * i, Bh[0], Bh[1], Bh[2], Bh[3]);
                 ldsm_x4(ka + TK * PQ * 2 + 32 * i, Bl[0], Bl[1], Bl[2], Bl[3]);
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < MW; ++x) {
+            if (16 * (MW * mw + x) >= rows) break;   // row tiles without rows
             const float al0 = sAlpha[16 * (MW * mw + x) + fr], al1 = sAlpha[16 * (MW * mw + x) + fr + 8];
             if (__any_sync(0xFFFFFFFFu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
                 }
 #pragma unroll
                 for (int x = 0; x < MW; ++x) {
+                    if (16 * (MW * mw + x) >= rows) break;
                     uint32_t ph[4], pl[4];
                     const uint32_t pa = smem_u32(sP + (16 * (MW * mw + x) + (lane & 15)) * PS + 16 * ks + 8 * (lane >> 4));
                     ldsm_x4(pa, ph[0], ph[1], ph[2], ph[3]);

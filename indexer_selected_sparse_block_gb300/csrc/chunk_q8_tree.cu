@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
             const __half *qa = sQ + (16 * rg + fr) * L::kPQ + 8 * fc;
             const uint8_t *kc = rK + (16 * kh + fr) * PK + 8 * fc, *ks = rK + (16 * kh + 2 * fc) * PK + DKQ;
 #pragma unroll 1
-            for (int b0 = 0; b0 < DKQ / 32; b0 += 2) {
+            for (int b0 = 0; b0 < (16 * rg < rows ? DKQ / 32 : 0); b0 += 2) {
                 float2 c[2][2];   // scales of both blocks, of keys 8 nt + 2 fc and the next
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < MW; ++x) {
+            if (16 * (MW * mw + x) >= rows) break;   // row tiles without rows
             const float al0 = sAlpha[16 * (MW * mw + x) + fr], al1 = sAlpha[16 * (MW * mw + x) + fr + 8];
             if (__any_sync(0xFFFFFFFFu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
                 }
 #pragma unroll
                 for (int x = 0; x < MW; ++x) {
+                    if (16 * (MW * mw + x) >= rows) break;
                     uint32_t ph[4], pl[4];
                     const uint32_t pa = smem_u32(sP + (16 * (MW * mw + x) + (lane & 15)) * kPS + 16 * ks + 8 * (lane >> 4));
                     ldsm_x4(pa, ph[0], ph[1], ph[2], ph[3]);
