@@ -34,7 +34,9 @@ struct F32T {
     static constexpr int kOffAlpha = kOffMax + 2 * kF32Rows * 4;
     static constexpr int kOffSv = kOffAlpha + kF32Rows * 4;           // int [kTK]
     static constexpr int kOffOdd = kOffSv + kTK * 4;                  // int [64] of queries, [kTK]: 1 key, 2 value
-    static constexpr int kBytes = kOffOdd + (kF32Rows + kTK) * 4;
+    static constexpr int kOffSwap = (kOffOdd + (kF32Rows + kTK) * 4 + 15) / 16 * 16;   // float4 [8][32]: scores of halves
+    static constexpr int kBytes = kOffSwap + (kNT == 1 ? 8 * 32 * 16 : 0);
+    static_assert(kNT == 1 || kNT == 2, "two warps' score tiles: 16 or 32 keys");
     static constexpr int kBlocks = DV / 32, kBW = kBlocks >= 8 ? kBlocks / 8 : 1, kMW = kBlocks >= 8 ? 4 : kBlocks / 2;
     static_assert(kOffCell % 8 == 0, "aligned");
 };
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
     float *sMax = reinterpret_cast<float *>(smem + L::kOffMax), *sAlpha = reinterpret_cast<float *>(smem + L::kOffAlpha);
     int *sSv = reinterpret_cast<int *>(smem + L::kOffSv), *sOddQ = reinterpret_cast<int *>(smem + L::kOffOdd),
         *sOdd = sOddQ + kF32Rows;
+    float4 *sSwap = reinterpret_cast<float4 *>(smem + L::kOffSwap);
     __shared__ Item s_item;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, fr = lane >> 2, fc = lane & 3;
     const int split = blockIdx.z, g = blockIdx.y;
@@ -213,42 +216,49 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
         __syncthreads();
         float s[NT][4];   // keys key0 + 8 nt + 2 fc, + 1 of both rows
         {
-            // a sum for each product, and, with one tile of keys, for every other step: chains of their own
-            constexpr int C = NT == 1 ? 2 : 1;
-            float d[C][NT][3][4] = {};
-            const uint32_t qa = smem_u32(sQ + (16 * rg + (lane & 15)) * PQ + 8 * (lane >> 4));
-            const uint32_t ka = smem_u32(sK + (NT == 1 ? (key0 + (lane & 7)) * PQ + 8 * (lane >> 3)
-                                                       : (key0 + (lane & 7) + 8 * (lane >> 4)) * PQ + 8 * ((lane >> 3) & 1)));
+            constexpr int W = 2 / NT;   // warps a sum: halves of the dims, of both tiles of keys, or one warp
+            constexpr int kSteps = DKQ / 16 / W;
+            float d[2][3][4] = {};   // a sum for each product: chains of their own
+            const int first = W == 2 ? kh * kSteps : 0, k8 = W == 2 ? 0 : key0;
+            const uint32_t qa = smem_u32(sQ + (16 * rg + (lane & 15)) * PQ + 8 * (lane >> 4) + 16 * first);
+            const uint32_t ka = smem_u32(sK + (k8 + (lane & 7) + 8 * (lane >> 4)) * PQ + 8 * ((lane >> 3) & 1) + 16 * first);
 #pragma unroll 2
-            for (int i = 0; i < (16 * rg < rows ? DKQ / 16 : 0); i += C) {
-                uint32_t Bh[4], Bl[4];
+            for (int i = 0; i < (16 * rg < rows ? kSteps : 0); ++i) {
+                uint32_t Ah[4], Al[4], Bh[4], Bl[4];
                 ldsm_x4(ka + 32 * i, Bh[0], Bh[1], Bh[2], Bh[3]);
+                ldsm_x4(qa + kF32Rows * PQ * 2 + 32 * i, Al[0], Al[1], Al[2], Al[3]);
+                ldsm_x4(qa + 32 * i, Ah[0], Ah[1], Ah[2], Ah[3]);
                 ldsm_x4(ka + TK * PQ * 2 + 32 * i, Bl[0], Bl[1], Bl[2], Bl[3]);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    uint32_t Ah[4], Al[4];
-                    ldsm_x4(qa + 32 * (i + c), Ah[0], Ah[1], Ah[2], Ah[3]);
-                    ldsm_x4(qa + kF32Rows * PQ * 2 + 32 * (i + c), Al[0], Al[1], Al[2], Al[3]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int x = 2 * (c + nt);
-                        mma_f16_16816(d[c][nt][0], Al, Bh[x], Bh[x + 1]);
-                        mma_f16_16816(d[c][nt][1], Ah, Bl[x], Bl[x + 1]);
-                        mma_f16_16816(d[c][nt][2], Ah, Bh[x], Bh[x + 1]);
-                    }
+                for (int nt = 0; nt < 2; ++nt) {
+                    mma_f16_16816(d[nt][0], Al, Bh[2 * nt], Bh[2 * nt + 1]);
+                    mma_f16_16816(d[nt][2], Ah, Bh[2 * nt], Bh[2 * nt + 1]);
+                    mma_f16_16816(d[nt][1], Ah, Bl[2 * nt], Bl[2 * nt + 1]);
                 }
             }
+            float sum[2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float v = d[0][nt][2][x], w = d[0][nt][0][x] + d[0][nt][1][x];
-                    if constexpr (C == 2) {
-                        v += d[1][nt][2][x];
-                        w += d[1][nt][0][x] + d[1][nt][1][x];
-                    }
-                    s[nt][x] = v + w;
-                }
+                for (int x = 0; x < 4; ++x) sum[nt][x] = d[nt][2][x] + (d[nt][0][x] + d[nt][1][x]);
+            if constexpr (W == 2) {   // a warp keeps the tile kh and gives the other
+                float4 *swap = sSwap + (rg * 2 + kh) * 32 + lane;
+                *swap = kh ? make_float4(sum[0][0], sum[0][1], sum[0][2], sum[0][3])
+                           : make_float4(sum[1][0], sum[1][1], sum[1][2], sum[1][3]);
+                named_barrier(1 + rg, 64);
+                const float4 o = sSwap[(rg * 2 + (kh ^ 1)) * 32 + lane];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[0][x] = kh ? sum[1][x] : sum[0][x];
+                s[0][0] += o.x;
+                s[0][1] += o.y;
+                s[0][2] += o.z;
+                s[0][3] += o.w;
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[nt][x] = sum[nt][x];
+            }
         }
         float mx[2];
 #pragma unroll
@@ -304,6 +314,8 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
                     e[c] = x == -INFINITY ? 0.f : exp2f(x - mn);
                     sum += e[c];
                     e[c] *= pow2(S - sSv[key + c] + kTop);
+                    // a value that is not finite counts by any weight (its finite ones are off by 2^-34 at most)
+                    if ((odd_v >> (key + c)) & 1 && x != -INFINITY) e[c] = fmaxf(e[c], 0x1p-24f);
                 }
                 __half2 hi, lo;
                 split_f16(e[0], e[1], hi, lo);

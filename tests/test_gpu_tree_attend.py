@@ -316,6 +316,24 @@ def test_odd_values_stay_in_their_branch(shape, dtype, out):
     c.check_odd(odd)
 
 
+@pytest.mark.parametrize("gap", [50.0, 200.0])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("shape", [W512, N128, N64])
+def test_odd_values_of_small_weights(shape, dtype, out, gap):
+    """A value that is not finite shows in what attends it by however small a weight (scores `gap` below others)."""
+    lens = [(150, 40), (0, 33), (64, 64)]
+    odd = [(0, 155, 0, 3, math.nan), (1, 7, 0, 0, math.inf), (2, 64, 0, 40, -math.inf)]
+    c = Trees(lens, 16, shape, dtype, out, seed=6, odd=odd)
+    c.Q[..., 0] = 16.0
+    for s, pos, i, _, _ in odd:
+        for x in (c.K, c.Kv):
+            x[c.cells[s][pos], i, 0] = -gap / (16.0 * c.scale)
+    assert c.call() == 0
+    c.check_odd(odd)
+    assert c.call(DRAFTED) == 0
+    c.check_odd(odd)
+
+
 @pytest.mark.parametrize("scale", [b"\x00\x7c", b"\x01\x7e"])     # an infinity, a NaN
 @pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
 def test_odd_scales_of_q8_rows_stay_in_their_branch(shape, scale):
