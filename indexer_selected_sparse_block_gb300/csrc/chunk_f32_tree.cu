@@ -18,26 +18,29 @@ namespace sfa {
 namespace chunk {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kTop = 10;   // the exponent of a scaled row's largest value
 
 template <int DKQ, int DV, bool VK>
 struct F32T {
-    static constexpr int kTK = DV == 512 ? 16 : 32, kNT = kTK / 16;   // keys of a tile; a warp's score tiles of 8 keys
+    static constexpr int kWarps = DV == 512 ? 16 : 8;
+    static constexpr int kTK = DV == 512 ? 16 : 32;                   // keys of a tile
+    static constexpr int kWG = kWarps / 4;                            // warps of 16 rows' scores: a tile of 16 keys
+    static constexpr int kParts = kWG / (kTK / 16);                   // by so many parts of the dims each
+    static constexpr int kLR = kTK == 16 ? 8 : 4;                     // softmax: lanes of a row
     static constexpr int kPQ = DKQ + 8, kPV = DV + 8, kPS = kTK + 8;  // pitches: ldmatrix without bank conflicts
     static constexpr int kOffK = 2 * kF32Rows * kPQ * 2;              // hi, lo of the queries before
     static constexpr int kOffV = kOffK + 2 * kTK * kPQ * 2;
     static constexpr int kOffP = kOffV + (VK ? 0 : 2 * kTK * kPV * 2);
-    static constexpr int kOffCell = kOffP + 2 * kF32Rows * kPS * 2;   // int64 [kTK]
-    static constexpr int kOffUnit = kOffCell + kTK * 8;               // int: rows' and keys' powers of two
-    static constexpr int kOffMax = kOffUnit + (kF32Rows + kTK) * 4;   // float [2][64]
-    static constexpr int kOffAlpha = kOffMax + 2 * kF32Rows * 4;
+    static constexpr int kOffS = kOffP + 2 * kF32Rows * kPS * 2;      // float [kParts][64][kPS]
+    static constexpr int kOffCell = kOffS + kParts * kF32Rows * kPS * 4;   // int64 [2][kTK]: this tile's and the next one's
+    static constexpr int kOffUnit = kOffCell + 2 * kTK * 8;               // int: rows' and keys' powers of two
+    static constexpr int kOffAlpha = kOffUnit + (kF32Rows + kTK) * 4;
     static constexpr int kOffSv = kOffAlpha + kF32Rows * 4;           // int [kTK]
     static constexpr int kOffOdd = kOffSv + kTK * 4;                  // int [64] of queries, [kTK]: 1 key, 2 value
-    static constexpr int kOffSwap = (kOffOdd + (kF32Rows + kTK) * 4 + 15) / 16 * 16;   // float4 [8][32]: scores of halves
-    static constexpr int kBytes = kOffSwap + (kNT == 1 ? 8 * 32 * 16 : 0);
-    static_assert(kNT == 1 || kNT == 2, "two warps' score tiles: 16 or 32 keys");
-    static constexpr int kBlocks = DV / 32, kBW = kBlocks >= 8 ? kBlocks / 8 : 1, kMW = kBlocks >= 8 ? 4 : kBlocks / 2;
+    static constexpr int kBytes = kOffOdd + (kF32Rows + kTK) * 4;
+    static constexpr int kBlocks = DV / 32;                           // values: blocks of 32 dims and row tiles of a warp
+    static constexpr int kBW = kBlocks >= kWarps ? kBlocks / kWarps : 1, kMW = kBlocks >= kWarps ? 4 : 4 * kBlocks / kWarps;
+    static_assert(kLR == 2 * kWG && kBytes + 64 <= 227 * 1024, "rows of a warp's softmax; shared memory");
     static_assert(kOffCell % 8 == 0, "aligned");
 };
 
@@ -63,24 +66,24 @@ __device__ __forceinline__ void split_f16(float x, float y, __half2 &hi, __half2
 template <int N>
 __device__ __forceinline__ int put_row(float2 (&v)[N], __half *to, int apart, bool &odd) {
     const int lane = threadIdx.x & 31;
-    float top = 0.f;
-    bool bad = false;
+    auto largest = [&]() {   // its bits
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (!finite(v[i].x)) {
-            v[i].x = 0.f;
-            bad = true;
+        for (int i = 0; i < N; ++i)
+            top = max(top, max(__float_as_uint(v[i].x) & 0x7FFFFFFFu, __float_as_uint(v[i].y) & 0x7FFFFFFFu));
+        return __reduce_max_sync(0xFFFFFFFFu, top);
+    };
+    uint32_t top = largest();
+    odd = top >= 0x7F800000u;
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!finite(v[i].x)) v[i].x = 0.f;
+            if (!finite(v[i].y)) v[i].y = 0.f;
         }
-        if (!finite(v[i].y)) {
-            v[i].y = 0.f;
-            bad = true;
-        }
-        top = fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+        top = largest();
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    odd = __any_sync(0xFFFFFFFFu, bad);
-    const int e = min(126, kTop - ((int)(__float_as_uint(top) >> 23) - 127));   // a row of zeros: 126
+    const int e = min(126, kTop - ((int)(top >> 23) - 127));   // a row of zeros: 126
     const float f = pow2(e);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -93,19 +96,18 @@ __device__ __forceinline__ int put_row(float2 (&v)[N], __half *to, int apart, bo
 }
 
 template <int DKQ, int DV, bool VK>
-__global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 : 2) chunk_f32_tree_kernel(const Params p) {
     using L = F32T<DKQ, DV, VK>;
-    constexpr int TK = L::kTK, NT = L::kNT, PQ = L::kPQ, PV = VK ? L::kPQ : L::kPV, PS = L::kPS, BW = L::kBW, MW = L::kMW;
-    constexpr int NQ = DKQ / 64, NV = DV / 64, RW = TK / 8;   // a lane's pairs of a row; a warp's rows of a tile
+    constexpr int TK = L::kTK, WG = L::kWG, LR = L::kLR, PQ = L::kPQ, PV = VK ? L::kPQ : L::kPV, PS = L::kPS, BW = L::kBW, MW = L::kMW;
+    constexpr int NQ = DKQ / 64, NV = DV / 64, RW = TK / L::kWarps;   // a lane's pairs of a row; a warp's rows of a tile
     extern __shared__ __align__(16) uint8_t smem[];
     __half *sQ = reinterpret_cast<__half *>(smem), *sK = reinterpret_cast<__half *>(smem + L::kOffK);
     __half *sV = VK ? sK : reinterpret_cast<__half *>(smem + L::kOffV), *sP = reinterpret_cast<__half *>(smem + L::kOffP);
-    int64_t *sCell = reinterpret_cast<int64_t *>(smem + L::kOffCell);
+    int64_t *sCells = reinterpret_cast<int64_t *>(smem + L::kOffCell);
     int *sEq = reinterpret_cast<int *>(smem + L::kOffUnit), *sEk = sEq + kF32Rows;
-    float *sMax = reinterpret_cast<float *>(smem + L::kOffMax), *sAlpha = reinterpret_cast<float *>(smem + L::kOffAlpha);
+    float *sS = reinterpret_cast<float *>(smem + L::kOffS), *sAlpha = reinterpret_cast<float *>(smem + L::kOffAlpha);
     int *sSv = reinterpret_cast<int *>(smem + L::kOffSv), *sOddQ = reinterpret_cast<int *>(smem + L::kOffOdd),
         *sOdd = sOddQ + kF32Rows;
-    float4 *sSwap = reinterpret_cast<float4 *>(smem + L::kOffSwap);
     __shared__ Item s_item;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, fr = lane >> 2, fc = lane & 3;
     const int split = blockIdx.z, g = blockIdx.y;
@@ -135,23 +137,30 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
 
     // a warp's rows of the tile of keys t0 .., on their way
     float2 kreg[RW][NQ], vreg[VK ? 1 : RW][NV];
-    int64_t cells[RW];
-    auto fetch = [&](int t0) {
+    int entry = 0;   // the page of one of them, looked up a tile ahead
+    auto look_up = [&](int t0) {
         const int t = t0 + warp * RW + lane % RW;
-        const int64_t mine = t < k1 ? cell_of(p, it.seq, t) : -1;
+        if (t < k1) entry = __ldg(p.table + (int64_t)it.seq * p.table_stride + p.page_div.div(t));
+    };
+    auto fetch = [&](int t0, int64_t *cells) {
+        const int t = t0 + warp * RW + lane % RW;
+        const bool page = entry >= 0 && entry < p.n_pages;
+        if (t < k1 && !page) set_status(p.status, SFA_DEV_BAD_CELL);
+        const int64_t mine = t < k1 && page ? (int64_t)entry * p.page + (t - p.page_div.div(t) * p.page) : -1;
+        if (lane < RW) cells[warp * RW + lane] = mine;
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            cells[i] = __shfl_sync(0xFFFFFFFFu, mine, i);
-            const int64_t row = cells[i] * p.h_kv + g;
+            const int64_t cell = RW == 1 ? mine : __shfl_sync(0xFFFFFFFFu, mine, i);
+            const int64_t row = cell * p.h_kv + g;
 #pragma unroll
             for (int x = 0; x < NQ; ++x)
-                kreg[i][x] = cells[i] >= 0 ? __ldg(reinterpret_cast<const float2 *>(Kg + row * DKQ + 64 * x + 2 * lane))
-                                           : make_float2(0.f, 0.f);
+                kreg[i][x] = cell >= 0 ? __ldg(reinterpret_cast<const float2 *>(Kg + row * DKQ + 64 * x + 2 * lane))
+                                       : make_float2(0.f, 0.f);
             if constexpr (!VK) {
 #pragma unroll
                 for (int x = 0; x < NV; ++x)
-                    vreg[i][x] = cells[i] >= 0 ? __ldg(reinterpret_cast<const float2 *>(Vg + row * DV + 64 * x + 2 * lane))
-                                               : make_float2(0.f, 0.f);
+                    vreg[i][x] = cell >= 0 ? __ldg(reinterpret_cast<const float2 *>(Vg + row * DV + 64 * x + 2 * lane))
+                                           : make_float2(0.f, 0.f);
             }
         }
     };
@@ -165,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
             odd_v = odd_k;   // V = K: perhaps of dims behind the values only
             if constexpr (!VK) sv = put_row<NV>(vreg[i], sV + key * PV, TK * PV, odd_v);
             if (lane == 0) {
-                sCell[key] = cells[i];
                 sEk[key] = e;
                 sSv[key] = sv;
                 sOdd[key] = (odd_k ? 1 : 0) | (odd_v ? 2 : 0);
@@ -173,9 +181,13 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
         }
     };
     const int n_tiles = (k1 - k0 + TK - 1) / TK;
-    if (n_tiles > 0) fetch(k0);
-    for (int i = 0; i < kF32Rows / 8; ++i) {   // queries: a warp has eight rows
-        const int row = warp * (kF32Rows / 8) + i;
+    if (n_tiles > 0) {
+        look_up(k0);
+        fetch(k0, sCells);
+        look_up(k0 + TK);
+    }
+#pragma unroll 1
+    for (int row = warp; row < kF32Rows; row += L::kWarps) {   // queries
         float2 v[NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
@@ -187,16 +199,13 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
             sOddQ[row] = odd;
         }
     }
-    const int rg = warp >> 1, kh = warp & 1, key0 = 8 * NT * kh;   // scores: rows 16 rg .., keys key0 ..
-    const uint32_t *mask[2];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // rows 16 rg + fr and 8 more, base 2; l of this lane's keys
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        const int row = 16 * rg + fr + 8 * y;
-        mask[y] = row < rows ? p.mask + (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.mask_words : nullptr;
-    }
+    const int rg = warp / WG, wg = warp % WG;   // scores: rows 16 rg ..; keys k8 .., dims from 16 first on
+    const int k8 = 16 * (wg / L::kParts), part = wg % L::kParts, first = part * (DKQ / 16 / L::kParts);
+    const int row = 16 * rg + wg * (32 / LR) + lane / LR, x0 = 2 * (lane % LR);   // softmax: keys x0 + 2 LR i, + 1
+    const uint32_t *mask = row < rows ? p.mask + (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.mask_words : nullptr;
+    float m = -INFINITY, l = 0.f;   // of that row, base 2; l of this lane's keys
     // values: blocks BW bw .. of row tiles MW mw ..
-    const int bw = L::kBlocks >= 8 ? warp : warp % L::kBlocks, mw = L::kBlocks >= 8 ? 0 : warp / L::kBlocks;
+    const int bw = warp % (L::kBlocks / BW), mw = warp / (L::kBlocks / BW);
     float acc[BW][MW][4][4];
 #pragma unroll
     for (int b = 0; b < BW; ++b)
@@ -212,18 +221,25 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
         const int t0 = k0 + t * TK;
         __syncthreads();   // the tile before is done with
         put();
-        if (t + 1 < n_tiles) fetch(t0 + TK);
+        if (t + 1 < n_tiles) {
+            fetch(t0 + TK, sCells + ((t + 1) & 1) * TK);
+            look_up(t0 + 2 * TK);
+        }
         __syncthreads();
-        float s[NT][4];   // keys key0 + 8 nt + 2 fc, + 1 of both rows
-        {
-            constexpr int W = 2 / NT;   // warps a sum: halves of the dims, of both tiles of keys, or one warp
-            constexpr int kSteps = DKQ / 16 / W;
-            float d[2][3][4] = {};   // a sum for each product: chains of their own
-            const int first = W == 2 ? kh * kSteps : 0, k8 = W == 2 ? 0 : key0;
+        // the tile's smallest power of two, and its keys that are and that have odd values
+        const int64_t *sCell = sCells + (t & 1) * TK;
+        const unsigned live = __ballot_sync(0xFFFFFFFFu, sCell[lane % TK] >= 0);
+        const int o = sOdd[lane % TK];
+        const unsigned odd_k = __ballot_sync(0xFFFFFFFFu, o & 1), odd_v = __ballot_sync(0xFFFFFFFFu, lane < TK && (o & 2));
+        const int S1 = min(S, __reduce_min_sync(0xFFFFFFFFu, sSv[lane % TK]));
+        const float down = t == 0 ? 1.f : pow2(S1 - S);
+        S = S1;
+        if (16 * rg < rows) {
+            float d[2][2][4] = {};   // the small products' sum and the large one's
             const uint32_t qa = smem_u32(sQ + (16 * rg + (lane & 15)) * PQ + 8 * (lane >> 4) + 16 * first);
             const uint32_t ka = smem_u32(sK + (k8 + (lane & 7) + 8 * (lane >> 4)) * PQ + 8 * ((lane >> 3) & 1) + 16 * first);
-#pragma unroll 2
-            for (int i = 0; i < (16 * rg < rows ? kSteps : 0); ++i) {
+#pragma unroll(L::kParts == 1 ? 2 : 1)
+            for (int i = 0; i < DKQ / 16 / L::kParts; ++i) {
                 uint32_t Ah[4], Al[4], Bh[4], Bl[4];
                 ldsm_x4(ka + 32 * i, Bh[0], Bh[1], Bh[2], Bh[3]);
                 ldsm_x4(qa + kF32Rows * PQ * 2 + 32 * i, Al[0], Al[1], Al[2], Al[3]);
@@ -232,85 +248,64 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     mma_f16_16816(d[nt][0], Al, Bh[2 * nt], Bh[2 * nt + 1]);
-                    mma_f16_16816(d[nt][2], Ah, Bh[2 * nt], Bh[2 * nt + 1]);
-                    mma_f16_16816(d[nt][1], Ah, Bl[2 * nt], Bl[2 * nt + 1]);
+                    mma_f16_16816(d[nt][1], Ah, Bh[2 * nt], Bh[2 * nt + 1]);
+                    mma_f16_16816(d[nt][0], Ah, Bl[2 * nt], Bl[2 * nt + 1]);
                 }
             }
-            float sum[2][4];
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sum[nt][x] = d[nt][2][x] + (d[nt][0][x] + d[nt][1][x]);
-            if constexpr (W == 2) {   // a warp keeps the tile kh and gives the other
-                float4 *swap = sSwap + (rg * 2 + kh) * 32 + lane;
-                *swap = kh ? make_float4(sum[0][0], sum[0][1], sum[0][2], sum[0][3])
-                           : make_float4(sum[1][0], sum[1][1], sum[1][2], sum[1][3]);
-                named_barrier(1 + rg, 64);
-                const float4 o = sSwap[(rg * 2 + (kh ^ 1)) * 32 + lane];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[0][x] = kh ? sum[1][x] : sum[0][x];
-                s[0][0] += o.x;
-                s[0][1] += o.y;
-                s[0][2] += o.z;
-                s[0][3] += o.w;
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) s[nt][x] = sum[nt][x];
-            }
+                for (int y = 0; y < 2; ++y) {
+                    const int x = 2 * y;
+                    *reinterpret_cast<float2 *>(sS + (part * kF32Rows + 16 * rg + fr + 8 * y) * PS + k8 + 8 * nt + 2 * fc) =
+                        make_float2(d[nt][1][x] + d[nt][0][x], d[nt][1][x + 1] + d[nt][0][x + 1]);
+                }
         }
-        float mx[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int row = 16 * rg + fr + 8 * y;
-            const uint32_t node = tree_bits(p, mask[y], cached, t0);
+        named_barrier(1 + rg, 32 * WG);   // the warps of these rows
+        if (16 * rg < rows) {
+            constexpr int KL = TK / LR;   // keys of a lane
+            const uint32_t node = live & tree_bits(p, mask, cached, t0);
             const int eq = sEq[row];
             const bool odd_q = sOddQ[row] != 0;
-            mx[y] = -INFINITY;
+            float s[KL], mx = -INFINITY;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < KL; i += 2) {
+                float2 v = *reinterpret_cast<const float2 *>(sS + row * PS + x0 + LR * i);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int key = key0 + 8 * nt + 2 * fc + c;
-                    float &x = s[nt][2 * y + c];
-                    const bool on = sCell[key] >= 0 && ((node >> key) & 1);
-                    const int e = -eq - sEk[key];   // in two steps: either may be out of range
-                    x = x * pow2(e >> 1) * pow2(e - (e >> 1));
-                    if (on && (odd_q || (sOdd[key] & 1)) && row < rows) {   // the plain product
-                        const float *q = Qg + row_of(row) * DKQ, *k = Kg + (sCell[key] * p.h_kv + g) * DKQ;
-                        x = 0.f;
-                        for (int i = 0; i < DKQ; ++i) x = fmaf(q[i], k[i], x);
-                    }
-                    x = on ? x * p.scale_log2 : -INFINITY;
-                    mx[y] = fmaxf(mx[y], x);
+                for (int j = 1; j < L::kParts; ++j) {
+                    const float2 w = *reinterpret_cast<const float2 *>(sS + (j * kF32Rows + row) * PS + x0 + LR * i);
+                    v.x += w.x;
+                    v.y += w.y;
                 }
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xFFFFFFFFu, mx[y], 1));
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xFFFFFFFFu, mx[y], 2));
-            if (fc == 0) sMax[kh * kF32Rows + row] = mx[y];
-        }
-        // the tile's smallest power of two, and whether it has odd values: the same in every warp
-        int low = sSv[lane % TK];
+                s[i] = v.x;
+                s[i + 1] = v.y;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
-        const unsigned odd_v = __ballot_sync(0xFFFFFFFFu, lane < TK && (sOdd[lane % TK] & 2));
-        const int S1 = min(S, low);
-        const float down = t == 0 ? 1.f : pow2(S1 - S);
-        S = S1;
-        named_barrier(1 + rg, 64);   // the two warps of these rows
+            for (int i = 0; i < KL; ++i) {
+                const int key = x0 + LR * (i & ~1) + (i & 1);
+                const bool on = (node >> key) & 1;
+                const int e = -eq - sEk[key];   // in two steps: either may be out of range
+                float x = s[i] * pow2(e >> 1) * pow2(e - (e >> 1));
+                if (on && (odd_q || ((odd_k >> key) & 1)) && row < rows) {   // the plain product
+                    const float *q = Qg + row_of(row) * DKQ, *k = Kg + (sCell[key] * p.h_kv + g) * DKQ;
+                    x = 0.f;
+                    for (int j = 0; j < DKQ; ++j) x = fmaf(q[j], k[j], x);
+                }
+                s[i] = on ? x * p.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i]);
+            }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int row = 16 * rg + fr + 8 * y;
-            const float mn = fmaxf(m[y], fmaxf(mx[y], sMax[(kh ^ 1) * kF32Rows + row]));
-            const float al = m[y] == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : exp2f(m[y] - mn);
+            for (int o = LR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            const float mn = fmaxf(m, mx);
+            const float al = m == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : exp2f(m - mn);
             float sum = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int key = key0 + 8 * nt + 2 * fc;
+            for (int i = 0; i < KL; i += 2) {
+                const int key = x0 + LR * i;
                 float e[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float x = s[nt][2 * y + c];
+                    const float x = s[i + c];
                     e[c] = x == -INFINITY ? 0.f : exp2f(x - mn);
                     sum += e[c];
                     e[c] *= pow2(S - sSv[key + c] + kTop);
@@ -322,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
                 *reinterpret_cast<__half2 *>(sP + row * PS + key) = hi;
                 *reinterpret_cast<__half2 *>(sP + (kF32Rows + row) * PS + key) = lo;
             }
-            m[y] = mn;
-            l[y] = l[y] * al + sum;
-            if (kh == 0 && fc == 0) sAlpha[row] = al * down;
+            m = mn;
+            l = l * al + sum;
+            if (lane % LR == 0) sAlpha[row] = al * down;
         }
         __syncthreads();
 #pragma unroll
@@ -394,30 +389,18 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
         }
     }
     // ------------------------------------------------------------------------------------ result
-    __syncthreads();   // sMax and sAlpha are read
+    __syncthreads();   // sAlpha is read
     const int64_t part0 = (int64_t)piece_part(p, blockIdx.x, g, split) * p.part_rows;
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        l[y] += __shfl_xor_sync(0xFFFFFFFFu, l[y], 1);
-        l[y] += __shfl_xor_sync(0xFFFFFFFFu, l[y], 2);
-        if (fc == 0) sMax[kh * kF32Rows + 16 * rg + fr + 8 * y] = l[y];
-    }
-    named_barrier(1 + rg, 64);
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        const int row = 16 * rg + fr + 8 * y;
-        const float sum = sMax[row] + sMax[kF32Rows + row];
-        const bool any = sum > 0.f || sum != sum;
-        if (kh == 0 && fc == 0) {
-            sAlpha[row] = whole ? (any ? 1.f / sum : 0.f) : 1.f;
-            if (row < rows) {
-                if (!whole) {
-                    p.part_ml[(part0 + row) * 2] = m[y];
-                    p.part_ml[(part0 + row) * 2 + 1] = sum;
-                } else if (p.lse) {
-                    p.lse[row_of(row)] = any ? (m[y] + log2f(sum)) / kLog2e : -INFINITY;
-                }
-            }
+    for (int o = LR / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    if (lane % LR == 0 && row < rows) {
+        const bool any = l > 0.f || l != l;
+        sAlpha[row] = whole ? (any ? 1.f / l : 0.f) : 1.f;
+        if (!whole) {
+            p.part_ml[(part0 + row) * 2] = m;
+            p.part_ml[(part0 + row) * 2 + 1] = l;
+        } else if (p.lse) {
+            p.lse[row_of(row)] = any ? (m + log2f(l)) / kLog2e : -INFINITY;
         }
     }
     __syncthreads();
@@ -446,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_f32_tree_ke
 template <int DKQ, int DV, bool VK>
 int launch(const Params &p, cudaStream_t st) {
     if (!ensure_max_dynamic_smem(chunk_f32_tree_kernel<DKQ, DV, VK>)) return SFA_ERR_CUDA;
-    if (launch_pdl(chunk_f32_tree_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(kThreads),
+    if (launch_pdl(chunk_f32_tree_kernel<DKQ, DV, VK>, dim3(p.items, p.h_kv, p.n_split), dim3(32 * F32T<DKQ, DV, VK>::kWarps),
                    (size_t)F32T<DKQ, DV, VK>::kBytes, st, p) != cudaSuccess) {
         cudaGetLastError();
         return SFA_ERR_CUDA;
