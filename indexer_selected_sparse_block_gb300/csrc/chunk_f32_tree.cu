@@ -22,11 +22,11 @@ constexpr int kTop = 10;   // the exponent of a scaled row's largest value
 
 template <int DKQ, int DV, bool VK>
 struct F32T {
-    static constexpr int kWarps = DV == 512 ? 16 : 8;
+    static constexpr int kWarps = DV == 512 && VK ? 16 : 8;   // with values apart: registers
     static constexpr int kTK = DV == 512 ? 16 : 32;                   // keys of a tile
     static constexpr int kWG = kWarps / 4;                            // warps of 16 rows' scores: a tile of 16 keys
     static constexpr int kParts = kWG / (kTK / 16);                   // by so many parts of the dims each
-    static constexpr int kLR = kTK == 16 ? 8 : 4;                     // softmax: lanes of a row
+    static constexpr int kLR = 2 * kWG;                     // softmax: lanes of a row
     static constexpr int kPQ = DKQ + 8, kPV = DV + 8, kPS = kTK + 8;  // pitches: ldmatrix without bank conflicts
     static constexpr int kOffK = 2 * kF32Rows * kPQ * 2;              // hi, lo of the queries before
     static constexpr int kOffV = kOffK + 2 * kTK * kPQ * 2;
@@ -40,7 +40,7 @@ struct F32T {
     static constexpr int kBytes = kOffOdd + (kF32Rows + kTK) * 4;
     static constexpr int kBlocks = DV / 32;                           // values: blocks of 32 dims and row tiles of a warp
     static constexpr int kBW = kBlocks >= kWarps ? kBlocks / kWarps : 1, kMW = kBlocks >= kWarps ? 4 : 4 * kBlocks / kWarps;
-    static_assert(kLR == 2 * kWG && kBytes + 64 <= 227 * 1024, "rows of a warp's softmax; shared memory");
+    static_assert(kBytes + 64 <= 227 * 1024, "shared memory");
     static_assert(kOffCell % 8 == 0, "aligned");
 };
 
