@@ -270,8 +270,10 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float x = s[nt][2 * y + c];
-                    const float e = x == -INFINITY ? 0.f : exp2f(x - mn);
+                    float e = x == -INFINITY ? 0.f : exp2f(x - mn);
                     sum += e;
+                    // a scale that is not finite counts by any weight, however small
+                    if (x != -INFINITY && e < 0x1p-126f) e = 0x1p-126f;
                     const __nv_bfloat16 hi = __float2bfloat16_rn(e);
                     __nv_bfloat16 *to = sP + row * kPS + 16 * kh + key_slot(8 * nt + 2 * fc + c);
                     to[0] = hi;

@@ -361,6 +361,32 @@ def test_odd_scales_of_q8_rows_stay_in_their_branch(shape, scale):
     check_close(lse if c.sep else torch.where(odd, ref_l, lse), ref_l, tol_l, "lse")
 
 
+@pytest.mark.parametrize("gap", [50.0, 200.0])
+@pytest.mark.parametrize("shape", [W512, N128, N64])
+def test_odd_scales_of_small_weights(shape, gap):
+    """An infinite scale of values shows in what attends it by however small a weight."""
+    a, n, node, blk = 70, 30, 4, 1
+    c = Trees([(a, n), (5, 9)], 16, shape, "q8", "f32", seed=9)
+    d = c.dkq
+    c.Q[..., 0] = 16.0
+    cell = c.cells[0][a + node]
+    # the key's first block: its first code -127 by the scale that gives the score, zeros otherwise
+    row = c.K[cell, 0]
+    row[:32] = 0
+    row[0] = 129                                                        # -127
+    row[d:d + 2] = torch.tensor([gap / (16.0 * c.scale * 127)], dtype=torch.float16, device=DEV).view(torch.uint8)
+    c.V[cell, 0, c.dv + 2 * blk:c.dv + 2 * blk + 2] = torch.tensor(list(b"\x00\x7c"), dtype=torch.uint8, device=DEV)
+    assert c.call() == 0
+    hit = torch.tensor([v[node] for v in c.seen[0]] + [False] * 9)
+    odd = hit[:, None] & (torch.arange(c.h_q) < c.h_q // c.h_kv)[None]
+    O = c.O.double().cpu()
+    dims = torch.zeros(c.dv, dtype=torch.bool)
+    dims[32 * blk:32 * blk + 32] = True
+    bad = odd[..., None] & dims
+    assert bool(hit.any()) and not bool(torch.isfinite(O[bad]).any())
+    assert bool(torch.isfinite(O[~bad]).all())
+
+
 @pytest.mark.parametrize("shape", [WIDE, N128])
 def test_odd_values_of_the_cached_tokens_stay_out_of_the_drafted_part(shape):
     c = Trees([(130, 10)], 16, shape, "bf16", "f32", odd=[(0, 129, 0, 1, math.nan), (0, 128, 0, 2, math.inf)])
