@@ -7,11 +7,18 @@
 //   values: a key's power goes into its weight, relative to the smallest one so far (S: the largest values),
 //           so that sum_k (p_k 2^(S - sv_k)) (2^sv_k v_k) = 2^S sum_k p_k v_k.
 // A row is read, scaled and cut once for all 64 rows (query, head) of the CTA's tile; the next tile's rows are on
-// their way to registers meanwhile.  Scores: a warp has 16 rows and half the tile's keys.  Values: a warp has 64
-// dims of all rows (narrow heads: 32 dims of 32 or 16 rows), sixteen keys' sum is added with rounding.
+// their way to registers meanwhile.  Scores: a warp has 16 rows and 16 keys, wide heads' by a quarter (a half) of
+// the dims, which the warps of a row group add up through shared memory; then a row's softmax is one warp's.
+// Values: a warp has 32 dims of all rows (with values apart 64; narrow heads: of 32 or 16 rows), sixteen keys' sum
+// is added with rounding.
 // Values that are not finite are taken out of the operands: a score with one is a plain product instead, and such
 // values are added one by one to the rows that attend them.
-// XXX
+// 17 trees of 3 behind 27053, 576 wide, 16 heads: 845 us, 57 TFLOP/s of the rows alone (1679 by three tf32 products on
+// 32 rows; 1010 with eight warps, each with its 16 rows' scores of 8 keys, which read the queries twice as often).
+// 15 of 20 behind 17048, 128 wide, 16 heads on 4: 1094 us (2626).  It is bound by its phases, rows to shared memory,
+// scores, softmax and values, which follow one another with a barrier each: scores at shared memory's rate (the
+// queries are read for each tile), the others at instructions' latency.  16 warps need all 64 thousand registers: with
+// values apart they would spill (1 tree of 133 behind 10852: 1167 us, eight warps 890).
 #include "chunk_common.cuh"
 
 namespace sfa {

@@ -89,7 +89,7 @@ __device__ __forceinline__ float scale_at(const uint8_t *row, int d, int block) 
 
 // ROUND, fp32 results: sixteen keys' sum is added to acc with rounding.  The tensor cores cut what they add to an
 // accumulator towards zero: 1.1e-9 of a result for a key of a piece's, which bf16 results do not show (3e-5 at 30000
-// keys; it costs 8%).
+// keys; it costs 8%: 360 us for the 335 above).
 template <int DKQ, int DV, bool VK, bool ROUND>
 __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_kernel(const Params p) {
     using L = Q8<DKQ, DV, VK>;
