@@ -13,10 +13,13 @@
 // asynchronous copies.  Scores: a warp has 16 rows and 16 keys.  Values: a warp has 64 dims of all rows (narrow
 // heads: 32 dims of 32 or 16 rows).  The dims of a lane's operands are eight (four) neighbours of a block: any
 // order does for the contraction, and a lane's results are eight neighbouring dims.
-// 2 trees of 13 nodes behind 34715, 576 wide, 16 heads: 335 us, 94 TFLOP/s of the rows alone (1091 by three tf32
+// 2 trees of 13 nodes behind 34715, 576 wide, 16 heads: 342 us, 92 TFLOP/s of the rows alone (1091 by three tf32
 // products on rows expanded in shared memory).  It is bound by instructions and the latency of short chains, on
 // eight warps with all registers: schedulers issue half the time, mma.sync is a third of its 600 TFLOP/s.  With 16
-// warps of half the value dims 350; 39 trees of 19 behind 786, 512 wide: 278, 290.
+// warps of half the value dims, scores by halves of the dims and a row's softmax in one warp 361; 39 trees of 19
+// behind 786, 512 wide: 290, 297; 27 of 104 behind 54: 397, 377.
+// Row tiles without rows are left out (128 wide, 1 tree of 3 behind 126486, 16 heads on 16: 554 us, 688 with them),
+// of wide heads' the last two at once: a test for each costs full tiles 4%.
 #include "chunk_common.cuh"
 
 namespace sfa {
@@ -89,7 +92,7 @@ __device__ __forceinline__ float scale_at(const uint8_t *row, int d, int block) 
 
 // ROUND, fp32 results: sixteen keys' sum is added to acc with rounding.  The tensor cores cut what they add to an
 // accumulator towards zero: 1.1e-9 of a result for a key of a piece's, which bf16 results do not show (3e-5 at 30000
-// keys; it costs 8%: 360 us for the 335 above).
+// keys; it costs 8%: 373 us for the 342 above).
 template <int DKQ, int DV, bool VK, bool ROUND>
 __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_kernel(const Params p) {
     using L = Q8<DKQ, DV, VK>;
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < MW; ++x) {
-            if (16 * (MW * mw + x) >= rows) break;   // row tiles without rows
+            if ((MW < 4 || x == 2) && 16 * (MW * mw + x) >= rows) break;
             const float al0 = sAlpha[16 * (MW * mw + x) + fr], al1 = sAlpha[16 * (MW * mw + x) + fr + 8];
             if (__any_sync(0xFFFFFFFFu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
                 }
 #pragma unroll
                 for (int x = 0; x < MW; ++x) {
-                    if (16 * (MW * mw + x) >= rows) break;
+                    if ((MW < 4 || x == 2) && 16 * (MW * mw + x) >= rows) break;
                     uint32_t ph[4], pl[4];
                     const uint32_t pa = smem_u32(sP + (16 * (MW * mw + x) + (lane & 15)) * kPS + 16 * ks + 8 * (lane >> 4));
                     ldsm_x4(pa, ph[0], ph[1], ph[2], ph[3]);
