@@ -4,8 +4,10 @@
 // to a largest value of 2^10 .. 2^11 by a power of two and cut in hi + lo of 11 bits each, which leaves 2^-22 of a
 // value (2^-35 of the row's largest at least), and of the four products the three larger ones are taken.
 //   scores: the rows' powers of two come back with the scale;
-//   values: a key's power goes into its weight, relative to the smallest one so far (S: the largest values),
-//           so that sum_k (p_k 2^(S - sv_k)) (2^sv_k v_k) = 2^S sum_k p_k v_k.
+//   values: a key's power goes into its weight, relative to a power u of the row (query, head) that its largest
+//           weights 2^-sv_k p_k set: sum_k (p_k 2^(-sv_k - u)) (2^sv_k v_k) = 2^-u sum_k p_k v_k.  So a token of large
+//           values costs only those rows precision to whose result it adds much.
+// The running maximum moves by more than 2^8 only, u by more than 2^4 (weights stay below 2^15).
 // A row is read, scaled and cut once for all 64 rows (query, head) of the CTA's tile; the next tile's rows are on
 // their way to registers meanwhile.  Scores: a warp has 16 rows and 16 keys, wide heads' by a quarter (a half) of
 // the dims, which the warps of a row group add up through shared memory; then a row's softmax is one warp's.
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
     const int row = 16 * rg + wg * (32 / LR) + lane / LR, x0 = 2 * (lane % LR);   // softmax: keys x0 + 2 LR i, + 1
     const uint32_t *mask = row < rows ? p.mask + (int64_t)(it.q.c0 + (r0 + row) / p.G) * p.mask_words : nullptr;
     float m = -INFINITY, l = 0.f;   // of that row, base 2; l of this lane's keys
+    int u = -1000;                  // and the power of two of its sums of values
     // values: blocks BW bw .. of row tiles MW mw ..
     const int bw = warp % (L::kBlocks / BW), mw = warp / (L::kBlocks / BW);
     float acc[BW][MW][4][4];
@@ -222,7 +225,6 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[b][x][i][c] = 0.f;
-    int S = 127;   // the values' power of two so far
 
     for (int t = 0; t < n_tiles; ++t) {
         const int t0 = k0 + t * TK;
@@ -233,14 +235,11 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             look_up(t0 + 2 * TK);
         }
         __syncthreads();
-        // the tile's smallest power of two, and its keys that are and that have odd values
+        // the tile's keys that are, and that have odd values
         const int64_t *sCell = sCells + (t & 1) * TK;
         const unsigned live = __ballot_sync(0xFFFFFFFFu, sCell[lane % TK] >= 0);
         const int o = sOdd[lane % TK];
         const unsigned odd_k = __ballot_sync(0xFFFFFFFFu, o & 1), odd_v = __ballot_sync(0xFFFFFFFFu, lane < TK && (o & 2));
-        const int S1 = min(S, __reduce_min_sync(0xFFFFFFFFu, sSv[lane % TK]));
-        const float down = t == 0 ? 1.f : pow2(S1 - S);
-        S = S1;
         if (16 * rg < rows) {
             float d[2][2][4] = {};   // the small products' sum and the large one's
             const uint32_t qa = smem_u32(sQ + (16 * rg + (lane & 15)) * PQ + 8 * (lane >> 4) + 16 * first);
@@ -303,21 +302,30 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             }
 #pragma unroll
             for (int o = LR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            const float mn = fmaxf(m, mx);
-            const float al = m == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : exp2f(m - mn);
+            const float mn = mx > m + 8.f ? mx : m, dm = m == -INFINITY || mn == m ? 0.f : m - mn;
+            const int whole_dm = (int)floorf(fmaxf(dm, -300.f));
             float sum = 0.f;
+            int top = -2000;   // the largest weights' power
+#pragma unroll
+            for (int i = 0; i < KL; ++i) {
+                s[i] = s[i] == -INFINITY ? -1.f : exp2f(s[i] - mn);   // below 0: not attended
+                if (s[i] >= 0.f || s[i] != s[i]) sum += s[i];
+                if (s[i] > 0.f) top = max(top, (int)(__float_as_uint(s[i]) >> 23) - 126 - sSv[x0 + LR * (i & ~1) + (i & 1)]);
+            }
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const int u0 = u + whole_dm;
+            u = top > u0 + 4 ? top : u0;
 #pragma unroll
             for (int i = 0; i < KL; i += 2) {
                 const int key = x0 + LR * i;
                 float e[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float x = s[i + c];
-                    e[c] = x == -INFINITY ? 0.f : exp2f(x - mn);
-                    sum += e[c];
-                    e[c] *= pow2(S - sSv[key + c] + kTop);
+                    const int a = min(kTop - sSv[key + c] - u, 252);   // in two steps: it may be out of range
+                    e[c] = s[i + c] < 0.f ? 0.f : s[i + c] * pow2(a >> 1) * pow2(a - (a >> 1));
                     // a value that is not finite counts by any weight (its finite ones are off by 2^-34 at most)
-                    if ((odd_v >> (key + c)) & 1 && x != -INFINITY) e[c] = fmaxf(e[c], 0x1p-24f);
+                    if ((odd_v >> (key + c)) & 1 && !(s[i + c] < 0.f)) e[c] = fmaxf(e[c], 0x1p-24f);
                 }
                 __half2 hi, lo;
                 split_f16(e[0], e[1], hi, lo);
@@ -325,8 +333,8 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
                 *reinterpret_cast<__half2 *>(sP + (kF32Rows + row) * PS + key) = lo;
             }
             m = mn;
-            l = l * al + sum;
-            if (lane % LR == 0) sAlpha[row] = al * down;
+            l = l * exp2f(dm) + sum;
+            if (lane % LR == 0) sAlpha[row] = exp2f(dm - whole_dm) * pow2(u0 - u);
         }
         __syncthreads();
 #pragma unroll
@@ -403,6 +411,7 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
     if (lane % LR == 0 && row < rows) {
         const bool any = l > 0.f || l != l;
         sAlpha[row] = whole ? (any ? 1.f / l : 0.f) : 1.f;
+        sEq[row] = u - kTop;
         if (!whole) {
             p.part_ml[(part0 + row) * 2] = m;
             p.part_ml[(part0 + row) * 2 + 1] = l;
@@ -418,12 +427,13 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             const int row = 16 * (MW * mw + x) + fr + 8 * y;
             if (row >= rows) continue;
             const float inv = sAlpha[row];
+            const int unit = sEq[row];
 #pragma unroll
             for (int b = 0; b < BW; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int d = 32 * (BW * bw + b) + 8 * i + 2 * fc;
-                    const float u = ldexpf(acc[b][x][i][2 * y] * inv, -S - kTop), v = ldexpf(acc[b][x][i][2 * y + 1] * inv, -S - kTop);
+                    const float u = ldexpf(acc[b][x][i][2 * y] * inv, unit), v = ldexpf(acc[b][x][i][2 * y + 1] * inv, unit);
                     if (whole && p.o_bf16)
                         *reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(p.O) + row_of(row) * DV + d) = pack_bf16(u, v);
                     else

@@ -454,6 +454,27 @@ def test_another_stream_and_host_results():
     assert torch.equal(O, c.O.cpu())
 
 
+@pytest.mark.parametrize("power", [20, 60, 100])
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("shape", [W512, N128, N64])
+def test_large_values_where_they_weigh_little(shape, dtype, out, power):
+    """Values 2^power times the others': of a node that few attend, of a node and a cached token whose scores are as
+    much lower, and of a node that its descendants attend as any other."""
+    lens = [(150, 40), (20, 33), (5000, 20), (64, 64)]
+    c = Trees(lens, 16, shape, dtype, out, seed=8)
+    c.Q[..., 0] = 16.0
+    large = [(0, 155, False), (1, 20 + 7, True), (1, 3, True), (2, 4000, True), (3, 64 + 40, False)]
+    for s, pos, low in large:
+        cell = c.cells[s][pos]
+        for x in (c.V, c.Vv):
+            x[cell] = x[cell] * 2.0 ** power
+        if low:
+            for x in (c.K, c.Kv):
+                x[cell, :, 0] = -math.log(2.0) * power / (16.0 * c.scale)
+    assert c.call() == 0
+    c.check()
+
+
 @pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
 @pytest.mark.parametrize("dtype", ["q8", "f32", "bf16"])
 def test_long_sums_are_rounded_not_cut(shape, dtype):
