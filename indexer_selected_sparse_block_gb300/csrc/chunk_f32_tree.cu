@@ -15,12 +15,12 @@
 // is added with rounding.
 // Values that are not finite are taken out of the operands: a score with one is a plain product instead, and such
 // values are added one by one to the rows that attend them.
-// 17 trees of 3 behind 27053, 576 wide, 16 heads: 845 us, 57 TFLOP/s of the rows alone (1679 by three tf32 products on
+// 17 trees of 3 behind 27053, 576 wide, 16 heads: 863 us, 55 TFLOP/s of the rows alone (1679 by three tf32 products on
 // 32 rows; 1010 with eight warps, each with its 16 rows' scores of 8 keys, which read the queries twice as often).
-// 15 of 20 behind 17048, 128 wide, 16 heads on 4: 1094 us (2626).  It is bound by its phases, rows to shared memory,
+// 15 of 20 behind 17048, 128 wide, 16 heads on 4: 1101 us (2626).  It is bound by its phases, rows to shared memory,
 // scores, softmax and values, which follow one another with a barrier each: scores at shared memory's rate (the
 // queries are read for each tile), the others at instructions' latency.  16 warps need all 64 thousand registers: with
-// values apart they would spill (1 tree of 133 behind 10852: 1167 us, eight warps 890).
+// values apart they would spill (1 tree of 133 behind 10852: 1167 us, eight warps 892).
 #include "chunk_common.cuh"
 
 namespace sfa {
@@ -31,21 +31,21 @@ constexpr int kTop = 10;   // the exponent of a scaled row's largest value
 
 template <int DKQ, int DV, bool VK>
 struct F32T {
-    static constexpr int kWarps = DV == 512 && VK ? 16 : 8;   // with values apart: registers
+    static constexpr int kWarps = DV == 512 && VK ? 16 : 8;           // with values apart: registers
     static constexpr int kTK = DV == 512 ? 16 : 32;                   // keys of a tile
     static constexpr int kWG = kWarps / 4;                            // warps of 16 rows' scores: a tile of 16 keys
     static constexpr int kParts = kWG / (kTK / 16);                   // by so many parts of the dims each
-    static constexpr int kLR = 2 * kWG;                     // softmax: lanes of a row
+    static constexpr int kLR = 2 * kWG;                               // softmax: lanes of a row
     static constexpr int kPQ = DKQ + 8, kPV = DV + 8, kPS = kTK + 8;  // pitches: ldmatrix without bank conflicts
     static constexpr int kOffK = 2 * kF32Rows * kPQ * 2;              // hi, lo of the queries before
     static constexpr int kOffV = kOffK + 2 * kTK * kPQ * 2;
     static constexpr int kOffP = kOffV + (VK ? 0 : 2 * kTK * kPV * 2);
     static constexpr int kOffS = kOffP + 2 * kF32Rows * kPS * 2;      // float [kParts][64][kPS]
     static constexpr int kOffCell = kOffS + kParts * kF32Rows * kPS * 4;   // int64 [2][kTK]: this tile's and the next one's
-    static constexpr int kOffUnit = kOffCell + 2 * kTK * 8;               // int: rows' and keys' powers of two
-    static constexpr int kOffAlpha = kOffUnit + (kF32Rows + kTK) * 4;
-    static constexpr int kOffSv = kOffAlpha + kF32Rows * 4;           // int [kTK]
-    static constexpr int kOffOdd = kOffSv + kTK * 4;                  // int [64] of queries, [kTK]: 1 key, 2 value
+    static constexpr int kOffUnit = kOffCell + 2 * kTK * 8;           // float2: keys' and values' powers of two, undone
+    static constexpr int kOffRow = kOffUnit + (VK ? 1 : 2) * kTK * 8; // int: rows' powers of two
+    static constexpr int kOffAlpha = kOffRow + kF32Rows * 4;
+    static constexpr int kOffOdd = kOffAlpha + kF32Rows * 4;          // int [64] of queries, [kTK]: 1 key, 2 value
     static constexpr int kBytes = kOffOdd + (kF32Rows + kTK) * 4;
     static constexpr int kBlocks = DV / 32;                           // values: blocks of 32 dims and row tiles of a warp
     static constexpr int kBW = kBlocks >= kWarps ? kBlocks / kWarps : 1, kMW = kBlocks >= kWarps ? 4 : 4 * kBlocks / kWarps;
@@ -63,6 +63,13 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 2^e as two factors, which may be out of range together.
+__device__ __forceinline__ float2 pow2_halves(int e) { return make_float2(pow2(e >> 1), pow2(e - (e >> 1))); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ void split_f16(float x, float y, __half2 &hi, __half2 &lo) {
     hi = __floats2half2_rn(x, y);
@@ -113,9 +120,10 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
     __half *sQ = reinterpret_cast<__half *>(smem), *sK = reinterpret_cast<__half *>(smem + L::kOffK);
     __half *sV = VK ? sK : reinterpret_cast<__half *>(smem + L::kOffV), *sP = reinterpret_cast<__half *>(smem + L::kOffP);
     int64_t *sCells = reinterpret_cast<int64_t *>(smem + L::kOffCell);
-    int *sEq = reinterpret_cast<int *>(smem + L::kOffUnit), *sEk = sEq + kF32Rows;
+    float2 *sUk = reinterpret_cast<float2 *>(smem + L::kOffUnit), *sUv = VK ? sUk : sUk + TK;
+    int *sEq = reinterpret_cast<int *>(smem + L::kOffRow);
     float *sS = reinterpret_cast<float *>(smem + L::kOffS), *sAlpha = reinterpret_cast<float *>(smem + L::kOffAlpha);
-    int *sSv = reinterpret_cast<int *>(smem + L::kOffSv), *sOddQ = reinterpret_cast<int *>(smem + L::kOffOdd),
+    int *sOddQ = reinterpret_cast<int *>(smem + L::kOffOdd),
         *sOdd = sOddQ + kF32Rows;
     __shared__ Item s_item;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, fr = lane >> 2, fc = lane & 3;
@@ -183,8 +191,8 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             odd_v = odd_k;   // V = K: perhaps of dims behind the values only
             if constexpr (!VK) sv = put_row<NV>(vreg[i], sV + key * PV, TK * PV, odd_v);
             if (lane == 0) {
-                sEk[key] = e;
-                sSv[key] = sv;
+                sUk[key] = pow2_halves(-e);
+                if constexpr (!VK) sUv[key] = pow2_halves(-sv);
                 sOdd[key] = (odd_k ? 1 : 0) | (odd_v ? 2 : 0);
             }
         }
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
         if (16 * rg < rows) {
             constexpr int KL = TK / LR;   // keys of a lane
             const uint32_t node = live & tree_bits(p, mask, cached, t0);
-            const int eq = sEq[row];
+            const float2 uq = pow2_halves(-sEq[row]);
             const bool odd_q = sOddQ[row] != 0;
             float s[KL], mx = -INFINITY;
 #pragma unroll
@@ -290,8 +298,8 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             for (int i = 0; i < KL; ++i) {
                 const int key = x0 + LR * (i & ~1) + (i & 1);
                 const bool on = (node >> key) & 1;
-                const int e = -eq - sEk[key];   // in two steps: either may be out of range
-                float x = s[i] * pow2(e >> 1) * pow2(e - (e >> 1));
+                const float2 uk = sUk[key];
+                float x = s[i] * uk.x * uq.x * uk.y * uq.y;
                 if (on && (odd_q || ((odd_k >> key) & 1)) && row < rows) {   // the plain product
                     const float *q = Qg + row_of(row) * DKQ, *k = Kg + (sCell[key] * p.h_kv + g) * DKQ;
                     x = 0.f;
@@ -302,30 +310,38 @@ __global__ void __launch_bounds__(32 * F32T<DKQ, DV, VK>::kWarps, DV == 512 ? 1 
             }
 #pragma unroll
             for (int o = LR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            const float mn = mx > m + 8.f ? mx : m, dm = m == -INFINITY || mn == m ? 0.f : m - mn;
+            const float mn = mx > m + 8.f ? mx : m, base = mn == -INFINITY ? 0.f : mn;
+            const float dm = m == -INFINITY || mn == m ? 0.f : m - mn;
             const int whole_dm = (int)floorf(fmaxf(dm, -300.f));
-            float sum = 0.f;
-            int top = -2000;   // the largest weights' power
+            unsigned odd_on = 0;
+            if (odd_v & node) {
+#pragma unroll
+                for (int i = 0; i < KL; ++i)
+                    odd_on |= s[i] != -INFINITY ? odd_v & (1u << (x0 + LR * (i & ~1) + (i & 1))) : 0u;
+            }
+            float sum = 0.f, w[KL], large = 0.f;   // the weights of the values as they were, the largest
 #pragma unroll
             for (int i = 0; i < KL; ++i) {
-                s[i] = s[i] == -INFINITY ? -1.f : exp2f(s[i] - mn);   // below 0: not attended
-                if (s[i] >= 0.f || s[i] != s[i]) sum += s[i];
-                if (s[i] > 0.f) top = max(top, (int)(__float_as_uint(s[i]) >> 23) - 126 - sSv[x0 + LR * (i & ~1) + (i & 1)]);
+                const float2 uv = sUv[x0 + LR * (i & ~1) + (i & 1)];
+                const float e = ex2(s[i] - base);
+                sum += e;
+                w[i] = e * uv.x * uv.y;
+                large = fmaxf(large, w[i]);
             }
 #pragma unroll
-            for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const int u0 = u + whole_dm;
+            for (int o = LR / 2; o > 0; o >>= 1) large = fmaxf(large, __shfl_xor_sync(0xFFFFFFFFu, large, o));
+            const int top = large > 0.f ? (int)(__float_as_uint(large) >> 23) - 126 : -2000, u0 = u + whole_dm;
             u = top > u0 + 4 ? top : u0;
+            const float2 uw = pow2_halves(min(kTop - u, 252));
 #pragma unroll
             for (int i = 0; i < KL; i += 2) {
                 const int key = x0 + LR * i;
                 float e[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int a = min(kTop - sSv[key + c] - u, 252);   // in two steps: it may be out of range
-                    e[c] = s[i + c] < 0.f ? 0.f : s[i + c] * pow2(a >> 1) * pow2(a - (a >> 1));
+                    e[c] = w[i + c] * uw.x * uw.y;
                     // a value that is not finite counts by any weight (its finite ones are off by 2^-34 at most)
-                    if ((odd_v >> (key + c)) & 1 && !(s[i + c] < 0.f)) e[c] = fmaxf(e[c], 0x1p-24f);
+                    if ((odd_on >> (key + c)) & 1) e[c] = fmaxf(e[c], 0x1p-24f);
                 }
                 __half2 hi, lo;
                 split_f16(e[0], e[1], hi, lo);
