@@ -32,6 +32,7 @@ class Trees:
                  scale=None, kscale=1.0, lost=()):
         self.dkq, self.dv, self.sep, self.h_q, self.h_kv = shape
         self.lens, self.page, self.dtype, self.out = lens, page, dtype, out
+        self.halves = 0.0
         r, g = random.Random(seed), torch.Generator(device=DEV).manual_seed(seed)
         n_pg = [-(-(a + n) // page) for a, n in lens]
         order = torch.randperm(sum(n_pg) + 2, generator=g, device=DEV)
@@ -112,7 +113,7 @@ class Trees:
                                  self.dv, drafted=self.part == sfa.SFA_PART_DRAFTED,
                                  # other caches: three tf32 products, 2^-19 of a product at most
                                  product=0.0 if bf16 else 2.0 ** -19,
-                                 p_round=0.0 if not bf16 else UBF if self.out == "bf16" else UBF ** 2,
+                                 p_round=self.halves if not bf16 else UBF if self.out == "bf16" else UBF ** 2,
                                  o_round=(2 if twice else 1) * UBF if self.out == "bf16" else 0.0)
 
     def check(self, seen=None):
@@ -298,6 +299,22 @@ def test_scales(shape, scale, kscale):
 
 
 ODD = [math.nan, math.inf, -math.inf]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "q8"])
+@pytest.mark.parametrize("shape", [WIDE, W512, N128, N64])
+@pytest.mark.parametrize("scale,kscale", [(-0.2, 1.0), (0.0, 1.0), (1.0, 4.0), (0.05, 2.0 ** -40)])
+def test_scales_of_other_caches(shape, dtype, scale, kscale):
+    if dtype == "q8" and kscale < 1:
+        kscale = 2.0 ** -10      # scales of blocks are binary16
+    c = Trees([(300, 20), (1000, 40), (0, 9)], 16, shape, dtype, "f32", scale=scale, kscale=kscale)
+    if dtype == "q8":
+        # p v with both in two bf16 halves, x = hi + lo + r: of x in [1, 2) lo is 2^-8 at most, r half a step of that,
+        # 2^-17; what is left out, r_p v, p r_v and lo_p lo_v, is 2^-17 + 2^-17 + 2^-16 of |p v| at most, 2 UBF^2; the
+        # bound takes a weight's rounding twice.  (Of scores near zero; elsewhere the scores' own bound is above it.)
+        c.halves = UBF ** 2
+    assert c.call() == 0
+    c.check()
 
 
 @pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
