@@ -812,6 +812,8 @@ int sfa_tree_accept(const int32_t *parent, const int32_t *token, const int32_t *
  *   caches: base and row bytes (even) of [n_cells][...] arrays, rows of any kind, q8_0 ones included
  *   path, path_stride, n_acc: as sfa_tree_accept writes them, or any nodes of the tree in ascending
  *        order; it ends where they do not ascend or leave the tree, or at path_stride (SFA_DEV_BAD_TREE)
+ * A sequence with nodes whose len_total[s] is 0 was emptied since its tree was drafted: nothing of it stays,
+ * len_out[s] is 0 and no page of its goes back (whoever emptied it has them).
  * A node without a cell (slot -1: the pages had run out) counts, and its row is not moved: its position
  * then holds another node's (SFA_DEV_BAD_CELL); as after any lack of pages, empty that sequence and feed
  * it again.  One launch.

@@ -208,6 +208,8 @@ __device__ __forceinline__ void commit_lists(const CommitParams &p) {
     auto after = [&](int s, int &k0, int &k1) {
         const Tree t = load_tree(p.cu, s, p.n_rows);
         const int total = max(p.total[s], 0);
+        k0 = k1 = 0;
+        if (t.n > 0 && p.total[s] == 0) return 0;   // emptied since its tree was drafted
         bool bad;
         const int limit = path_limit(p, s, t, bad);
         if (t.bad || p.total[s] < t.n) flags |= SFA_DEV_BAD_QUERY;

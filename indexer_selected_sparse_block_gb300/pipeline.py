@@ -406,18 +406,39 @@ class SfaPagedCache:
 
     def release(self, seq: int, stream=None):
         """Empties sequence seq: its pages go to the end of the free list.  On `stream`, behind what
-        it holds: the one that the steps run on.  (Reads the sequence's length and the list's head
-        on the host, so it is not for capture.)"""
+        it holds: the one that the steps run on.  Between a draft and its commit, its tree goes too:
+        the commit keeps nothing of it (path, n_acc and next_token of that sequence then say nothing,
+        and attention of its nodes is flagged), and of the others' trees what it would have kept.
+        (Reads lengths and the list's head on the host, so it is not for capture.)"""
         with torch.cuda.stream(stream):
             n = -(-int(self.length[seq]) // self.page_size)
             pages = self.page_table[seq, :n]
             pages = pages[pages >= 0]
-            head = int(self.free_head)
-            free = torch.cat([self.free_pages[head:], pages])
+            first = head = int(self.free_head)
+            own = pages[:0]
+            if self._drafted():
+                # the list's pages from `head` to `first` are the trees': of this sequence or of others
+                first, end = int(self._head_out), -(-int(self.len_total[seq]) // self.page_size)
+                own = self.page_table[seq, n:end]
+                self.len_total[seq] = 0
+            taken = self.free_pages[head:first]
+            is_own = torch.isin(taken, own)
+            free = torch.cat([taken[~is_own], self.free_pages[first:], pages, taken[is_own]])
             # in place: a captured step keeps reading these buffers
-            self.free_pages[self.n_pages - free.numel():] = free
-            self.free_head.fill_(self.n_pages - free.numel())
+            head = self.n_pages - free.numel()
+            self.free_pages[head:] = free
+            self.free_head.fill_(head)
+            self._head_out.fill_(head + int((~is_own).sum()))
             self.page_table[seq].fill_(-1)
             if self.cell_of is not None:
                 self.cell_of[seq].fill_(-1)
             self.length[seq] = 0
+
+    def _drafted(self) -> bool:
+        """Whether trees wait for their commit, on the device as replays leave it: every sequence holds what it
+        held when they were drafted, or was released since.  Steps and commits of no token and no node look
+        the same, and are: the lists are as they were behind the draft."""
+        if self.tree_mask is None:
+            return False
+        before = self.len_total - self.cu_new.diff()
+        return bool(((self.length == before) | ((self.length | self.len_total) == 0)).all())
