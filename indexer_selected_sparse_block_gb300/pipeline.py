@@ -330,6 +330,7 @@ class SfaPagedCache:
                               self.n_pages, self.page_table, self.cu_new, self.len_total,
                               self.q_seq, self.q_pos, self.slot, self._head_out,
                               cell_of=self.cell_of, dev_status=self.status, stream=stream)
+        self._parent = None                    # a tree before has no cells any more
         if tree is not None:
             B.sfa_build_tree_maps(tree, self.cu_new, self.len_total, self.tree_mask, self.q_pos,
                                   cached_pos=self.cached_pos, dev_status=self.status, stream=stream)
@@ -348,7 +349,6 @@ class SfaPagedCache:
         most) and their rows K, V, X [n_tok_cap][...], packed sequence by sequence, into them.  rope: the
         last n_rot dims of K's rows are turned on the way, and of Q's [n_tok_cap][h_q][dkq] in place."""
         self._place(len_new, K, V, X, rope, Q, stream)
-        self._parent = None
         copies = [(self.length.unsqueeze(0), self.len_total.unsqueeze(0)),
                   (self.free_head, self._head_out)]
         B.sfa_copy_cache_rows_multi(copies, stream=stream)
