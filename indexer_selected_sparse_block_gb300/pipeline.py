@@ -30,6 +30,8 @@ entry points then take them as ``SFA_Q8_0``; the index keys stay bf16.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _binding as B
@@ -249,6 +251,11 @@ class SfaStep:
         return self.O
 
 
+def _capturing() -> bool:
+    """Whether calls are recorded instead of run."""
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
 class SfaPagedCache:
     """A paged cache of n_seq sequences with its device-side bookkeeping: the cells of K (V, and
     the index keys X), the page table, the free list, the lengths, and the per-step buffers.
@@ -379,6 +386,7 @@ class SfaPagedCache:
             raise ValueError("a cache for drafted trees is made with n_draft_max")
         self._place(len_new, K, V, X, rope, Q, stream, tree=parent)
         self._parent = parent
+        self._commits = math.inf if _capturing() else 1     # that may follow, as far as can be seen here
 
     def attend_tree(self, Q, n_new_max: int, n_kv_max: int, scale: float, O, lse=None,
                     part: int = B.SFA_PART_ALL, workspace=None, stream=None):
@@ -392,16 +400,24 @@ class SfaPagedCache:
     def commit(self, token, target, root_target=None, stream=None):
         """Of the last draft the path that the model agrees with stays: token [n_tok_cap] the nodes' tokens,
         target [n_tok_cap] the model's choice behind each, root_target [n_seq] behind the cached tokens (None:
-        the first root is taken).  path, n_acc and next_token say which, how many and what comes next.  Once a
-        draft (a second time would move rows that have moved); the parents given to draft are read again."""
+        the first root is taken).  path, n_acc and next_token say which, how many and what comes next; the
+        parents given to draft are read again.  Once a draft: a second time, which would move rows that have
+        moved, is refused.  Behind a captured draft that is the caller's to keep: one commit, called or
+        replayed, for each of its replays, and where a commit is captured alone, the runs that warm it up
+        behind a draft of no node."""
         if self._parent is None:
             raise ValueError("no drafted tree to commit")
+        run = not _capturing()
+        if run and self._commits < 1:
+            raise ValueError("the drafted tree is committed already")
         B.sfa_tree_accept(self._parent, token, target, self.cu_new, self.path, self.n_acc, self.next_token,
                           root_target=root_target, dev_status=self.status, stream=stream)
         B.sfa_tree_commit([c for c in (self.K, self.V, self.X) if c is not None], self.slot, self.cu_new,
                           self.path, self.n_acc, self.len_total, self.page_size, self.page_table,
                           self.free_pages, self._head_out, self.length, self.free_head,
                           dev_status=self.status, stream=stream)
+        if run:
+            self._commits -= 1
         return self.next_token
 
     def release(self, seq: int, stream=None):
