@@ -5,7 +5,8 @@
 // node's mask names, 16 at a time: every row of its tile attends every key, so there is no mask in the
 // products, and a value that is not finite reaches the nodes that attend it and no other.
 //   S = Q K^T: each of the four warps over a quarter of the head dims, summed in shared memory;
-//   O += P V:  each warp a quarter of the value dims, the weights as three bf16 parts (2^-27).
+//   O += P V:  each warp a quarter of the value dims, the weights as three bf16 parts (2^-27); keys with a score of
+//              minus infinity take their sixteen there one by one.
 // It is a chain of latencies a CTA (offsets, mask, page table, rows, scores, softmax, values) on the five CTAs that an
 // SM's shared memory and registers hold.  32 trees of 64 nodes, 16 heads, 576 wide, fp32 results: 28.5 us, 3.8 TB/s
 // of what has to move, Q and O (105 MB, 16 us); on tiles of all nodes 55.  Four CTAs 31.0; stores of 8 bytes a lane and
@@ -43,6 +44,38 @@ __device__ __forceinline__ void gather(uint32_t to, const void *src, const int64
         cp_async16(to + r * P * 2 + c * 16,
                    reinterpret_cast<const __nv_bfloat16 *>(src) + ((cell < 0 ? 0 : cell) * h_kv + g) * D + c * 8,
                    cell < 0 ? 0u : 16u);
+    }
+}
+
+// O += P V key by key, where a score is minus infinity: in the products its weight of zero would bring values
+// that are not finite into that row.  The scores are in sRed still; a key without a cell is zeros.
+template <int DV, int NT, int PV>
+__device__ __forceinline__ void add_values(const Params &p, const float *sRed, const __nv_bfloat16 *sP, const float *sAlpha,
+                                           const uint8_t *sV, bool more, float (&acc)[NT][4]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int r = (lane >> 2) + 8 * c;
+        const float al = more ? sAlpha[r] : 1.f;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            acc[x][2 * c] *= al;
+            acc[x][2 * c + 1] *= al;
+        }
+#pragma unroll 1
+        for (int k = 0; k < kKeys; ++k) {
+            const float *f = sRed + r * kPR + k;
+            if (((f[0] + f[16 * kPR]) + (f[2 * 16 * kPR] + f[3 * 16 * kPR])) * p.scale_log2 == -INFINITY) continue;
+            const __nv_bfloat16 *w = sP + r * kPP + k;
+            const float e = __bfloat162float(w[0]) + (__bfloat162float(w[16 * kPP]) + __bfloat162float(w[2 * 16 * kPP]));
+            const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(sV) + (k * PV + warp * (DV / 4)) / 2 + (lane & 3);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                const float2 y = __bfloat1622float2(v[4 * x]);
+                acc[x][2 * c] = fmaf(e, y.x, acc[x][2 * c]);
+                acc[x][2 * c + 1] = fmaf(e, y.y, acc[x][2 * c + 1]);
+            }
+        }
     }
 }
 
@@ -135,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_ker
                         make_float2(sc[x][2 * c], sc[x][2 * c + 1]);
         }
         __syncthreads();
+        bool minus_inf = false;   // the score of a key that is
         {   // softmax of row tid / 8, keys tid % 8 and 8 more
             const int r = tid >> 3, k = tid & 7;
             float v[2], mx = -INFINITY;
@@ -142,7 +176,10 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_ker
             for (int x = 0; x < 2; ++x) {
                 const float *f = sRed + r * kPR + k + 8 * x;
                 v[x] = (f[0] + f[16 * kPR]) + (f[2 * 16 * kPR] + f[3 * 16 * kPR]);
-                v[x] = sCell[k + 8 * x] >= 0 ? v[x] * p.scale_log2 : -INFINITY;
+                v[x] *= p.scale_log2;
+                const bool key = sCell[k + 8 * x] >= 0;
+                minus_inf = minus_inf || (key && v[x] == -INFINITY);
+                v[x] = key ? v[x] : -INFINITY;
                 mx = fmaxf(mx, v[x]);
             }
 #pragma unroll
@@ -167,8 +204,9 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 5 : 8) drafted_nodes_ker
             l = l * al + sum;
             if (k == 0) sAlpha[r] = al;
         }
-        __syncthreads();
-        {
+        if (__syncthreads_or(minus_inf)) {
+            add_values<DV, NT, PV>(p, sRed, sP, sAlpha, smem + (VK ? L::kOffK : L::kOffV), k0 > 0, acc);
+        } else {
             const float al0 = sAlpha[lane >> 2], al1 = sAlpha[(lane >> 2) + 8];
             uint32_t A[3][4];
             const uint32_t pa = smem_u32(sP) + ((lane & 15) * kPP + 8 * (lane >> 4)) * 2;
