@@ -763,7 +763,7 @@ int sfa_build_tree_maps(const int32_t *parent, const int32_t *cu_new, const int3
  * (trees of up to 256 nodes, a rule on sizes), keeps the weights to 2^-27; q8_0 caches are multiplied as
  * codes, the scores fp32 sums of exact products of a block each, weights and values as two bf16 halves
  * (2^-17 of each, 2^-15 of a product at most); a bf16 query is binary16 there, scaled by a power of two
- * (what is below 2^-35 of its largest value loses bits).  fp32 caches: queries, keys and values are two
+ * (a value below 2^-31 of its row's largest is off by 2^-39 of that at most, others are exact).  fp32 caches: queries, keys and values are two
  * binary16 halves each of a row scaled by a power of two (2^-22 of a value, what is below 2^-13 of its row's
  * largest 2^-35 of that), the three larger products of the four; a weight times its row of values is as
  * close against the largest such.

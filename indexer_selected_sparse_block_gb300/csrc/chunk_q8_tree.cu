@@ -6,8 +6,9 @@
 //           multiply-add: exact products, fp32 sums;
 //   o_id += sum_k p_ik (scale_kb code_kd)                weights and values as two bf16 parts each (2^-17), the
 //           three larger products of the four; a lane expands the values where it needs them, in registers.
-// bf16 queries are binary16 times a power of two of their row (a value below 2^-35 of the row's largest
-// loses bits).  No value is ever expanded in memory: a tile is its raw rows.
+// bf16 queries are binary16 times a power of two of their row, its largest value brought to 2^14 .. 2^15: exact down
+// to 2^-17, which is 2^-31 of the row's largest at most; a smaller value is off by 2^-25, 2^-39 of the largest.  No
+// value is ever expanded in memory: a tile is its raw rows.
 //
 // One CTA: 64 rows (query, head) of one KV head against 32 keys at a time, three tiles of raw rows by
 // asynchronous copies.  Scores: a warp has 16 rows and 16 keys.  Values: a warp has 64 dims of all rows (narrow
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
         if (t < n_tiles) fetch(k0 + t * kKeys, t);
         cp_async_commit();
     }
-    // queries: a warp has eight rows, each brought to a largest value of 2^10 .. 2^11
+    // queries: a warp has eight rows, each brought to a largest value of 2^14 .. 2^15
     for (int i = 0; i < kQ8Rows / 8; ++i) {
         const int row = warp * (kQ8Rows / 8) + i;
         constexpr int N = (DKQ + 63) / 64;   // pairs of a lane
@@ -168,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, DV == 512 ? 1 : 2) chunk_q8_tree_ker
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        // 2^e: a row of zeros, or with an infinity, keeps its values' size
-        const int e = top > 0.f && top < INFINITY ? max(-100, min(100, 10 - ((int)(__float_as_uint(top) >> 23) - 127))) : 0;
+        // 2^e, -113 to 126: a row of zeros, or with an infinity, keeps its values' size
+        const int e = top > 0.f && top < INFINITY ? min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
         const float f = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int x = 0; x < N; ++x)
