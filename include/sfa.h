@@ -656,9 +656,11 @@ int sfa_chunk_attend_paged(const void *Q, const void *K, const void *V, int dtyp
  * turned in pairs, pair j by the angle pos * f_j,
  *   (u, v) -> magnitude * (u cos - v sin, u sin + v cos),
  * pairs 0: pair j is dims (j, j + n_rot/2);  pairs 1: dims (2j, 2j + 1).
- * turns[j] is f_j / 2 pi in units of 2^-64 turns, rounded: the low 64 bits of pos * turns[j] are the
- * angle's fraction of a turn to 2^-34, however far the position, with no 64-bit floating-point
- * arithmetic on the device.  A plain struct of the caller's: it is read when a call is made.
+ * turns[j] is f_j / 2 pi, a quotient of doubles, in units of 2^-64 turns, rounded: off by
+ * |f_j| 2^-55 + 2^-65 turns at most.  The low 64 bits of pos * turns[j] are the angle's fraction of a
+ * turn, off by pos times that (f_j = 1: 2^-35 turns at position 2^20, 2^-24 at 2^31), with no 64-bit
+ * floating-point arithmetic on the device.  A plain struct of the caller's: it is read when a call is
+ * made.
  *
  * sfa_rope_frequencies -- n_rot/2 frequencies f_j = base^(-2j / n_rot) (radians a position, double),
  * scaled for contexts `factor` times as long as the trained ones:

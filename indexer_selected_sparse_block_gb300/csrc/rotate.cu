@@ -37,8 +37,8 @@ struct Params {
     uint64_t turns[SFA_MAX_ROT / 2];
 };
 
-// cos and sin of pos * f_j.  The product's low 64 bits are the fraction of a turn; what is left of the
-// nearest quarter turn, at most an eighth, is exact to fp32's last bit when it meets sinpi and cospi.
+// cos and sin of pos * f_j.  The product's low 64 bits are the fraction of a turn, as exact as the table's
+// entry; what is left of the nearest quarter turn, at most an eighth, meets sinpi and cospi rounded to fp32.
 __device__ __forceinline__ float2 turn(const Params &p, int pos, int j) {
     const uint64_t u = (uint64_t)(uint32_t)pos * p.turns[j];
     const uint32_t q = (uint32_t)((u + (1ull << 61)) >> 62);
@@ -311,9 +311,10 @@ extern "C" int sfa_rope_init(sfa_rope *rope, int n_rot, int pairs, const double 
     rope->pairs = pairs;
     rope->magnitude = (float)magnitude;
     for (int j = 0; j < n_rot / 2; ++j) {
-        const double t = freq[j] / 6.283185307179586476925, frac = t - floor(t);   // [0, 1]
-        const double u = frac * 0x1p64;
-        rope->turns[j] = u >= 0x1p64 ? 0 : (uint64_t)u;
+        // what is left of the nearest whole turn is exact, of either sign; -1/2 and 1/2 are the same
+        const double t = freq[j] / 6.283185307179586476925, rest = t - nearbyint(t);
+        const uint64_t u = (uint64_t)nearbyint(fabs(rest) * 0x1p64);
+        rope->turns[j] = rest < 0. ? 0 - u : u;
     }
     return SFA_OK;
 }
