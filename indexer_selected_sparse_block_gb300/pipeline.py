@@ -391,9 +391,11 @@ class SfaPagedCache:
     def attend_tree(self, Q, n_new_max: int, n_kv_max: int, scale: float, O, lse=None,
                     part: int = B.SFA_PART_ALL, workspace=None, stream=None):
         """O (and lse) of the drafted nodes over the cached tokens and their ancestors, or (part
-        SFA_PART_DRAFTED) over their ancestors alone."""
+        SFA_PART_DRAFTED) over their ancestors alone.  Q [n][h_q][dkq], O and lse of any n up to n_tok_cap that
+        holds the nodes."""
+        mask = self.tree_mask if Q.shape[0] >= self.tree_mask.shape[0] else self.tree_mask[:Q.shape[0]]
         B.sfa_tree_attend_paged(Q, self.K, self.V, self.page_table, self.page_size, self.cu_new,
-                                self.len_total, self.tree_mask, n_new_max, n_kv_max, scale, O, lse=lse,
+                                self.len_total, mask, n_new_max, n_kv_max, scale, O, lse=lse,
                                 part=part, workspace=workspace, dev_status=self.status, stream=stream)
         return O
 
