@@ -734,7 +734,8 @@ int sfa_rotate_rows(int n, const sfa_row_rotation *rotations, const sfa_rope *ro
  *        tree is node i itself or an ancestor.  Rows behind cu_new[n_seq] get 0.
  *   q_pos [n_rows] int32: a_s + the node's depth (0 for a root); rows behind the last node -1.
  *   cached_pos [n_rows] int32, nullable: a_s - 1, the position as which the sparse calls see a node
- *        (their kept blocks and tail then end with the cached tokens), -1 likewise.
+ *        (their kept blocks and tail then end with the cached tokens), -1 likewise; of a tree behind no
+ *        cached token it is -1 as well, where those calls give O = 0, lse = -inf and SFA_DEV_BAD_QUERY.
  * A node whose parent is none (SFA_DEV_BAD_TREE) is taken for a root.  Nodes past 32 * mask_words get an
  * empty mask and position -1 (SFA_DEV_BAD_TREE).  Offsets that do not ascend within [0, n_rows] give an
  * empty tree, and len_total[s] below its nodes' number a_s = 0 (SFA_DEV_BAD_QUERY).
