@@ -207,12 +207,12 @@ __device__ __forceinline__ void commit_lists(const CommitParams &p) {
     // length of sequence s afterwards, and the table entries [k0, k1) that it gives back
     auto after = [&](int s, int &k0, int &k1) {
         const Tree t = load_tree(p.cu, s, p.n_rows);
-        const int total = max(p.total[s], 0);
-        k0 = k1 = 0;
-        if (t.n > 0 && p.total[s] == 0) return 0;   // emptied since its tree was drafted
+        const int held = p.total[s], total = max(held, 0);
         bool bad;
-        const int limit = path_limit(p, s, t, bad);
-        if (t.bad || p.total[s] < t.n) flags |= SFA_DEV_BAD_QUERY;
+        const int most = path_limit(p, s, t, bad);
+        const bool gone = t.n > 0 && held == 0;   // emptied since its tree was drafted
+        const int limit = gone ? 0 : most;
+        if (!gone && (t.bad || held < t.n)) flags |= SFA_DEV_BAD_QUERY;
         int m = 0, last = -1;
         for (int k = 0; k < limit && m == k; k += kAhead) {
             int x[kAhead];
@@ -224,7 +224,7 @@ __device__ __forceinline__ void commit_lists(const CommitParams &p) {
                     ++m;
                 }
         }
-        if (bad || m < limit) flags |= SFA_DEV_BAD_TREE;
+        if (!gone && (bad || m < limit)) flags |= SFA_DEV_BAD_TREE;
         const int len = max(total - t.n, 0) + m;
         auto pages = [&](int n) { return n > 0 ? p.page_div.div(n - 1) + 1 : 0; };
         k0 = pages(len);
