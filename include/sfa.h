@@ -812,7 +812,8 @@ int sfa_tree_accept(const int32_t *parent, const int32_t *token, const int32_t *
  *   sequence by sequence, in their table's order, up to entry *free_head, the first entry not taken
  *   before; *free_head_out is it afterwards (may be free_head).  Their entries of page_table stay as they
  *   are, behind the sequence's end, until a later step takes pages for them.
- *   caches: base and row bytes (even) of [n_cells][...] arrays, rows of any kind, q8_0 ones included
+ *   caches: base (16-byte aligned) and row bytes (even, at most 2^24) of [n_cells][...] arrays, rows of any
+ *        kind, q8_0 ones included
  *   path, path_stride, n_acc: as sfa_tree_accept writes them, or any nodes of the tree in ascending
  *        order; it ends where they do not ascend or leave the tree, or at path_stride (SFA_DEV_BAD_TREE)
  * A sequence with nodes whose len_total[s] is 0 was emptied since its tree was drafted: nothing of it stays,

@@ -8,9 +8,10 @@
 //   O += P V:  each warp a quarter of the value dims, the weights as three bf16 parts (2^-27); keys with a score of
 //              minus infinity take their sixteen there one by one.
 // It is a chain of latencies a CTA (offsets, mask, page table, rows, scores, softmax, values) on the five CTAs that an
-// SM's shared memory and registers hold.  32 trees of 64 nodes, 16 heads, 576 wide, fp32 results: 28.5 us, 3.8 TB/s
-// of what has to move, Q and O (105 MB, 16 us); on tiles of all nodes 55.  Four CTAs 31.0; stores of 8 bytes a lane and
-// a barrier more 28.8; operands from global memory straight into registers, values by movmatrix, 38.
+// SM's shared memory and registers hold.  32 trees of 64 nodes, 16 heads, 576 wide, fp32 results: 28.8 us, 3.6 TB/s
+// of what has to move, Q and O (105 MB, 16 us); on tiles of all nodes 55.  Four CTAs 2.5 us more; stores of 8 bytes a
+// lane and a barrier more, 0.3; operands from global memory straight into registers, values by movmatrix, 10.  The
+// test for scores of minus infinity costs 0.3.
 #include "chunk_common.cuh"
 
 namespace sfa {
